@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/fadam.h.
+"""ctypes declarations of the C ABI in include/fadam.h and include/fadam_ops.h.
 
 Argument marshalling only: every step of the update runs in libfadam.so.
 Loading fails loudly when the library has not been built; there is no
@@ -99,6 +99,77 @@ SIGNATURES = [
     ("fadam_version", _i32, []),
 ]
 
+
+# ---- the training operators (fadam_ops.h) ----------------------------------------
+
+XENT_MEAN, XENT_ACCUMULATE = 1, 2
+WGRAD_ACCUMULATE = 1
+CHECKPOINT8_GROUP = 128
+BLOCK_NORM_MAX_WIDTH = 16384
+
+
+class Xent(ctypes.Structure):
+    """fadam_xent."""
+    _fields_ = ([(n, _vp) for n in ("x", "w", "targets", "loss", "row_loss", "lse", "grad_x",
+                                    "grad_w")]
+                + [(n, _i64) for n in ("rows", "width", "vocab", "x_stride", "w_stride",
+                                       "grad_x_stride", "grad_w_stride", "ignore_index",
+                                       "chunk_rows")]
+                + [("loss_scale", _f32), ("dtype", _i32), ("grad_w_dtype", _i32), ("flags", _u32)])
+
+
+class Kept8(ctypes.Structure):
+    """fadam_checkpoint8."""
+    _fields_ = [("codes", _vp), ("scales", _vp)]
+
+
+class Wgrad(ctypes.Structure):
+    """fadam_wgrad."""
+    _fields_ = ([("dy", _vp), ("x", Kept8), ("out", _vp)]
+                + [(n, _i64) for n in ("rows", "n", "width", "dy_stride", "out_stride")]
+                + [("dtype", _i32), ("out_dtype", _i32), ("flags", _u32), ("reserved", _u32)])
+
+
+class BlockNorm(ctypes.Structure):
+    """fadam_block_norm."""
+    _fields_ = ([(n, _vp) for n in ("f", "h", "post_weight", "pre_weight", "gate", "h_out",
+                                    "x_out", "rstd_post", "rstd_pre")]
+                + [("f_kept", Kept8), ("h_kept", Kept8)]
+                + [(n, _i64) for n in ("rows", "width", "gate_rows", "f_stride", "h_stride")]
+                + [("residual_scale", _f32), ("eps", _f32), ("block_dtype", _i32),
+                   ("residual_dtype", _i32), ("param_dtype", _i32), ("reserved", _i32)])
+
+
+class BlockNormGrad(ctypes.Structure):
+    """fadam_block_norm_grad."""
+    _fields_ = ([(n, _vp) for n in ("grad_h_out", "grad_x_out", "f", "h_out")]
+                + [("f_kept", Kept8), ("h_kept", Kept8)]
+                + [(n, _vp) for n in ("rstd_post", "rstd_pre", "post_weight", "pre_weight",
+                                      "gate", "grad_f", "grad_h", "grad_post_weight",
+                                      "grad_pre_weight", "grad_gate")]
+                + [(n, _i64) for n in ("rows", "width", "gate_rows", "grad_h_out_stride",
+                                       "grad_x_out_stride", "f_stride", "h_out_stride")]
+                + [("residual_scale", _f32), ("block_dtype", _i32), ("residual_dtype", _i32),
+                   ("param_dtype", _i32)])
+
+
+_size = ctypes.POINTER(ctypes.c_size_t)
+# (name, restype, argtypes) for every function fadam_ops.h declares
+OPS_SIGNATURES = [
+    ("fadam_xent_workspace", _i32, [ctypes.POINTER(Xent), _size]),
+    ("fadam_xent_run", _i32, [ctypes.POINTER(Xent), _vp, ctypes.c_size_t, _vp]),
+    ("fadam_checkpoint8_pack", _i32, [_vp, _i64, _i64, _i64, _i32, ctypes.POINTER(Kept8), _vp]),
+    ("fadam_checkpoint8_restore", _i32, [ctypes.POINTER(Kept8), _i64, _i64, _vp, _i64, _i32, _vp]),
+    ("fadam_checkpoint8_wgrad_workspace", _i32, [ctypes.POINTER(Wgrad), _size]),
+    ("fadam_checkpoint8_wgrad", _i32, [ctypes.POINTER(Wgrad), _vp, ctypes.c_size_t, _vp]),
+    ("fadam_block_norm_forward", _i32, [ctypes.POINTER(BlockNorm), _vp]),
+    ("fadam_block_norm_backward_workspace", _i32, [ctypes.POINTER(BlockNormGrad), _size]),
+    ("fadam_block_norm_backward", _i32, [ctypes.POINTER(BlockNormGrad), _vp, ctypes.c_size_t,
+                                         _vp]),
+    ("fadam_ops_status", _i32, [ctypes.POINTER(_i32)]),
+    ("fadam_ops_last_error", ctypes.c_char_p, []),
+]
+
 _LIB = None
 
 
@@ -124,7 +195,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it first with "
                 "`python -c 'import __graft_entry__ as g; g.build()'` (no fallback path exists)")
         L = ctypes.CDLL(LIB_PATH)
-        for name, res, args in SIGNATURES:
+        for name, res, args in SIGNATURES + OPS_SIGNATURES:
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -135,3 +206,8 @@ def lib() -> ctypes.CDLL:
 def check(status: int, where: str) -> None:
     if status != OK:
         raise FadamError(status, where, lib().fadam_last_error().decode())
+
+
+def check_ops(status: int, where: str) -> None:
+    if status != OK:
+        raise FadamError(status, where, lib().fadam_ops_last_error().decode())

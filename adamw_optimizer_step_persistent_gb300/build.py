@@ -24,6 +24,12 @@ SOURCES = ["fadam_plan.cu"] + [f"fadam_kernels_s{s}_g{g}.cu"
     f"fadam_kernels_{kind}s{s}_g{g}.cu" for kind in ("scaled_", "recip_", "recip_scaled_")
     for s in ("bf16", "f16") for g in ("f32", "bf16", "f16")]
 HEADERS = ["fadam_internal.h", "fadam_kernel.cuh"]
+# the training operators (fadam_ops.h), in the same library
+OPS_SOURCES = [f"ops/{f}.cu" for f in ("ops_host", "xent", "checkpoint8", "block_norm", "block_norm_bf16",
+                                       "block_norm_f16", "block_norm_f32")]
+OPS_HEADERS = [f"ops/{f}" for f in ("ops_internal.h", "ops_device.cuh", "gemm.cuh",
+                                    "gemm_store.cuh", "rows.cuh", "block_norm.cuh",
+                                    "block_norm_internal.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -43,8 +49,8 @@ def _stale(lib: str) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps.append(os.path.join(INCLUDE, "fadam.h"))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + OPS_SOURCES + OPS_HEADERS]
+    deps += [os.path.join(INCLUDE, f) for f in ("fadam.h", "fadam_ops.h")]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -64,8 +70,8 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB
     extra += [f"-D{d}" for d in defines]
     procs = []
     objs = []
-    for src in SOURCES:
-        obj = os.path.join(out_dir, os.path.splitext(src)[0] + ".o")
+    for src in OPS_SOURCES + SOURCES:
+        obj = os.path.join(out_dir, os.path.splitext(os.path.basename(src))[0] + ".o")
         objs.append(obj)
         cmd = [nvcc, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c",
                os.path.join(CSRC, src), "-o", obj]

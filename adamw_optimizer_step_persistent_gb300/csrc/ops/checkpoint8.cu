@@ -1,0 +1,238 @@
+// Activations kept in 8 bits: groups of 128 of a row with one fp32 scale, and
+// the weight gradient of a linear layer from its input's checkpoint.
+//
+// Packing and restoring are one pass over memory: a thread takes eight
+// elements (16 bytes in, 8 bytes out for 16-bit activations), half a warp a
+// group, whose largest magnitude it finds with four shuffles.
+#include "gemm_store.cuh"
+#include "rows.cuh"
+
+namespace fadam_ops {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Threads take consecutive groups of eight of the matrix, rows padded to
+// whole warps (a warp never spans two rows).
+template <class E>
+__global__ void __launch_bounds__(kThreads)
+    pack_kernel(const E* x, int64_t rows, int width, int64_t x_stride, int8_t* codes, float* scales,
+                bool wide) {
+  const int per_row = (width + 255) / 256 * 32;  // threads of a row
+  const int groups = (width + kGroup - 1) / kGroup;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < rows * per_row;
+       i += int64_t(gridDim.x) * kThreads) {
+    const int64_t row = i / per_row;
+    const int col = int(i - row * per_row) * 8;
+    float v[8];
+    load8<E>(x + row * x_stride, col, width, wide, v);
+    keep8(v, codes + row * width, scales + row * groups, col, width, wide);
+  }
+}
+
+template <class E>
+__global__ void __launch_bounds__(kThreads)
+    restore_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
+                   int64_t x_stride, bool wide) {
+  const int per_row = (width + 7) / 8;
+  const int groups = (width + kGroup - 1) / kGroup;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < rows * per_row;
+       i += int64_t(gridDim.x) * kThreads) {
+    const int64_t row = i / per_row;
+    const int col = int(i - row * per_row) * 8;
+    float v[8];
+    kept8(codes + row * width, scales + row * groups, col, width, wide, v);
+    store_row8<E>(x + row * x_stride, col, width, wide, v);
+  }
+}
+
+unsigned grid_for(int64_t threads) {
+  const int64_t blocks = ceil_div(threads, kThreads);
+  return unsigned(blocks < 152 * 64 ? blocks : 152 * 64);
+}
+
+template <class E>
+fadam_status pack(const void* x, int64_t rows, int64_t width, int64_t stride,
+                  const fadam_checkpoint8& out, cudaStream_t stream) {
+  const bool wide = width % 8 == 0 && !misaligned(x, 16) && stride * sizeof(E) % 16 == 0 &&
+                    !misaligned(out.codes, 8);
+  pack_kernel<E><<<grid_for(rows * round_up(width, 256) / 8), kThreads, 0, stream>>>(
+      static_cast<const E*>(x), rows, int(width), stride, out.codes, out.scales, wide);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "checkpoint8 pack launch");
+}
+
+template <class E>
+fadam_status restore(const fadam_checkpoint8& in, int64_t rows, int64_t width, void* x,
+                     int64_t stride, cudaStream_t stream) {
+  const bool wide = width % 8 == 0 && !misaligned(x, 16) && stride * sizeof(E) % 16 == 0 &&
+                    !misaligned(in.codes, 8);
+  restore_kernel<E><<<grid_for(rows * ceil_div(width, 8)), kThreads, 0, stream>>>(
+      in.codes, in.scales, rows, int(width), static_cast<E*>(x), stride, wide);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "checkpoint8 restore launch");
+}
+
+fadam_status check_matrix(const void* x, int64_t rows, int64_t width, int64_t stride, int32_t dtype,
+                          const fadam_checkpoint8* kept) {
+  if (elem_size(dtype) == 0) return fail(FADAM_EDTYPE, "dtype %d is not fp32, bf16 or fp16", dtype);
+  if (rows < 0 || width < 1) return fail(FADAM_EINVAL, "%lld rows of width %lld", (long long)rows,
+                                         (long long)width);
+  if (rows > int64_t(1) << 30 || width > int64_t(1) << 30)
+    return fail(FADAM_ELIMIT, "rows or width beyond 2^30");
+  if (stride < width) return fail(FADAM_EINVAL, "stride %lld is below the width %lld",
+                                  (long long)stride, (long long)width);
+  if (!kept) return fail(FADAM_EINVAL, "the checkpoint is NULL");
+  if (rows > 0 && (!x || !kept->codes || !kept->scales))
+    return fail(FADAM_EINVAL, "x, codes and scales must be non-NULL");
+  if (misaligned(x, elem_size(dtype)) || misaligned(kept->scales, 4))
+    return fail(FADAM_EALIGN, "a pointer is not aligned to its element size");
+  return FADAM_OK;
+}
+
+// ---- the weight gradient -----------------------------------------------------------
+
+struct Layout {
+  int splits;
+  int64_t x_ld, dy_ld;
+  void* x;        // the restored checkpoint
+  void* dy_rows;  // an aligned copy of dy, where its own rows are not
+  float* parts;
+  size_t bytes;
+};
+
+Layout layout(const fadam_wgrad& d, char* base, int sm_count) {
+  Layout l{};
+  Carver c{base};
+  l.splits = choose_splits(d.n, d.width, d.rows, sm_count / 2);
+  l.x_ld = round_up(d.width, 8);
+  l.dy_ld = d.dy_stride;
+  l.x = c.take(2 * d.rows * l.x_ld);
+  if (!bulk_readable(d.dy, d.dy_stride)) {
+    l.dy_ld = round_up(d.n, 8);
+    l.dy_rows = c.take(2 * d.rows * l.dy_ld);
+  }
+  if (l.splits > 1) l.parts = static_cast<float*>(c.take(4 * int64_t(l.splits) * d.n * d.width));
+  l.bytes = c.used;
+  return l;
+}
+
+template <class E>
+__global__ void __launch_bounds__(kThreads)
+    align_kernel(const E* from, int64_t from_ld, E* to, int64_t to_ld, int64_t rows, int64_t width) {
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+    for (int64_t i = threadIdx.x; i < width; i += kThreads) to[row * to_ld + i] = from[row * from_ld + i];
+}
+
+template <class T, class Out>
+fadam_status run(const fadam_wgrad& d, const Layout& l, const DeviceFacts& dev, cudaStream_t stream) {
+  using E = typename T::type;
+  fadam_status st;
+  const void* dy = d.dy;
+  if (l.dy_rows) {
+    align_kernel<E><<<unsigned(d.rows < 8192 ? d.rows : 8192), kThreads, 0, stream>>>(
+        static_cast<const E*>(d.dy), d.dy_stride, static_cast<E*>(l.dy_rows), l.dy_ld, d.rows, d.n);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "row copy launch");
+    dy = l.dy_rows;
+  }
+  if ((st = restore<E>(d.x, d.rows, d.width, l.x, l.x_ld, stream))) return st;
+  CUtensorMap a, b;
+  if ((st = matrix_map(&a, dy, d.rows, d.n, l.dy_ld, box_rows(true)))) return st;
+  if ((st = matrix_map(&b, l.x, d.rows, d.width, l.x_ld, box_rows(true)))) return st;
+  StoreArgs s{};
+  s.out = d.out;
+  s.ld = d.out_stride;
+  s.m = d.n;
+  s.n = d.width;
+  s.constant = 1.0f;
+  s.accumulate = (d.flags & FADAM_WGRAD_ACCUMULATE) != 0;
+  s.wide = wide_stores(d.out, d.out_stride, sizeof(typename Out::type));
+  const GemmShape shape = gemm_shape(d.n, d.width, d.rows, l.splits, 8, dev.status);
+  return store_product<T, true, true, Out>(a, b, shape, s, l.parts, dev.sm_count, stream);
+}
+
+fadam_status check(const fadam_wgrad* d) {
+  if (!d) return fail(FADAM_EINVAL, "the descriptor is NULL");
+  if (!is_16bit(d->dtype)) return fail(FADAM_EDTYPE, "dtype %d is not bf16 or fp16", d->dtype);
+  if (d->out_dtype != d->dtype && d->out_dtype != FADAM_DT_F32)
+    return fail(FADAM_EDTYPE, "out dtype %d is neither fp32 nor dy's %d", d->out_dtype, d->dtype);
+  if (d->flags & ~FADAM_WGRAD_ACCUMULATE) return fail(FADAM_EINVAL, "unknown flag bits 0x%x", d->flags);
+  const fadam_status st = check_matrix(d->dy, d->rows, d->n, d->dy_stride, d->dtype, &d->x);
+  if (st) return st;
+  if (d->width < 1 || d->out_stride < d->width)
+    return fail(FADAM_EINVAL, "width %lld, out stride %lld", (long long)d->width,
+                (long long)d->out_stride);
+  if (d->width > int64_t(1) << 30) return fail(FADAM_ELIMIT, "width beyond 2^30");
+  if (!d->out) return fail(FADAM_EINVAL, "out is NULL");
+  if (misaligned(d->out, elem_size(d->out_dtype)))
+    return fail(FADAM_EALIGN, "a pointer is not aligned to its element size");
+  return FADAM_OK;
+}
+
+}  // namespace
+}  // namespace fadam_ops
+
+using namespace fadam_ops;
+
+extern "C" fadam_status fadam_checkpoint8_pack(const void* x, int64_t rows, int64_t width,
+                                               int64_t x_stride, int32_t dtype,
+                                               const fadam_checkpoint8* out, fadam_stream stream_) {
+  clear_error();
+  const fadam_status st = check_matrix(x, rows, width, x_stride, dtype, out);
+  if (st || rows == 0) return st;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype == FADAM_DT_BF16) return pack<__nv_bfloat16>(x, rows, width, x_stride, *out, stream);
+  if (dtype == FADAM_DT_F16) return pack<__half>(x, rows, width, x_stride, *out, stream);
+  return pack<float>(x, rows, width, x_stride, *out, stream);
+}
+
+extern "C" fadam_status fadam_checkpoint8_restore(const fadam_checkpoint8* in, int64_t rows,
+                                                  int64_t width, void* x, int64_t x_stride,
+                                                  int32_t dtype, fadam_stream stream_) {
+  clear_error();
+  const fadam_status st = check_matrix(x, rows, width, x_stride, dtype, in);
+  if (st || rows == 0) return st;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype == FADAM_DT_BF16) return restore<__nv_bfloat16>(*in, rows, width, x, x_stride, stream);
+  if (dtype == FADAM_DT_F16) return restore<__half>(*in, rows, width, x, x_stride, stream);
+  return restore<float>(*in, rows, width, x, x_stride, stream);
+}
+
+extern "C" fadam_status fadam_checkpoint8_wgrad_workspace(const fadam_wgrad* desc, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FADAM_EINVAL, "bytes is NULL");
+  fadam_status st = check(desc);
+  if (st) return st;
+  DeviceFacts dev;
+  if ((st = device_facts(&dev))) return st;
+  *bytes = desc->rows == 0 ? 0 : layout(*desc, nullptr, dev.sm_count).bytes;
+  return FADAM_OK;
+}
+
+extern "C" fadam_status fadam_checkpoint8_wgrad(const fadam_wgrad* desc, void* workspace,
+                                                size_t bytes, fadam_stream stream_) {
+  clear_error();
+  fadam_status st = check(desc);
+  if (st) return st;
+  const fadam_wgrad& d = *desc;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (d.rows == 0) {
+    if (d.flags & FADAM_WGRAD_ACCUMULATE) return FADAM_OK;
+    const int size = elem_size(d.out_dtype);
+    const cudaError_t e =
+        cudaMemset2DAsync(d.out, d.out_stride * size, 0, d.width * size, d.n, stream);
+    return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "cudaMemset2DAsync");
+  }
+  DeviceFacts dev;
+  if ((st = device_facts(&dev))) return st;
+  const Layout l = layout(d, static_cast<char*>(workspace), dev.sm_count);
+  if (!workspace || bytes < l.bytes)
+    return fail(FADAM_EINVAL, "the workspace has %zu bytes, %zu are needed",
+                workspace ? bytes : size_t(0), l.bytes);
+  if (misaligned(workspace, 256)) return fail(FADAM_EALIGN, "the workspace is not 256-byte aligned");
+  const bool wide = d.out_dtype == FADAM_DT_F32;
+  if (d.dtype == FADAM_DT_BF16)
+    return wide ? run<BF16, F32>(d, l, dev, stream) : run<BF16, BF16>(d, l, dev, stream);
+  return wide ? run<F16, F32>(d, l, dev, stream) : run<F16, F16>(d, l, dev, stream);
+}

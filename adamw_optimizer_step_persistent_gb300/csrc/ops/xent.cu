@@ -1,0 +1,460 @@
+// Softmax cross entropy of x W^T over a large vocabulary, with its gradients.
+//
+//   z = x W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,y(t)
+//   dz_tv = s (exp(z_tv - lse_t) - [v = y(t)]),  dx = dz W,  dW = dz^T x
+//
+// Three products on the tensor cores (gemm.cuh).  The first never writes a
+// logit: a piece of 128 of a row's logits is reduced in registers to its
+// maximum and its sum of exponentials, and (for the gradients) its
+// exponentials relative to that maximum are kept in 16 bits.  A second kernel
+// joins a row's pieces to its lse and turns the kept exponentials into dz in
+// place, and two more products give dx and dW: 6 T V D operations where a
+// second computation of the logits would make it 8.  The kept exponentials
+// are those of a chunk of rows, so the scratch memory is bounded however many
+// rows there are.
+//
+// Roundings to 16 bits: the exponentials are kept in fp16 whatever the
+// inputs' type (they are in [0, 1]; 2^-12 relative down to 6e-5 of the piece's
+// largest, 3e-8 absolute below that), dz once more in the inputs' type,
+// because the tensor cores take it from there.  fp16 dz is held times 2^15
+// (|dz| <= 1 before s), so that a probability of 1e-8 still has all its bits.
+// Everything else (products' sums, maxima, sums, lse, loss) is fp32; the
+// factor s is applied to the fp32 sums.
+#include "gemm_store.cuh"
+
+namespace fadam_ops {
+namespace {
+
+struct Control {
+  unsigned int finished;  // blocks of the current row launch
+  float scale;            // loss_scale / (rows that count, if the mean is taken)
+};
+
+// What the first product's epilogue needs to reduce the logits.
+struct LogitEpilogue {
+  int64_t rows, vocab, pieces;
+  const int64_t* targets;
+  float2* stats;     // [rows, pieces]: maximum and sum of exponentials
+  float* target_z;   // [rows]
+  __half* kept;      // [rows, pitch] or NULL
+  int64_t pitch;
+
+  __device__ __forceinline__ void operator()(float (&v)[kPiece], int64_t row, int64_t col,
+                                             int) const {
+    if (row >= rows || col >= vocab) return;
+    const int width = int(min(int64_t(kPiece), vocab - col));
+    const int64_t at = targets[row] - col;
+    if (at >= 0 && at < width) {
+      float z = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) z = i == at ? v[i] : z;
+      target_z[row] = z;
+    }
+    if (width < kPiece) {
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i)
+        if (i >= width) v[i] = -INFINITY;
+    }
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < kPiece; ++i) top = fmaxf(top, v[i]);
+    const float base = top == -INFINITY ? 0.0f : top;  // nothing above -inf: all terms are 0
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      v[i] = exp2f((v[i] - base) * 1.4426950408889634f);
+      sum += v[i];
+    }
+    stats[row * pieces + col / kPiece] = make_float2(top, sum);
+    if (kept) {
+      uint4* to = reinterpret_cast<uint4*>(kept + row * pitch + col);
+#pragma unroll
+      for (int i = 0; i < kPiece; i += 8)
+        to[i / 8] = make_uint4(pack2<__half>(v[i], v[i + 1]), pack2<__half>(v[i + 2], v[i + 3]),
+                               pack2<__half>(v[i + 4], v[i + 5]), pack2<__half>(v[i + 6], v[i + 7]));
+    }
+  }
+};
+
+struct RowArgs {
+  int64_t rows, vocab, pieces, pitch, width, x_ld, kept_x_ld;
+  int64_t first_row, all_rows;   // of this chunk, and of the whole call
+  const float2* stats;
+  const float* target_z;
+  const int64_t* targets;        // of the whole call
+  int64_t ignore_index;
+  float loss_scale;
+  int mean;
+  float* loss;
+  float* row_loss;
+  float* lse;
+  void* dz;                      // [rows, pitch]: exponentials in, dz out; or NULL
+  const void* x;                 // [rows, width]
+  void* kept_x;                  // x with ignored rows zero, or NULL
+  float dz_scale;
+  Control* control;
+};
+
+constexpr int kRowThreads = 256;
+
+__device__ __forceinline__ float block_sum(float v, float* shared) {
+#pragma unroll
+  for (int i = 16; i; i /= 2) v += __shfl_xor_sync(~0u, v, i);
+  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kRowThreads / 32; ++i) s += shared[i];
+  __syncthreads();
+  return s;
+}
+__device__ __forceinline__ float block_max(float v, float* shared) {
+#pragma unroll
+  for (int i = 16; i; i /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, i));
+  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
+  __syncthreads();
+  float s = shared[0];
+#pragma unroll
+  for (int i = 1; i < kRowThreads / 32; ++i) s = fmaxf(s, shared[i]);
+  __syncthreads();
+  return s;
+}
+
+// One block per row: lse and loss from the row's pieces, dz in place of the
+// kept exponentials, and the row of x that dW's product reads (a row that is
+// ignored must not reach dW even where x is not finite: 0 * inf is NaN).
+// The last block of a chunk adds up the losses in a fixed order.
+template <class T>
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
+  using E = typename T::type;
+  __shared__ float shared[kRowThreads / 32];
+  __shared__ double sums[kRowThreads];
+  __shared__ int64_t counts[kRowThreads];
+  __shared__ bool last;
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const float2* st = a.stats + row * a.pieces;
+
+  float top = -INFINITY;
+  for (int64_t i = tid; i < a.pieces; i += kRowThreads) top = fmaxf(top, st[i].x);
+  top = block_max(top, shared);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  for (int64_t i = tid; i < a.pieces; i += kRowThreads) {
+    const float2 p = st[i];
+    sum += p.x == -INFINITY ? p.y : p.y * expf(p.x - base);
+  }
+  sum = block_sum(sum, shared);
+  const float lse = base + logf(sum);
+
+  const int64_t target = a.targets[a.first_row + row];
+  const bool ignored = target == a.ignore_index;
+  const bool valid = target >= 0 && target < a.vocab;
+  // a target outside the vocabulary shows as NaN in the loss and the gradients
+  if (tid == 0) {
+    a.lse[a.first_row + row] = lse;
+    a.row_loss[a.first_row + row] = ignored ? 0.0f : valid ? lse - a.target_z[row] : NAN;
+  }
+
+  if (a.dz) {
+    uint4* dz = reinterpret_cast<uint4*>(static_cast<__half*>(a.dz) + row * a.pitch);
+    for (int64_t c = tid; c * 8 < a.vocab; c += kRowThreads) {
+      const uint4 raw = dz[c];
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      const float peak = st[c * 8 / kPiece].x;
+      const float f = !valid && !ignored ? NAN
+                      : peak == -INFINITY ? a.dz_scale : a.dz_scale * expf(peak - lse);
+      uint32_t out[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 p = unpack2<__half>(w[i]);
+        p.x *= f;
+        p.y *= f;
+        if (target == c * 8 + 2 * i) p.x -= a.dz_scale;
+        if (target == c * 8 + 2 * i + 1) p.y -= a.dz_scale;
+        out[i] = ignored ? 0u : pack2<E>(p.x, p.y);
+      }
+      dz[c] = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
+  if (a.kept_x) {
+    const E* from = static_cast<const E*>(a.x) + row * a.x_ld;
+    E* to = static_cast<E*>(a.kept_x) + row * a.kept_x_ld;
+    for (int64_t i = tid; i < a.width; i += kRowThreads)
+      to[i] = ignored ? from_float<E>(0.0f) : from[i];
+  }
+
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(&a.control->finished, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  // the losses of the rows so far (of all of them in the last chunk), and how
+  // many rows of the whole call count
+  __threadfence();
+  double total = 0.0;
+  int64_t count = 0;
+  for (int64_t i = tid; i < a.first_row + a.rows; i += kRowThreads) total += __ldcg(a.row_loss + i);
+  for (int64_t i = tid; i < a.all_rows; i += kRowThreads) count += a.targets[i] != a.ignore_index;
+  sums[tid] = total;
+  counts[tid] = count;
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 1; i < kRowThreads; ++i) {
+      total += sums[i];
+      count += counts[i];
+    }
+    const double share = a.mean ? 1.0 / double(count > 0 ? count : 1) : 1.0;
+    *a.loss = float(total * share);
+    a.control->scale = float(a.loss_scale * share);
+    a.control->finished = 0;
+  }
+}
+
+// Rows copied to where bulk copies can read them (16-byte aligned rows).
+template <class E>
+__global__ void __launch_bounds__(256) align_rows_kernel(const E* from, int64_t from_ld, E* to,
+                                                         int64_t to_ld, int64_t rows, int64_t width) {
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+    for (int64_t i = threadIdx.x; i < width; i += 256) to[row * to_ld + i] = from[row * from_ld + i];
+}
+
+// ---- host ------------------------------------------------------------------------
+
+struct Layout {
+  int64_t chunk, chunks, pieces, pitch, width_ld;
+  int splits;  // of dx's product
+  Control* control;
+  float2* stats;
+  float* target_z;
+  void* kept;
+  void* kept_x;
+  void* x_rows;   // aligned copies, where the caller's rows are not
+  void* w_rows;
+  float* parts;
+  float* carry;
+  size_t bytes;
+};
+
+// Rows of one chunk: as many as keep the exponentials within 4 GiB, in whole
+// tiles.  (One chunk of 8192 rows x 131072 entries is 2 GiB; a second chunk
+// costs dW's fp32 sum one more trip through memory.)
+int64_t chunk_rows(const fadam_xent& d) {
+  if (!d.grad_x && !d.grad_w) return d.rows;
+  if (d.chunk_rows > 0) return d.chunk_rows < d.rows ? d.chunk_rows : d.rows;
+  const int64_t fit = (int64_t(4) << 30) / (round_up(d.vocab, kPiece) * 2);
+  const int64_t whole = fit / kTileM * kTileM;
+  const int64_t chunk = whole < kTileM ? kTileM : whole;
+  return chunk < d.rows ? chunk : d.rows;
+}
+
+Layout layout(const fadam_xent& d, char* base, int sm_count) {
+  Layout l{};
+  Carver c{base};
+  const bool grads = d.grad_x || d.grad_w;
+  l.chunk = chunk_rows(d);
+  l.chunks = ceil_div(d.rows, l.chunk);
+  l.pieces = ceil_div(d.vocab, kPiece);
+  l.pitch = l.pieces * kPiece;
+  l.width_ld = round_up(d.width, 8);
+  l.splits = choose_splits(l.chunk, d.width, d.vocab, sm_count / 2);
+  l.control = static_cast<Control*>(c.take(sizeof(Control)));
+  l.stats = static_cast<float2*>(c.take(sizeof(float2) * l.chunk * l.pieces));
+  l.target_z = static_cast<float*>(c.take(sizeof(float) * l.chunk));
+  if (grads) l.kept = c.take(2 * l.chunk * l.pitch);
+  if (d.grad_w) l.kept_x = c.take(2 * l.chunk * l.width_ld);
+  if (!bulk_readable(d.x, d.x_stride)) l.x_rows = c.take(2 * d.rows * l.width_ld);
+  if (!bulk_readable(d.w, d.w_stride)) l.w_rows = c.take(2 * d.vocab * l.width_ld);
+  if (d.grad_x && l.splits > 1)
+    l.parts = static_cast<float*>(c.take(4 * int64_t(l.splits) * l.chunk * d.width));
+  if (d.grad_w && l.chunks > 1) l.carry = static_cast<float*>(c.take(4 * d.vocab * d.width));
+  l.bytes = c.used;
+  return l;
+}
+
+template <class T>
+fadam_status align_rows(const void* from, int64_t from_ld, void* to, int64_t to_ld, int64_t rows,
+                        int64_t width, cudaStream_t stream) {
+  using E = typename T::type;
+  align_rows_kernel<E><<<unsigned(rows < 8192 ? rows : 8192), 256, 0, stream>>>(
+      static_cast<const E*>(from), from_ld, static_cast<E*>(to), to_ld, rows, width);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "row copy launch");
+}
+
+template <class T, class OutW>
+fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, cudaStream_t stream) {
+  using E = typename T::type;
+  const bool grads = d.grad_x || d.grad_w;
+  cudaError_t e = cudaMemsetAsync(l.control, 0, sizeof(Control), stream);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+  const E* x = static_cast<const E*>(d.x);
+  const E* w = static_cast<const E*>(d.w);
+  int64_t x_ld = d.x_stride, w_ld = d.w_stride;
+  fadam_status st;
+  if (l.x_rows) {
+    if ((st = align_rows<T>(d.x, d.x_stride, l.x_rows, l.width_ld, d.rows, d.width, stream))) return st;
+    x = static_cast<const E*>(l.x_rows);
+    x_ld = l.width_ld;
+  }
+  if (l.w_rows) {
+    if ((st = align_rows<T>(d.w, d.w_stride, l.w_rows, l.width_ld, d.vocab, d.width, stream))) return st;
+    w = static_cast<const E*>(l.w_rows);
+    w_ld = l.width_ld;
+  }
+  CUtensorMap w_k, w_mn;
+  if ((st = matrix_map(&w_k, w, d.vocab, d.width, w_ld, box_rows(false)))) return st;
+  if ((st = matrix_map(&w_mn, w, d.vocab, d.width, w_ld, box_rows(true)))) return st;
+  // fp16 dz is held times 2^15
+  const float dz_scale = T::code == FADAM_DT_F16 ? 32768.0f : 1.0f;
+
+  for (int64_t first = 0; first < d.rows; first += l.chunk) {
+    const int64_t rows = d.rows - first < l.chunk ? d.rows - first : l.chunk;
+    const bool last_chunk = first + rows == d.rows;
+    CUtensorMap map;
+    if ((st = matrix_map(&map, x + first * x_ld, rows, d.width, x_ld, box_rows(false)))) return st;
+    LogitEpilogue epi{rows, d.vocab, l.pieces, d.targets + first, l.stats, l.target_z,
+                      static_cast<__half*>(l.kept), l.pitch};
+    GemmShape shape = gemm_shape(rows, d.vocab, d.width, 1, 8, dev.status);
+    if ((st = launch_gemm<T, false, false>(map, w_k, shape, epi, dev.sm_count, stream))) return st;
+
+    RowArgs r{};
+    r.rows = rows;
+    r.vocab = d.vocab;
+    r.pieces = l.pieces;
+    r.pitch = l.pitch;
+    r.width = d.width;
+    r.x_ld = x_ld;
+    r.kept_x_ld = l.width_ld;
+    r.first_row = first;
+    r.all_rows = d.rows;
+    r.stats = l.stats;
+    r.target_z = l.target_z;
+    r.targets = d.targets;
+    r.ignore_index = d.ignore_index;
+    r.loss_scale = d.loss_scale;
+    r.mean = (d.flags & FADAM_XENT_MEAN) != 0;
+    r.loss = d.loss;
+    r.row_loss = d.row_loss;
+    r.lse = d.lse;
+    r.dz = l.kept;
+    r.x = x + first * x_ld;
+    r.kept_x = l.kept_x;
+    r.dz_scale = dz_scale;
+    r.control = l.control;
+    row_kernel<T><<<unsigned(rows), kRowThreads, 0, stream>>>(r);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "row launch");
+    if (!grads) continue;
+
+    if (d.grad_x) {
+      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(false)))) return st;
+      StoreArgs s{};
+      s.out = static_cast<E*>(d.grad_x) + first * d.grad_x_stride;
+      s.ld = d.grad_x_stride;
+      s.m = rows;
+      s.n = d.width;
+      s.scale = &l.control->scale;
+      s.constant = 1.0f / dz_scale;
+      s.targets = d.targets + first;
+      s.ignore_index = d.ignore_index;
+      s.wide = wide_stores(s.out, s.ld, 2);
+      shape = gemm_shape(rows, d.width, d.vocab, l.splits, 8, dev.status);
+      if ((st = store_product<T, false, true, T>(map, w_mn, shape, s, l.parts, dev.sm_count, stream)))
+        return st;
+    }
+    if (d.grad_w) {
+      CUtensorMap x_mn;
+      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(true)))) return st;
+      if ((st = matrix_map(&x_mn, l.kept_x, rows, d.width, l.width_ld, box_rows(true)))) return st;
+      StoreArgs s{};
+      s.out = d.grad_w;
+      s.ld = d.grad_w_stride;
+      s.m = d.vocab;
+      s.n = d.width;
+      s.scale = &l.control->scale;
+      s.constant = 1.0f / dz_scale;
+      s.carry = l.carry;
+      s.read_carry = first > 0;
+      s.write_carry = !last_chunk;
+      s.accumulate = (d.flags & FADAM_XENT_ACCUMULATE) != 0;
+      s.wide = wide_stores(s.out, s.ld, sizeof(typename OutW::type));
+      shape = gemm_shape(d.vocab, d.width, rows, 1, 8, dev.status);
+      if ((st = store_product<T, true, true, OutW>(map, x_mn, shape, s, nullptr, dev.sm_count, stream)))
+        return st;
+    }
+  }
+  return FADAM_OK;
+}
+
+fadam_status check(const fadam_xent* d) {
+  if (!d) return fail(FADAM_EINVAL, "the descriptor is NULL");
+  if (!is_16bit(d->dtype)) return fail(FADAM_EDTYPE, "dtype %d is not bf16 or fp16", d->dtype);
+  if (d->grad_w && d->grad_w_dtype != d->dtype && d->grad_w_dtype != FADAM_DT_F32)
+    return fail(FADAM_EDTYPE, "grad_w dtype %d is neither fp32 nor the inputs' %d", d->grad_w_dtype,
+                d->dtype);
+  if (d->flags & ~(FADAM_XENT_MEAN | FADAM_XENT_ACCUMULATE))
+    return fail(FADAM_EINVAL, "unknown flag bits 0x%x", d->flags);
+  if (d->rows < 0 || d->width < 1 || d->vocab < 1 || d->chunk_rows < 0)
+    return fail(FADAM_EINVAL, "%lld rows of width %lld over a vocabulary of %lld, chunk %lld",
+                (long long)d->rows, (long long)d->width, (long long)d->vocab,
+                (long long)d->chunk_rows);
+  const int64_t most = int64_t(1) << 30;
+  if (d->rows > most || d->width > most || d->vocab > most)
+    return fail(FADAM_ELIMIT, "rows, width or vocab beyond 2^30");
+  if (d->x_stride < d->width || d->w_stride < d->width ||
+      (d->grad_x && d->grad_x_stride < d->width) || (d->grad_w && d->grad_w_stride < d->width))
+    return fail(FADAM_EINVAL, "a row stride is below the width %lld", (long long)d->width);
+  if (!d->loss || !d->w || (d->rows > 0 && (!d->x || !d->targets || !d->row_loss || !d->lse)))
+    return fail(FADAM_EINVAL, "x, w, targets, loss, row_loss and lse must be non-NULL");
+  if (misaligned(d->x, 2) || misaligned(d->w, 2) || misaligned(d->grad_x, 2) ||
+      misaligned(d->grad_w, elem_size(d->grad_w ? d->grad_w_dtype : d->dtype)) ||
+      misaligned(d->targets, 8) || misaligned(d->loss, 4) || misaligned(d->row_loss, 4) ||
+      misaligned(d->lse, 4))
+    return fail(FADAM_EALIGN, "a pointer is not aligned to its element size");
+  if (!(d->loss_scale == d->loss_scale) || d->loss_scale - d->loss_scale != 0.0f)
+    return fail(FADAM_EINVAL, "loss_scale is not finite");
+  return FADAM_OK;
+}
+
+}  // namespace
+}  // namespace fadam_ops
+
+using namespace fadam_ops;
+
+extern "C" fadam_status fadam_xent_workspace(const fadam_xent* desc, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FADAM_EINVAL, "bytes is NULL");
+  fadam_status st = check(desc);
+  if (st) return st;
+  DeviceFacts dev;
+  if ((st = device_facts(&dev))) return st;
+  *bytes = desc->rows == 0 ? 0 : layout(*desc, nullptr, dev.sm_count).bytes;
+  return FADAM_OK;
+}
+
+extern "C" fadam_status fadam_xent_run(const fadam_xent* desc, void* workspace, size_t bytes,
+                                       fadam_stream stream_) {
+  clear_error();
+  fadam_status st = check(desc);
+  if (st) return st;
+  const fadam_xent& d = *desc;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (d.rows == 0) {  // nothing to learn from: no loss, and no gradient unless one is there
+    cudaError_t e = cudaMemsetAsync(d.loss, 0, sizeof(float), stream);
+    if (e == cudaSuccess && d.grad_w && !(d.flags & FADAM_XENT_ACCUMULATE))
+      e = cudaMemset2DAsync(d.grad_w, d.grad_w_stride * elem_size(d.grad_w_dtype), 0,
+                            d.width * elem_size(d.grad_w_dtype), d.vocab, stream);
+    return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "cudaMemsetAsync");
+  }
+  DeviceFacts dev;
+  if ((st = device_facts(&dev))) return st;
+  const Layout l = layout(d, static_cast<char*>(workspace), dev.sm_count);
+  if (!workspace || bytes < l.bytes)
+    return fail(FADAM_EINVAL, "the workspace has %zu bytes, %zu are needed",
+                workspace ? bytes : size_t(0), l.bytes);
+  if (misaligned(workspace, 256)) return fail(FADAM_EALIGN, "the workspace is not 256-byte aligned");
+  const bool wide_w = d.grad_w && d.grad_w_dtype == FADAM_DT_F32;
+  if (d.dtype == FADAM_DT_BF16)
+    return wide_w ? run<BF16, F32>(d, l, dev, stream) : run<BF16, BF16>(d, l, dev, stream);
+  return wide_w ? run<F16, F32>(d, l, dev, stream) : run<F16, F16>(d, l, dev, stream);
+}
