@@ -48,27 +48,20 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const SumJobs jobs) {
 
 
 struct Plan {
-  int slices, ctas;
+  NormRuns runs;
   float *gate_parts, *post_parts, *pre_parts;
   size_t bytes;
 };
 
-// The backward pass keeps as many CTAs as the GPU holds (512 threads an SM),
-// and cuts each gate's rows into as many runs as give every CTA one.
 Plan plan_backward(const fadam_block_norm_grad& d, char* base, int sm_count) {
   Plan p{};
   Carver c{base};
-  const int per_sm = 512 / row_shape(d.width).threads;
-  const int64_t most = int64_t(sm_count) * (per_sm < 1 ? 1 : per_sm);
-  const int64_t per_gate = d.rows / d.gate_rows;
-  int64_t slices = most / d.gate_rows;
-  if (slices > per_gate) slices = per_gate;
-  p.slices = slices < 1 ? 1 : int(slices);
-  const int64_t units = d.gate_rows * p.slices;
-  p.ctas = int(units < most ? units : most);
-  p.pre_parts = static_cast<float*>(c.take(sizeof(float) * p.ctas * d.width));
-  if (d.post_weight) p.post_parts = static_cast<float*>(c.take(sizeof(float) * p.ctas * d.width));
-  if (d.gate && p.slices > 1) p.gate_parts = static_cast<float*>(c.take(sizeof(float) * units * d.width));
+  p.runs = norm_runs(d.rows, d.gate_rows, d.width, sm_count);
+  const size_t part = sizeof(float) * p.runs.ctas * d.width;
+  p.pre_parts = static_cast<float*>(c.take(part));
+  if (d.post_weight) p.post_parts = static_cast<float*>(c.take(part));
+  if (d.gate && p.runs.slices > 1)
+    p.gate_parts = static_cast<float*>(c.take(sizeof(float) * d.gate_rows * p.runs.slices * d.width));
   p.bytes = c.used;
   return p;
 }
@@ -160,9 +153,11 @@ using namespace fadam_ops;
 
 extern "C" fadam_status fadam_block_norm_forward(const fadam_block_norm* desc, fadam_stream stream_) {
   clear_error();
-  const fadam_status st = check(desc);
+  fadam_status st = check(desc);
   if (st || desc->rows == 0) return st;
   const fadam_block_norm& d = *desc;
+  DeviceFacts dev;
+  if ((st = device_facts(&dev))) return st;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int b = elem_size(d.block_dtype), h = elem_size(d.residual_dtype);
   NormArgs a{};
@@ -179,10 +174,10 @@ extern "C" fadam_status fadam_block_norm_forward(const fadam_block_norm* desc, f
   a.f_scales = d.f_kept.scales;
   a.h_codes = d.h_kept.codes;
   a.h_scales = d.h_kept.scales;
-  a.rows = d.rows;
   a.f_stride = d.f_stride;
   a.h_stride = d.h_stride;
-  a.rows_per_gate = d.rows / d.gate_rows;
+  a.runs = norm_runs(d.rows, d.gate_rows, d.width, dev.sm_count);
+  a.ring.status = dev.status;
   a.width = int(d.width);
   a.alpha = d.residual_scale;
   a.eps = d.eps;
@@ -253,16 +248,13 @@ extern "C" fadam_status fadam_block_norm_backward(const fadam_block_norm_grad* d
   a.gate_out = p.gate_parts ? nullptr : d.grad_gate;
   a.post_parts = p.post_parts;
   a.pre_parts = p.pre_parts;
-  a.rows = d.rows;
-  a.gates = d.gate_rows;
-  a.rows_per_gate = d.rows / d.gate_rows;
   a.gh_stride = d.grad_h_out_stride;
   a.gx_stride = d.grad_x_out_stride;
   a.f_stride = d.f_stride;
   a.h_stride = d.h_out_stride;
   a.width = int(d.width);
-  a.slices = p.slices;
-  a.ctas = p.ctas;
+  a.runs = p.runs;
+  a.ring.status = dev.status;
   a.alpha = d.residual_scale;
   a.params_f32 = d.param_dtype == FADAM_DT_F32;
   a.wide = d.width % 8 == 0 && (!d.grad_h_out || wide_rows(d.grad_h_out, d.grad_h_out_stride, h)) &&
@@ -279,10 +271,10 @@ extern "C" fadam_status fadam_block_norm_backward(const fadam_block_norm_grad* d
   if (st) return st;
   SumJobs jobs{};
   const int width = int(d.width);
-  jobs.job[0] = {p.pre_parts, d.grad_pre_weight, 1, p.ctas, width, d.param_dtype};
-  if (p.post_parts) jobs.job[1] = {p.post_parts, d.grad_post_weight, 1, p.ctas, width, d.param_dtype};
+  jobs.job[0] = {p.pre_parts, d.grad_pre_weight, 1, p.runs.ctas, width, d.param_dtype};
+  if (p.post_parts) jobs.job[1] = {p.post_parts, d.grad_post_weight, 1, p.runs.ctas, width, d.param_dtype};
   if (p.gate_parts)
-    jobs.job[2] = {p.gate_parts, d.grad_gate, d.gate_rows, p.slices, width, d.param_dtype};
+    jobs.job[2] = {p.gate_parts, d.grad_gate, d.gate_rows, p.runs.slices, width, d.param_dtype};
   const int64_t blocks = (p.gate_parts ? d.gate_rows : 1) * ceil_div(d.width, 32);
   column_sums_kernel<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), 3), 256, 0, stream>>>(jobs);
   const cudaError_t e = cudaGetLastError();

@@ -6,7 +6,29 @@
 
 namespace fadam_ops {
 
-constexpr int kMaxWarps = 16;  // of a CTA
+constexpr int kMaxWarps = 16;  // of a CTA: at 128 registers a thread, an SM's worth
+constexpr int kMaxNormStages = 8;
+// Shared memory of an SM that its CTAs' rings and parameters share.
+constexpr size_t kNormSharedBytes = 216 * 1024;
+
+// The tensors that a row's stage in shared memory holds, one after the other.
+struct RingSource {
+  const void* base;
+  int64_t stride;  // bytes from one row to the next
+  int bytes;       // of one row
+};
+struct RingArgs {
+  RingSource source[4];
+  int sources, bytes, stages;
+  int* status;
+};
+
+// Rows are taken in runs that share one row of the gate: run u holds slice
+// u % slices of the rows of gate u / slices.
+struct NormRuns {
+  int64_t gates, rows_per_gate;
+  int slices, ctas;
+};
 
 struct NormArgs {
   const void *f, *h, *post, *pre, *gate;
@@ -14,8 +36,10 @@ struct NormArgs {
   float *r1, *r2;
   int8_t *f_codes, *h_codes;
   float *f_scales, *h_scales;
-  int64_t rows, f_stride, h_stride, rows_per_gate;
-  int width;
+  int64_t f_stride, h_stride;
+  NormRuns runs;
+  RingArgs ring;
+  int width, threads;
   float alpha, eps;
   bool params_f32, wide;
 };
@@ -27,26 +51,45 @@ struct NormGradArgs {
   const float *r1, *r2;
   const void *post, *pre, *gate;
   void *df, *dh;
-  float* gate_parts;   // [gates, slices, width], or NULL
+  float* gate_parts;   // [runs, width], or NULL
   void* gate_out;      // [gates, width] in place of gate_parts, when there is one slice
   float* post_parts;   // [CTAs, width], or NULL
   float* pre_parts;    // [CTAs, width]
-  int64_t rows, gates, rows_per_gate;
   int64_t gh_stride, gx_stride, f_stride, h_stride;
-  int width, slices, ctas;
+  NormRuns runs;
+  RingArgs ring;
+  int width, threads;
   float alpha;
   bool params_f32, wide;
 };
 
-// Threads and vectors per thread for a row: whole warps, at most 512 threads,
-// as few vectors as that allows (1, 2 or 4).
+// Threads and vectors of eight columns per thread for a row: whole warps, two
+// vectors a thread (four beyond 512 threads).
 struct RowShape {
   int threads, nv;
 };
 inline RowShape row_shape(int64_t width) {
   const int64_t vectors = ceil_div(width, 8);
-  const int nv = vectors <= 512 ? 1 : vectors <= 1024 ? 2 : 4;
+  const int nv = vectors <= 2 * kMaxWarps * 32 ? 2 : 4;
   return {int(round_up(ceil_div(vectors, nv), 32)), nv};
+}
+
+// CTAs that an SM's registers hold at once.
+inline int norm_ctas_per_sm(int threads) {
+  const int fit = kMaxWarps * 32 / threads;
+  return fit < 8 ? fit : 8;
+}
+
+// Every CTA gets a run, and a gate's rows are cut into as many as that takes.
+inline NormRuns norm_runs(int64_t rows, int64_t gates, int64_t width, int sm_count) {
+  const int64_t most = int64_t(sm_count) * norm_ctas_per_sm(row_shape(width).threads);
+  NormRuns r{gates, rows / gates, 1, 1};
+  int64_t slices = most / gates;
+  if (slices > r.rows_per_gate) slices = r.rows_per_gate;
+  r.slices = slices < 1 ? 1 : int(slices);
+  const int64_t runs = gates * r.slices;
+  r.ctas = int(runs < most ? runs : most);
+  return r;
 }
 
 // The kernels' launches, by block dtype and whether the residual stream is fp32.

@@ -1,9 +1,10 @@
 // Activations kept in 8 bits: groups of 128 of a row with one fp32 scale, and
 // the weight gradient of a linear layer from its input's checkpoint.
 //
-// Packing and restoring are one pass over memory: a thread takes eight
-// elements (16 bytes in, 8 bytes out for 16-bit activations), half a warp a
-// group, whose largest magnitude it finds with four shuffles.
+// Packing and restoring are one pass over memory: a thread takes vectors of
+// eight elements (16 bytes in, 8 bytes out for 16-bit activations) of
+// consecutive rows, half a warp a group, whose largest magnitude it finds
+// with four shuffles.
 #include "gemm_store.cuh"
 #include "rows.cuh"
 
@@ -12,43 +13,115 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Threads take consecutive groups of eight of the matrix, rows padded to
-// whole warps (a warp never spans two rows).
-template <class E>
+// A CTA takes `threads` vectors of eight columns (a chunk of a row, or all of
+// it) of R rows, one vector of each row per thread: R independent loads.
+struct ChunkGrid {
+  int threads, chunks, unroll;
+  unsigned ctas;
+};
+// Four rows to a thread where that still leaves every SM eight CTAs of work,
+// else one: at 8192 x 11008 bf16 a pass took NNN us with four rows, NNN with one.
+ChunkGrid chunk_grid(int64_t rows, int64_t width) {
+  ChunkGrid g;
+  const int64_t vectors = ceil_div(width, 8);
+  g.threads = int(vectors < kThreads ? round_up(vectors, 32) : kThreads);
+  g.chunks = int(ceil_div(vectors, g.threads));
+  g.unroll = ceil_div(rows, 4) * g.chunks >= 152 * 8 ? 4 : 1;
+  g.ctas = unsigned(ceil_div(rows, g.unroll) * g.chunks);
+  return g;
+}
+
+// Rows of whole aligned vectors.
+template <class E, int R>
 __global__ void __launch_bounds__(kThreads)
     pack_kernel(const E* x, int64_t rows, int width, int64_t x_stride, int8_t* codes, float* scales,
-                bool wide) {
-  const int per_row = (width + 255) / 256 * 32;  // threads of a row
+                int chunks) {
+  const unsigned block = blockIdx.x / unsigned(chunks);
+  const int col = int((blockIdx.x - block * chunks) * blockDim.x + threadIdx.x) * 8;
+  const int64_t row0 = int64_t(block) * R;
   const int groups = (width + kGroup - 1) / kGroup;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < rows * per_row;
-       i += int64_t(gridDim.x) * kThreads) {
-    const int64_t row = i / per_row;
-    const int col = int(i - row * per_row) * 8;
-    float v[8];
-    load8<E>(x + row * x_stride, col, width, wide, v);
-    keep8(v, codes + row * width, scales + row * groups, col, width, wide);
+  const int left = int(min(rows - row0, int64_t(R)));
+  x += row0 * x_stride + col;
+  codes += row0 * width + col;
+  scales += row0 * groups + col / kGroup;
+  Raw<E> v[R];
+  int8_t* to[R];
+  float* scale[R];
+  bool valid[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    valid[r] = r < left && col < width;
+    v[r] = valid[r] ? load_raw(x + r * x_stride) : zero_raw<E>();
+    to[r] = codes + r * int64_t(width);
+    scale[r] = scales + r * groups;
+  }
+  keep_vectors<E, R>(v, to, scale, valid);
+}
+
+template <class E, int R>
+__global__ void __launch_bounds__(kThreads)
+    restore_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
+                   int64_t x_stride, int chunks) {
+  const unsigned block = blockIdx.x / unsigned(chunks);
+  const int col = int((blockIdx.x - block * chunks) * blockDim.x + threadIdx.x) * 8;
+  if (col >= width) return;
+  const int64_t row0 = int64_t(block) * R;
+  const int groups = (width + kGroup - 1) / kGroup;
+  const int left = int(min(rows - row0, int64_t(R)));
+  x += row0 * x_stride + col;
+  codes += row0 * width + col;
+  scales += row0 * groups + col / kGroup;
+  uint2 raw[R];
+  float scale[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < left) {
+      raw[r] = __ldg(reinterpret_cast<const uint2*>(codes + r * int64_t(width)));
+      scale[r] = __ldg(scales + r * groups);
+    }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < left) {
+      Pair v[4];
+      codes_pairs(raw[r], scale[r], v);
+      store_raw(x + r * x_stride, narrow<E>(v));
+    }
+}
+
+// Any rows: a warp to a group.
+template <class E>
+__global__ void __launch_bounds__(kThreads)
+    pack_any_kernel(const E* x, int64_t rows, int width, int64_t x_stride, int8_t* codes, float* scales) {
+  const int groups = (width + kGroup - 1) / kGroup;
+  const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
+  for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < rows * groups; i += warps) {
+    const int64_t row = i / groups;
+    keep_group(x + row * x_stride, int(i - row * groups) * kGroup, width, codes + row * width,
+               scales + row * groups);
   }
 }
 
 template <class E>
 __global__ void __launch_bounds__(kThreads)
-    restore_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
-                   int64_t x_stride, bool wide) {
-  const int per_row = (width + 7) / 8;
+    restore_any_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
+                       int64_t x_stride) {
   const int groups = (width + kGroup - 1) / kGroup;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < rows * per_row;
-       i += int64_t(gridDim.x) * kThreads) {
-    const int64_t row = i / per_row;
-    const int col = int(i - row * per_row) * 8;
-    float v[8];
-    kept8(codes + row * width, scales + row * groups, col, width, wide, v);
-    store_row8<E>(x + row * x_stride, col, width, wide, v);
+  const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
+  for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < rows * groups; i += warps) {
+    const int64_t row = i / groups;
+    const int group = int(i - row * groups);
+    const float scale = scales[i];
+#pragma unroll
+    for (int k = 0; k < kGroup / 32; ++k) {
+      const int col = group * kGroup + k * 32 + threadIdx.x % 32;
+      if (col < width) x[row * x_stride + col] = from_float<E>(float(codes[row * width + col]) * scale);
+    }
   }
 }
 
-unsigned grid_for(int64_t threads) {
-  const int64_t blocks = ceil_div(threads, kThreads);
-  return unsigned(blocks < 152 * 64 ? blocks : 152 * 64);
+unsigned any_grid(int64_t rows, int64_t width) {
+  const int64_t ctas = ceil_div(rows * ceil_div(width, kGroup), kThreads / 32);
+  return unsigned(ctas < 152 * 16 ? ctas : 152 * 16);
 }
 
 template <class E>
@@ -56,8 +129,16 @@ fadam_status pack(const void* x, int64_t rows, int64_t width, int64_t stride,
                   const fadam_checkpoint8& out, cudaStream_t stream) {
   const bool wide = width % 8 == 0 && !misaligned(x, 16) && stride * sizeof(E) % 16 == 0 &&
                     !misaligned(out.codes, 8);
-  pack_kernel<E><<<grid_for(rows * round_up(width, 256) / 8), kThreads, 0, stream>>>(
-      static_cast<const E*>(x), rows, int(width), stride, out.codes, out.scales, wide);
+  const E* from = static_cast<const E*>(x);
+  if (wide) {
+    const ChunkGrid g = chunk_grid(rows, width);
+    auto* kernel = g.unroll == 4 ? pack_kernel<E, 4> : pack_kernel<E, 1>;
+    kernel<<<g.ctas, g.threads, 0, stream>>>(from, rows, int(width), stride, out.codes, out.scales,
+                                             g.chunks);
+  } else {
+    pack_any_kernel<E><<<any_grid(rows, width), kThreads, 0, stream>>>(from, rows, int(width), stride,
+                                                                      out.codes, out.scales);
+  }
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "checkpoint8 pack launch");
 }
@@ -67,8 +148,16 @@ fadam_status restore(const fadam_checkpoint8& in, int64_t rows, int64_t width, v
                      int64_t stride, cudaStream_t stream) {
   const bool wide = width % 8 == 0 && !misaligned(x, 16) && stride * sizeof(E) % 16 == 0 &&
                     !misaligned(in.codes, 8);
-  restore_kernel<E><<<grid_for(rows * ceil_div(width, 8)), kThreads, 0, stream>>>(
-      in.codes, in.scales, rows, int(width), static_cast<E*>(x), stride, wide);
+  E* to = static_cast<E*>(x);
+  if (wide) {
+    const ChunkGrid g = chunk_grid(rows, width);
+    auto* kernel = g.unroll == 4 ? restore_kernel<E, 4> : restore_kernel<E, 1>;
+    kernel<<<g.ctas, g.threads, 0, stream>>>(in.codes, in.scales, rows, int(width), to, stride,
+                                             g.chunks);
+  } else {
+    restore_any_kernel<E><<<any_grid(rows, width), kThreads, 0, stream>>>(in.codes, in.scales, rows,
+                                                                          int(width), to, stride);
+  }
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "checkpoint8 restore launch");
 }

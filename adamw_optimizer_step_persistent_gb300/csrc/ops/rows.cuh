@@ -1,5 +1,6 @@
-// Rows of activations, eight elements to a thread at a time: loads and stores
-// of any of the three types, and the 8-bit codes of a group.
+// Rows of activations in registers: vectors of eight elements, as four pairs
+// of floats (the packed fp32 instructions take two elements each), loads and
+// stores of any of the three types, and the 8-bit codes of a group.
 #pragma once
 
 #include "ops_device.cuh"
@@ -7,119 +8,314 @@
 namespace fadam_ops {
 
 constexpr int kGroup = FADAM_CHECKPOINT8_GROUP;
-constexpr int kLanesPerGroup = kGroup / 8;  // threads that hold one group
 // A group whose largest magnitude is below this is kept as zeros: its 127 / a
 // could be infinite.
 constexpr float kTinyGroup = 7.888609052210118e-31f;  // 2^-100
 
-// Elements [col, col + 8) of a row of `width`, zeros beyond it.  `wide`: the
-// row starts on 16 bytes and width is a multiple of 8.
+// ---- pairs ------------------------------------------------------------------------
+
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair make_pair(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair both(float a) { return make_pair(a, a); }
+__device__ __forceinline__ float sum2(Pair p) {
+  const float2 v = split(p);
+  return v.x + v.y;
+}
+
+// ---- vectors ----------------------------------------------------------------------
+
+// Eight elements as they lie in memory.
 template <class E>
-__device__ __forceinline__ void load8(const E* row, int col, int width, bool wide, float (&v)[8]) {
-  if (wide) {
-    if (col >= width) {
+struct Raw {
+  uint32_t w[2 * sizeof(E)];
+};
+
+template <class E>
+__device__ __forceinline__ Raw<E> load_raw(const E* p) {
+  Raw<E> r;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    } else if constexpr (sizeof(E) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(row + col);
-      const float4 b = *reinterpret_cast<const float4*>(row + col + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 raw = *reinterpret_cast<const uint4*>(row + col);
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = unpack2<E>(w[i]);
-        v[2 * i] = p.x;
-        v[2 * i + 1] = p.y;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < width ? to_float(row[col + i]) : 0.0f;
+  for (int i = 0; i < int(sizeof(E)) / 2; ++i) {
+    const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+    r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
   }
+  return r;
+}
+template <class E>
+__device__ __forceinline__ void store_raw(E* p, const Raw<E>& r) {
+#pragma unroll
+  for (int i = 0; i < int(sizeof(E)) / 2; ++i)
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
 }
 
 template <class E>
-__device__ __forceinline__ void store_row8(E* row, int col, int width, bool wide, const float (&v)[8]) {
-  if (wide) {
-    if (col >= width) return;
+__device__ __forceinline__ void widen(const Raw<E>& r, Pair (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(E) == 4) {
-      *reinterpret_cast<float4*>(row + col) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(row + col + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      v[i] = make_pair(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
     } else {
-      *reinterpret_cast<uint4*>(row + col) = make_uint4(pack2<E>(v[0], v[1]), pack2<E>(v[2], v[3]),
-                                                        pack2<E>(v[4], v[5]), pack2<E>(v[6], v[7]));
+      const float2 p = unpack2<E>(r.w[i]);
+      v[i] = make_pair(p.x, p.y);
     }
+  }
+}
+template <class E>
+__device__ __forceinline__ Raw<E> narrow(const Pair (&v)[4]) {
+  Raw<E> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = split(v[i]);
+    if constexpr (sizeof(E) == 4) {
+      r.w[2 * i] = __float_as_uint(p.x);
+      r.w[2 * i + 1] = __float_as_uint(p.y);
+    } else {
+      r.w[i] = pack2<E>(p.x, p.y);
+    }
+  }
+  return r;
+}
+
+// Where a thread's eight elements of vector j lie in a row: next to each other
+// when the row consists of whole aligned vectors (`wide`), else each one next
+// to the other threads' (so that element-wise accesses coalesce).
+struct Columns {
+  int threads, tid, width;
+  bool wide;
+  __device__ __forceinline__ int first(int j) const { return (j * threads + tid) * 8; }
+  __device__ __forceinline__ int lone(int j, int i) const { return (j * 8 + i) * threads + tid; }
+};
+
+template <class E>
+__device__ __forceinline__ Raw<E> zero_raw() {
+  Raw<E> r;
+#pragma unroll
+  for (int i = 0; i < int(2 * sizeof(E)); ++i) r.w[i] = 0;
+  return r;
+}
+
+// Vector j of a row, zeros beyond its end.
+template <class E>
+__device__ __forceinline__ Raw<E> load_vector(const E* row, const Columns& c, int j) {
+  Raw<E> r = zero_raw<E>();
+  if (c.wide) {
+    if (c.first(j) < c.width) r = load_raw(row + c.first(j));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (col + i < width) row[col + i] = from_float<E>(v[i]);
+      if (c.lone(j, i) < c.width) {
+        if constexpr (sizeof(E) == 4)
+          r.w[i] = __float_as_uint(row[c.lone(j, i)]);
+        else
+          r.w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[c.lone(j, i)]) << (i % 2 * 16);
+      }
   }
+  return r;
+}
+template <class E>
+__device__ __forceinline__ void store_vector(E* row, const Columns& c, int j, const Raw<E>& r) {
+  if (c.wide) {
+    if (c.first(j) < c.width) store_raw(row + c.first(j), r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c.lone(j, i) < c.width) {
+        if constexpr (sizeof(E) == 4)
+          row[c.lone(j, i)] = __uint_as_float(r.w[i]);
+        else
+          reinterpret_cast<uint16_t*>(row)[c.lone(j, i)] = uint16_t(r.w[i / 2] >> (i % 2 * 16));
+      }
+  }
+}
+template <class E>
+__device__ __forceinline__ void load_pairs(const E* row, const Columns& c, int j, Pair (&v)[4]) {
+  widen<E>(load_vector(row, c, j), v);
+}
+template <class E>
+__device__ __forceinline__ void store_pairs(E* row, const Columns& c, int j, const Pair (&v)[4]) {
+  store_vector(row, c, j, narrow<E>(v));
 }
 
 // Parameters may be fp32 under 16-bit activations.
 template <class E>
-__device__ __forceinline__ void load_param8(const void* p, int64_t offset, bool f32, int col,
-                                            int width, bool wide, float (&v)[8]) {
+__device__ __forceinline__ void load_param(const void* p, int64_t offset, bool f32, const Columns& c,
+                                           int j, Pair (&v)[4]) {
   if (f32)
-    load8<float>(static_cast<const float*>(p) + offset, col, width, wide, v);
+    load_pairs(static_cast<const float*>(p) + offset, c, j, v);
   else
-    load8<E>(static_cast<const E*>(p) + offset, col, width, wide, v);
+    load_pairs(static_cast<const E*>(p) + offset, c, j, v);
 }
 
-// Keeps a thread's eight elements, with the 15 other threads of the half warp
-// that hold the rest of the group: every lane of the warp must call it.
-// Lanes beyond the row hold zeros.  Column col + i has code i; the group's
-// first lane writes the scale.
-__device__ __forceinline__ void keep8(const float (&v)[8], int8_t* codes, float* scales, int col,
-                                      int width, bool wide) {
-  // the largest magnitude by its bits: a NaN's are above an infinity's
+// ---- 8-bit codes ----------------------------------------------------------------------
+
+// The bits of the largest magnitude; a NaN's are above an infinity's.
+template <class E>
+__device__ __forceinline__ uint32_t top_bits(const Raw<E>& r) {
+  uint32_t top = 0;
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, r.w[i] & 0x7fffffffu);
+    return top;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, r.w[i] & 0x7fff7fffu);
+    return max(top >> 16, top & 0xffffu);
+  }
+}
+template <class E>
+__device__ __forceinline__ float from_bits(uint32_t bits) {
+  if constexpr (sizeof(E) == 4) return __uint_as_float(bits);
+  else return unpack2<E>(bits).x;
+}
+
+// A group's scale, and what its elements are multiplied by (0 in a group of
+// zeros, NaN in one that is not finite).
+struct Scaling {
+  float scale, inverse;
+};
+__device__ __forceinline__ Scaling scaling(float a) {
+  const bool finite = a < INFINITY, tiny = a < kTinyGroup;
+  const float inverse = __fdiv_rn(127.0f, tiny ? 1.0f : a);
+  return {finite ? tiny ? 0.0f : __fdiv_rn(a, 127.0f) : __uint_as_float(0x7fffffffu),
+          tiny ? 0.0f : finite ? inverse : 0.0f};
+}
+
+// Eight codes.  x * inverse + 1.5 * 2^23 rounds the product to an integer
+// (nearest even) whose low byte is the code; |code| <= 127 because inverse is
+// 127 / a rounded once.  (What is not finite is multiplied by 0: its codes
+// mean nothing beside a NaN scale.)
+template <class E>
+__device__ __forceinline__ uint2 code8(const Raw<E>& r, float inverse) {
+  Pair v[4];
+  widen<E>(r, v);
+  uint32_t bits[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = split(add2(mul2(v[i], both(inverse)), both(12582912.0f)));
+    bits[2 * i] = __float_as_uint(p.x);
+    bits[2 * i + 1] = __float_as_uint(p.y);
+  }
+  uint32_t word[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    word[i] = __byte_perm(__byte_perm(bits[4 * i], bits[4 * i + 1], 0x0040),
+                          __byte_perm(bits[4 * i + 2], bits[4 * i + 3], 0x0040), 0x5410);
+  return make_uint2(word[0], word[1]);
+}
+
+// Keeps vectors of N rows (or N vectors of one row) in 8 bits; half a warp
+// holds a group of each.  Every lane of the warp calls it, lanes beyond the
+// row with zeros and valid = false.  The N divisions of a group are shared out
+// over its lanes.  N is a power of two, at most 16.
+template <class E, int N>
+__device__ __forceinline__ void keep_vectors(const Raw<E> (&r)[N], int8_t* const (&codes)[N],
+                                             float* const (&scales)[N], const bool (&valid)[N]) {
+  uint32_t top[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) top[n] = top_bits(r[n]);
+#pragma unroll
+  for (int i = 8; i; i /= 2)
+#pragma unroll
+    for (int n = 0; n < N; ++n) top[n] = max(top[n], __shfl_xor_sync(~0u, top[n], i));
+  const int lane = threadIdx.x % 16;
+  uint32_t mine = top[0];
+#pragma unroll
+  for (int n = 1; n < N; ++n) mine = lane % N == n ? top[n] : mine;
+  const Scaling s = scaling(from_bits<E>(mine));
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const float inverse = __shfl_sync(~0u, s.inverse, n, 16);
+    if (valid[n]) *reinterpret_cast<uint2*>(codes[n]) = code8(r[n], inverse);
+  }
+  // lane n of the group has the scale of its n-th vector
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const bool first_valid = __shfl_sync(~0u, int(valid[n]), 0, 16);
+    if (lane == n && first_valid) *scales[n] = s.scale;
+  }
+}
+
+// A warp keeps one group [col0, col0 + 128) of a row, element by element.
+template <class E>
+__device__ __forceinline__ void keep_group(const E* row, int col0, int width, int8_t* codes,
+                                           float* scales) {
+  const int lane = threadIdx.x % 32;
+  float v[kGroup / 32];
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int i = kLanesPerGroup / 2; i; i /= 2) top = max(top, __shfl_xor_sync(~0u, top, i));
-  if (col >= width) return;
-  const float a = __uint_as_float(top);
-  const bool finite = top < 0x7f800000u, tiny = finite && a < kTinyGroup;
-  const float inverse = tiny || !finite ? 0.0f : __fdiv_rn(127.0f, a);
-  if (col % kGroup == 0)
-    scales[col / kGroup] = tiny ? 0.0f : finite ? __fdiv_rn(a, 127.0f) : __uint_as_float(0x7fffffffu);
-  uint32_t word[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int code = finite ? __float2int_rn(__fmul_rn(v[i], inverse)) : 0;
-    word[i / 4] |= (uint32_t(code) & 0xffu) << (i % 4 * 8);
+  for (int i = 0; i < kGroup / 32; ++i) {
+    const int col = col0 + i * 32 + lane;
+    v[i] = col < width ? to_float(row[col]) : 0.0f;
+    top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
   }
-  if (wide) {
-    *reinterpret_cast<uint2*>(codes + col) = make_uint2(word[0], word[1]);
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < width) codes[col + i] = int8_t(word[i / 4] >> (i % 4 * 8) & 0xffu);
+  for (int i = 16; i; i /= 2) top = max(top, __shfl_xor_sync(~0u, top, i));
+  const Scaling s = scaling(__uint_as_float(top));
+  if (lane == 0) scales[col0 / kGroup] = s.scale;
+#pragma unroll
+  for (int i = 0; i < kGroup / 32; ++i) {
+    const int col = col0 + i * 32 + lane;
+    const uint32_t bits = __float_as_uint(__fadd_rn(__fmul_rn(v[i], s.inverse), 12582912.0f));
+    if (col < width) codes[col] = int8_t(bits & 0xffu);
   }
 }
 
-// Eight kept elements.
-__device__ __forceinline__ void kept8(const int8_t* codes, const float* scales, int col, int width,
-                                      bool wide, float (&v)[8]) {
-  if (col >= width) {
+// Eight codes times `factor`.  A code's byte with its sign bit flipped, in the
+// low mantissa bits of 2^23, is 2^23 + 128 + code exactly: cheaper than eight
+// integer conversions.
+__device__ __forceinline__ void codes_pairs(uint2 raw, float factor, Pair (&v)[4]) {
+  raw.x ^= 0x80808080u;
+  raw.y ^= 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    return;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? raw.x : raw.y;
+    const Pair p = make_pair(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + i % 2 * 2)),
+                             __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7541 + i % 2 * 2)));
+    v[i] = mul2(add2(p, both(-8388736.0f)), both(factor));
   }
-  const float scale = scales[col / kGroup];
-  if (wide) {
-    const uint2 raw = *reinterpret_cast<const uint2*>(codes + col);
+}
+
+// Vector j of a kept row times `factor`; `scale` is that of the vector's group
+// when the row is wide.
+__device__ __forceinline__ void load_kept(const int8_t* codes, const float* scales, float scale,
+                                          float factor, const Columns& c, int j, Pair (&v)[4]) {
+  if (c.wide) {
+    uint2 raw = make_uint2(0, 0);
+    if (c.first(j) < c.width) raw = *reinterpret_cast<const uint2*>(codes + c.first(j));
+    codes_pairs(raw, scale * factor, v);
+  } else {
+    float e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t w = i < 4 ? raw.x : raw.y;
-      v[i] = float(int(w << (24 - i % 4 * 8)) >> 24) * scale;
+      const int col = c.lone(j, i);
+      e[i] = col < c.width ? float(codes[col]) * (scales[col / kGroup] * factor) : 0.0f;
     }
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < width ? float(codes[col + i]) * scale : 0.0f;
+    for (int i = 0; i < 4; ++i) v[i] = make_pair(e[2 * i], e[2 * i + 1]);
   }
 }
 

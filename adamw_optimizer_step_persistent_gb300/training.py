@@ -13,15 +13,18 @@ strided (no copy is made).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple, Optional, Union
 
 import torch
 
 from . import _abi
-from .optimizer import _ptr, _stream_handle, dtype_code
+from .optimizer import _ptr, dtype_code
 
 _16BIT = (torch.bfloat16, torch.float16)
+_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else lambda i: torch.cuda.current_stream(i).cuda_stream
 
 
 class LinearCrossEntropy(NamedTuple):
@@ -84,18 +87,37 @@ def _collapses(t: torch.Tensor) -> bool:
     return all(a[1] == b[0] * b[1] for a, b in zip(dims, dims[1:]))
 
 
-def _same_device(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}, not on a CUDA device")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _device(t: torch.Tensor, what: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{what} is on {t.device}, not on a CUDA device")
+    return index
 
 
-def _workspace(size_of, desc, where: str, device: torch.device) -> Optional[torch.Tensor]:
+def _check_device(index: int, what: str, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a tensor is on {t.device}, {what} on cuda:{index}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _current(index: int):
+    """A context in which the device is the current one (most often it is)."""
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _workspace(size_of, desc, where: str, like: torch.Tensor):
+    """(tensor or None, address, bytes) of the workspace that a call needs."""
     need = ctypes.c_size_t()
-    _abi.check_ops(size_of(ctypes.byref(desc), ctypes.byref(need)), where)
-    return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+    status = size_of(desc, need)
+    if status:
+        _abi.check_ops(status, where)
+    if not need.value:
+        return None, None, 0
+    ws = like.new_empty(need.value, dtype=torch.uint8)
+    return ws, ws.data_ptr(), need.value
 
 
 def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, *,
@@ -134,58 +156,63 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
         raise ValueError("accumulate needs a grad_weight buffer")
     if grad_weight is not None and not grads:
         raise ValueError("a grad_weight buffer without grads")
-    device = x.device
-    _same_device(device, weight=weight, targets=targets, grad_weight=grad_weight)
+    index = _device(x, "x")
+    _check_device(index, "x", weight, targets, grad_weight)
     vocab, _, w_stride = _rows(weight, "weight")
     targets = targets.contiguous()
-    with torch.cuda.device(device):
-        row_loss, lse = torch.empty(2, *targets.shape, dtype=torch.float32, device=device)
-        loss = torch.empty((), dtype=torch.float32, device=device)
-        grad_x, gw_stride = None, width
+    code = dtype_code(x.dtype)
+    grad_x, gw_stride, gw_code = None, width, code
+    if grads and grad_weight is not None:
+        if (grad_weight.shape != weight.shape
+                or grad_weight.dtype not in (weight.dtype, torch.float32)):
+            raise ValueError("grad_weight must have the weight's shape, and its dtype or fp32")
+        gw_stride, gw_code = _rows(grad_weight, "grad_weight")[2], dtype_code(grad_weight.dtype)
+    with _current(index):
+        row_loss = x.new_empty(targets.shape, dtype=torch.float32)
+        lse = torch.empty_like(row_loss)
+        loss = x.new_empty((), dtype=torch.float32)
         if grads:
-            grad_x = torch.empty(x.shape, dtype=x.dtype, device=device)
+            grad_x = x.new_empty(x.shape)
             if grad_weight is None:
-                grad_weight = torch.empty(vocab, width, dtype=weight.dtype, device=device)
-            elif (grad_weight.shape != weight.shape
-                  or grad_weight.dtype not in (weight.dtype, torch.float32)):
-                raise ValueError("grad_weight must have the weight's shape, and its dtype or fp32")
-            gw_stride = _rows(grad_weight, "grad_weight")[2]
+                grad_weight = weight.new_empty(vocab, width)
         flags = ((_abi.XENT_MEAN if reduction == "mean" else 0)
                  | (_abi.XENT_ACCUMULATE if accumulate else 0))
         desc = _abi.Xent(
-            x=x.data_ptr(), w=weight.data_ptr(), targets=targets.data_ptr(), loss=loss.data_ptr(),
-            row_loss=row_loss.data_ptr(), lse=lse.data_ptr(), grad_x=_ptr(grad_x),
-            grad_w=_ptr(grad_weight), rows=rows, width=width, vocab=vocab, x_stride=x_stride,
-            w_stride=w_stride, grad_x_stride=width, grad_w_stride=gw_stride,
-            ignore_index=int(ignore_index), chunk_rows=int(chunk_rows),
-            loss_scale=float(loss_scale), dtype=dtype_code(x.dtype),
-            grad_w_dtype=dtype_code(grad_weight.dtype if grads else x.dtype), flags=flags)
+            x.data_ptr(), weight.data_ptr(), targets.data_ptr(), loss.data_ptr(),
+            row_loss.data_ptr(), lse.data_ptr(), _ptr(grad_x), _ptr(grad_weight), rows, width,
+            vocab, x_stride, w_stride, width, gw_stride, int(ignore_index), int(chunk_rows),
+            float(loss_scale), code, gw_code, flags)
         lib = _abi.lib()
-        ws = _workspace(lib.fadam_xent_workspace, desc, "fadam_xent_workspace", device)
-        _abi.check_ops(lib.fadam_xent_run(ctypes.byref(desc), _ptr(ws), ws.numel() if ws is not None
-                                          else 0, _stream_handle(device)), "fadam_xent_run")
+        ws, at, size = _workspace(lib.fadam_xent_workspace, desc, "fadam_xent_workspace", x)
+        status = lib.fadam_xent_run(desc, at, size, _stream(index))
+    if status:
+        _abi.check_ops(status, "fadam_xent_run")
     return LinearCrossEntropy(loss, row_loss, lse, grad_x, grad_weight)
 
 
 # ---- 8-bit checkpoints ---------------------------------------------------------------
 
 def _empty_checkpoint(like: torch.Tensor) -> Checkpoint8:
-    groups = -(-like.shape[-1] // _abi.CHECKPOINT8_GROUP)
-    return Checkpoint8(torch.empty(like.shape, dtype=torch.int8, device=like.device),
-                       torch.empty(*like.shape[:-1], groups, dtype=torch.float32,
-                                   device=like.device), like.dtype)
+    shape = like.shape
+    groups = -(-shape[-1] // _abi.CHECKPOINT8_GROUP)
+    return Checkpoint8(like.new_empty(shape, dtype=torch.int8),
+                       like.new_empty(shape[:-1] + (groups,), dtype=torch.float32), like.dtype)
 
 
 def _kept(c: Optional[Checkpoint8]) -> _abi.Kept8:
-    return _abi.Kept8() if c is None else _abi.Kept8(c.codes.data_ptr(), c.scales.data_ptr())
+    return _NOT_KEPT if c is None else _abi.Kept8(c.codes.data_ptr(), c.scales.data_ptr())
+
+
+_NOT_KEPT = _abi.Kept8()
 
 
 def _check_checkpoint(c: Checkpoint8, what: str) -> None:
-    groups = -(-c.codes.shape[-1] // _abi.CHECKPOINT8_GROUP)
-    if (c.codes.dtype != torch.int8 or c.scales.dtype != torch.float32
-            or not c.codes.is_contiguous() or not c.scales.is_contiguous()
-            or c.scales.shape != (*c.codes.shape[:-1], groups)
-            or c.codes.device != c.scales.device):
+    codes, scales = c.codes, c.scales
+    groups = -(-codes.shape[-1] // _abi.CHECKPOINT8_GROUP)
+    if (codes.dtype != torch.int8 or scales.dtype != torch.float32
+            or not codes.is_contiguous() or not scales.is_contiguous()
+            or scales.shape != codes.shape[:-1] + (groups,)
+            or codes.get_device() != scales.get_device()):
         raise ValueError(f"{what} is not a checkpoint: contiguous int8 codes [..., width] and fp32 "
                          "scales [..., ceil(width / 128)] on one device")
 
@@ -196,27 +223,29 @@ def checkpoint8(x: torch.Tensor) -> Checkpoint8:
     element, each off by at most 1/254 of its group's largest magnitude.  A
     group that holds an infinity or a NaN is restored as NaN throughout."""
     rows, width, stride = _rows(x, "x")
-    _same_device(x.device)
+    index = _device(x, "x")
     code = dtype_code(x.dtype)
-    with torch.cuda.device(x.device):
+    with _current(index):
         out = _empty_checkpoint(x)
-        _abi.check_ops(_abi.lib().fadam_checkpoint8_pack(
-            x.data_ptr(), rows, width, stride, code, ctypes.byref(_kept(out)),
-            _stream_handle(x.device)), "fadam_checkpoint8_pack")
+        status = _abi.lib().fadam_checkpoint8_pack(x.data_ptr(), rows, width, stride, code,
+                                                   _kept(out), _stream(index))
+    if status:
+        _abi.check_ops(status, "fadam_checkpoint8_pack")
     return out
 
 
 def checkpoint8_restore(c: Checkpoint8) -> torch.Tensor:
     """The activation that ``checkpoint8`` kept, in its dtype."""
     _check_checkpoint(c, "c")
-    device = c.codes.device
-    _same_device(device)
+    index = _device(c.codes, "c")
     rows, width, stride = _rows(c.codes, "c")
-    with torch.cuda.device(device):
-        x = torch.empty(c.codes.shape, dtype=c.dtype, device=device)
-        _abi.check_ops(_abi.lib().fadam_checkpoint8_restore(
-            ctypes.byref(_kept(c)), rows, width, x.data_ptr(), stride, dtype_code(c.dtype),
-            _stream_handle(device)), "fadam_checkpoint8_restore")
+    code = dtype_code(c.dtype)
+    with _current(index):
+        x = c.codes.new_empty(c.codes.shape, dtype=c.dtype)
+        status = _abi.lib().fadam_checkpoint8_restore(_kept(c), rows, width, x.data_ptr(), stride,
+                                                      code, _stream(index))
+    if status:
+        _abi.check_ops(status, "fadam_checkpoint8_restore")
     return x
 
 
@@ -236,25 +265,25 @@ def checkpoint8_weight_grad(grad_y: torch.Tensor, c: Checkpoint8, *,
                          "have different rows")
     if accumulate and out is None:
         raise ValueError("accumulate needs an out buffer")
-    device = grad_y.device
-    _same_device(device, checkpoint=c.codes, out=out)
+    index = _device(grad_y, "grad_y")
+    _check_device(index, "grad_y", c.codes, out)
     rows, n, stride = _rows(grad_y, "grad_y")
     width = c.codes.shape[-1]
-    with torch.cuda.device(device):
+    if out is not None and (out.shape != (n, width)
+                            or out.dtype not in (grad_y.dtype, torch.float32)):
+        raise ValueError(f"out must be [{n}, {width}] of grad_y's dtype or fp32")
+    with _current(index):
         if out is None:
-            out = torch.empty(n, width, dtype=grad_y.dtype, device=device)
-        elif out.shape != (n, width) or out.dtype not in (grad_y.dtype, torch.float32):
-            raise ValueError(f"out must be [{n}, {width}] of grad_y's dtype or fp32")
-        desc = _abi.Wgrad(dy=grad_y.data_ptr(), x=_kept(c), out=out.data_ptr(), rows=rows, n=n,
-                          width=width, dy_stride=stride, out_stride=_rows(out, "out")[2],
-                          dtype=dtype_code(grad_y.dtype), out_dtype=dtype_code(out.dtype),
-                          flags=_abi.WGRAD_ACCUMULATE if accumulate else 0)
+            out = grad_y.new_empty(n, width)
+        desc = _abi.Wgrad(grad_y.data_ptr(), _kept(c), out.data_ptr(), rows, n, width, stride,
+                          _rows(out, "out")[2], dtype_code(grad_y.dtype), dtype_code(out.dtype),
+                          _abi.WGRAD_ACCUMULATE if accumulate else 0)
         lib = _abi.lib()
-        ws = _workspace(lib.fadam_checkpoint8_wgrad_workspace, desc,
-                        "fadam_checkpoint8_wgrad_workspace", device)
-        _abi.check_ops(lib.fadam_checkpoint8_wgrad(
-            ctypes.byref(desc), _ptr(ws), ws.numel() if ws is not None else 0,
-            _stream_handle(device)), "fadam_checkpoint8_wgrad")
+        ws, at, size = _workspace(lib.fadam_checkpoint8_wgrad_workspace, desc,
+                                  "fadam_checkpoint8_wgrad_workspace", grad_y)
+        status = lib.fadam_checkpoint8_wgrad(desc, at, size, _stream(index))
+    if status:
+        _abi.check_ops(status, "fadam_checkpoint8_wgrad")
     return out
 
 
@@ -307,26 +336,24 @@ def block_norm(f: torch.Tensor, h: torch.Tensor, pre_weight: torch.Tensor, *,
         raise TypeError(f"h must be {f.dtype} or fp32, got {h.dtype}")
     block = dtype_code(f.dtype)
     params, gate_rows = _norm_params(width, rows, f.dtype, pre_weight, post_weight, gate)
-    device = f.device
-    _same_device(device, h=h, pre_weight=pre_weight, post_weight=post_weight, gate=gate)
-    with torch.cuda.device(device):
-        h_out = torch.empty(h.shape, dtype=h.dtype, device=device)
-        x_out = torch.empty(f.shape, dtype=f.dtype, device=device)
-        r2 = torch.empty(f.shape[:-1], dtype=torch.float32, device=device)
+    index = _device(f, "f")
+    _check_device(index, "f", h, pre_weight, post_weight, gate)
+    h_stride = _rows(h, "h")[2]
+    with _current(index):
+        h_out = h.new_empty(h.shape)
+        x_out = f.new_empty(f.shape)
+        r2 = f.new_empty(f.shape[:-1], dtype=torch.float32)
         r1 = torch.empty_like(r2) if post_weight is not None else None
         f_kept = _empty_checkpoint(f) if checkpoint else None
         h_kept = _empty_checkpoint(h) if checkpoint else None
         desc = _abi.BlockNorm(
-            f=f.data_ptr(), h=h.data_ptr(), post_weight=_ptr(post_weight),
-            pre_weight=pre_weight.data_ptr(), gate=_ptr(gate), h_out=h_out.data_ptr(),
-            x_out=x_out.data_ptr(), rstd_post=_ptr(r1), rstd_pre=r2.data_ptr(),
-            f_kept=_kept(f_kept), h_kept=_kept(h_kept), rows=rows, width=width,
-            gate_rows=gate_rows, f_stride=f_stride, h_stride=_rows(h, "h")[2],
-            residual_scale=float(residual_scale), eps=float(eps), block_dtype=block,
-            residual_dtype=dtype_code(h.dtype), param_dtype=dtype_code(params))
-        _abi.check_ops(_abi.lib().fadam_block_norm_forward(ctypes.byref(desc),
-                                                           _stream_handle(device)),
-                       "fadam_block_norm_forward")
+            f.data_ptr(), h.data_ptr(), _ptr(post_weight), pre_weight.data_ptr(), _ptr(gate),
+            h_out.data_ptr(), x_out.data_ptr(), _ptr(r1), r2.data_ptr(), _kept(f_kept),
+            _kept(h_kept), rows, width, gate_rows, f_stride, h_stride, float(residual_scale),
+            float(eps), block, dtype_code(h.dtype), dtype_code(params))
+        status = _abi.lib().fadam_block_norm_forward(desc, _stream(index))
+    if status:
+        _abi.check_ops(status, "fadam_block_norm_forward")
     return BlockNorm(h_out, x_out, r1, r2, f_kept, h_kept)
 
 
@@ -367,34 +394,31 @@ def block_norm_backward(grad_h_out: Optional[torch.Tensor], grad_x_out: torch.Te
         if r is not None and (r.dtype != torch.float32 or r.shape != grad_x_out.shape[:-1]
                               or not r.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous fp32 {tuple(grad_x_out.shape[:-1])}")
-    device = grad_x_out.device
-    _same_device(device, grad_h_out=grad_h_out, f=f[0] if isinstance(f, Checkpoint8) else f,
-                 h_out=h_out[0] if isinstance(h_out, Checkpoint8) else h_out, rstd_post=rstd_post,
-                 rstd_pre=rstd_pre, pre_weight=pre_weight, post_weight=post_weight, gate=gate)
-    with torch.cuda.device(device):
-        grad_f = torch.empty(grad_x_out.shape, dtype=block, device=device)
-        grad_h = torch.empty(grad_x_out.shape, dtype=dtypes[1], device=device)
+    index = _device(grad_x_out, "grad_x_out")
+    _check_device(index, "grad_x_out", grad_h_out, f[0] if isinstance(f, Checkpoint8) else f,
+                  h_out[0] if isinstance(h_out, Checkpoint8) else h_out, rstd_post, rstd_pre,
+                  pre_weight, post_weight, gate)
+    gh_stride = width if grad_h_out is None else _rows(grad_h_out, "grad_h_out")[2]
+    with _current(index):
+        grad_f = grad_x_out.new_empty(grad_x_out.shape)
+        grad_h = torch.empty_like(grad_f) if dtypes[1] == block else grad_x_out.new_empty(
+            grad_x_out.shape, dtype=dtypes[1])
         grad_pre = torch.empty_like(pre_weight)
         grad_post = None if post_weight is None else torch.empty_like(post_weight)
         grad_gate = None if gate is None else torch.empty_like(gate)
         desc = _abi.BlockNormGrad(
-            grad_h_out=_ptr(grad_h_out), grad_x_out=grad_x_out.data_ptr(), f=_ptr(saved[0][0]),
-            h_out=_ptr(saved[1][0]), f_kept=_kept(saved[0][1]), h_kept=_kept(saved[1][1]),
-            rstd_post=_ptr(rstd_post), rstd_pre=rstd_pre.data_ptr(),
-            post_weight=_ptr(post_weight), pre_weight=pre_weight.data_ptr(), gate=_ptr(gate),
-            grad_f=grad_f.data_ptr(), grad_h=grad_h.data_ptr(), grad_post_weight=_ptr(grad_post),
-            grad_pre_weight=grad_pre.data_ptr(), grad_gate=_ptr(grad_gate), rows=rows, width=width,
-            gate_rows=gate_rows,
-            grad_h_out_stride=width if grad_h_out is None else _rows(grad_h_out, "grad_h_out")[2],
-            grad_x_out_stride=gx_stride, f_stride=strides[0], h_out_stride=strides[1],
-            residual_scale=float(residual_scale), block_dtype=dtype_code(block),
-            residual_dtype=dtype_code(dtypes[1]), param_dtype=dtype_code(params))
+            _ptr(grad_h_out), grad_x_out.data_ptr(), _ptr(saved[0][0]), _ptr(saved[1][0]),
+            _kept(saved[0][1]), _kept(saved[1][1]), _ptr(rstd_post), rstd_pre.data_ptr(),
+            _ptr(post_weight), pre_weight.data_ptr(), _ptr(gate), grad_f.data_ptr(),
+            grad_h.data_ptr(), _ptr(grad_post), grad_pre.data_ptr(), _ptr(grad_gate), rows, width,
+            gate_rows, gh_stride, gx_stride, strides[0], strides[1], float(residual_scale),
+            dtype_code(block), dtype_code(dtypes[1]), dtype_code(params))
         lib = _abi.lib()
-        ws = _workspace(lib.fadam_block_norm_backward_workspace, desc,
-                        "fadam_block_norm_backward_workspace", device)
-        _abi.check_ops(lib.fadam_block_norm_backward(
-            ctypes.byref(desc), _ptr(ws), ws.numel() if ws is not None else 0,
-            _stream_handle(device)), "fadam_block_norm_backward")
+        ws, at, size = _workspace(lib.fadam_block_norm_backward_workspace, desc,
+                                  "fadam_block_norm_backward_workspace", grad_x_out)
+        status = lib.fadam_block_norm_backward(desc, at, size, _stream(index))
+    if status:
+        _abi.check_ops(status, "fadam_block_norm_backward")
     return BlockNormGrads(grad_f, grad_h, grad_post, grad_pre, grad_gate)
 
 
