@@ -6,8 +6,8 @@
 namespace fadam_ops {
 namespace {
 
-// out[o, c] = sum over `parts` of in[o, part, c], in the parts' order within
-// each of eight lanes and then over the lanes.
+// out[o, c] = sum over `parts` of in[o, part, c]: 32 columns to a CTA, each
+// warp every 32nd part, then the warps' sums, in a fixed order.
 struct SumArgs {
   const float* in;
   void* out;
@@ -17,25 +17,32 @@ struct SumArgs {
 struct SumJobs {
   SumArgs job[3];
 };
-__global__ void __launch_bounds__(256) column_sums_kernel(const SumJobs jobs) {
-  __shared__ float shared[8][33];
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) column_sums_kernel(const __grid_constant__ SumJobs jobs) {
+  __shared__ float shared[kSumWarps][33];
   const SumArgs& a = jobs.job[blockIdx.y];
   if (!a.out) return;
-  const int lane = threadIdx.x % 32, part0 = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t blocks_per_row = (a.width + 31) / 32;
   for (int64_t b = blockIdx.x; b < a.outer * blocks_per_row; b += gridDim.x) {
     const int64_t o = b / blocks_per_row;
     const int col = int(b - o * blocks_per_row) * 32 + lane;
     float sum = 0.0f;
-    if (col < a.width)
-      for (int p = part0; p < a.parts; p += 8) sum += a.in[(o * a.parts + p) * a.width + col];
+    if (col < a.width) {
+      const float* in = a.in + o * a.parts * a.width + col;
+#pragma unroll 8
+      for (int p = warp; p < a.parts; p += kSumWarps) sum += in[int64_t(p) * a.width];
+    }
     __syncthreads();
-    shared[part0][lane] = sum;
+    shared[warp][lane] = sum;
     __syncthreads();
-    if (part0 == 0 && col < a.width) {
+    // each warp adds up one column
+    sum = shared[lane][warp];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) sum += shared[i][lane];
-      const int64_t at = o * a.width + col;
+    for (int i = 16; i; i /= 2) sum += __shfl_xor_sync(~0u, sum, i);
+    const int to = int(b - o * blocks_per_row) * 32 + warp;
+    if (lane == 0 && to < a.width) {
+      const int64_t at = o * a.width + to;
       if (a.dtype == FADAM_DT_F32)
         static_cast<float*>(a.out)[at] = sum;
       else if (a.dtype == FADAM_DT_BF16)
@@ -45,7 +52,6 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const SumJobs jobs) {
     }
   }
 }
-
 
 struct Plan {
   NormRuns runs;
@@ -276,7 +282,8 @@ extern "C" fadam_status fadam_block_norm_backward(const fadam_block_norm_grad* d
   if (p.gate_parts)
     jobs.job[2] = {p.gate_parts, d.grad_gate, d.gate_rows, p.runs.slices, width, d.param_dtype};
   const int64_t blocks = (p.gate_parts ? d.gate_rows : 1) * ceil_div(d.width, 32);
-  column_sums_kernel<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), 3), 256, 0, stream>>>(jobs);
+  column_sums_kernel<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), 3), kSumWarps * 32, 0,
+                       stream>>>(jobs);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "column sums launch");
 }

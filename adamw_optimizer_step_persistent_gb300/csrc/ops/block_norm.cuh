@@ -507,7 +507,7 @@ template <class Args>
 fadam_status launch_norm(void (*kernel)(Args), const Args& a, int threads, size_t smem,
                          cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
+  if (smem > 40 * 1024)  // beyond 48 KB, static arrays included, it has to be asked for
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   kernel<<<unsigned(a.runs.ctas), threads, smem, stream>>>(a);

@@ -81,8 +81,11 @@ inline int norm_ctas_per_sm(int threads) {
 }
 
 // Every CTA gets a run, and a gate's rows are cut into as many as that takes.
+// Beyond a CTA per SM each gets four rows at least, or reading the parameters
+// and writing the sums would cost more than the rows.
 inline NormRuns norm_runs(int64_t rows, int64_t gates, int64_t width, int sm_count) {
-  const int64_t most = int64_t(sm_count) * norm_ctas_per_sm(row_shape(width).threads);
+  int64_t most = int64_t(sm_count) * norm_ctas_per_sm(row_shape(width).threads);
+  if (most > rows / 4) most = rows / 4 > sm_count ? rows / 4 : sm_count;
   NormRuns r{gates, rows / gates, 1, 1};
   int64_t slices = most / gates;
   if (slices > r.rows_per_gate) slices = r.rows_per_gate;

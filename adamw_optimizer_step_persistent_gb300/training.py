@@ -100,6 +100,14 @@ def _check_device(index: int, what: str, *tensors: Optional[torch.Tensor]) -> No
             raise ValueError(f"a tensor is on {t.device}, {what} on cuda:{index}")
 
 
+def _like(t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """A new contiguous tensor of t's shape (empty_like is the cheapest call
+    there is, but keeps the strides of what is dense in another order)."""
+    if t.is_contiguous():
+        return torch.empty_like(t, dtype=dtype) if dtype is not None else torch.empty_like(t)
+    return t.new_empty(t.shape, dtype=dtype)
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -168,13 +176,13 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
             raise ValueError("grad_weight must have the weight's shape, and its dtype or fp32")
         gw_stride, gw_code = _rows(grad_weight, "grad_weight")[2], dtype_code(grad_weight.dtype)
     with _current(index):
-        row_loss = x.new_empty(targets.shape, dtype=torch.float32)
+        row_loss = torch.empty_like(targets, dtype=torch.float32)
         lse = torch.empty_like(row_loss)
         loss = x.new_empty((), dtype=torch.float32)
         if grads:
-            grad_x = x.new_empty(x.shape)
+            grad_x = _like(x)
             if grad_weight is None:
-                grad_weight = weight.new_empty(vocab, width)
+                grad_weight = _like(weight)
         flags = ((_abi.XENT_MEAN if reduction == "mean" else 0)
                  | (_abi.XENT_ACCUMULATE if accumulate else 0))
         desc = _abi.Xent(
@@ -195,7 +203,7 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
 def _empty_checkpoint(like: torch.Tensor) -> Checkpoint8:
     shape = like.shape
     groups = -(-shape[-1] // _abi.CHECKPOINT8_GROUP)
-    return Checkpoint8(like.new_empty(shape, dtype=torch.int8),
+    return Checkpoint8(_like(like, torch.int8),
                        like.new_empty(shape[:-1] + (groups,), dtype=torch.float32), like.dtype)
 
 
@@ -241,7 +249,7 @@ def checkpoint8_restore(c: Checkpoint8) -> torch.Tensor:
     rows, width, stride = _rows(c.codes, "c")
     code = dtype_code(c.dtype)
     with _current(index):
-        x = c.codes.new_empty(c.codes.shape, dtype=c.dtype)
+        x = torch.empty_like(c.codes, dtype=c.dtype)
         status = _abi.lib().fadam_checkpoint8_restore(_kept(c), rows, width, x.data_ptr(), stride,
                                                       code, _stream(index))
     if status:
@@ -340,8 +348,8 @@ def block_norm(f: torch.Tensor, h: torch.Tensor, pre_weight: torch.Tensor, *,
     _check_device(index, "f", h, pre_weight, post_weight, gate)
     h_stride = _rows(h, "h")[2]
     with _current(index):
-        h_out = h.new_empty(h.shape)
-        x_out = f.new_empty(f.shape)
+        h_out = _like(h)
+        x_out = _like(f)
         r2 = f.new_empty(f.shape[:-1], dtype=torch.float32)
         r1 = torch.empty_like(r2) if post_weight is not None else None
         f_kept = _empty_checkpoint(f) if checkpoint else None
@@ -400,9 +408,8 @@ def block_norm_backward(grad_h_out: Optional[torch.Tensor], grad_x_out: torch.Te
                   pre_weight, post_weight, gate)
     gh_stride = width if grad_h_out is None else _rows(grad_h_out, "grad_h_out")[2]
     with _current(index):
-        grad_f = grad_x_out.new_empty(grad_x_out.shape)
-        grad_h = torch.empty_like(grad_f) if dtypes[1] == block else grad_x_out.new_empty(
-            grad_x_out.shape, dtype=dtypes[1])
+        grad_f = _like(grad_x_out)
+        grad_h = torch.empty_like(grad_f, dtype=dtypes[1])
         grad_pre = torch.empty_like(pre_weight)
         grad_post = None if post_weight is None else torch.empty_like(post_weight)
         grad_gate = None if gate is None else torch.empty_like(gate)
