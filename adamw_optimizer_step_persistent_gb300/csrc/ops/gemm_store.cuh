@@ -2,6 +2,8 @@
 // parts of a product whose k was split.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm.cuh"
 
 namespace fadam_ops {
@@ -14,7 +16,7 @@ struct StoreArgs {
   int64_t m, n;
   const float* scale;    // device scalar, NULL for 1
   float constant;        // another factor
-  float* carry;          // fp32 [m, n]: products summed over several launches
+  float* carry;          // fp32 [m, scratch_ld(n)]: products summed over several launches
   int32_t read_carry;    // the sum starts from carry
   int32_t write_carry;   // the sum goes back to carry, not to out
   int32_t accumulate;    // out's old value is added to the scaled sum
@@ -34,109 +36,144 @@ inline bool wide_stores(const void* out, int64_t ld, int size) {
   return !misaligned(out, 16) && ld * size % 16 == 0;
 }
 
-// Eight consecutive columns of one row, `v` scaled already.
-template <class Out>
-__device__ __forceinline__ void store8(Out* out, const float* v, bool accumulate) {
-  float r[8];
-  if (accumulate) {
-    float old[8];
-    if (sizeof(Out) == 4) {
-      *reinterpret_cast<float4*>(old) = *reinterpret_cast<const float4*>(out);
-      *reinterpret_cast<float4*>(old + 4) = *reinterpret_cast<const float4*>(out + 4);
-    } else {
-      const uint4 raw = *reinterpret_cast<const uint4*>(out);
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Out* p = reinterpret_cast<const Out*>(&w[i]);
-        old[2 * i] = to_float(p[0]);
-        old[2 * i + 1] = to_float(p[1]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = v[i] + old[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = v[i];
-  }
-  if constexpr (sizeof(Out) == 4) {
-    *reinterpret_cast<float4*>(out) = make_float4(r[0], r[1], r[2], r[3]);
-    *reinterpret_cast<float4*>(out + 4) = make_float4(r[4], r[5], r[6], r[7]);
-  } else {
-    *reinterpret_cast<uint4*>(out) = make_uint4(pack2<Out>(r[0], r[1]), pack2<Out>(r[2], r[3]),
-                                                pack2<Out>(r[4], r[5]), pack2<Out>(r[6], r[7]));
-  }
-}
+// Scratch rows of sums: fp32, padded so that every row starts on 16 bytes.
+__host__ __device__ inline int64_t scratch_ld(int64_t n) { return (n + 3) / 4 * 4; }
 
 template <class Out>
 struct StoreEpilogue {
   StoreArgs s;
-  float* parts;  // fp32 [splits, m, n] when k is split: joined by join_kernel
+  float* parts;  // fp32 [splits, m, scratch_ld(n)] when k is split: joined by join_kernel
 
-  __device__ __forceinline__ void operator()(float (&v)[kPiece], int64_t row, int64_t col,
-                                             int split) const {
-    if (row >= s.m || col >= s.n) return;
-    const int width = int(min(int64_t(kPiece), s.n - col));
-    if (parts) {
-      put(parts + (split * s.m + row) * s.n + col, v, width);
+  __device__ __forceinline__ void operator()(const GemmPiece& at) const {
+    const int64_t row = at.row0 + threadIdx.x % 32;
+    const bool sums = parts || s.write_carry;
+    const bool zero = !sums && row < s.m && s.masked(row);
+    const float f = sums ? 1.0f : s.factor();
+    if (sizeof(Out) == 2 && !sums && !s.read_carry && !s.accumulate) {
+#pragma unroll 1
+      for (int c = 0; c < at.width; c += 64) {
+        float v[64];
+        at.load(c, v);
+        if (c + 64 >= at.width) at.release();
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = zero ? 0.0f : v[i] * f;
+        if (s.wide && s.n % 8 == 0)
+          emit_rows<8>(
+              v, at, c, s.m,
+              [](const float* p) {
+                return make_uint4(pack2<Half>(p[0], p[1]), pack2<Half>(p[2], p[3]),
+                                  pack2<Half>(p[4], p[5]), pack2<Half>(p[6], p[7]));
+              },
+              [&](int64_t r, int64_t col, uint4 u) {
+                *reinterpret_cast<uint4*>(static_cast<Out*>(s.out) + r * s.ld + col) = u;
+              });
+        else
+          store_elements(v, at, c);
+      }
       return;
     }
-    if (s.read_carry) {
-      const float* c = s.carry + row * s.n + col;
+    const int64_t ld = scratch_ld(s.n);
+#pragma unroll 1
+    for (int c = 0; c < at.width; c += 32) {
+      float v[32];
+      at.load(c, v);
+      if (c + 32 >= at.width) at.release();
+      if (zero)
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i)
-        if (i < width) v[i] += c[i];
-    }
-    if (s.write_carry) {
-      put(s.carry + row * s.n + col, v, width);
-      return;
-    }
-    const float f = s.factor();
-    const bool zero = s.masked(row);
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[i] = zero ? 0.0f : v[i] * f;
-    Out* out = static_cast<Out*>(s.out) + row * s.ld + col;
-    if (s.wide && width == kPiece) {
-#pragma unroll
-      for (int i = 0; i < kPiece; i += 8) store8<Out>(out + i, v + i, s.accumulate);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i)
-        if (i < width) out[i] = from_float<Out>(s.accumulate ? v[i] + to_float(out[i]) : v[i]);
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+      emit_rows<4>(
+          v, at, c, s.m,
+          [](const float* p) {
+            return make_uint4(__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
+                              __float_as_uint(p[3]));
+          },
+          [&](int64_t r, int64_t col, uint4 u) {
+            if (parts) {
+              *reinterpret_cast<uint4*>(parts + (at.split * s.m + r) * ld + col) = u;
+              return;
+            }
+            float4 sum = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                     __uint_as_float(u.w));
+            float4* carry = reinterpret_cast<float4*>(s.carry + r * ld + col);
+            if (s.read_carry) {
+              const float4 o = *carry;
+              sum = make_float4(sum.x + o.x, sum.y + o.y, sum.z + o.z, sum.w + o.w);
+            }
+            if (s.write_carry)
+              *carry = sum;
+            else
+              put4(r, col, sum, f);
+          });
     }
   }
 
-  // fp32 scratch rows: 16-byte stores where the row's start allows them
-  static __device__ __forceinline__ void put(float* to, const float (&v)[kPiece], int width) {
-    if (width == kPiece && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
-#pragma unroll
-      for (int i = 0; i < kPiece; i += 4)
-        *reinterpret_cast<float4*>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  // Four columns: scale, add what is there, round, store.
+  __device__ __forceinline__ void put4(int64_t row, int64_t col, float4 v, float f) const {
+    const float e[4] = {v.x, v.y, v.z, v.w};
+    Out* out = static_cast<Out*>(s.out) + row * s.ld + col;
+    const int left = int(min(int64_t(4), s.n - col));
+    if (s.wide && left == 4) {
+      if constexpr (sizeof(Out) == 4) {
+        float4* to = reinterpret_cast<float4*>(out);
+        const float4 o = s.accumulate ? *to : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        *to = make_float4(e[0] * f + o.x, e[1] * f + o.y, e[2] * f + o.z, e[3] * f + o.w);
+      } else {
+        uint2* to = reinterpret_cast<uint2*>(out);
+        float2 a = make_float2(0.0f, 0.0f), b = a;
+        if (s.accumulate) {
+          const uint2 old = *to;
+          a = unpack2<Out>(old.x);
+          b = unpack2<Out>(old.y);
+        }
+        *to = make_uint2(pack2<Out>(e[0] * f + a.x, e[1] * f + a.y),
+                         pack2<Out>(e[2] * f + b.x, e[3] * f + b.y));
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i)
-        if (i < width) to[i] = v[i];
+      for (int i = 0; i < 4; ++i)
+        if (i < left) out[i] = from_float<Out>(e[i] * f + (s.accumulate ? to_float(out[i]) : 0.0f));
     }
+  }
+
+  // 64 columns of 16-bit rows that do not start on 16 bytes: through the
+  // staging memory, then a row at a time, element by element.
+  using Half = typename std::conditional<sizeof(Out) == 2, Out, __half>::type;
+  __device__ __forceinline__ void store_elements(const float (&v)[64], const GemmPiece& at, int c) const {
+    const int lane = threadIdx.x % 32;
+    uint32_t* staging = reinterpret_cast<uint32_t*>(at.staging);
+    // pair p of row r at word 32 r + (p ^ r): no two lanes on one bank
+#pragma unroll
+    for (int p = 0; p < 32; ++p) staging[lane * 32 + (p ^ lane)] = pack2<Half>(v[2 * p], v[2 * p + 1]);
+    __syncwarp();
+    uint16_t* out = reinterpret_cast<uint16_t*>(s.out) + at.row0 * s.ld + at.col + c + lane;
+    const int rows = int(min(int64_t(32), s.m - at.row0)), left = at.width - c - lane;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r, out += s.ld) {
+      const uint32_t a = staging[r * 32 + ((lane / 2) ^ r)], b = staging[r * 32 + ((16 + lane / 2) ^ r)];
+      if (left > 0) out[0] = uint16_t(lane % 2 ? a >> 16 : a);
+      if (left > 32) out[32] = uint16_t(lane % 2 ? b >> 16 : b);
+    }
+    __syncwarp();
   }
 };
 
 // out = round(scale * sum over the parts), in the parts' order.
 template <class Out>
-__global__ void __launch_bounds__(256) join_kernel(const float* parts, int splits, StoreArgs s) {
-  const int64_t total = s.m * s.n;
+__global__ void __launch_bounds__(256) join_kernel(const float* parts, int splits, StoreEpilogue<Out> e) {
+  const StoreArgs& s = e.s;
+  const int64_t ld = scratch_ld(s.n), per_row = ld / 4, total = s.m * per_row;
   const float f = s.factor();
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    float sum = 0.0f;
-    for (int p = 0; p < splits; ++p) sum += parts[p * total + i];
-    const int64_t row = i / s.n, col = i - row * s.n;
-    Out* out = static_cast<Out*>(s.out) + row * s.ld + col;
-    if (s.read_carry) sum += s.carry[i];
-    if (s.write_carry) {
-      s.carry[i] = sum;
-      continue;
+    const int64_t row = i / per_row;
+    const float4* p = reinterpret_cast<const float4*>(parts) + i;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) {
+      const float4 v = p[k * total];
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
     }
-    sum = s.masked(row) ? 0.0f : sum * f;
-    *out = from_float<Out>(s.accumulate ? sum + to_float(*out) : sum);
+    if (s.masked(row)) sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    e.put4(row, (i - row * per_row) * 4, sum, f);
   }
 }
 
@@ -144,25 +181,16 @@ __global__ void __launch_bounds__(256) join_kernel(const float* parts, int split
 template <class T, bool A_MN, bool B_MN, class Out>
 fadam_status store_product(const CUtensorMap& a, const CUtensorMap& b, const GemmShape& shape,
                            const StoreArgs& args, float* parts, int sm_count, cudaStream_t stream) {
+  using E = typename Out::type;
   float* where = shape.splits > 1 ? parts : nullptr;
-  const fadam_status st = launch_gemm<T, A_MN, B_MN>(
-      a, b, shape, StoreEpilogue<typename Out::type>{args, where}, sm_count, stream);
+  const fadam_status st =
+      launch_gemm<T, A_MN, B_MN>(a, b, shape, StoreEpilogue<E>{args, where}, sm_count, stream);
   if (st || !where) return st;
-  const int64_t blocks = ceil_div(args.m * args.n, 256);
-  join_kernel<typename Out::type><<<unsigned(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(
-      where, shape.splits, args);
+  const int64_t blocks = ceil_div(args.m * scratch_ld(args.n) / 4, 256);
+  join_kernel<E><<<unsigned(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(
+      where, shape.splits, StoreEpilogue<E>{args, nullptr});
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "join launch");
-}
-
-// Into how many parts to cut k: one, unless the tiles leave most CTA pairs
-// idle and each part keeps at least eight steps.
-inline int choose_splits(int64_t m, int64_t n, int64_t k, int pairs) {
-  const int64_t tiles = ceil_div(m, kTileM) * ceil_div(n, kTileN);
-  const int64_t steps = ceil_div(k, kTileK);
-  int64_t splits = pairs / tiles;
-  if (splits > steps / 8) splits = steps / 8;
-  return splits < 2 ? 1 : int(splits);
 }
 
 }  // namespace fadam_ops

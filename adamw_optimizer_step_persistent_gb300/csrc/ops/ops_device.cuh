@@ -96,8 +96,11 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 }
 
 // Arrive at a barrier of any CTA of the cluster (an address from map_rank).
+// Relaxed: it orders no memory accesses (a release would wait for the global
+// stores before it); what it hands over is tensor memory, ordered by
+// tcgen05.wait and fence_before_sync.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity) {

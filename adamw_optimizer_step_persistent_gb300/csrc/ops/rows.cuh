@@ -204,10 +204,12 @@ __device__ __forceinline__ Scaling scaling(float a) {
           tiny ? 0.0f : finite ? inverse : 0.0f};
 }
 
-// Eight codes.  x * inverse + 1.5 * 2^23 rounds the product to an integer
-// (nearest even) whose low byte is the code; |code| <= 127 because inverse is
-// 127 / a rounded once.  (What is not finite is multiplied by 0: its codes
-// mean nothing beside a NaN scale.)
+// Eight codes.  x * inverse, rounded, + 1.5 * 2^23 rounds the product to an
+// integer (nearest even) whose low byte is the code; |code| <= 127 because
+// inverse is 127 / a rounded once.  (What is not finite is multiplied by 0:
+// its codes mean nothing beside a NaN scale.)  The products are not packed: a
+// packed multiply and the add that follows were contracted (one code in 10^5,
+// next to a tie, then differed from that of the two operations).
 template <class E>
 __device__ __forceinline__ uint2 code8(const Raw<E>& r, float inverse) {
   Pair v[4];
@@ -215,7 +217,8 @@ __device__ __forceinline__ uint2 code8(const Raw<E>& r, float inverse) {
   uint32_t bits[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 p = split(add2(mul2(v[i], both(inverse)), both(12582912.0f)));
+    const float2 e = split(v[i]);
+    const float2 p = split(add2(make_pair(__fmul_rn(e.x, inverse), __fmul_rn(e.y, inverse)), both(12582912.0f)));
     bits[2 * i] = __float_as_uint(p.x);
     bits[2 * i + 1] = __float_as_uint(p.y);
   }

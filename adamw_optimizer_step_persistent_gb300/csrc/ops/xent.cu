@@ -4,7 +4,7 @@
 //   dz_tv = s (exp(z_tv - lse_t) - [v = y(t)]),  dx = dz W,  dW = dz^T x
 //
 // Three products on the tensor cores (gemm.cuh).  The first never writes a
-// logit: a piece of 128 of a row's logits is reduced in registers to its
+// logit: a piece of (most often) 128 of a row's logits is reduced in registers to its
 // maximum and its sum of exponentials, and (for the gradients) its
 // exponentials relative to that maximum are kept in 16 bits.  A second kernel
 // joins a row's pieces to its lse and turns the kept exponentials into dz in
@@ -32,52 +32,81 @@ struct Control {
 
 // What the first product's epilogue needs to reduce the logits.
 struct LogitEpilogue {
-  int64_t rows, vocab, pieces;
+  int64_t rows, pieces;
+  int piece;         // columns of a piece
   const int64_t* targets;
   float2* stats;     // [rows, pieces]: maximum and sum of exponentials
   float* target_z;   // [rows]
   __half* kept;      // [rows, pitch] or NULL
   int64_t pitch;
 
-  __device__ __forceinline__ void operator()(float (&v)[kPiece], int64_t row, int64_t col,
-                                             int) const {
-    if (row >= rows || col >= vocab) return;
-    const int width = int(min(int64_t(kPiece), vocab - col));
-    const int64_t at = targets[row] - col;
-    if (at >= 0 && at < width) {
-      float z = 0.0f;
+  __device__ __forceinline__ void operator()(const GemmPiece& p) const {
+    const int64_t row = p.row0 + threadIdx.x % 32;
+    const int64_t at = row < rows ? targets[row] - p.col : -1;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < p.width; c += 64) {
+      float v[64];
+      load(p, c, v);
+      float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) z = i == at ? v[i] : z;
-      target_z[row] = z;
+      for (int i = 4; i < 64; ++i) m[i % 4] = fmaxf(m[i % 4], v[i]);
+      top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+      if (at >= c && at < c + 64 && at < p.width) {
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) z = c + i == at ? v[i] : z;
+        target_z[row] = z;
+      }
     }
-    if (width < kPiece) {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i)
-        if (i >= width) v[i] = -INFINITY;
-    }
-    float top = v[0];
-#pragma unroll
-    for (int i = 1; i < kPiece; ++i) top = fmaxf(top, v[i]);
     const float base = top == -INFINITY ? 0.0f : top;  // nothing above -inf: all terms are 0
-    float sum = 0.0f;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int c = 0; c < p.width; c += 64) {
+      float v[64];
+      load(p, c, v);
+      if (c + 64 >= p.width) p.release();
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) {
-      v[i] = exp2f((v[i] - base) * 1.4426950408889634f);
-      sum += v[i];
+      for (int i = 0; i < 64; ++i) {
+        v[i] = exp2_fast((v[i] - base) * 1.4426950408889634f);
+        sum[i % 4] += v[i];
+      }
+      if (kept)
+        emit_rows<8>(
+            v, p, c, rows,
+            [](const float* e) {
+              return make_uint4(pack2<__half>(e[0], e[1]), pack2<__half>(e[2], e[3]),
+                                pack2<__half>(e[4], e[5]), pack2<__half>(e[6], e[7]));
+            },
+            [&](int64_t r, int64_t col, uint4 u) {
+              *reinterpret_cast<uint4*>(kept + r * pitch + col) = u;
+            });
     }
-    stats[row * pieces + col / kPiece] = make_float2(top, sum);
-    if (kept) {
-      uint4* to = reinterpret_cast<uint4*>(kept + row * pitch + col);
+    if (row < rows)
+      stats[row * pieces + p.col / piece] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+  }
+
+  // 64 columns, those beyond the vocabulary (or the piece) as if their logits were -inf.
+  static __device__ __forceinline__ void load(const GemmPiece& p, int c, float (&v)[64]) {
+    p.load(c, v);
+    if (p.width - c < 64)
 #pragma unroll
-      for (int i = 0; i < kPiece; i += 8)
-        to[i / 8] = make_uint4(pack2<__half>(v[i], v[i + 1]), pack2<__half>(v[i + 2], v[i + 3]),
-                               pack2<__half>(v[i + 4], v[i + 5]), pack2<__half>(v[i + 6], v[i + 7]));
-    }
+      for (int i = 0; i < 64; ++i)
+        if (c + i >= p.width) v[i] = -INFINITY;
+  }
+
+  // 2^x for x <= 0; what is below 2^-126 is 0 (its share of a sum that is at
+  // least 1 is below every rounding).
+  static __device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
   }
 };
 
 struct RowArgs {
   int64_t rows, vocab, pieces, pitch, width, x_ld, kept_x_ld;
+  int piece;                     // columns of a piece, a multiple of 16
   int64_t first_row, all_rows;   // of this chunk, and of the whole call
   const float2* stats;
   const float* target_z;
@@ -96,56 +125,56 @@ struct RowArgs {
 };
 
 constexpr int kRowThreads = 256;
+constexpr int kRowUnroll = 4;  // vectors of eight per thread in flight
 
-__device__ __forceinline__ float block_sum(float v, float* shared) {
-#pragma unroll
-  for (int i = 16; i; i /= 2) v += __shfl_xor_sync(~0u, v, i);
-  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
-  __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kRowThreads / 32; ++i) s += shared[i];
-  __syncthreads();
-  return s;
-}
-__device__ __forceinline__ float block_max(float v, float* shared) {
-#pragma unroll
-  for (int i = 16; i; i /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, i));
-  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
-  __syncthreads();
-  float s = shared[0];
-#pragma unroll
-  for (int i = 1; i < kRowThreads / 32; ++i) s = fmaxf(s, shared[i]);
-  __syncthreads();
-  return s;
-}
+// log of a sum of exponentials, as the largest term and the sum relative to it.
+struct LogSum {
+  float top, sum;
+  __device__ __forceinline__ void add(LogSum o) {
+    const float t = fmaxf(top, o.top);
+    const float base = t == -INFINITY ? 0.0f : t;
+    sum = sum * expf(top - base) + o.sum * expf(o.top - base);
+    top = t;
+  }
+};
 
 // One block per row: lse and loss from the row's pieces, dz in place of the
 // kept exponentials, and the row of x that dW's product reads (a row that is
 // ignored must not reach dW even where x is not finite: 0 * inf is NaN).
 // The last block of a chunk adds up the losses in a fixed order.
 template <class T>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
   using E = typename T::type;
-  __shared__ float shared[kRowThreads / 32];
-  __shared__ double sums[kRowThreads];
-  __shared__ int64_t counts[kRowThreads];
+  __shared__ LogSum warps[kRowThreads / 32];
+  __shared__ double sums[kRowThreads / 32];
+  __shared__ int64_t counts[kRowThreads / 32];
   __shared__ bool last;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
   const float2* st = a.stats + row * a.pieces;
+  const int vectors = a.dz ? int((a.vocab + 7) / 8) : 0;
+  uint4* dz = reinterpret_cast<uint4*>(static_cast<__half*>(a.dz) + row * a.pitch);
 
-  float top = -INFINITY;
-  for (int64_t i = tid; i < a.pieces; i += kRowThreads) top = fmaxf(top, st[i].x);
-  top = block_max(top, shared);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
+  // the first exponentials are on their way while the pieces are joined
+  uint4 raw[kRowUnroll];
+#pragma unroll
+  for (int u = 0; u < kRowUnroll; ++u)
+    if (tid + u * kRowThreads < vectors) raw[u] = dz[tid + u * kRowThreads];
+
+  LogSum total{-INFINITY, 0.0f};
   for (int64_t i = tid; i < a.pieces; i += kRowThreads) {
     const float2 p = st[i];
-    sum += p.x == -INFINITY ? p.y : p.y * expf(p.x - base);
+    total.add({p.x, p.y});
   }
-  sum = block_sum(sum, shared);
-  const float lse = base + logf(sum);
+#pragma unroll
+  for (int i = 16; i; i /= 2)
+    total.add({__shfl_xor_sync(~0u, total.top, i), __shfl_xor_sync(~0u, total.sum, i)});
+  if (tid % 32 == 0) warps[tid / 32] = total;
+  __syncthreads();
+  total = warps[0];
+#pragma unroll
+  for (int i = 1; i < kRowThreads / 32; ++i) total.add(warps[i]);
+  const float lse = (total.top == -INFINITY ? 0.0f : total.top) + logf(total.sum);
 
   const int64_t target = a.targets[a.first_row + row];
   const bool ignored = target == a.ignore_index;
@@ -156,32 +185,54 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
     a.row_loss[a.first_row + row] = ignored ? 0.0f : valid ? lse - a.target_z[row] : NAN;
   }
 
-  if (a.dz) {
-    uint4* dz = reinterpret_cast<uint4*>(static_cast<__half*>(a.dz) + row * a.pitch);
-    for (int64_t c = tid; c * 8 < a.vocab; c += kRowThreads) {
-      const uint4 raw = dz[c];
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-      const float peak = st[c * 8 / kPiece].x;
-      const float f = !valid && !ignored ? NAN
-                      : peak == -INFINITY ? a.dz_scale : a.dz_scale * expf(peak - lse);
-      uint32_t out[4];
+  // vector c lies in piece c / per_piece; both advance with c
+  const int per_piece = a.piece / 8;
+  const int step = kRowThreads / per_piece, step_rest = kRowThreads % per_piece;
+  int piece = tid / per_piece, rest = tid % per_piece;
+  for (int first = tid; first < vectors; first += kRowUnroll * kRowThreads) {
+    uint4 now[kRowUnroll];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float2 p = unpack2<__half>(w[i]);
-        p.x *= f;
-        p.y *= f;
-        if (target == c * 8 + 2 * i) p.x -= a.dz_scale;
-        if (target == c * 8 + 2 * i + 1) p.y -= a.dz_scale;
-        out[i] = ignored ? 0u : pack2<E>(p.x, p.y);
+    for (int u = 0; u < kRowUnroll; ++u) {
+      now[u] = raw[u];
+      const int ahead = first + (kRowUnroll + u) * kRowThreads;
+      if (ahead < vectors) raw[u] = dz[ahead];
+    }
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const int c = first + u * kRowThreads;
+      if (c < vectors) {
+        const float peak = st[piece].x;
+        const float f = !valid && !ignored ? NAN
+                        : peak == -INFINITY ? a.dz_scale : a.dz_scale * expf(peak - lse);
+        const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+        uint32_t out[4];
+        const int64_t at = target - int64_t(c) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 p = unpack2<__half>(w[i]);
+          p.x = at == 2 * i ? p.x * f - a.dz_scale : p.x * f;
+          p.y = at == 2 * i + 1 ? p.y * f - a.dz_scale : p.y * f;
+          out[i] = ignored ? 0u : pack2<E>(p.x, p.y);
+        }
+        dz[c] = make_uint4(out[0], out[1], out[2], out[3]);
       }
-      dz[c] = make_uint4(out[0], out[1], out[2], out[3]);
+      piece += step;
+      rest += step_rest;
+      if (rest >= per_piece) {
+        rest -= per_piece;
+        ++piece;
+      }
     }
   }
   if (a.kept_x) {
     const E* from = static_cast<const E*>(a.x) + row * a.x_ld;
     E* to = static_cast<E*>(a.kept_x) + row * a.kept_x_ld;
-    for (int64_t i = tid; i < a.width; i += kRowThreads)
-      to[i] = ignored ? from_float<E>(0.0f) : from[i];
+    const int whole = int(a.width / 8);
+    for (int i = tid; i < whole; i += kRowThreads)
+      reinterpret_cast<uint4*>(to)[i] =
+          ignored ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(from)[i];
+    if (tid < a.width % 8)
+      to[whole * 8 + tid] = ignored ? from_float<E>(0.0f) : from[whole * 8 + tid];
   }
 
   __threadfence();
@@ -192,20 +243,27 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowArgs a) {
   // the losses of the rows so far (of all of them in the last chunk), and how
   // many rows of the whole call count
   __threadfence();
-  double total = 0.0;
+  double loss = 0.0;
   int64_t count = 0;
-  for (int64_t i = tid; i < a.first_row + a.rows; i += kRowThreads) total += __ldcg(a.row_loss + i);
+  for (int64_t i = tid; i < a.first_row + a.rows; i += kRowThreads) loss += __ldcg(a.row_loss + i);
   for (int64_t i = tid; i < a.all_rows; i += kRowThreads) count += a.targets[i] != a.ignore_index;
-  sums[tid] = total;
-  counts[tid] = count;
+#pragma unroll
+  for (int i = 16; i; i /= 2) {
+    loss += __shfl_xor_sync(~0u, loss, i);
+    count += __shfl_xor_sync(~0u, count, i);
+  }
+  if (tid % 32 == 0) {
+    sums[tid / 32] = loss;
+    counts[tid / 32] = count;
+  }
   __syncthreads();
   if (tid == 0) {
-    for (int i = 1; i < kRowThreads; ++i) {
-      total += sums[i];
+    for (int i = 1; i < kRowThreads / 32; ++i) {
+      loss += sums[i];
       count += counts[i];
     }
     const double share = a.mean ? 1.0 / double(count > 0 ? count : 1) : 1.0;
-    *a.loss = float(total * share);
+    *a.loss = float(loss * share);
     a.control->scale = float(a.loss_scale * share);
     a.control->finished = 0;
   }
@@ -223,7 +281,8 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const E* from, int64_t 
 
 struct Layout {
   int64_t chunk, chunks, pieces, pitch, width_ld;
-  int splits;  // of dx's product
+  int logit_tile, dx_tile, dw_tile;  // columns of the products' tiles
+  int splits;                        // of dx's product
   Control* control;
   float2* stats;
   float* target_z;
@@ -242,7 +301,7 @@ struct Layout {
 int64_t chunk_rows(const fadam_xent& d) {
   if (!d.grad_x && !d.grad_w) return d.rows;
   if (d.chunk_rows > 0) return d.chunk_rows < d.rows ? d.chunk_rows : d.rows;
-  const int64_t fit = (int64_t(4) << 30) / (round_up(d.vocab, kPiece) * 2);
+  const int64_t fit = (int64_t(4) << 30) / (round_up(d.vocab, 64) * 2);
   const int64_t whole = fit / kTileM * kTileM;
   const int64_t chunk = whole < kTileM ? kTileM : whole;
   return chunk < d.rows ? chunk : d.rows;
@@ -254,10 +313,14 @@ Layout layout(const fadam_xent& d, char* base, int sm_count) {
   const bool grads = d.grad_x || d.grad_w;
   l.chunk = chunk_rows(d);
   l.chunks = ceil_div(d.rows, l.chunk);
-  l.pieces = ceil_div(d.vocab, kPiece);
-  l.pitch = l.pieces * kPiece;
+  const int pairs = sm_count / 2;
+  l.logit_tile = choose_tile_n(l.chunk, d.vocab, d.width, false, false, pairs);
+  l.dx_tile = choose_tile_n(l.chunk, d.width, d.vocab, true, true, pairs);
+  l.dw_tile = choose_tile_n(d.vocab, d.width, l.chunk, true, false, pairs);
+  l.pieces = ceil_div(d.vocab, l.logit_tile / 2);
+  l.pitch = round_up(d.vocab, 64);
   l.width_ld = round_up(d.width, 8);
-  l.splits = choose_splits(l.chunk, d.width, d.vocab, sm_count / 2);
+  l.splits = choose_splits(l.chunk, d.width, d.vocab, l.dx_tile, pairs);
   l.control = static_cast<Control*>(c.take(sizeof(Control)));
   l.stats = static_cast<float2*>(c.take(sizeof(float2) * l.chunk * l.pieces));
   l.target_z = static_cast<float*>(c.take(sizeof(float) * l.chunk));
@@ -266,8 +329,8 @@ Layout layout(const fadam_xent& d, char* base, int sm_count) {
   if (!bulk_readable(d.x, d.x_stride)) l.x_rows = c.take(2 * d.rows * l.width_ld);
   if (!bulk_readable(d.w, d.w_stride)) l.w_rows = c.take(2 * d.vocab * l.width_ld);
   if (d.grad_x && l.splits > 1)
-    l.parts = static_cast<float*>(c.take(4 * int64_t(l.splits) * l.chunk * d.width));
-  if (d.grad_w && l.chunks > 1) l.carry = static_cast<float*>(c.take(4 * d.vocab * d.width));
+    l.parts = static_cast<float*>(c.take(4 * int64_t(l.splits) * l.chunk * scratch_ld(d.width)));
+  if (d.grad_w && l.chunks > 1) l.carry = static_cast<float*>(c.take(4 * d.vocab * scratch_ld(d.width)));
   l.bytes = c.used;
   return l;
 }
@@ -303,8 +366,8 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     w_ld = l.width_ld;
   }
   CUtensorMap w_k, w_mn;
-  if ((st = matrix_map(&w_k, w, d.vocab, d.width, w_ld, box_rows(false)))) return st;
-  if ((st = matrix_map(&w_mn, w, d.vocab, d.width, w_ld, box_rows(true)))) return st;
+  if ((st = matrix_map(&w_k, w, d.vocab, d.width, w_ld, box_rows(false, l.logit_tile / 2)))) return st;
+  if ((st = matrix_map(&w_mn, w, d.vocab, d.width, w_ld, box_rows(true, 0)))) return st;
   // fp16 dz is held times 2^15
   const float dz_scale = T::code == FADAM_DT_F16 ? 32768.0f : 1.0f;
 
@@ -312,16 +375,17 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     const int64_t rows = d.rows - first < l.chunk ? d.rows - first : l.chunk;
     const bool last_chunk = first + rows == d.rows;
     CUtensorMap map;
-    if ((st = matrix_map(&map, x + first * x_ld, rows, d.width, x_ld, box_rows(false)))) return st;
-    LogitEpilogue epi{rows, d.vocab, l.pieces, d.targets + first, l.stats, l.target_z,
+    if ((st = matrix_map(&map, x + first * x_ld, rows, d.width, x_ld, box_rows(false, 128)))) return st;
+    LogitEpilogue epi{rows, l.pieces, l.logit_tile / 2, d.targets + first, l.stats, l.target_z,
                       static_cast<__half*>(l.kept), l.pitch};
-    GemmShape shape = gemm_shape(rows, d.vocab, d.width, 1, 8, dev.status);
+    GemmShape shape = gemm_shape(rows, d.vocab, d.width, l.logit_tile, 1, dev.status);
     if ((st = launch_gemm<T, false, false>(map, w_k, shape, epi, dev.sm_count, stream))) return st;
 
     RowArgs r{};
     r.rows = rows;
     r.vocab = d.vocab;
     r.pieces = l.pieces;
+    r.piece = l.logit_tile / 2;
     r.pitch = l.pitch;
     r.width = d.width;
     r.x_ld = x_ld;
@@ -347,7 +411,7 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     if (!grads) continue;
 
     if (d.grad_x) {
-      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(false)))) return st;
+      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(false, 128)))) return st;
       StoreArgs s{};
       s.out = static_cast<E*>(d.grad_x) + first * d.grad_x_stride;
       s.ld = d.grad_x_stride;
@@ -358,14 +422,14 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
       s.targets = d.targets + first;
       s.ignore_index = d.ignore_index;
       s.wide = wide_stores(s.out, s.ld, 2);
-      shape = gemm_shape(rows, d.width, d.vocab, l.splits, 8, dev.status);
+      shape = gemm_shape(rows, d.width, d.vocab, l.dx_tile, l.splits, dev.status);
       if ((st = store_product<T, false, true, T>(map, w_mn, shape, s, l.parts, dev.sm_count, stream)))
         return st;
     }
     if (d.grad_w) {
       CUtensorMap x_mn;
-      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(true)))) return st;
-      if ((st = matrix_map(&x_mn, l.kept_x, rows, d.width, l.width_ld, box_rows(true)))) return st;
+      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(true, 0)))) return st;
+      if ((st = matrix_map(&x_mn, l.kept_x, rows, d.width, l.width_ld, box_rows(true, 0)))) return st;
       StoreArgs s{};
       s.out = d.grad_w;
       s.ld = d.grad_w_stride;
@@ -378,7 +442,7 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
       s.write_carry = !last_chunk;
       s.accumulate = (d.flags & FADAM_XENT_ACCUMULATE) != 0;
       s.wide = wide_stores(s.out, s.ld, sizeof(typename OutW::type));
-      shape = gemm_shape(d.vocab, d.width, rows, 1, 8, dev.status);
+      shape = gemm_shape(d.vocab, d.width, rows, l.dw_tile, 1, dev.status);
       if ((st = store_product<T, true, true, OutW>(map, x_mn, shape, s, nullptr, dev.sm_count, stream)))
         return st;
     }
