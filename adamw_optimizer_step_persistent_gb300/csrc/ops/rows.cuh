@@ -193,14 +193,15 @@ __device__ __forceinline__ float from_bits(uint32_t bits) {
 }
 
 // A group's scale, and what its elements are multiplied by (0 in a group of
-// zeros, NaN in one that is not finite).
+// zeros or one that is not finite).  The scale is rounded towards zero: 127
+// times it is then never above a, which may be the type's largest value.
 struct Scaling {
   float scale, inverse;
 };
 __device__ __forceinline__ Scaling scaling(float a) {
   const bool finite = a < INFINITY, tiny = a < kTinyGroup;
   const float inverse = __fdiv_rn(127.0f, tiny ? 1.0f : a);
-  return {finite ? tiny ? 0.0f : __fdiv_rn(a, 127.0f) : __uint_as_float(0x7fffffffu),
+  return {finite ? tiny ? 0.0f : __fdiv_rz(a, 127.0f) : __uint_as_float(0x7fffffffu),
           tiny ? 0.0f : finite ? inverse : 0.0f};
 }
 

@@ -99,9 +99,9 @@ fadam_status fadam_xent_run(const fadam_xent* desc, void* workspace, size_t byte
 /* A matrix kept in 8 bits: codes [rows, width] and, for each started group of
  * 128 elements of a row, one fp32 scale [rows, ceil(width / 128)], both
  * contiguous.  Element = code * scale, |code| <= 127.  With a the group's
- * largest magnitude: scale = a / 127, code = x * (127 / a) rounded to nearest
- * even, so an element is off by at most a / 254 (and rounding errors of 2^-23
- * of a).  A group with a < 2^-100 is kept as zeros; one with an infinity or a
+ * largest magnitude: scale = a / 127 rounded towards zero (so that 127 scale
+ * <= a), code = x * (127 / a) rounded to nearest even; an element is off by at
+ * most a / 254 (and rounding errors of 2^-23 of a).  A group with a < 2^-100 is kept as zeros; one with an infinity or a
  * NaN gets a NaN scale and is NaN throughout when restored. */
 typedef struct {
   int8_t* codes;
