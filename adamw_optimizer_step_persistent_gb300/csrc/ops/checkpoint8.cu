@@ -182,7 +182,7 @@ fadam_status check_matrix(const void* x, int64_t rows, int64_t width, int64_t st
 // ---- the weight gradient -----------------------------------------------------------
 
 struct Layout {
-  int tile, splits;
+  GemmPlan plan;
   int64_t x_ld, dy_ld;
   void* x;        // the restored checkpoint
   void* dy_rows;  // an aligned copy of dy, where its own rows are not
@@ -193,8 +193,7 @@ struct Layout {
 Layout layout(const fadam_wgrad& d, char* base, int sm_count) {
   Layout l{};
   Carver c{base};
-  l.tile = choose_tile_n(d.n, d.width, d.rows, true, true, sm_count / 2);
-  l.splits = choose_splits(d.n, d.width, d.rows, l.tile, sm_count / 2);
+  l.plan = plan_gemm(d.n, d.width, d.rows, true, true, sm_count / 2);
   l.x_ld = round_up(d.width, 8);
   l.dy_ld = d.dy_stride;
   l.x = c.take(2 * d.rows * l.x_ld);
@@ -202,7 +201,7 @@ Layout layout(const fadam_wgrad& d, char* base, int sm_count) {
     l.dy_ld = round_up(d.n, 8);
     l.dy_rows = c.take(2 * d.rows * l.dy_ld);
   }
-  if (l.splits > 1) l.parts = static_cast<float*>(c.take(4 * int64_t(l.splits) * d.n * scratch_ld(d.width)));
+  if (const size_t parts = split_bytes(d.n, l.plan)) l.parts = static_cast<float*>(c.take(parts));
   l.bytes = c.used;
   return l;
 }
@@ -238,7 +237,7 @@ fadam_status run(const fadam_wgrad& d, const Layout& l, const DeviceFacts& dev, 
   s.constant = 1.0f;
   s.accumulate = (d.flags & FADAM_WGRAD_ACCUMULATE) != 0;
   s.wide = wide_stores(d.out, d.out_stride, sizeof(typename Out::type));
-  const GemmShape shape = gemm_shape(d.n, d.width, d.rows, l.tile, l.splits, dev.status);
+  const GemmShape shape = gemm_shape(d.n, d.width, d.rows, l.plan, dev.status);
   return store_product<T, true, true, Out>(a, b, shape, s, l.parts, dev.sm_count, stream);
 }
 

@@ -29,7 +29,8 @@ constexpr int kStages = 6;
 constexpr int kOperandBytes = 128 * kTileK * 2;  // one operand of one stage in one CTA
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpilogueWarps = 8;
-constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kLoadA = kEpilogueWarps, kLoadB = kLoadA + 1, kMultiply = kLoadA + 2;  // the other warps
+constexpr int kGemmThreads = (kEpilogueWarps + 3) * 32;
 constexpr int kPiece = 128;  // most columns of a tile that one epilogue warp takes
 constexpr int kTmemColumns = 512;
 constexpr int kStagingBytes = 4096;  // of one epilogue warp: 32 rows of 128 bytes
@@ -45,80 +46,113 @@ constexpr size_t kGemmSmem =
     1024 + size_t(kStages) * kStageBytes + kEpilogueWarps * kStagingBytes + sizeof(GemmBarriers);
 static_assert(kGemmSmem <= 227 * 1024, "shared memory of one CTA");
 
-// How the work is cut: tiles in groups of `group_m` rows of tiles, within a
-// group one column of tiles after the other, so that CTA pairs that run at
-// the same time share operands in L2; each tile's k steps in `splits` parts.
+// How the work is cut.  Tiles go in groups of `group_m` rows of tiles, within
+// a group one column of tiles after the other, so that CTA pairs that run at
+// the same time share operands in L2.  The first `full` tiles are whole items;
+// the rest are cut along k into `splits` items each, whose sums go to scratch
+// memory and are joined by a second kernel.
 struct GemmShape {
   int64_t m, n;
   int32_t tile_n;  // a multiple of 32, at most kTileN
   int32_t m_tiles, n_tiles, group_m;
-  int32_t k_steps, splits, steps_per_split;
-  int64_t items;
+  int32_t full, splits;
+  int32_t k_steps, steps_per_split;
+  int32_t items;
+  int32_t a_box, b_box;  // rows of a k-major operand's box
   int* status;
 };
 
-// Into how many parts to cut k: one, unless the tiles leave most CTA pairs
-// idle and each part keeps at least eight steps.
-inline int choose_splits(int64_t m, int64_t n, int64_t k, int tile_n, int pairs) {
-  const int64_t tiles = ceil_div(m, kTileM) * ceil_div(n, tile_n);
-  const int64_t steps = ceil_div(k, kTileK);
-  int64_t splits = pairs / tiles;
-  if (splits > steps / 8) splits = steps / 8;
-  return splits < 2 ? 1 : int(splits);
+// A product's plan: the tile's columns, and how its tiles become items.
+struct GemmPlan {
+  int tile_n, full, splits;
+  int64_t rest;  // tiles that are split
+};
+
+// Rows of a split tile's sums in scratch memory.
+__host__ __device__ inline int64_t split_rows(int64_t m) { return m < kTileM ? m : kTileM; }
+inline size_t split_bytes(int64_t m, const GemmPlan& p) {
+  return p.splits > 1 ? size_t(p.rest) * p.splits * split_rows(m) * p.tile_n * sizeof(float) : 0;
 }
 
-// The tile's columns.  What a step costs is what it loads (256 rows of A, the
-// tile's of B), so a narrower tile pays only where it saves waves of tiles:
-// 11008 x 4096 outputs of 8192 rows took 434 us in ten waves of 256 columns,
-// 613 us in eleven of 224.  Narrower than 256 by 128 only where B's own index
-// is contiguous (its boxes are 64 wide and start on 128 bytes).
-inline int choose_tile_n(int64_t m, int64_t n, int64_t k, bool b_mn, bool split, int pairs) {
-  int best = kTileN;
-  int64_t least = 0;
+// The plan with the least estimated time, in steps of a 256-column tile.  A
+// step costs what it loads (256 rows of A, the tile's of B), so a narrower
+// tile pays only where it saves waves of tiles: 11008 x 4096 outputs of 8192
+// rows took 434 us in ten waves of 256 columns, 613 us in eleven of 224.  An
+// item costs six steps more (the ring's fill, the epilogue's end), split sums
+// their way through memory.  Where B's own index is contiguous its boxes are
+// 64 wide and start on 128 bytes, so its tiles are 256 or 128.
+inline GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, bool b_mn, bool may_split, int pairs) {
+  GemmPlan best{};
+  double least = 0;
+  const int64_t steps = ceil_div(k, kTileK);
   for (int t = kTileN; t >= (b_mn ? 128 : 64); t -= b_mn ? 128 : 32) {
-    const int parts = split ? choose_splits(m, n, k, t, pairs) : 1;
-    const int64_t waves = ceil_div(ceil_div(m, kTileM) * ceil_div(n, t) * parts, pairs);
-    const int64_t cost = waves * (kTileM + t) * 64 / parts;
-    if (t == kTileN || cost * 102 < least * 100) {
-      best = t;
-      least = cost;
+    const int64_t tiles = ceil_div(m, kTileM) * ceil_div(n, t);
+    const double step = double(kTileM + t) / (2 * kTileM);
+    // whole waves first; split the rest, or the rest and one wave
+    for (int64_t full = tiles / pairs * pairs; full >= 0; full -= pairs) {
+      const int64_t rest = tiles - full;
+      for (int64_t s = 1; s <= (may_split && rest ? 32 : 1) && (s == 1 || steps / s >= 8); ++s) {
+        const double sums = s > 1 ? double(rest) * s * split_rows(m) * t * 8 / 6.7e12 / 0.34e-6 + 12 : 0;
+        const double cost = (full / pairs * (steps + 6) +
+                             ceil_div(rest * s, pairs) * (ceil_div(steps, s) + 6)) * step + sums;
+        if (least == 0 || cost < least * 0.99) {
+          least = cost;
+          best = {t, int(s > 1 ? full : tiles), int(s), s > 1 ? rest : 0};
+        }
+      }
+      if (full < pairs || tiles - full > pairs) break;
     }
   }
   return best;
 }
 
-inline GemmShape gemm_shape(int64_t m, int64_t n, int64_t k, int tile_n, int splits, int* status) {
+inline GemmShape gemm_shape(int64_t m, int64_t n, int64_t k, const GemmPlan& plan, int* status) {
   GemmShape s{};
   s.m = m;
   s.n = n;
-  s.tile_n = tile_n;
+  s.tile_n = plan.tile_n;
   s.m_tiles = int32_t(ceil_div(m, kTileM));
-  s.n_tiles = int32_t(ceil_div(n, tile_n));
+  s.n_tiles = int32_t(ceil_div(n, plan.tile_n));
   s.group_m = 8;
   s.k_steps = int32_t(ceil_div(k, kTileK));
-  s.steps_per_split = int32_t(ceil_div(s.k_steps, splits));
+  const int32_t tiles = s.m_tiles * s.n_tiles;
+  s.full = plan.splits > 1 && plan.full < tiles ? plan.full : tiles;
+  s.steps_per_split = int32_t(ceil_div(s.k_steps, plan.splits));
   s.splits = int32_t(ceil_div(s.k_steps, s.steps_per_split));
-  s.items = int64_t(s.m_tiles) * s.n_tiles * s.splits;
+  s.items = s.full + (tiles - s.full) * s.splits;
+  s.a_box = m < 128 ? int32_t(round_up(m, 8)) : 128;
+  s.b_box = plan.tile_n / 2;
   s.status = status;
   return s;
 }
 
 struct GemmItem {
-  int m0, n0, split, step0, steps;
+  int m0, n0, step0, steps;
+  int slot;  // of a split tile's part: (tile - full) * splits + split; else -1
 };
 
-__device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int64_t item) {
+__device__ __forceinline__ void gemm_tile(const GemmShape& s, unsigned tile, int& m0, int& n0) {
+  const unsigned per_group = unsigned(s.group_m) * unsigned(s.n_tiles);
+  const unsigned group = tile / per_group, in_group = tile - group * per_group;
+  const unsigned rows = min(unsigned(s.group_m), unsigned(s.m_tiles) - group * s.group_m);
+  const unsigned col = in_group / rows;
+  n0 = int(col) * s.tile_n;
+  m0 = int(group * s.group_m + in_group - col * rows) * kTileM;
+}
+// The steps of an item alone, for the thread that needs no more.
+__device__ __forceinline__ int gemm_steps(const GemmShape& s, int item, int& step0) {
+  if (item < s.full) {
+    step0 = 0;
+    return s.k_steps;
+  }
+  step0 = int(unsigned(item - s.full) % unsigned(s.splits)) * s.steps_per_split;
+  return min(s.steps_per_split, s.k_steps - step0);
+}
+__device__ __forceinline__ GemmItem gemm_item(const GemmShape& s, int item) {
   GemmItem it;
-  const int64_t tile = item / s.splits;
-  it.split = int(item - tile * s.splits);
-  const int64_t per_group = int64_t(s.group_m) * s.n_tiles;
-  const int group = int(tile / per_group);
-  const int in_group = int(tile - group * per_group);
-  const int rows = min(s.group_m, s.m_tiles - group * s.group_m);
-  it.n0 = in_group / rows * s.tile_n;
-  it.m0 = (group * s.group_m + in_group % rows) * kTileM;
-  it.step0 = it.split * s.steps_per_split;
-  it.steps = min(s.steps_per_split, s.k_steps - it.step0);
+  it.steps = gemm_steps(s, item, it.step0);
+  it.slot = item < s.full ? -1 : item - s.full;
+  gemm_tile(s, item < s.full ? item : s.full + unsigned(item - s.full) / unsigned(s.splits), it.m0, it.n0);
   return it;
 }
 
@@ -132,33 +166,77 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
          uint64_t(1) << 46 | uint64_t(2) << 61;
 }
 
-// One operand's share of one step: `rows` (at most 128) of its rows from
-// `row`, 64 of k from `k`.  Returns the bytes that will arrive.
+// One operand's share of one step, for one CTA: its rows from `row`, 64 of k
+// from `k`, in one box of `box` rows (or up to two of 64 columns where its own
+// index is contiguous).  Boxes that lie wholly outside the matrix's `limit`
+// rows are left out: what their place holds reaches only results that are not
+// stored.
 template <bool MN>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int rows,
-                                             int k, uint32_t bar) {
-  if (MN) {
-    load_box_pair(dst, map, row, k, bar);
-    if (rows > 64) load_box_pair(dst + kOperandBytes / 2, map, row + 64, k, bar);
-  } else {
-    load_box_pair(dst, map, k, row, bar);
-  }
+__device__ __forceinline__ int operand_boxes(int row, int box, int64_t limit) {
+  if (row >= limit) return 0;
+  return MN && box > 64 && row + 64 < limit ? 2 : 1;
 }
-// Rows of the boxes that a map must have for it, and the bytes of its boxes.
-inline int box_rows(bool mn, int rows) { return mn ? kTileK : rows; }
-__host__ __device__ inline int operand_bytes(bool mn, int rows) {
-  return (mn ? (rows + 63) / 64 * 64 : rows) * kTileK * 2;
+template <bool MN>
+__device__ __forceinline__ int box_bytes(int box) { return (MN ? 64 : box) * kTileK * 2; }
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int boxes,
+                                             int k, uint32_t bar) {
+  if (boxes > 0) load_box_pair(dst, map, MN ? row : k, MN ? k : row, bar);
+  if (MN && boxes > 1) load_box_pair(dst + kOperandBytes / 2, map, row + 64, k, bar);
+}
+// Rows of the boxes of an operand's map.
+inline int box_rows(bool mn, int box) { return mn ? kTileK : box; }
+
+// The thread that loads one operand: its boxes of every step of this CTA's
+// items into the ring.  The pair's first CTA counts what arrives in both.
+template <bool MN>
+__device__ __forceinline__ void load_loop(const GemmShape& shape, const CUtensorMap* map,
+                                          GemmBarriers* bars, uint32_t to, bool is_a, int box,
+                                          uint32_t rank) {
+  prefetch_map(map);
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int apart = is_a ? 128 : shape.tile_n / 2;  // from the first CTA's rows to the second's
+  const int64_t limit = is_a ? shape.m : shape.n;
+  int stage = 0;
+  unsigned parity = 1;  // a barrier that no phase has completed passes for parity 1
+  int64_t count = 0;    // steps issued
+  bool ok = true;
+  for (int item = pair; ok && item < shape.items; item += pairs) {
+    const GemmItem it = gemm_item(shape, item);
+    const int first = is_a ? it.m0 : it.n0, row = first + int(rank) * apart;
+    const int boxes = operand_boxes<MN>(row, box, limit);
+    const int bytes = (operand_boxes<MN>(first, box, limit) +
+                       operand_boxes<MN>(first + apart, box, limit)) * box_bytes<MN>(box);
+    int k = it.step0 * kTileK;
+    for (int i = 0; i < it.steps; ++i, ++count, k += kTileK) {
+      ok = bar_wait(shared_addr(&bars->empty[stage]), parity, shape.status);
+      if (!ok) break;
+      const uint32_t full = shared_addr(&bars->full[stage]);
+      if (rank == 0) bar_expect(full, bytes);
+      load_operand<MN>(to + stage * kStageBytes, map, row, boxes, k, map_rank(full, 0));
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1;
+      }
+    }
+  }
+  // every stage's copies have landed and been used before the CTA ends
+  for (int i = 0; i < kStages; ++i)
+    if (int64_t at = count - 1 - i; at >= 0)
+      bar_wait(shared_addr(&bars->empty[at % kStages]), unsigned(at / kStages) & 1, shape.status);
 }
 
 // What an epilogue warp works on: rows row0 .. row0 + 31 (one to a lane) and
-// `width` columns from `col` of the product, the part of k, the columns'
-// address in tensor memory, its staging memory.
+// `width` columns from `col` of the product, the columns' address in tensor
+// memory, its staging memory.
 struct GemmPiece {
   int64_t row0, col;
-  int width, split;
+  int width;
+  int slot;            // of a split tile's part, or -1
+  int tile_row, tile_col;  // row0 and col within the tile
   uint32_t tmem;
   uint32_t acc_empty;  // the accumulator's barrier, in the pair's first CTA
-  unsigned char* staging;
+  uint32_t staging;    // shared address
 
   // N (a multiple of 32) columns from column c of this lane's row.
   template <int N>
@@ -181,23 +259,30 @@ struct GemmPiece {
 // staging memory, 128 bytes of each row (their 16-byte words exchanged by row
 // so that no bank is hit twice).  `pack(v + i)` makes 16 bytes of kPerUnit
 // elements; emit(row, column, unit) gets every unit that starts inside the
-// piece.
+// piece, by its row and column there.
 template <int kPerUnit, class Pack, class Emit>
 __device__ __forceinline__ void emit_rows(const float (&v)[8 * kPerUnit], const GemmPiece& at, int c,
                                           int64_t rows, Pack pack, Emit emit) {
   const int lane = threadIdx.x % 32;
-  uint4* staging = reinterpret_cast<uint4*>(at.staging);
 #pragma unroll
-  for (int u = 0; u < 8; ++u) staging[lane * 8 + (u ^ (lane & 7))] = pack(v + u * kPerUnit);
+  for (int u = 0; u < 8; ++u)
+    store_shared(at.staging + (lane * 8 + (u ^ (lane & 7))) * 16, pack(v + u * kPerUnit));
   __syncwarp();
   const int u = lane % 8, col = c + u * kPerUnit;
+  uint4 unit[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = i * 4 + lane / 8;
-    const uint4 unit = staging[r * 8 + (u ^ (r & 7))];
-    if (at.row0 + r < rows && col < at.width) emit(at.row0 + r, at.col + col, unit);
+    unit[i] = load_shared(at.staging + (r * 8 + (u ^ (r & 7))) * 16);
   }
   __syncwarp();
+  if (col >= at.width) return;
+  const int left = int(min(int64_t(32), rows - at.row0));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + lane / 8;
+    if (r < left) emit(r, col, unit[i]);
+  }
 }
 
 // Epi: operator()(const GemmPiece&) is called by whole warps, loads the piece,
@@ -209,15 +294,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 const __grid_constant__ GemmShape shape, const __grid_constant__ Epi epi) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t tiles = (shared_addr(smem_raw) + 1023) & ~1023u;
-  unsigned char* staging = smem_raw + (tiles - shared_addr(smem_raw)) + size_t(kStages) * kStageBytes;
-  GemmBarriers* bars = reinterpret_cast<GemmBarriers*>(staging + kEpilogueWarps * kStagingBytes);
+  const uint32_t staging = tiles + kStages * kStageBytes;
+  GemmBarriers* bars = reinterpret_cast<GemmBarriers*>(
+      smem_raw + (staging + kEpilogueWarps * kStagingBytes - shared_addr(smem_raw)));
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      bar_init(shared_addr(&bars->full[i]), 1);
+      bar_init(shared_addr(&bars->full[i]), 2);  // what A's and B's loads expect
       bar_init(shared_addr(&bars->empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -226,43 +312,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kEpilogueWarps + 1) tmem_alloc_pair(shared_addr(&bars->tmem), kTmemColumns);
+  if (warp == kMultiply) tmem_alloc_pair(shared_addr(&bars->tmem), kTmemColumns);
   fence_before_sync();
   __syncthreads();
   cluster_sync();
   fence_after_sync();
   const uint32_t tmem = bars->tmem;
 
-  if (warp == kEpilogueWarps) {
-    if (lane == 0) {
-      prefetch_map(&map_a);
-      prefetch_map(&map_b);
-      const int half = shape.tile_n / 2;
-      const int step_bytes = 2 * (operand_bytes(A_MN, 128) + operand_bytes(B_MN, half));
-      int64_t count = 0;  // steps issued
-      bool ok = true;
-      for (int64_t item = pair; ok && item < shape.items; item += pairs) {
-        const GemmItem it = gemm_item(shape, item);
-        for (int i = 0; ok && i < it.steps; ++i, ++count) {
-          const int stage = int(count % kStages);
-          const unsigned parity = unsigned(count / kStages) & 1;
-          // a barrier that no phase has completed passes for the other parity
-          ok = bar_wait(shared_addr(&bars->empty[stage]), parity ^ 1, shape.status);
-          if (!ok) break;
-          if (rank == 0) bar_expect(shared_addr(&bars->full[stage]), step_bytes);
-          const uint32_t full = map_rank(shared_addr(&bars->full[stage]), 0);
-          const uint32_t a = tiles + stage * kStageBytes, b = a + kOperandBytes;
-          const int k = (it.step0 + i) * kTileK;
-          load_operand<A_MN>(a, &map_a, it.m0 + int(rank) * 128, 128, k, full);
-          load_operand<B_MN>(b, &map_b, it.n0 + int(rank) * half, half, k, full);
-        }
-      }
-      // every stage's copies have landed and been used before the CTA ends
-      for (int i = 0; i < kStages; ++i)
-        if (int64_t at = count - 1 - i; at >= 0)
-          bar_wait(shared_addr(&bars->empty[at % kStages]), unsigned(at / kStages) & 1, shape.status);
-    }
-  } else if (warp == kEpilogueWarps + 1) {
+  if (warp == kLoadA) {
+    if (lane == 0) load_loop<A_MN>(shape, &map_a, bars, tiles, true, A_MN ? 128 : shape.a_box, rank);
+  } else if (warp == kLoadB) {
+    if (lane == 0) load_loop<B_MN>(shape, &map_b, bars, tiles + kOperandBytes, false, shape.b_box, rank);
+  } else if (warp == kMultiply) {
     if (rank == 0 && lane == 0) {
       constexpr uint32_t kType = T::code == FADAM_DT_BF16 ? 1 : 0;
       // fp32 result, operand types, which operands are not k-major, the tile
@@ -272,17 +333,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       // 16 of k further on: 32 bytes of a row, or 16 rows
       constexpr uint64_t a_step = A_MN ? (16 * 128) >> 4 : 32 >> 4;
       constexpr uint64_t b_step = B_MN ? (16 * 128) >> 4 : 32 >> 4;
-      int64_t count = 0, tile = 0;
+      int stage = 0, tile = 0;
+      unsigned parity = 0;
       bool ok = true;
-      for (int64_t item = pair; ok && item < shape.items; item += pairs, ++tile) {
-        const GemmItem it = gemm_item(shape, item);
-        const int acc = int(tile & 1);
+      for (int item = pair; ok && item < shape.items; item += pairs, ++tile) {
+        int step0;
+        const int steps = gemm_steps(shape, item, step0);
+        const int acc = tile & 1;
         ok = bar_wait(shared_addr(&bars->acc_empty[acc]), (unsigned(tile >> 1) & 1) ^ 1, shape.status);
         if (!ok) break;
         fence_after_sync();
-        for (int i = 0; i < it.steps; ++i, ++count) {
-          const int stage = int(count % kStages);
-          ok = bar_wait(shared_addr(&bars->full[stage]), unsigned(count / kStages) & 1, shape.status);
+        for (int i = 0; i < steps; ++i) {
+          ok = bar_wait(shared_addr(&bars->full[stage]), parity, shape.status);
           if (!ok) break;
           fence_after_sync();
           const uint32_t a = tiles + stage * kStageBytes;
@@ -291,6 +353,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           for (int k = 0; k < kTileK / 16; ++k)
             mma_pair(tmem + acc * kTileN, da + k * a_step, db + k * b_step, idesc, i > 0 || k > 0);
           commit_pair(shared_addr(&bars->empty[stage]));
+          if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1;
+          }
         }
         commit_pair(shared_addr(&bars->acc_full[acc]));
       }
@@ -300,16 +366,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + half * half_n;
     GemmPiece at;
     at.staging = staging + warp * kStagingBytes;
-    int64_t tile = 0;
-    for (int64_t item = pair; item < shape.items; item += pairs, ++tile) {
+    at.tile_row = int(rank) * 128 + quarter * 32;
+    at.tile_col = half * half_n;
+    int tile = 0;
+    for (int item = pair; item < shape.items; item += pairs, ++tile) {
       const GemmItem it = gemm_item(shape, item);
-      const int acc = int(tile & 1);
+      const int acc = tile & 1;
       if (!bar_wait(shared_addr(&bars->acc_full[acc]), unsigned(tile >> 1) & 1, shape.status)) break;
       fence_after_sync();
-      at.row0 = int64_t(it.m0) + rank * 128 + quarter * 32;
-      at.col = int64_t(it.n0) + half * half_n;
+      at.row0 = int64_t(it.m0) + at.tile_row;
+      at.col = int64_t(it.n0) + at.tile_col;
       at.width = int(min(int64_t(half_n), shape.n - at.col));
-      at.split = it.split;
+      at.slot = it.slot;
       at.tmem = lanes + acc * kTileN;
       at.acc_empty = map_rank(shared_addr(&bars->acc_empty[acc]), 0);
       if (at.row0 < shape.m && at.width > 0)
@@ -322,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   fence_before_sync();
   __syncthreads();
   cluster_sync();
-  if (warp == kEpilogueWarps + 1) tmem_free_pair(tmem, kTmemColumns);
+  if (warp == kMultiply) tmem_free_pair(tmem, kTmemColumns);
 }
 
 // Launch over all SMs, a pair of CTAs per two SMs.
@@ -333,7 +401,7 @@ fadam_status launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmS
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              int(kGemmSmem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  const int64_t pairs = shape.items < sm_count / 2 ? shape.items : sm_count / 2;
+  const int pairs = shape.items < sm_count / 2 ? shape.items : sm_count / 2;
   kernel<<<unsigned(2 * pairs), kGemmThreads, kGemmSmem, stream>>>(a, b, shape, epi);
   const cudaError_t l = cudaGetLastError();
   return l == cudaSuccess ? FADAM_OK : cuda_fail(l, "matrix product launch");

@@ -42,14 +42,16 @@ __host__ __device__ inline int64_t scratch_ld(int64_t n) { return (n + 3) / 4 * 
 template <class Out>
 struct StoreEpilogue {
   StoreArgs s;
-  float* parts;  // fp32 [splits, m, scratch_ld(n)] when k is split: joined by join_kernel
+  float* parts;  // fp32 [slots, split_rows(m), tile_n]: sums of split tiles, joined by join_kernel
+  int tile_n;
 
   __device__ __forceinline__ void operator()(const GemmPiece& at) const {
     const int64_t row = at.row0 + threadIdx.x % 32;
-    const bool sums = parts || s.write_carry;
+    const bool sums = at.slot >= 0 || s.write_carry;
     const bool zero = !sums && row < s.m && s.masked(row);
     const float f = sums ? 1.0f : s.factor();
     if (sizeof(Out) == 2 && !sums && !s.read_carry && !s.accumulate) {
+      Out* out = static_cast<Out*>(s.out) + at.row0 * s.ld + at.col;
 #pragma unroll 1
       for (int c = 0; c < at.width; c += 64) {
         float v[64];
@@ -64,15 +66,15 @@ struct StoreEpilogue {
                 return make_uint4(pack2<Half>(p[0], p[1]), pack2<Half>(p[2], p[3]),
                                   pack2<Half>(p[4], p[5]), pack2<Half>(p[6], p[7]));
               },
-              [&](int64_t r, int64_t col, uint4 u) {
-                *reinterpret_cast<uint4*>(static_cast<Out*>(s.out) + r * s.ld + col) = u;
-              });
+              [&](int r, int col, uint4 u) { *reinterpret_cast<uint4*>(out + r * s.ld + col) = u; });
         else
           store_elements(v, at, c);
       }
       return;
     }
-    const int64_t ld = scratch_ld(s.n);
+    float* part = at.slot < 0 ? nullptr
+                              : parts + at.slot * split_rows(s.m) * tile_n + int64_t(at.tile_row) * tile_n +
+                                    at.tile_col;
 #pragma unroll 1
     for (int c = 0; c < at.width; c += 32) {
       float v[32];
@@ -87,28 +89,31 @@ struct StoreEpilogue {
             return make_uint4(__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
                               __float_as_uint(p[3]));
           },
-          [&](int64_t r, int64_t col, uint4 u) {
-            if (parts) {
-              *reinterpret_cast<uint4*>(parts + (at.split * s.m + r) * ld + col) = u;
-              return;
-            }
-            float4 sum = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                     __uint_as_float(u.w));
-            float4* carry = reinterpret_cast<float4*>(s.carry + r * ld + col);
-            if (s.read_carry) {
-              const float4 o = *carry;
-              sum = make_float4(sum.x + o.x, sum.y + o.y, sum.z + o.z, sum.w + o.w);
-            }
-            if (s.write_carry)
-              *carry = sum;
+          [&](int r, int col, uint4 u) {
+            if (part)
+              *reinterpret_cast<uint4*>(part + r * tile_n + col) = u;
             else
-              put4(r, col, sum, f);
+              finish4(at.row0 + r, at.col + col,
+                      make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                  __uint_as_float(u.w)), f);
           });
     }
   }
 
-  // Four columns: scale, add what is there, round, store.
-  __device__ __forceinline__ void put4(int64_t row, int64_t col, float4 v, float f) const {
+  // Four columns of a whole sum: add what is carried; carry on, or scale, add
+  // what is there, round, store.
+  __device__ __forceinline__ void finish4(int64_t row, int64_t col, float4 v, float f) const {
+    if (s.read_carry || s.write_carry) {
+      float4* carry = reinterpret_cast<float4*>(s.carry + row * scratch_ld(s.n) + col);
+      if (s.read_carry) {
+        const float4 o = *carry;
+        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+      }
+      if (s.write_carry) {
+        *carry = v;
+        return;
+      }
+    }
     const float e[4] = {v.x, v.y, v.z, v.w};
     Out* out = static_cast<Out*>(s.out) + row * s.ld + col;
     const int left = int(min(int64_t(4), s.n - col));
@@ -140,55 +145,67 @@ struct StoreEpilogue {
   using Half = typename std::conditional<sizeof(Out) == 2, Out, __half>::type;
   __device__ __forceinline__ void store_elements(const float (&v)[64], const GemmPiece& at, int c) const {
     const int lane = threadIdx.x % 32;
-    uint32_t* staging = reinterpret_cast<uint32_t*>(at.staging);
-    // pair p of row r at word 32 r + (p ^ r): no two lanes on one bank
+    // unit u of row r at unit 8 r + (u ^ r % 8): 16-byte stores without a bank hit twice
 #pragma unroll
-    for (int p = 0; p < 32; ++p) staging[lane * 32 + (p ^ lane)] = pack2<Half>(v[2 * p], v[2 * p + 1]);
+    for (int u = 0; u < 8; ++u)
+      store_shared(at.staging + (lane * 8 + (u ^ (lane & 7))) * 16,
+                   make_uint4(pack2<Half>(v[8 * u], v[8 * u + 1]), pack2<Half>(v[8 * u + 2], v[8 * u + 3]),
+                              pack2<Half>(v[8 * u + 4], v[8 * u + 5]), pack2<Half>(v[8 * u + 6], v[8 * u + 7])));
     __syncwarp();
     uint16_t* out = reinterpret_cast<uint16_t*>(s.out) + at.row0 * s.ld + at.col + c + lane;
     const int rows = int(min(int64_t(32), s.m - at.row0)), left = at.width - c - lane;
 #pragma unroll 8
     for (int r = 0; r < rows; ++r, out += s.ld) {
-      const uint32_t a = staging[r * 32 + ((lane / 2) ^ r)], b = staging[r * 32 + ((16 + lane / 2) ^ r)];
-      if (left > 0) out[0] = uint16_t(lane % 2 ? a >> 16 : a);
-      if (left > 32) out[32] = uint16_t(lane % 2 ? b >> 16 : b);
+      const uint32_t row = at.staging + r * 128 + lane % 8 * 2;
+      if (left > 0) out[0] = load_shared_u16(row + ((lane / 8) ^ (r & 7)) * 16);
+      if (left > 32) out[32] = load_shared_u16(row + ((4 + lane / 8) ^ (r & 7)) * 16);
     }
     __syncwarp();
   }
 };
 
-// out = round(scale * sum over the parts), in the parts' order.
+// The split tiles' parts added up in their order and finished.
 template <class Out>
-__global__ void __launch_bounds__(256) join_kernel(const float* parts, int splits, StoreEpilogue<Out> e) {
+__global__ void __launch_bounds__(256)
+    join_kernel(const __grid_constant__ StoreEpilogue<Out> e, const __grid_constant__ GemmShape shape) {
   const StoreArgs& s = e.s;
-  const int64_t ld = scratch_ld(s.n), per_row = ld / 4, total = s.m * per_row;
+  const int64_t rows = split_rows(s.m), per_part = rows * e.tile_n;
+  const int per_row = e.tile_n / 4;
+  const int tiles = shape.m_tiles * shape.n_tiles - shape.full;
   const float f = s.factor();
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    const int64_t row = i / per_row;
-    const float4* p = reinterpret_cast<const float4*>(parts) + i;
+  const unsigned per_tile = unsigned(rows) * unsigned(per_row);
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < int64_t(tiles) * per_tile;
+       i += int64_t(gridDim.x) * 256) {
+    const int tile = int(i / per_tile);
+    const unsigned at = unsigned(i - int64_t(tile) * per_tile);
+    const int r = int(at / unsigned(per_row)), c = int(at - unsigned(r) * per_row) * 4;
+    int m0, n0;
+    gemm_tile(shape, unsigned(shape.full + tile), m0, n0);
+    const int64_t row = int64_t(m0) + r, col = int64_t(n0) + c;
+    if (row >= s.m || col >= s.n) continue;
+    const float* p = e.parts + int64_t(tile) * shape.splits * per_part + r * e.tile_n + c;
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int k = 0; k < splits; ++k) {
-      const float4 v = p[k * total];
+    for (int k = 0; k < shape.splits; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(p + k * per_part);
       sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
     }
     if (s.masked(row)) sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    e.put4(row, (i - row * per_row) * 4, sum, f);
+    e.finish4(row, col, sum, f);
   }
 }
 
-// A product with the storing epilogue, k split when `parts` is not NULL.
+// A product with the storing epilogue; `parts` has the plan's split_bytes.
 template <class T, bool A_MN, bool B_MN, class Out>
 fadam_status store_product(const CUtensorMap& a, const CUtensorMap& b, const GemmShape& shape,
                            const StoreArgs& args, float* parts, int sm_count, cudaStream_t stream) {
   using E = typename Out::type;
-  float* where = shape.splits > 1 ? parts : nullptr;
-  const fadam_status st =
-      launch_gemm<T, A_MN, B_MN>(a, b, shape, StoreEpilogue<E>{args, where}, sm_count, stream);
-  if (st || !where) return st;
-  const int64_t blocks = ceil_div(args.m * scratch_ld(args.n) / 4, 256);
-  join_kernel<E><<<unsigned(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(
-      where, shape.splits, StoreEpilogue<E>{args, nullptr});
+  const StoreEpilogue<E> epi{args, parts, shape.tile_n};
+  const fadam_status st = launch_gemm<T, A_MN, B_MN>(a, b, shape, epi, sm_count, stream);
+  const int64_t split = int64_t(shape.m_tiles) * shape.n_tiles - shape.full;
+  if (st || split == 0) return st;
+  const int64_t blocks = ceil_div(split * split_rows(args.m) * (shape.tile_n / 4), 256);
+  join_kernel<E><<<unsigned(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(epi, shape);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "join launch");
 }

@@ -78,8 +78,8 @@ struct LogitEpilogue {
               return make_uint4(pack2<__half>(e[0], e[1]), pack2<__half>(e[2], e[3]),
                                 pack2<__half>(e[4], e[5]), pack2<__half>(e[6], e[7]));
             },
-            [&](int64_t r, int64_t col, uint4 u) {
-              *reinterpret_cast<uint4*>(kept + r * pitch + col) = u;
+            [&](int r, int col, uint4 u) {
+              *reinterpret_cast<uint4*>(kept + (p.row0 + r) * pitch + p.col + col) = u;
             });
     }
     if (row < rows)
@@ -121,6 +121,7 @@ struct RowArgs {
   const void* x;                 // [rows, width]
   void* kept_x;                  // x with ignored rows zero, or NULL
   float dz_scale;
+  int segments;
   Control* control;
 };
 
@@ -138,7 +139,8 @@ struct LogSum {
   }
 };
 
-// One block per row: lse and loss from the row's pieces, dz in place of the
+// One block per row (or `segments` of them, each with a share of the row's
+// exponentials, where there are few rows): lse and loss from the row's pieces, dz in place of the
 // kept exponentials, and the row of x that dW's product reads (a row that is
 // ignored must not reach dW even where x is not finite: 0 * inf is NaN).
 // The last block of a chunk adds up the losses in a fixed order.
@@ -149,17 +151,20 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   __shared__ double sums[kRowThreads / 32];
   __shared__ int64_t counts[kRowThreads / 32];
   __shared__ bool last;
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.x / unsigned(a.segments);
+  const int segment = int(blockIdx.x % unsigned(a.segments));
   const int tid = threadIdx.x;
   const float2* st = a.stats + row * a.pieces;
-  const int vectors = a.dz ? int((a.vocab + 7) / 8) : 0;
+  const int all_vectors = a.dz ? int((a.vocab + 7) / 8) : 0;
+  const int begin = int(int64_t(all_vectors) * segment / a.segments);
+  const int vectors = int(int64_t(all_vectors) * (segment + 1) / a.segments);  // the segment's end
   uint4* dz = reinterpret_cast<uint4*>(static_cast<__half*>(a.dz) + row * a.pitch);
 
   // the first exponentials are on their way while the pieces are joined
   uint4 raw[kRowUnroll];
 #pragma unroll
   for (int u = 0; u < kRowUnroll; ++u)
-    if (tid + u * kRowThreads < vectors) raw[u] = dz[tid + u * kRowThreads];
+    if (begin + tid + u * kRowThreads < vectors) raw[u] = dz[begin + tid + u * kRowThreads];
 
   LogSum total{-INFINITY, 0.0f};
   for (int64_t i = tid; i < a.pieces; i += kRowThreads) {
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   const bool ignored = target == a.ignore_index;
   const bool valid = target >= 0 && target < a.vocab;
   // a target outside the vocabulary shows as NaN in the loss and the gradients
-  if (tid == 0) {
+  if (tid == 0 && segment == 0) {
     a.lse[a.first_row + row] = lse;
     a.row_loss[a.first_row + row] = ignored ? 0.0f : valid ? lse - a.target_z[row] : NAN;
   }
@@ -188,8 +193,8 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   // vector c lies in piece c / per_piece; both advance with c
   const int per_piece = a.piece / 8;
   const int step = kRowThreads / per_piece, step_rest = kRowThreads % per_piece;
-  int piece = tid / per_piece, rest = tid % per_piece;
-  for (int first = tid; first < vectors; first += kRowUnroll * kRowThreads) {
+  int piece = (begin + tid) / per_piece, rest = (begin + tid) % per_piece;
+  for (int first = begin + tid; first < vectors; first += kRowUnroll * kRowThreads) {
     uint4 now[kRowUnroll];
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
       }
     }
   }
-  if (a.kept_x) {
+  if (a.kept_x && segment == 0) {
     const E* from = static_cast<const E*>(a.x) + row * a.x_ld;
     E* to = static_cast<E*>(a.kept_x) + row * a.kept_x_ld;
     const int whole = int(a.width / 8);
@@ -281,8 +286,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const E* from, int64_t 
 
 struct Layout {
   int64_t chunk, chunks, pieces, pitch, width_ld;
-  int logit_tile, dx_tile, dw_tile;  // columns of the products' tiles
-  int splits;                        // of dx's product
+  GemmPlan logits, dx, dw;
   Control* control;
   float2* stats;
   float* target_z;
@@ -295,13 +299,15 @@ struct Layout {
   size_t bytes;
 };
 
-// Rows of one chunk: as many as keep the exponentials within 4 GiB, in whole
-// tiles.  (One chunk of 8192 rows x 131072 entries is 2 GiB; a second chunk
-// costs dW's fp32 sum one more trip through memory.)
+// Rows of one chunk: as many as keep the exponentials within 4 GiB (the loss
+// alone: the pieces' maxima and sums within 1 GiB), in whole tiles.  (One chunk
+// of 8192 rows x 131072 entries is 2 GiB; a second chunk costs dW's fp32 sum
+// one more trip through memory.)
 int64_t chunk_rows(const fadam_xent& d) {
-  if (!d.grad_x && !d.grad_w) return d.rows;
-  if (d.chunk_rows > 0) return d.chunk_rows < d.rows ? d.chunk_rows : d.rows;
-  const int64_t fit = (int64_t(4) << 30) / (round_up(d.vocab, 64) * 2);
+  const bool grads = d.grad_x || d.grad_w;
+  if (grads && d.chunk_rows > 0) return d.chunk_rows < d.rows ? d.chunk_rows : d.rows;
+  const int64_t fit = grads ? (int64_t(4) << 30) / (round_up(d.vocab, 64) * 2)
+                            : (int64_t(1) << 30) / (ceil_div(d.vocab, 32) * int64_t(sizeof(float2)));
   const int64_t whole = fit / kTileM * kTileM;
   const int64_t chunk = whole < kTileM ? kTileM : whole;
   return chunk < d.rows ? chunk : d.rows;
@@ -314,13 +320,12 @@ Layout layout(const fadam_xent& d, char* base, int sm_count) {
   l.chunk = chunk_rows(d);
   l.chunks = ceil_div(d.rows, l.chunk);
   const int pairs = sm_count / 2;
-  l.logit_tile = choose_tile_n(l.chunk, d.vocab, d.width, false, false, pairs);
-  l.dx_tile = choose_tile_n(l.chunk, d.width, d.vocab, true, true, pairs);
-  l.dw_tile = choose_tile_n(d.vocab, d.width, l.chunk, true, false, pairs);
-  l.pieces = ceil_div(d.vocab, l.logit_tile / 2);
+  l.logits = plan_gemm(l.chunk, d.vocab, d.width, false, false, pairs);
+  l.dx = plan_gemm(l.chunk, d.width, d.vocab, true, true, pairs);
+  l.dw = plan_gemm(d.vocab, d.width, l.chunk, true, true, pairs);
+  l.pieces = ceil_div(d.vocab, l.logits.tile_n / 2);
   l.pitch = round_up(d.vocab, 64);
   l.width_ld = round_up(d.width, 8);
-  l.splits = choose_splits(l.chunk, d.width, d.vocab, l.dx_tile, pairs);
   l.control = static_cast<Control*>(c.take(sizeof(Control)));
   l.stats = static_cast<float2*>(c.take(sizeof(float2) * l.chunk * l.pieces));
   l.target_z = static_cast<float*>(c.take(sizeof(float) * l.chunk));
@@ -328,8 +333,9 @@ Layout layout(const fadam_xent& d, char* base, int sm_count) {
   if (d.grad_w) l.kept_x = c.take(2 * l.chunk * l.width_ld);
   if (!bulk_readable(d.x, d.x_stride)) l.x_rows = c.take(2 * d.rows * l.width_ld);
   if (!bulk_readable(d.w, d.w_stride)) l.w_rows = c.take(2 * d.vocab * l.width_ld);
-  if (d.grad_x && l.splits > 1)
-    l.parts = static_cast<float*>(c.take(4 * int64_t(l.splits) * l.chunk * scratch_ld(d.width)));
+  size_t parts = d.grad_x ? split_bytes(l.chunk, l.dx) : 0;
+  if (d.grad_w && split_bytes(d.vocab, l.dw) > parts) parts = split_bytes(d.vocab, l.dw);
+  if (parts) l.parts = static_cast<float*>(c.take(parts));
   if (d.grad_w && l.chunks > 1) l.carry = static_cast<float*>(c.take(4 * d.vocab * scratch_ld(d.width)));
   l.bytes = c.used;
   return l;
@@ -366,7 +372,7 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     w_ld = l.width_ld;
   }
   CUtensorMap w_k, w_mn;
-  if ((st = matrix_map(&w_k, w, d.vocab, d.width, w_ld, box_rows(false, l.logit_tile / 2)))) return st;
+  if ((st = matrix_map(&w_k, w, d.vocab, d.width, w_ld, box_rows(false, l.logits.tile_n / 2)))) return st;
   if ((st = matrix_map(&w_mn, w, d.vocab, d.width, w_ld, box_rows(true, 0)))) return st;
   // fp16 dz is held times 2^15
   const float dz_scale = T::code == FADAM_DT_F16 ? 32768.0f : 1.0f;
@@ -375,17 +381,18 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     const int64_t rows = d.rows - first < l.chunk ? d.rows - first : l.chunk;
     const bool last_chunk = first + rows == d.rows;
     CUtensorMap map;
-    if ((st = matrix_map(&map, x + first * x_ld, rows, d.width, x_ld, box_rows(false, 128)))) return st;
-    LogitEpilogue epi{rows, l.pieces, l.logit_tile / 2, d.targets + first, l.stats, l.target_z,
+    GemmShape shape = gemm_shape(rows, d.vocab, d.width, l.logits, dev.status);
+    if ((st = matrix_map(&map, x + first * x_ld, rows, d.width, x_ld, box_rows(false, shape.a_box))))
+      return st;
+    LogitEpilogue epi{rows, l.pieces, l.logits.tile_n / 2, d.targets + first, l.stats, l.target_z,
                       static_cast<__half*>(l.kept), l.pitch};
-    GemmShape shape = gemm_shape(rows, d.vocab, d.width, l.logit_tile, 1, dev.status);
     if ((st = launch_gemm<T, false, false>(map, w_k, shape, epi, dev.sm_count, stream))) return st;
 
     RowArgs r{};
     r.rows = rows;
     r.vocab = d.vocab;
     r.pieces = l.pieces;
-    r.piece = l.logit_tile / 2;
+    r.piece = l.logits.tile_n / 2;
     r.pitch = l.pitch;
     r.width = d.width;
     r.x_ld = x_ld;
@@ -406,12 +413,16 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     r.kept_x = l.kept_x;
     r.dz_scale = dz_scale;
     r.control = l.control;
-    row_kernel<T><<<unsigned(rows), kRowThreads, 0, stream>>>(r);
+    // two blocks to an SM at least, each with 2048 vectors or more
+    const int64_t most = ceil_div(d.vocab, 8 * 2048), few = ceil_div(2 * dev.sm_count, rows);
+    r.segments = grads ? int(few < most ? few : most) : 1;
+    row_kernel<T><<<unsigned(rows * r.segments), kRowThreads, 0, stream>>>(r);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "row launch");
     if (!grads) continue;
 
     if (d.grad_x) {
-      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(false, 128)))) return st;
+      shape = gemm_shape(rows, d.width, d.vocab, l.dx, dev.status);
+      if ((st = matrix_map(&map, l.kept, rows, d.vocab, l.pitch, box_rows(false, shape.a_box)))) return st;
       StoreArgs s{};
       s.out = static_cast<E*>(d.grad_x) + first * d.grad_x_stride;
       s.ld = d.grad_x_stride;
@@ -422,7 +433,6 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
       s.targets = d.targets + first;
       s.ignore_index = d.ignore_index;
       s.wide = wide_stores(s.out, s.ld, 2);
-      shape = gemm_shape(rows, d.width, d.vocab, l.dx_tile, l.splits, dev.status);
       if ((st = store_product<T, false, true, T>(map, w_mn, shape, s, l.parts, dev.sm_count, stream)))
         return st;
     }
@@ -442,8 +452,8 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
       s.write_carry = !last_chunk;
       s.accumulate = (d.flags & FADAM_XENT_ACCUMULATE) != 0;
       s.wide = wide_stores(s.out, s.ld, sizeof(typename OutW::type));
-      shape = gemm_shape(d.vocab, d.width, rows, l.dw_tile, 1, dev.status);
-      if ((st = store_product<T, true, true, OutW>(map, x_mn, shape, s, nullptr, dev.sm_count, stream)))
+      shape = gemm_shape(d.vocab, d.width, rows, l.dw, dev.status);
+      if ((st = store_product<T, true, true, OutW>(map, x_mn, shape, s, l.parts, dev.sm_count, stream)))
         return st;
     }
   }
