@@ -18,13 +18,15 @@ struct SumJobs {
   SumArgs job[3];
 };
 constexpr int kSumWarps = 32;
-__global__ void __launch_bounds__(kSumWarps * 32) column_sums_kernel(const __grid_constant__ SumJobs jobs) {
+__global__ void __launch_bounds__(kSumWarps * 32) column_sums_kernel(const __grid_constant__ SumJobs jobs, int blocks) {
   __shared__ float shared[kSumWarps][33];
-  const SumArgs& a = jobs.job[blockIdx.y];
+  chain_wait();
+  chain_next();
+  const SumArgs& a = jobs.job[blockIdx.x / unsigned(blocks)];
   if (!a.out) return;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t blocks_per_row = (a.width + 31) / 32;
-  for (int64_t b = blockIdx.x; b < a.outer * blocks_per_row; b += gridDim.x) {
+  for (int64_t b = blockIdx.x % unsigned(blocks); b < a.outer * blocks_per_row; b += blocks) {
     const int64_t o = b / blocks_per_row;
     const int col = int(b - o * blocks_per_row) * 32 + lane;
     float sum = 0.0f;
@@ -282,8 +284,7 @@ extern "C" fadam_status fadam_block_norm_backward(const fadam_block_norm_grad* d
   if (p.gate_parts)
     jobs.job[2] = {p.gate_parts, d.grad_gate, d.gate_rows, p.runs.slices, width, d.param_dtype};
   const int64_t blocks = (p.gate_parts ? d.gate_rows : 1) * ceil_div(d.width, 32);
-  column_sums_kernel<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), 3), kSumWarps * 32, 0,
-                       stream>>>(jobs);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "column sums launch");
+  const int grid = int(blocks < 4096 ? blocks : 4096);
+  return launch_chained("column sums launch", column_sums_kernel, 3 * grid, kSumWarps * 32, 0, stream, jobs,
+                        grid);
 }

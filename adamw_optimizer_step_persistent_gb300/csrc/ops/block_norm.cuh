@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   const Columns c{a.threads, int(threadIdx.x), a.width, MODE == kRing || a.wide};
   const int width = a.width;
   const float inv_width = 1.0f / float(width);
+  chain_wait();
   // (a ring of no stages when rows are loaded directly)
   Ring ring(a.ring, a.runs, bars, dynamic);
   Pair pre[NV][4];
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       if (!a.post) sync_rows(c.threads);  // one buffer's barrier guards the other's reuse
     }
   }
+  chain_next();
   if (MODE == kRing) ring.drain();
 }
 
@@ -316,6 +318,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   // [vector][pair][thread]
   Pair* params = reinterpret_cast<Pair*>(dynamic + (MODE == kRing ? a.ring.stages * a.ring.bytes : 0));
   Pair* sums = params + (kPreAgain ? 1 : 2) * NV * 4 * threads;
+  chain_wait();
   Ring ring(a.ring, a.runs, bars, dynamic);
   constexpr int NS = kSharedSums ? 1 : NV;
   Pair q_reg[NS][4], p_reg[NS][4], pre_again[4];
@@ -498,6 +501,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     for (int i = 0; i < 4; ++i) v[i] = p(j, i);
     store_pairs(a.pre_parts + int64_t(blockIdx.x) * width, c, j, v);
   }
+  chain_next();
   if (MODE == kRing) ring.drain();
 }
 
@@ -510,9 +514,7 @@ fadam_status launch_norm(void (*kernel)(Args), const Args& a, int threads, size_
   if (smem > 40 * 1024)  // beyond 48 KB, static arrays included, it has to be asked for
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  kernel<<<unsigned(a.runs.ctas), threads, smem, stream>>>(a);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "block norm launch");
+  return launch_chained("block norm launch", kernel, a.runs.ctas, threads, smem, stream, a);
 }
 
 // Whether rows go through the ring, and with how many stages: rows of whole

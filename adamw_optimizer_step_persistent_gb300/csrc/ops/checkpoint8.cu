@@ -36,6 +36,8 @@ template <class E, int R>
 __global__ void __launch_bounds__(kThreads)
     pack_kernel(const E* x, int64_t rows, int width, int64_t x_stride, int8_t* codes, float* scales,
                 int chunks) {
+  chain_wait();
+  chain_next();
   const unsigned block = blockIdx.x / unsigned(chunks);
   const int col = int((blockIdx.x - block * chunks) * blockDim.x + threadIdx.x) * 8;
   const int64_t row0 = int64_t(block) * R;
@@ -62,6 +64,8 @@ template <class E, int R>
 __global__ void __launch_bounds__(kThreads)
     restore_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
                    int64_t x_stride, int chunks) {
+  chain_wait();
+  chain_next();
   const unsigned block = blockIdx.x / unsigned(chunks);
   const int col = int((blockIdx.x - block * chunks) * blockDim.x + threadIdx.x) * 8;
   if (col >= width) return;
@@ -92,6 +96,8 @@ __global__ void __launch_bounds__(kThreads)
 template <class E>
 __global__ void __launch_bounds__(kThreads)
     pack_any_kernel(const E* x, int64_t rows, int width, int64_t x_stride, int8_t* codes, float* scales) {
+  chain_wait();
+  chain_next();
   const int groups = (width + kGroup - 1) / kGroup;
   const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
   for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < rows * groups; i += warps) {
@@ -105,6 +111,8 @@ template <class E>
 __global__ void __launch_bounds__(kThreads)
     restore_any_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
                        int64_t x_stride) {
+  chain_wait();
+  chain_next();
   const int groups = (width + kGroup - 1) / kGroup;
   const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
   for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < rows * groups; i += warps) {
@@ -129,18 +137,14 @@ fadam_status pack(const void* x, int64_t rows, int64_t width, int64_t stride,
                   const fadam_checkpoint8& out, cudaStream_t stream) {
   const bool wide = width % 8 == 0 && !misaligned(x, 16) && stride * sizeof(E) % 16 == 0 &&
                     !misaligned(out.codes, 8);
+  const char* what = "checkpoint8 pack launch";
   const E* from = static_cast<const E*>(x);
-  if (wide) {
-    const ChunkGrid g = chunk_grid(rows, width);
-    auto* kernel = g.unroll == 4 ? pack_kernel<E, 4> : pack_kernel<E, 1>;
-    kernel<<<g.ctas, g.threads, 0, stream>>>(from, rows, int(width), stride, out.codes, out.scales,
-                                             g.chunks);
-  } else {
-    pack_any_kernel<E><<<any_grid(rows, width), kThreads, 0, stream>>>(from, rows, int(width), stride,
-                                                                      out.codes, out.scales);
-  }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "checkpoint8 pack launch");
+  if (!wide)
+    return launch_chained(what, pack_any_kernel<E>, any_grid(rows, width), kThreads, 0, stream, from, rows,
+                          int(width), stride, out.codes, out.scales);
+  const ChunkGrid g = chunk_grid(rows, width);
+  return launch_chained(what, g.unroll == 4 ? pack_kernel<E, 4> : pack_kernel<E, 1>, g.ctas, g.threads, 0,
+                        stream, from, rows, int(width), stride, out.codes, out.scales, g.chunks);
 }
 
 template <class E>
@@ -148,18 +152,16 @@ fadam_status restore(const fadam_checkpoint8& in, int64_t rows, int64_t width, v
                      int64_t stride, cudaStream_t stream) {
   const bool wide = width % 8 == 0 && !misaligned(x, 16) && stride * sizeof(E) % 16 == 0 &&
                     !misaligned(in.codes, 8);
+  const char* what = "checkpoint8 restore launch";
   E* to = static_cast<E*>(x);
-  if (wide) {
-    const ChunkGrid g = chunk_grid(rows, width);
-    auto* kernel = g.unroll == 4 ? restore_kernel<E, 4> : restore_kernel<E, 1>;
-    kernel<<<g.ctas, g.threads, 0, stream>>>(in.codes, in.scales, rows, int(width), to, stride,
-                                             g.chunks);
-  } else {
-    restore_any_kernel<E><<<any_grid(rows, width), kThreads, 0, stream>>>(in.codes, in.scales, rows,
-                                                                          int(width), to, stride);
-  }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "checkpoint8 restore launch");
+  const int8_t* codes = in.codes;
+  const float* scales = in.scales;
+  if (!wide)
+    return launch_chained(what, restore_any_kernel<E>, any_grid(rows, width), kThreads, 0, stream, codes,
+                          scales, rows, int(width), to, stride);
+  const ChunkGrid g = chunk_grid(rows, width);
+  return launch_chained(what, g.unroll == 4 ? restore_kernel<E, 4> : restore_kernel<E, 1>, g.ctas,
+                        g.threads, 0, stream, codes, scales, rows, int(width), to, stride, g.chunks);
 }
 
 fadam_status check_matrix(const void* x, int64_t rows, int64_t width, int64_t stride, int32_t dtype,
@@ -209,6 +211,8 @@ Layout layout(const fadam_wgrad& d, char* base, int sm_count) {
 template <class E>
 __global__ void __launch_bounds__(kThreads)
     align_kernel(const E* from, int64_t from_ld, E* to, int64_t to_ld, int64_t rows, int64_t width) {
+  chain_wait();
+  chain_next();
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
     for (int64_t i = threadIdx.x; i < width; i += kThreads) to[row * to_ld + i] = from[row * from_ld + i];
 }
@@ -219,10 +223,10 @@ fadam_status run(const fadam_wgrad& d, const Layout& l, const DeviceFacts& dev, 
   fadam_status st;
   const void* dy = d.dy;
   if (l.dy_rows) {
-    align_kernel<E><<<unsigned(d.rows < 8192 ? d.rows : 8192), kThreads, 0, stream>>>(
-        static_cast<const E*>(d.dy), d.dy_stride, static_cast<E*>(l.dy_rows), l.dy_ld, d.rows, d.n);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "row copy launch");
+    if ((st = launch_chained("row copy launch", align_kernel<E>, d.rows < 8192 ? d.rows : 8192, kThreads, 0,
+                             stream, static_cast<const E*>(d.dy), d.dy_stride,
+                             static_cast<E*>(l.dy_rows), l.dy_ld, d.rows, d.n)))
+      return st;
     dy = l.dy_rows;
   }
   if ((st = restore<E>(d.x, d.rows, d.width, l.x, l.x_ld, stream))) return st;

@@ -95,7 +95,9 @@ inline GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k, bool b_mn, bool may_s
         const double sums = s > 1 ? double(rest) * s * split_rows(m) * t * 8 / 6.7e12 / 0.34e-6 + 12 : 0;
         const double cost = (full / pairs * (steps + 6) +
                              ceil_div(rest * s, pairs) * (ceil_div(steps, s) + 6)) * step + sums;
-        if (least == 0 || cost < least * 0.99) {
+        // (filling the last wave also lowers the clock that the card's power allows:
+        // less than 7% estimated came to nothing)
+        if (least == 0 || cost < least * (s > 1 ? 0.93 : 0.98)) {
           least = cost;
           best = {t, int(s > 1 ? full : tiles), int(s), s > 1 ? rest : 0};
         }
@@ -285,8 +287,9 @@ __device__ __forceinline__ void emit_rows(const float (&v)[8 * kPerUnit], const 
   }
 }
 
-// Epi: operator()(const GemmPiece&) is called by whole warps, loads the piece,
-// and calls release() once.  (Rows beyond m and columns from `width` on hold
+// Epi: begin() is called by one thread of the launch at its start.
+// operator()(const GemmPiece&) is called by whole warps, loads the piece, and
+// calls release() once.  (Rows beyond m and columns from `width` on hold
 // nothing of the product.)
 template <class T, bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
@@ -318,6 +321,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   cluster_sync();
   fence_after_sync();
   const uint32_t tmem = bars->tmem;
+  chain_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) epi.begin();
 
   if (warp == kLoadA) {
     if (lane == 0) load_loop<A_MN>(shape, &map_a, bars, tiles, true, A_MN ? 128 : shape.a_box, rank);
@@ -387,6 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   }
   __syncwarp();
+  chain_next();
   fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -402,9 +408,8 @@ fadam_status launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmS
                                              int(kGemmSmem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   const int pairs = shape.items < sm_count / 2 ? shape.items : sm_count / 2;
-  kernel<<<unsigned(2 * pairs), kGemmThreads, kGemmSmem, stream>>>(a, b, shape, epi);
-  const cudaError_t l = cudaGetLastError();
-  return l == cudaSuccess ? FADAM_OK : cuda_fail(l, "matrix product launch");
+  return launch_chained("matrix product launch", kernel, 2 * pairs, kGemmThreads, kGemmSmem, stream, a,
+                        b, shape, epi);
 }
 
 }  // namespace fadam_ops

@@ -45,6 +45,7 @@ struct StoreEpilogue {
   float* parts;  // fp32 [slots, split_rows(m), tile_n]: sums of split tiles, joined by join_kernel
   int tile_n;
 
+  __device__ __forceinline__ void begin() const {}
   __device__ __forceinline__ void operator()(const GemmPiece& at) const {
     const int64_t row = at.row0 + threadIdx.x % 32;
     const bool sums = at.slot >= 0 || s.write_carry;
@@ -168,6 +169,8 @@ struct StoreEpilogue {
 template <class Out>
 __global__ void __launch_bounds__(256)
     join_kernel(const __grid_constant__ StoreEpilogue<Out> e, const __grid_constant__ GemmShape shape) {
+  chain_wait();
+  chain_next();
   const StoreArgs& s = e.s;
   const int64_t rows = split_rows(s.m), per_part = rows * e.tile_n;
   const int per_row = e.tile_n / 4;
@@ -205,9 +208,8 @@ fadam_status store_product(const CUtensorMap& a, const CUtensorMap& b, const Gem
   const int64_t split = int64_t(shape.m_tiles) * shape.n_tiles - shape.full;
   if (st || split == 0) return st;
   const int64_t blocks = ceil_div(split * split_rows(args.m) * (shape.tile_n / 4), 256);
-  join_kernel<E><<<unsigned(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(epi, shape);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "join launch");
+  return launch_chained("join launch", join_kernel<E>, blocks < 4096 ? blocks : 4096, 256, 0, stream, epi,
+                        shape);
 }
 
 }  // namespace fadam_ops

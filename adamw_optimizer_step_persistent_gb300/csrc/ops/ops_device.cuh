@@ -67,6 +67,15 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// ---- chained launches ------------------------------------------------------------------
+
+// Every thread calls chain_wait() before it touches memory that the launches
+// before this one may read or write: it returns when they have completed.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// This CTA needs no more than it has: once all have said so (or ended), the
+// next launch's CTAs may be placed.
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ---- barriers --------------------------------------------------------------------
 
 // Wall time after which a wait gives up.

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "fadam_ops.h"
 
 namespace fadam_ops {
@@ -40,6 +42,27 @@ fadam_status matrix_map(CUtensorMap* map, const void* base, int64_t rows, int64_
 // What a matrix needs for that: a 16-byte aligned base and row stride.
 inline bool bulk_readable(const void* base, int64_t ld) {
   return !misaligned(base, 16) && ld % 8 == 0;
+}
+
+// Launches a kernel that may begin while the launch before it on the stream
+// still runs: it sets itself up and calls chain_wait() (ops_device.cuh) before
+// it touches memory.  A chain's setup and launch latency then lie under its
+// predecessor's end.
+template <class... Params, class... Args>
+fadam_status launch_chained(const char* what, void (*kernel)(Params...), int64_t grid, int block,
+                            size_t smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(unsigned(grid));
+  config.blockDim = dim3(unsigned(block));
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&config, kernel, std::forward<Args>(args)...);
+  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, what);
 }
 
 // Hands out consecutive 256-byte aligned pieces of a workspace; with a NULL

@@ -26,7 +26,7 @@ namespace fadam_ops {
 namespace {
 
 struct Control {
-  unsigned int finished;  // blocks of the current row launch
+  unsigned int finished;  // blocks of the current row launch (the first product sets it to 0)
   float scale;            // loss_scale / (rows that count, if the mean is taken)
 };
 
@@ -39,7 +39,9 @@ struct LogitEpilogue {
   float* target_z;   // [rows]
   __half* kept;      // [rows, pitch] or NULL
   int64_t pitch;
+  Control* control;
 
+  __device__ __forceinline__ void begin() const { control->finished = 0; }
   __device__ __forceinline__ void operator()(const GemmPiece& p) const {
     const int64_t row = p.row0 + threadIdx.x % 32;
     const int64_t at = row < rows ? targets[row] - p.col : -1;
@@ -151,8 +153,11 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   __shared__ double sums[kRowThreads / 32];
   __shared__ int64_t counts[kRowThreads / 32];
   __shared__ bool last;
-  const int64_t row = blockIdx.x / unsigned(a.segments);
-  const int segment = int(blockIdx.x % unsigned(a.segments));
+  // the last rows first: the product before has left them in L2, and the one
+  // after begins with the first
+  const unsigned block = gridDim.x - 1 - blockIdx.x;
+  const int64_t row = block / unsigned(a.segments);
+  const int segment = int(block % unsigned(a.segments));
   const int tid = threadIdx.x;
   const float2* st = a.stats + row * a.pieces;
   const int all_vectors = a.dz ? int((a.vocab + 7) / 8) : 0;
@@ -160,6 +165,8 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   const int vectors = int(int64_t(all_vectors) * (segment + 1) / a.segments);  // the segment's end
   uint4* dz = reinterpret_cast<uint4*>(static_cast<__half*>(a.dz) + row * a.pitch);
 
+  chain_wait();
+  chain_next();
   // the first exponentials are on their way while the pieces are joined
   uint4 raw[kRowUnroll];
 #pragma unroll
@@ -270,7 +277,6 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
     const double share = a.mean ? 1.0 / double(count > 0 ? count : 1) : 1.0;
     *a.loss = float(loss * share);
     a.control->scale = float(a.loss_scale * share);
-    a.control->finished = 0;
   }
 }
 
@@ -278,6 +284,8 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
 template <class E>
 __global__ void __launch_bounds__(256) align_rows_kernel(const E* from, int64_t from_ld, E* to,
                                                          int64_t to_ld, int64_t rows, int64_t width) {
+  chain_wait();
+  chain_next();
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
     for (int64_t i = threadIdx.x; i < width; i += 256) to[row * to_ld + i] = from[row * from_ld + i];
 }
@@ -345,18 +353,14 @@ template <class T>
 fadam_status align_rows(const void* from, int64_t from_ld, void* to, int64_t to_ld, int64_t rows,
                         int64_t width, cudaStream_t stream) {
   using E = typename T::type;
-  align_rows_kernel<E><<<unsigned(rows < 8192 ? rows : 8192), 256, 0, stream>>>(
-      static_cast<const E*>(from), from_ld, static_cast<E*>(to), to_ld, rows, width);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "row copy launch");
+  return launch_chained("row copy launch", align_rows_kernel<E>, rows < 8192 ? rows : 8192, 256, 0, stream,
+                        static_cast<const E*>(from), from_ld, static_cast<E*>(to), to_ld, rows, width);
 }
 
 template <class T, class OutW>
 fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, cudaStream_t stream) {
   using E = typename T::type;
   const bool grads = d.grad_x || d.grad_w;
-  cudaError_t e = cudaMemsetAsync(l.control, 0, sizeof(Control), stream);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   const E* x = static_cast<const E*>(d.x);
   const E* w = static_cast<const E*>(d.w);
   int64_t x_ld = d.x_stride, w_ld = d.w_stride;
@@ -385,7 +389,7 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     if ((st = matrix_map(&map, x + first * x_ld, rows, d.width, x_ld, box_rows(false, shape.a_box))))
       return st;
     LogitEpilogue epi{rows, l.pieces, l.logits.tile_n / 2, d.targets + first, l.stats, l.target_z,
-                      static_cast<__half*>(l.kept), l.pitch};
+                      static_cast<__half*>(l.kept), l.pitch, l.control};
     if ((st = launch_gemm<T, false, false>(map, w_k, shape, epi, dev.sm_count, stream))) return st;
 
     RowArgs r{};
@@ -413,11 +417,11 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     r.kept_x = l.kept_x;
     r.dz_scale = dz_scale;
     r.control = l.control;
-    // two blocks to an SM at least, each with 2048 vectors or more
-    const int64_t most = ceil_div(d.vocab, 8 * 2048), few = ceil_div(2 * dev.sm_count, rows);
+    // sixteen blocks to an SM at least, each with 1024 vectors or more
+    const int64_t most = ceil_div(d.vocab, 8 * 1024), few = ceil_div(16 * dev.sm_count, rows);
     r.segments = grads ? int(few < most ? few : most) : 1;
-    row_kernel<T><<<unsigned(rows * r.segments), kRowThreads, 0, stream>>>(r);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "row launch");
+    if ((st = launch_chained("row launch", row_kernel<T>, rows * r.segments, kRowThreads, 0, stream, r)))
+      return st;
     if (!grads) continue;
 
     if (d.grad_x) {
