@@ -130,17 +130,6 @@ struct RowArgs {
 constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 4;  // vectors of eight per thread in flight
 
-// log of a sum of exponentials, as the largest term and the sum relative to it.
-struct LogSum {
-  float top, sum;
-  __device__ __forceinline__ void add(LogSum o) {
-    const float t = fmaxf(top, o.top);
-    const float base = t == -INFINITY ? 0.0f : t;
-    sum = sum * expf(top - base) + o.sum * expf(o.top - base);
-    top = t;
-  }
-};
-
 // One block per row (or `segments` of them, each with a share of the row's
 // exponentials, where there are few rows): lse and loss from the row's pieces, dz in place of the
 // kept exponentials, and the row of x that dW's product reads (a row that is
@@ -149,7 +138,7 @@ struct LogSum {
 template <class T>
 __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
   using E = typename T::type;
-  __shared__ LogSum warps[kRowThreads / 32];
+  __shared__ float tops[kRowThreads / 32], terms[kRowThreads / 32];
   __shared__ double sums[kRowThreads / 32];
   __shared__ int64_t counts[kRowThreads / 32];
   __shared__ bool last;
@@ -167,72 +156,88 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
 
   chain_wait();
   chain_next();
+  const int64_t target = a.targets[a.first_row + row];
+  const bool ignored = target == a.ignore_index;
+  const bool valid = target >= 0 && target < a.vocab;
   // the first exponentials are on their way while the pieces are joined
   uint4 raw[kRowUnroll];
 #pragma unroll
   for (int u = 0; u < kRowUnroll; ++u)
     if (begin + tid + u * kRowThreads < vectors) raw[u] = dz[begin + tid + u * kRowThreads];
 
-  LogSum total{-INFINITY, 0.0f};
+  float top = -INFINITY;
+  for (int64_t i = tid; i < a.pieces; i += kRowThreads) top = fmaxf(top, st[i].x);
+#pragma unroll
+  for (int i = 16; i; i /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
+  if (tid % 32 == 0) tops[tid / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRowThreads / 32; ++i) top = fmaxf(top, tops[i]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
   for (int64_t i = tid; i < a.pieces; i += kRowThreads) {
     const float2 p = st[i];
-    total.add({p.x, p.y});
+    sum += p.y * expf(p.x - base);  // (a piece of -inf alone: 0 * 0)
   }
 #pragma unroll
-  for (int i = 16; i; i /= 2)
-    total.add({__shfl_xor_sync(~0u, total.top, i), __shfl_xor_sync(~0u, total.sum, i)});
-  if (tid % 32 == 0) warps[tid / 32] = total;
+  for (int i = 16; i; i /= 2) sum += __shfl_xor_sync(~0u, sum, i);
+  if (tid % 32 == 0) terms[tid / 32] = sum;
   __syncthreads();
-  total = warps[0];
+  sum = 0.0f;
 #pragma unroll
-  for (int i = 1; i < kRowThreads / 32; ++i) total.add(warps[i]);
-  const float lse = (total.top == -INFINITY ? 0.0f : total.top) + logf(total.sum);
+  for (int i = 0; i < kRowThreads / 32; ++i) sum += terms[i];
+  const float lse = base + logf(sum);
 
-  const int64_t target = a.targets[a.first_row + row];
-  const bool ignored = target == a.ignore_index;
-  const bool valid = target >= 0 && target < a.vocab;
   // a target outside the vocabulary shows as NaN in the loss and the gradients
   if (tid == 0 && segment == 0) {
     a.lse[a.first_row + row] = lse;
     a.row_loss[a.first_row + row] = ignored ? 0.0f : valid ? lse - a.target_z[row] : NAN;
   }
 
-  // vector c lies in piece c / per_piece; both advance with c
-  const int per_piece = a.piece / 8;
-  const int step = kRowThreads / per_piece, step_rest = kRowThreads % per_piece;
-  int piece = (begin + tid) / per_piece, rest = (begin + tid) % per_piece;
-  for (int first = begin + tid; first < vectors; first += kRowUnroll * kRowThreads) {
-    uint4 now[kRowUnroll];
+  if (ignored) {
+    for (int c = begin + tid; c < vectors; c += kRowThreads) dz[c] = make_uint4(0, 0, 0, 0);
+  } else {
+    const float scale = valid ? a.dz_scale : NAN;
+    const int target_vector = valid ? int(target / 8) : -1;
+    // vector c lies in piece c / per_piece; both advance with c
+    const int per_piece = a.piece / 8;
+    const int step = kRowThreads / per_piece, step_rest = kRowThreads % per_piece;
+    int piece = (begin + tid) / per_piece, rest = (begin + tid) % per_piece;
+    for (int first = begin + tid; first < vectors; first += kRowUnroll * kRowThreads) {
+      uint4 now[kRowUnroll];
 #pragma unroll
-    for (int u = 0; u < kRowUnroll; ++u) {
-      now[u] = raw[u];
-      const int ahead = first + (kRowUnroll + u) * kRowThreads;
-      if (ahead < vectors) raw[u] = dz[ahead];
-    }
-#pragma unroll
-    for (int u = 0; u < kRowUnroll; ++u) {
-      const int c = first + u * kRowThreads;
-      if (c < vectors) {
-        const float peak = st[piece].x;
-        const float f = !valid && !ignored ? NAN
-                        : peak == -INFINITY ? a.dz_scale : a.dz_scale * expf(peak - lse);
-        const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
-        uint32_t out[4];
-        const int64_t at = target - int64_t(c) * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float2 p = unpack2<__half>(w[i]);
-          p.x = at == 2 * i ? p.x * f - a.dz_scale : p.x * f;
-          p.y = at == 2 * i + 1 ? p.y * f - a.dz_scale : p.y * f;
-          out[i] = ignored ? 0u : pack2<E>(p.x, p.y);
-        }
-        dz[c] = make_uint4(out[0], out[1], out[2], out[3]);
+      for (int u = 0; u < kRowUnroll; ++u) {
+        now[u] = raw[u];
+        const int ahead = first + (kRowUnroll + u) * kRowThreads;
+        if (ahead < vectors) raw[u] = dz[ahead];
       }
-      piece += step;
-      rest += step_rest;
-      if (rest >= per_piece) {
-        rest -= per_piece;
-        ++piece;
+#pragma unroll
+      for (int u = 0; u < kRowUnroll; ++u) {
+        const int c = first + u * kRowThreads;
+        if (c < vectors) {
+          const float f = scale * exp2f((st[piece].x - lse) * 1.4426950408889634f);
+          const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
+          float p[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 e = unpack2<__half>(w[i]);
+            p[2 * i] = e.x * f;
+            p[2 * i + 1] = e.y * f;
+          }
+          if (c == target_vector) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i == int(target % 8)) p[i] -= a.dz_scale;
+          }
+          dz[c] = make_uint4(pack2<E>(p[0], p[1]), pack2<E>(p[2], p[3]), pack2<E>(p[4], p[5]),
+                             pack2<E>(p[6], p[7]));
+        }
+        piece += step;
+        rest += step_rest;
+        if (rest >= per_piece) {
+          rest -= per_piece;
+          ++piece;
+        }
       }
     }
   }
@@ -417,8 +422,8 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     r.kept_x = l.kept_x;
     r.dz_scale = dz_scale;
     r.control = l.control;
-    // sixteen blocks to an SM at least, each with 1024 vectors or more
-    const int64_t most = ceil_div(d.vocab, 8 * 1024), few = ceil_div(16 * dev.sm_count, rows);
+    // eight blocks to an SM at least, each with 1024 vectors or more
+    const int64_t most = ceil_div(d.vocab, 8 * 1024), few = ceil_div(8 * dev.sm_count, rows);
     r.segments = grads ? int(few < most ? few : most) : 1;
     if ((st = launch_chained("row launch", row_kernel<T>, rows * r.segments, kRowThreads, 0, stream, r)))
       return st;
