@@ -6,8 +6,8 @@
 // Three products on the tensor cores (gemm.cuh).  The first never writes a
 // logit: a piece of (most often) 128 of a row's logits is reduced in registers to its
 // maximum and its sum of exponentials, and (for the gradients) its
-// exponentials relative to that maximum are kept in 16 bits.  A second kernel
-// joins a row's pieces to its lse and turns the kept exponentials into dz in
+// exponentials relative to that maximum are kept in 16 bits.  Then a row's
+// pieces are joined to its lse, the kept exponentials are turned into dz in
 // place, and two more products give dx and dW: 6 T V D operations where a
 // second computation of the logits would make it 8.  The kept exponentials
 // are those of a chunk of rows, so the scratch memory is bounded however many
@@ -26,7 +26,7 @@ namespace fadam_ops {
 namespace {
 
 struct Control {
-  unsigned int finished;  // blocks of the current row launch (the first product sets it to 0)
+  unsigned int finished;  // blocks of the current lse launch (the first product sets it to 0)
   float scale;            // loss_scale / (rows that count, if the mean is taken)
 };
 
@@ -119,7 +119,7 @@ struct RowArgs {
   float* loss;
   float* row_loss;
   float* lse;
-  void* dz;                      // [rows, pitch]: exponentials in, dz out; or NULL
+  void* dz;                      // [rows, pitch]: exponentials in, dz out
   const void* x;                 // [rows, width]
   void* kept_x;                  // x with ignored rows zero, or NULL
   float dz_scale;
@@ -128,20 +128,108 @@ struct RowArgs {
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kRowUnroll = 4;  // vectors of eight per thread in flight
+constexpr int kRowUnroll = 2;  // vectors of eight per thread, and as many in flight
 
-// One block per row (or `segments` of them, each with a share of the row's
-// exponentials, where there are few rows): lse and loss from the row's pieces, dz in place of the
-// kept exponentials, and the row of x that dW's product reads (a row that is
-// ignored must not reach dW even where x is not finite: 0 * inf is NaN).
-// The last block of a chunk adds up the losses in a fixed order.
-template <class T>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs a) {
-  using E = typename T::type;
-  __shared__ float tops[kRowThreads / 32], terms[kRowThreads / 32];
+// A warp per row: lse and loss from the row's pieces.  The last block adds up
+// the losses, in a fixed order, and counts the rows that count.
+__global__ void __launch_bounds__(kRowThreads) lse_kernel(const __grid_constant__ RowArgs a) {
   __shared__ double sums[kRowThreads / 32];
   __shared__ int64_t counts[kRowThreads / 32];
   __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid % 32;
+  const int64_t row = int64_t(blockIdx.x) * (kRowThreads / 32) + tid / 32;
+  chain_wait();
+  chain_next();
+  if (row < a.rows) {
+    const float2* st = a.stats + row * a.pieces;
+    // eight pieces to a lane at a time, all on their way at once
+    float top = -INFINITY;
+    for (int64_t i = lane; i < a.pieces; i += 8 * 32) {
+      float t[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) t[u] = i + u * 32 < a.pieces ? st[i + u * 32].x : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) top = fmaxf(top, t[u]);
+    }
+#pragma unroll
+    for (int i = 16; i; i /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int64_t i = lane; i < a.pieces; i += 8 * 32) {
+      float2 p[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        p[u] = i + u * 32 < a.pieces ? st[i + u * 32] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += p[u].y * expf(p[u].x - base);  // (a piece of -inf alone: 0 * 0)
+    }
+#pragma unroll
+    for (int i = 16; i; i /= 2) sum += __shfl_xor_sync(~0u, sum, i);
+    if (lane == 0) {
+      const float lse = base + logf(sum);
+      const int64_t target = a.targets[a.first_row + row];
+      a.lse[a.first_row + row] = lse;
+      // a target outside the vocabulary shows as NaN in the loss and the gradients
+      a.row_loss[a.first_row + row] = target == a.ignore_index                ? 0.0f
+                                      : target >= 0 && target < a.vocab ? lse - a.target_z[row]
+                                                                              : NAN;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(&a.control->finished, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  // the losses of the rows so far (of all of them in the last chunk), and how
+  // many rows of the whole call count
+  __threadfence();
+  double loss = 0.0;
+  int64_t count = 0;
+  for (int64_t i = tid; i < a.all_rows; i += 8 * kRowThreads) {
+    float l[8];
+    int64_t t[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t at = i + u * kRowThreads;
+      l[u] = at < a.first_row + a.rows ? __ldcg(a.row_loss + at) : 0.0f;
+      t[u] = at < a.all_rows ? a.targets[at] : a.ignore_index;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      loss += l[u];
+      count += t[u] != a.ignore_index;
+    }
+  }
+#pragma unroll
+  for (int i = 16; i; i /= 2) {
+    loss += __shfl_xor_sync(~0u, loss, i);
+    count += __shfl_xor_sync(~0u, count, i);
+  }
+  if (lane == 0) {
+    sums[tid / 32] = loss;
+    counts[tid / 32] = count;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 1; i < kRowThreads / 32; ++i) {
+      loss += sums[i];
+      count += counts[i];
+    }
+    const double share = a.mean ? 1.0 / double(count > 0 ? count : 1) : 1.0;
+    *a.loss = float(loss * share);
+    a.control->scale = float(a.loss_scale * share);
+  }
+}
+
+// dz in place of the kept exponentials, and the row of x that dW's product
+// reads (a row that is ignored must not reach dW even where x is not finite:
+// 0 * inf is NaN).  A block per row, or `segments` of them, each with a share
+// of the row.  Bound by memory, 2 bytes in and out for each exponential: 8192
+// rows of 131072 take 718 us (6.0 TB/s) with two vectors of a thread in flight,
+// 765 us with four.
+template <class T>
+__global__ void __launch_bounds__(kRowThreads) dz_kernel(const __grid_constant__ RowArgs a) {
+  using E = typename T::type;
   // the last rows first: the product before has left them in L2, and the one
   // after begins with the first
   const unsigned block = gridDim.x - 1 - blockIdx.x;
@@ -149,7 +237,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   const int segment = int(block % unsigned(a.segments));
   const int tid = threadIdx.x;
   const float2* st = a.stats + row * a.pieces;
-  const int all_vectors = a.dz ? int((a.vocab + 7) / 8) : 0;
+  const int all_vectors = int((a.vocab + 7) / 8);
   const int begin = int(int64_t(all_vectors) * segment / a.segments);
   const int vectors = int(int64_t(all_vectors) * (segment + 1) / a.segments);  // the segment's end
   uint4* dz = reinterpret_cast<uint4*>(static_cast<__half*>(a.dz) + row * a.pitch);
@@ -159,44 +247,14 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
   const int64_t target = a.targets[a.first_row + row];
   const bool ignored = target == a.ignore_index;
   const bool valid = target >= 0 && target < a.vocab;
-  // the first exponentials are on their way while the pieces are joined
-  uint4 raw[kRowUnroll];
-#pragma unroll
-  for (int u = 0; u < kRowUnroll; ++u)
-    if (begin + tid + u * kRowThreads < vectors) raw[u] = dz[begin + tid + u * kRowThreads];
-
-  float top = -INFINITY;
-  for (int64_t i = tid; i < a.pieces; i += kRowThreads) top = fmaxf(top, st[i].x);
-#pragma unroll
-  for (int i = 16; i; i /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, i));
-  if (tid % 32 == 0) tops[tid / 32] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kRowThreads / 32; ++i) top = fmaxf(top, tops[i]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
-  for (int64_t i = tid; i < a.pieces; i += kRowThreads) {
-    const float2 p = st[i];
-    sum += p.y * expf(p.x - base);  // (a piece of -inf alone: 0 * 0)
-  }
-#pragma unroll
-  for (int i = 16; i; i /= 2) sum += __shfl_xor_sync(~0u, sum, i);
-  if (tid % 32 == 0) terms[tid / 32] = sum;
-  __syncthreads();
-  sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kRowThreads / 32; ++i) sum += terms[i];
-  const float lse = base + logf(sum);
-
-  // a target outside the vocabulary shows as NaN in the loss and the gradients
-  if (tid == 0 && segment == 0) {
-    a.lse[a.first_row + row] = lse;
-    a.row_loss[a.first_row + row] = ignored ? 0.0f : valid ? lse - a.target_z[row] : NAN;
-  }
-
   if (ignored) {
     for (int c = begin + tid; c < vectors; c += kRowThreads) dz[c] = make_uint4(0, 0, 0, 0);
   } else {
+    uint4 raw[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u)
+      if (begin + tid + u * kRowThreads < vectors) raw[u] = dz[begin + tid + u * kRowThreads];
+    const float lse = a.lse[a.first_row + row];
     const float scale = valid ? a.dz_scale : NAN;
     const int target_vector = valid ? int(target / 8) : -1;
     // vector c lies in piece c / per_piece; both advance with c
@@ -217,20 +275,18 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
         if (c < vectors) {
           const float f = scale * exp2f((st[piece].x - lse) * 1.4426950408889634f);
           const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
-          float p[8];
+          uint32_t out[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 e = unpack2<__half>(w[i]);
-            p[2 * i] = e.x * f;
-            p[2 * i + 1] = e.y * f;
+            out[i] = pack2<E>(e.x * f, e.y * f);
           }
-          if (c == target_vector) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i == int(target % 8)) p[i] -= a.dz_scale;
+          dz[c] = make_uint4(out[0], out[1], out[2], out[3]);
+          if (c == target_vector) {  // this thread has the target
+            const uint32_t pair = target & 4 ? (target & 2 ? w[3] : w[2]) : (target & 2 ? w[1] : w[0]);
+            const float2 e = unpack2<__half>(pair);
+            reinterpret_cast<E*>(dz)[target] = from_float<E>((target & 1 ? e.y : e.x) * f - a.dz_scale);
           }
-          dz[c] = make_uint4(pack2<E>(p[0], p[1]), pack2<E>(p[2], p[3]), pack2<E>(p[4], p[5]),
-                             pack2<E>(p[6], p[7]));
         }
         piece += step;
         rest += step_rest;
@@ -250,38 +306,6 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
           ignored ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(from)[i];
     if (tid < a.width % 8)
       to[whole * 8 + tid] = ignored ? from_float<E>(0.0f) : from[whole * 8 + tid];
-  }
-
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(&a.control->finished, 1u) == gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
-  // the losses of the rows so far (of all of them in the last chunk), and how
-  // many rows of the whole call count
-  __threadfence();
-  double loss = 0.0;
-  int64_t count = 0;
-  for (int64_t i = tid; i < a.first_row + a.rows; i += kRowThreads) loss += __ldcg(a.row_loss + i);
-  for (int64_t i = tid; i < a.all_rows; i += kRowThreads) count += a.targets[i] != a.ignore_index;
-#pragma unroll
-  for (int i = 16; i; i /= 2) {
-    loss += __shfl_xor_sync(~0u, loss, i);
-    count += __shfl_xor_sync(~0u, count, i);
-  }
-  if (tid % 32 == 0) {
-    sums[tid / 32] = loss;
-    counts[tid / 32] = count;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kRowThreads / 32; ++i) {
-      loss += sums[i];
-      count += counts[i];
-    }
-    const double share = a.mean ? 1.0 / double(count > 0 ? count : 1) : 1.0;
-    *a.loss = float(loss * share);
-    a.control->scale = float(a.loss_scale * share);
   }
 }
 
@@ -422,12 +446,15 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     r.kept_x = l.kept_x;
     r.dz_scale = dz_scale;
     r.control = l.control;
-    // eight blocks to an SM at least, each with 1024 vectors or more
-    const int64_t most = ceil_div(d.vocab, 8 * 1024), few = ceil_div(8 * dev.sm_count, rows);
-    r.segments = grads ? int(few < most ? few : most) : 1;
-    if ((st = launch_chained("row launch", row_kernel<T>, rows * r.segments, kRowThreads, 0, stream, r)))
+    if ((st = launch_chained("lse launch", lse_kernel, ceil_div(rows, kRowThreads / 32), kRowThreads, 0,
+                             stream, r)))
       return st;
     if (!grads) continue;
+    // eight blocks to an SM at least, each with 1024 vectors or more
+    const int64_t most = ceil_div(d.vocab, 8 * 1024), few = ceil_div(8 * dev.sm_count, rows);
+    r.segments = int(few < most ? few : most);
+    if ((st = launch_chained("dz launch", dz_kernel<T>, rows * r.segments, kRowThreads, 0, stream, r)))
+      return st;
 
     if (d.grad_x) {
       shape = gemm_shape(rows, d.width, d.vocab, l.dx, dev.status);
