@@ -69,7 +69,7 @@ Plan plan_backward(const fadam_block_norm_grad& d, char* base, int sm_count) {
   p.pre_parts = static_cast<float*>(c.take(part));
   if (d.post_weight) p.post_parts = static_cast<float*>(c.take(part));
   if (d.gate && p.runs.slices > 1)
-    p.gate_parts = static_cast<float*>(c.take(sizeof(float) * d.gate_rows * p.runs.slices * d.width));
+    p.gate_parts = static_cast<float*>(c.take(sizeof(float) * int64_t(p.runs.runs) * d.width));
   p.bytes = c.used;
   return p;
 }

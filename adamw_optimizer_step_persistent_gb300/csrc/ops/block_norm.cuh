@@ -34,16 +34,18 @@
 namespace fadam_ops {
 namespace {
 
-constexpr int kRing = 0, kDirect = 1;
+// How a row reaches the registers: through the ring, or loaded by each thread,
+// whole vectors or element by element.
+constexpr int kRing = 0, kVectors = 1, kElements = 2;
 
 struct Run {
-  int64_t gate, begin, end;
+  int gate, begin, end;
 };
-__device__ __forceinline__ Run norm_run(const NormRuns& r, int64_t run) {
-  const int64_t gate = run / r.slices, slice = run - gate * r.slices;
-  const int64_t first = gate * r.rows_per_gate;
-  return {gate, first + r.rows_per_gate * slice / r.slices,
-          first + r.rows_per_gate * (slice + 1) / r.slices};
+__device__ __forceinline__ Run norm_run(const NormRuns& r, int run) {
+  const int gate = int(unsigned(run) / unsigned(r.slices)), slice = run - gate * r.slices;
+  const int first = gate * r.rows_per_gate;
+  return {gate, first + int(int64_t(r.rows_per_gate) * slice / r.slices),
+          first + int(int64_t(r.rows_per_gate) * (slice + 1) / r.slices)};
 }
 
 // The ring.  Thread 0 feeds it: the CTA's rows in order, `stages` of them
@@ -53,7 +55,7 @@ struct Ring {
   const NormRuns& runs;
   uint64_t* full;          // [stages] barriers
   uint32_t stages;         // shared address of the stages
-  int64_t run, row, end;   // thread 0: the next row to copy
+  int run, row, end;       // thread 0: the next row to copy
   int next, stage;         // stage it goes to; stage that is worked on
   unsigned parity;         // of the latter's barrier
   bool ok;                 // no wait has given up (the warps stay together either way)
@@ -76,7 +78,7 @@ struct Ring {
   __device__ __forceinline__ void feed() {
     if (row == end) {
       run += gridDim.x;
-      if (run >= runs.gates * runs.slices) {
+      if (run >= runs.runs) {
         run -= gridDim.x;
         return;
       }
@@ -91,7 +93,7 @@ struct Ring {
     for (int i = 0; i < 4; ++i)
       if (i < args.sources) {
         const RingSource& s = args.source[i];
-        load_bytes(to, static_cast<const char*>(s.base) + row * s.stride, s.bytes, bar);
+        load_bytes(to, static_cast<const char*>(s.base) + int64_t(row) * s.stride, s.bytes, bar);
         to += s.bytes;
       }
     ++row;
@@ -170,13 +172,13 @@ __device__ __forceinline__ void block_sums(float (&v)[4], float* shared, int thr
 // A row's vectors kept in 8 bits: from registers where they lie next to each
 // other, else (h_out: after the CTA has written it) from memory, a warp to a
 // group.
-template <class E, int NV>
+template <class E, int NV, bool kWide>
 __device__ __forceinline__ void keep_row(const Raw<E> (&r)[NV], const E* row, int64_t index,
-                                         int8_t* codes, float* scales, const Columns& c) {
+                                         int8_t* codes, float* scales, const Columns<NV, kWide>& c) {
   const int groups = (c.width + kGroup - 1) / kGroup;
   codes += index * c.width;
   scales += index * groups;
-  if (c.wide) {
+  if constexpr (kWide) {
     int8_t* to[NV];
     float* scale[NV];
     bool valid[NV];
@@ -199,7 +201,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   __shared__ float shared[2][4 * kMaxWarps];
   __shared__ __align__(8) uint64_t bars[kMaxNormStages];
   extern __shared__ __align__(128) unsigned char dynamic[];
-  const Columns c{a.threads, int(threadIdx.x), a.width, MODE == kRing || a.wide};
+  constexpr bool kWide = MODE != kElements;
+  const Columns<NV, kWide> c(a.threads, int(threadIdx.x), a.width);
   const int width = a.width;
   const float inv_width = 1.0f / float(width);
   chain_wait();
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
   for (int j = 0; j < NV; ++j) load_param<F>(a.pre, 0, a.params_f32, c, j, pre[j]);
 
-  for (int64_t u = blockIdx.x; u < a.runs.gates * a.runs.slices; u += gridDim.x) {
+  for (int u = blockIdx.x; u < a.runs.runs; u += gridDim.x) {
     const Run run = norm_run(a.runs, u);
     Pair scale[NV][4];  // alpha gate post_weight
 #pragma unroll
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       for (int i = 0; i < 4; ++i) scale[j][i] = both(a.alpha);
       Pair v[4];
       if (a.gate) {
-        load_param<F>(a.gate, run.gate * width, a.params_f32, c, j, v);
+        load_param<F>(a.gate, int64_t(run.gate) * width, a.params_f32, c, j, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) scale[j][i] = mul2(scale[j][i], v[i]);
       }
@@ -228,7 +231,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         for (int i = 0; i < 4; ++i) scale[j][i] = mul2(scale[j][i], v[i]);
       }
     }
-    for (int64_t row = run.begin; row < run.end; ++row) {
+    for (int at_row = run.begin; at_row < run.end; ++at_row) {
+      const int64_t row = at_row;
       Raw<F> f_raw[NV];
       Pair h[NV][4];
       if (MODE == kRing) {
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         }
       }
       if (a.f_codes)
-        keep_row<F, NV>(f_raw, static_cast<const F*>(a.f) + row * a.f_stride, row, a.f_codes,
+        keep_row<F, NV, kWide>(f_raw, static_cast<const F*>(a.f) + row * a.f_stride, row, a.f_codes,
                         a.f_scales, c);
       const float r2 = rsqrtf(block_sum(sum2(s), shared[1], c.threads) * inv_width + a.eps);
       if (c.tid == 0) a.r2[row] = r2;
@@ -286,11 +290,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         store_pairs(static_cast<F*>(a.x_out) + row * width, c, j, x);
       }
       if (a.h_codes) {
-        if (!c.wide) {  // the row is read back
+        if (!kWide) {  // the row is read back
           __threadfence_block();
           sync_rows(c.threads);
         }
-        keep_row<H, NV>(out, static_cast<const H*>(a.h_out) + row * width, row, a.h_codes,
+        keep_row<H, NV, kWide>(out, static_cast<const H*>(a.h_out) + row * width, row, a.h_codes,
                         a.h_scales, c);
       }
       if (!a.post) sync_rows(c.threads);  // one buffer's barrier guards the other's reuse
@@ -312,10 +316,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   __shared__ float shared[2][4 * kMaxWarps];
   __shared__ __align__(8) uint64_t bars[kMaxNormStages];
   extern __shared__ __align__(128) unsigned char dynamic[];
-  const Columns c{a.threads, int(threadIdx.x), a.width, MODE == kRing || a.wide};
+  constexpr bool kWide = MODE != kElements;
+  const Columns<NV, kWide> c(a.threads, int(threadIdx.x), a.width);
   const int width = a.width, groups = (width + kGroup - 1) / kGroup, threads = a.threads, tid = c.tid;
   const float inv_width = 1.0f / float(width);
-  // [vector][pair][thread]
+  // [vector][pair / 2][thread][2]
   Pair* params = reinterpret_cast<Pair*>(dynamic + (MODE == kRing ? a.ring.stages * a.ring.bytes : 0));
   Pair* sums = params + (kPreAgain ? 1 : 2) * NV * 4 * threads;
   chain_wait();
@@ -324,15 +329,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   Pair q_reg[NS][4], p_reg[NS][4], pre_again[4];
   // column sums: Q of the current run, and P
   auto q = [&](int j, int i) -> Pair& {
-    if constexpr (kSharedSums) return sums[(j * 4 + i) * threads + tid]; else return q_reg[j][i];
+    if constexpr (kSharedSums) return sums[((j * 2 + i / 2) * threads + tid) * 2 + i % 2]; else return q_reg[j][i];
   };
   auto p = [&](int j, int i) -> Pair& {
-    if constexpr (kSharedSums) return sums[((NV + j) * 4 + i) * threads + tid]; else return p_reg[j][i];
+    if constexpr (kSharedSums) return sums[(((NV + j) * 2 + i / 2) * threads + tid) * 2 + i % 2]; else return p_reg[j][i];
   };
   // parameters: a = alpha gate post_weight of the current gate, and pre_weight
-  auto scale = [&](int j, int i) -> Pair& { return params[(j * 4 + i) * threads + tid]; };
+  auto scale = [&](int j, int i) -> Pair& { return params[((j * 2 + i / 2) * threads + tid) * 2 + i % 2]; };
   auto pre = [&](int j, int i) -> Pair& {
-    if constexpr (kPreAgain) return pre_again[i]; else return params[((NV + j) * 4 + i) * threads + tid];
+    if constexpr (kPreAgain) return pre_again[i]; else return params[(((NV + j) * 2 + i / 2) * threads + tid) * 2 + i % 2];
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
   }
 
   int turn = 0;
-  for (int64_t u = blockIdx.x; u < a.runs.gates * a.runs.slices; u += gridDim.x) {
+  for (int u = blockIdx.x; u < a.runs.runs; u += gridDim.x) {
     const Run run = norm_run(a.runs, u);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] = both(a.alpha);
       if (a.gate) {
-        load_param<F>(a.gate, run.gate * width, a.params_f32, c, j, v);
+        load_param<F>(a.gate, int64_t(run.gate) * width, a.params_f32, c, j, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], v[i]);
       }
@@ -378,13 +383,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int group = min(c.first(j), width - 1) / kGroup;
-        f_scale[j] = c.wide && a.f_codes ? __ldg(a.f_scales + row * groups + group) : 0.0f;
-        h_scale[j] = c.wide && a.h_codes ? __ldg(a.h_scales + row * groups + group) : 0.0f;
+        f_scale[j] = kWide && a.f_codes ? __ldg(a.f_scales + row * groups + group) : 0.0f;
+        h_scale[j] = kWide && a.h_codes ? __ldg(a.h_scales + row * groups + group) : 0.0f;
       }
     };
     fetch(run.begin);
 
-    for (int64_t row = run.begin; row < run.end; ++row, turn ^= 1) {
+    for (int at_row = run.begin; at_row < run.end; ++at_row, turn ^= 1) {
+      const int64_t row = at_row;
       const float r1 = r1_next, r2 = r2_next;
       Pair fh[NV][4], hh[NV][4], eg[NV][4];
       Pair s1 = both(0.0f), s2 = s1, s3 = s1;
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
           s3 = fma2(af, hh[j][i], s3);
         }
       }
-      if (row + 1 < run.end) fetch(row + 1);
+      if (at_row + 1 < run.end) fetch(at_row + 1);
       float s[4] = {sum2(s1), sum2(s2), sum2(s3), 0.0f};
       block_sums(s, shared[turn], threads);
       if (MODE == kRing) ring.release();
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = g[i] = both(1.0f);
       if (a.post) load_param<F>(a.post, 0, a.params_f32, c, j, v);
-      if (a.gate) load_param<F>(a.gate, run.gate * width, a.params_f32, c, j, g);
+      if (a.gate) load_param<F>(a.gate, int64_t(run.gate) * width, a.params_f32, c, j, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const Pair sum = mul2(both(a.alpha), q(j, i));
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       }
       if (a.post_parts) {  // summed over this CTA's runs
         float* part = a.post_parts + int64_t(blockIdx.x) * width;
-        if (u != blockIdx.x) {
+        if (u != int(blockIdx.x)) {
           Pair old[4];
           load_pairs(part, c, j, old);
 #pragma unroll
@@ -485,12 +491,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         store_pairs(part, c, j, g);
       }
       if (a.gate_parts) {
-        store_pairs(a.gate_parts + u * width, c, j, v);
+        store_pairs(a.gate_parts + int64_t(u) * width, c, j, v);
       } else if (a.gate_out) {
         if (a.params_f32)
-          store_pairs(static_cast<float*>(a.gate_out) + run.gate * width, c, j, v);
+          store_pairs(static_cast<float*>(a.gate_out) + int64_t(run.gate) * width, c, j, v);
         else
-          store_pairs(static_cast<F*>(a.gate_out) + run.gate * width, c, j, v);
+          store_pairs(static_cast<F*>(a.gate_out) + int64_t(run.gate) * width, c, j, v);
       }
     }
   }
@@ -528,16 +534,18 @@ inline bool plan_ring(RingArgs& ring, const NormRuns& runs, bool wide, int threa
     wide = wide && !misaligned(s.base, 16) && s.stride % 16 == 0 && s.bytes % 16 == 0;
   }
   const size_t share = kNormSharedBytes / norm_ctas_per_sm(threads);
-  if (!wide || runs.gates * runs.rows_per_gate <= runs.ctas || share < other_bytes) return false;
+  if (!wide || int64_t(runs.gates) * runs.rows_per_gate <= runs.ctas || share < other_bytes) return false;
   const size_t fit = (share - other_bytes) / ring.bytes;
   ring.stages = int(fit < kMaxNormStages ? fit : kMaxNormStages);
   return ring.stages >= 2;
 }
 
-template <class Args>
-Args without_ring(Args a) {
-  a.ring.stages = 0;
-  return a;
+template <class F, class H, int NV>
+fadam_status forward(const NormArgs& a, int mode, size_t smem, cudaStream_t stream) {
+  return launch_norm<const NormArgs>(mode == kRing      ? norm_forward_kernel<F, H, NV, kRing>
+                                     : mode == kVectors ? norm_forward_kernel<F, H, NV, kVectors>
+                                                        : norm_forward_kernel<F, H, NV, kElements>,
+                                     a, a.threads, smem, stream);
 }
 
 template <class F, class H>
@@ -547,13 +555,13 @@ fadam_status norm_forward(NormArgs a, cudaStream_t stream) {
   a.ring.sources = 2;
   a.ring.source[0] = {a.f, a.f_stride * int64_t(sizeof(F)), a.width * int(sizeof(F))};
   a.ring.source[1] = {a.h, a.h_stride * int64_t(sizeof(H)), a.width * int(sizeof(H))};
-  if (plan_ring(a.ring, a.runs, a.wide, r.threads, 0))
-    return launch_norm<const NormArgs>(r.nv == 2 ? norm_forward_kernel<F, H, 2, kRing>
-                                                 : norm_forward_kernel<F, H, 4, kRing>,
-                                       a, r.threads, size_t(a.ring.stages) * a.ring.bytes, stream);
-  return launch_norm<const NormArgs>(r.nv == 2 ? norm_forward_kernel<F, H, 2, kDirect>
-                                               : norm_forward_kernel<F, H, 4, kDirect>,
-                                     without_ring(a), r.threads, 0, stream);
+  int mode = kRing;
+  if (!plan_ring(a.ring, a.runs, a.wide, r.threads, 0)) {
+    a.ring.stages = 0;
+    mode = a.wide ? kVectors : kElements;
+  }
+  const size_t smem = size_t(a.ring.stages) * a.ring.bytes;
+  return r.nv == 2 ? forward<F, H, 2>(a, mode, smem, stream) : forward<F, H, 4>(a, mode, smem, stream);
 }
 
 template <class F, class H>
@@ -569,12 +577,20 @@ fadam_status norm_backward(NormGradArgs a, cudaStream_t stream) {
                                : RingSource{a.h, a.h_stride * h, a.width * h};
   a.ring.source[3] = {a.gh, a.gh_stride * h, a.width * h};
   const size_t array = size_t(r.nv) * 8 * r.threads * sizeof(float);
-  if (r.nv == 2 && plan_ring(a.ring, a.runs, a.wide, r.threads, 2 * array))
-    return launch_norm<const NormGradArgs>(norm_backward_kernel<F, H, 2, kRing>, a, r.threads,
-                                           size_t(a.ring.stages) * a.ring.bytes + 2 * array, stream);
-  return launch_norm<const NormGradArgs>(r.nv == 2 ? norm_backward_kernel<F, H, 2, kDirect>
-                                                   : norm_backward_kernel<F, H, 4, kDirect>,
-                                         without_ring(a), r.threads, (r.nv == 2 ? 2 : 3) * array, stream);
+  int mode = kRing;
+  if (r.nv > 2 || !plan_ring(a.ring, a.runs, a.wide, r.threads, 2 * array)) {
+    a.ring.stages = 0;
+    mode = a.wide ? kVectors : kElements;
+  }
+  const size_t smem = size_t(a.ring.stages) * a.ring.bytes + (r.nv == 2 ? 2 : 3) * array;
+  if (r.nv > 2)
+    return launch_norm<const NormGradArgs>(mode == kVectors ? norm_backward_kernel<F, H, 4, kVectors>
+                                                            : norm_backward_kernel<F, H, 4, kElements>,
+                                           a, r.threads, smem, stream);
+  return launch_norm<const NormGradArgs>(mode == kRing      ? norm_backward_kernel<F, H, 2, kRing>
+                                         : mode == kVectors ? norm_backward_kernel<F, H, 2, kVectors>
+                                                            : norm_backward_kernel<F, H, 2, kElements>,
+                                         a, r.threads, smem, stream);
 }
 
 }  // namespace

@@ -26,8 +26,8 @@ struct RingArgs {
 // Rows are taken in runs that share one row of the gate: run u holds slice
 // u % slices of the rows of gate u / slices.
 struct NormRuns {
-  int64_t gates, rows_per_gate;
-  int slices, ctas;
+  int gates, rows_per_gate;
+  int slices, ctas, runs;
 };
 
 struct NormArgs {
@@ -86,13 +86,11 @@ inline int norm_ctas_per_sm(int threads) {
 inline NormRuns norm_runs(int64_t rows, int64_t gates, int64_t width, int sm_count) {
   int64_t most = int64_t(sm_count) * norm_ctas_per_sm(row_shape(width).threads);
   if (most > rows / 4) most = rows / 4 > sm_count ? rows / 4 : sm_count;
-  NormRuns r{gates, rows / gates, 1, 1};
   int64_t slices = most / gates;
-  if (slices > r.rows_per_gate) slices = r.rows_per_gate;
-  r.slices = slices < 1 ? 1 : int(slices);
-  const int64_t runs = gates * r.slices;
-  r.ctas = int(runs < most ? runs : most);
-  return r;
+  if (slices > rows / gates) slices = rows / gates;
+  if (slices < 1) slices = 1;
+  const int64_t runs = gates * slices;
+  return {int(gates), int(rows / gates), int(slices), int(runs < most ? runs : most), int(runs)};
 }
 
 // The kernels' launches, by block dtype and whether the residual stream is fp32.

@@ -100,14 +100,21 @@ __device__ __forceinline__ Raw<E> narrow(const Pair (&v)[4]) {
   return r;
 }
 
-// Where a thread's eight elements of vector j lie in a row: next to each other
-// when the row consists of whole aligned vectors (`wide`), else each one next
-// to the other threads' (so that element-wise accesses coalesce).
+// Where a thread's NV vectors of eight elements lie in a row.  kWide, rows of
+// whole aligned vectors: a vector's elements next to each other, consecutive
+// threads' vectors too.  Else a warp has NV * 256 consecutive elements and its
+// lanes take them in turn, so that element-wise accesses coalesce and differ
+// by constants.
+template <int NV, bool kWide>
 struct Columns {
   int threads, tid, width;
-  bool wide;
+  int lone0, left;  // the first element of a row that is not wide, and how far it is from the end
+  __device__ __forceinline__ Columns(int threads, int tid, int width)
+      : threads(threads), tid(tid), width(width), lone0(tid / 32 * NV * 256 + tid % 32),
+        left(width - lone0) {}
   __device__ __forceinline__ int first(int j) const { return (j * threads + tid) * 8; }
-  __device__ __forceinline__ int lone(int j, int i) const { return (j * 8 + i) * threads + tid; }
+  __device__ __forceinline__ int lone(int j, int i) const { return lone0 + (j * 8 + i) * 32; }
+  __device__ __forceinline__ bool valid(int j, int i) const { return (j * 8 + i) * 32 < left; }
 };
 
 template <class E>
@@ -119,51 +126,53 @@ __device__ __forceinline__ Raw<E> zero_raw() {
 }
 
 // Vector j of a row, zeros beyond its end.
-template <class E>
-__device__ __forceinline__ Raw<E> load_vector(const E* row, const Columns& c, int j) {
+template <class E, int NV, bool kWide>
+__device__ __forceinline__ Raw<E> load_vector(const E* row, const Columns<NV, kWide>& c, int j) {
   Raw<E> r = zero_raw<E>();
-  if (c.wide) {
+  if constexpr (kWide) {
     if (c.first(j) < c.width) r = load_raw(row + c.first(j));
   } else {
+    const E* at = row + c.lone0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c.lone(j, i) < c.width) {
+      if (c.valid(j, i)) {
         if constexpr (sizeof(E) == 4)
-          r.w[i] = __float_as_uint(row[c.lone(j, i)]);
+          r.w[i] = __float_as_uint(at[(j * 8 + i) * 32]);
         else
-          r.w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[c.lone(j, i)]) << (i % 2 * 16);
+          r.w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(at)[(j * 8 + i) * 32]) << (i % 2 * 16);
       }
   }
   return r;
 }
-template <class E>
-__device__ __forceinline__ void store_vector(E* row, const Columns& c, int j, const Raw<E>& r) {
-  if (c.wide) {
+template <class E, int NV, bool kWide>
+__device__ __forceinline__ void store_vector(E* row, const Columns<NV, kWide>& c, int j, const Raw<E>& r) {
+  if constexpr (kWide) {
     if (c.first(j) < c.width) store_raw(row + c.first(j), r);
   } else {
+    E* at = row + c.lone0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c.lone(j, i) < c.width) {
+      if (c.valid(j, i)) {
         if constexpr (sizeof(E) == 4)
-          row[c.lone(j, i)] = __uint_as_float(r.w[i]);
+          at[(j * 8 + i) * 32] = __uint_as_float(r.w[i]);
         else
-          reinterpret_cast<uint16_t*>(row)[c.lone(j, i)] = uint16_t(r.w[i / 2] >> (i % 2 * 16));
+          reinterpret_cast<uint16_t*>(at)[(j * 8 + i) * 32] = uint16_t(r.w[i / 2] >> (i % 2 * 16));
       }
   }
 }
-template <class E>
-__device__ __forceinline__ void load_pairs(const E* row, const Columns& c, int j, Pair (&v)[4]) {
+template <class E, class C>
+__device__ __forceinline__ void load_pairs(const E* row, const C& c, int j, Pair (&v)[4]) {
   widen<E>(load_vector(row, c, j), v);
 }
-template <class E>
-__device__ __forceinline__ void store_pairs(E* row, const Columns& c, int j, const Pair (&v)[4]) {
+template <class E, class C>
+__device__ __forceinline__ void store_pairs(E* row, const C& c, int j, const Pair (&v)[4]) {
   store_vector(row, c, j, narrow<E>(v));
 }
 
 // Parameters may be fp32 under 16-bit activations.
-template <class E>
-__device__ __forceinline__ void load_param(const void* p, int64_t offset, bool f32, const Columns& c,
-                                           int j, Pair (&v)[4]) {
+template <class E, class C>
+__device__ __forceinline__ void load_param(const void* p, int64_t offset, bool f32, const C& c, int j,
+                                           Pair (&v)[4]) {
   if (f32)
     load_pairs(static_cast<const float*>(p) + offset, c, j, v);
   else
@@ -305,19 +314,20 @@ __device__ __forceinline__ void codes_pairs(uint2 raw, float factor, Pair (&v)[4
 
 // Vector j of a kept row times `factor`; `scale` is that of the vector's group
 // when the row is wide.
+template <int NV, bool kWide>
 __device__ __forceinline__ void load_kept(const int8_t* codes, const float* scales, float scale,
-                                          float factor, const Columns& c, int j, Pair (&v)[4]) {
-  if (c.wide) {
+                                          float factor, const Columns<NV, kWide>& c, int j, Pair (&v)[4]) {
+  if constexpr (kWide) {
     uint2 raw = make_uint2(0, 0);
     if (c.first(j) < c.width) raw = *reinterpret_cast<const uint2*>(codes + c.first(j));
     codes_pairs(raw, scale * factor, v);
   } else {
     float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int col = c.lone(j, i);
-      e[i] = col < c.width ? float(codes[col]) * (scales[col / kGroup] * factor) : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i)
+      e[i] = c.valid(j, i) ? float(codes[c.lone0 + (j * 8 + i) * 32]) *
+                                 (scales[c.lone(j, i) / kGroup] * factor)
+                           : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = make_pair(e[2 * i], e[2 * i + 1]);
   }
