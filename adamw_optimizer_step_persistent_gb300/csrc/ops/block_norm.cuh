@@ -48,14 +48,16 @@ __device__ __forceinline__ Run norm_run(const NormRuns& r, int run) {
           first + int(int64_t(r.rows_per_gate) * (slice + 1) / r.slices)};
 }
 
-// The ring.  Thread 0 feeds it: the CTA's rows in order, `stages` of them
-// ahead of the one that is worked on.
+// The ring.  The first lanes of the CTA's first warps feed it, each its share
+// of the row's tensors (one thread for all of them would hold up its warp, and
+// with it every row's barrier): the CTA's rows in order, `stages` of them ahead
+// of the one that is worked on.
 struct Ring {
   const RingArgs& args;
   const NormRuns& runs;
   uint64_t* full;          // [stages] barriers
   uint32_t stages;         // shared address of the stages
-  int run, row, end;       // thread 0: the next row to copy
+  int run, row, end;       // feeding threads: the next row to copy
   int next, stage;         // stage it goes to; stage that is worked on
   unsigned parity;         // of the latter's barrier
   bool ok;                 // no wait has given up (the warps stay together either way)
@@ -66,36 +68,35 @@ struct Ring {
     if (threadIdx.x == 0) {
       for (int i = 0; i < args.stages; ++i) bar_init(shared_addr(full + i), 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      const Run first = norm_run(runs, run);
-      row = first.begin;
-      end = first.end;
     }
     __syncthreads();
-    if (threadIdx.x == 0)
+    const Run first = norm_run(runs, run);
+    row = first.begin;
+    end = first.end;
+    if (feeds())
       for (int i = 0; i < args.stages; ++i) feed();
+  }
+
+  __device__ __forceinline__ bool feeds() const {
+    return threadIdx.x % 32 == 0 && int(threadIdx.x) / 32 < args.sources;
   }
 
   __device__ __forceinline__ void feed() {
     if (row == end) {
+      if (run + int(gridDim.x) >= runs.runs) return;
       run += gridDim.x;
-      if (run >= runs.runs) {
-        run -= gridDim.x;
-        return;
-      }
       const Run r = norm_run(runs, run);
       row = r.begin;
       end = r.end;
     }
     const uint32_t bar = shared_addr(full + next);
-    uint32_t to = stages + next * args.bytes;
-    bar_expect(bar, args.bytes);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < args.sources) {
-        const RingSource& s = args.source[i];
-        load_bytes(to, static_cast<const char*>(s.base) + int64_t(row) * s.stride, s.bytes, bar);
-        to += s.bytes;
-      }
+    const uint32_t to = stages + next * args.bytes;
+    // (a copy may land before what is expected is known: the phase waits for the arrival)
+    if (threadIdx.x == 0) bar_expect(bar, args.bytes);
+    for (int i = threadIdx.x / 32; i < args.sources; i += blockDim.x / 32) {
+      const RingSource& s = args.source[i];
+      load_bytes(to + s.offset, static_cast<const char*>(s.base) + row * s.stride, s.bytes, bar);
+    }
     ++row;
     next = next + 1 == args.stages ? 0 : next + 1;
   }
@@ -107,7 +108,7 @@ struct Ring {
   }
   // Every thread has read the row (the caller has passed a barrier since).
   __device__ __forceinline__ void release() {
-    if (threadIdx.x == 0 && ok) feed();
+    if (feeds() && ok) feed();
     if (++stage == args.stages) {
       stage = 0;
       parity ^= 1;
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           f_raw[j] = load_vector(reinterpret_cast<const F*>(at), c, j);
-          load_pairs(reinterpret_cast<const H*>(at + a.ring.source[0].bytes), c, j, h[j]);
+          load_pairs(reinterpret_cast<const H*>(at + a.ring.source[1].offset), c, j, h[j]);
         }
       } else {
 #pragma unroll
@@ -395,8 +396,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
       Pair fh[NV][4], hh[NV][4], eg[NV][4];
       Pair s1 = both(0.0f), s2 = s1, s3 = s1;
       const unsigned char* at = dynamic + (MODE == kRing ? ring.wait() : 0);
-      const int to_f = a.ring.source[0].bytes, to_h = to_f + a.ring.source[1].bytes,
-                to_gh = to_h + a.ring.source[2].bytes;
+      const int to_f = a.ring.source[1].offset, to_h = a.ring.source[2].offset,
+                to_gh = a.ring.source[3].offset;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         Pair gx[4];
@@ -529,7 +530,8 @@ inline bool plan_ring(RingArgs& ring, const NormRuns& runs, bool wide, int threa
                       size_t other_bytes) {
   ring.bytes = 0;
   for (int i = 0; i < ring.sources; ++i) {
-    const RingSource& s = ring.source[i];
+    RingSource& s = ring.source[i];
+    s.offset = ring.bytes;
     ring.bytes += s.bytes;
     wide = wide && !misaligned(s.base, 16) && s.stride % 16 == 0 && s.bytes % 16 == 0;
   }

@@ -16,6 +16,7 @@ struct RingSource {
   const void* base;
   int64_t stride;  // bytes from one row to the next
   int bytes;       // of one row
+  int offset;      // in the stage
 };
 struct RingArgs {
   RingSource source[4];
