@@ -59,6 +59,7 @@ struct GemmShape {
   int32_t k_steps, steps_per_split;
   int32_t items;
   int32_t a_box, b_box;  // rows of a k-major operand's box
+  int32_t chunk;         // steps of k that a chunked product sums on the tensor cores
   int* status;
 };
 
@@ -124,6 +125,10 @@ inline GemmShape gemm_shape(int64_t m, int64_t n, int64_t k, const GemmPlan& pla
   s.items = s.full + (tiles - s.full) * s.splits;
   s.a_box = m < 128 ? int32_t(round_up(m, 8)) : 128;
   s.b_box = plan.tile_n / 2;
+  // Over 4096 of k, lse is off by 1.5e-6 of itself with one chunk, 3.5e-7 with
+  // chunks of 16 steps, 6e-8 with four.  One row of tiles waits for memory and
+  // four cost it nothing; 2048 x 32000 logits take 302, 307 and 337 us.
+  s.chunk = s.m_tiles == 1 ? 4 : 16;
   s.status = status;
   return s;
 }
@@ -240,11 +245,15 @@ struct GemmPiece {
   uint32_t acc_empty;  // the accumulator's barrier, in the pair's first CTA
   uint32_t staging;    // shared address
 
-  // N (a multiple of 32) columns from column c of this lane's row.
+  // 16, or a multiple of 32, columns from column c of this lane's row.
   template <int N>
   __device__ __forceinline__ void load(int c, float (&v)[N]) const {
+    if constexpr (N == 16) {
+      tmem_load16(tmem + c, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 32) tmem_load32(tmem + c + i, v + i);
+      for (int i = 0; i < N; i += 32) tmem_load32(tmem + c + i, v + i);
+    }
     tmem_wait<N>(v);
   }
   // The accumulator has been read.
@@ -289,7 +298,12 @@ __device__ __forceinline__ void emit_rows(const float (&v)[8 * kPerUnit], const 
 
 // Epi: begin() is called by one thread of the launch at its start.
 // operator()(const GemmPiece&) is called by whole warps, loads the piece, and
-// calls release() once.  (Rows beyond m and columns from `width` on hold
+// calls release() once.  With kChunked the tensor cores sum only `chunk` steps
+// of k at a time and the epilogue's warps add the chunks, in fp32 rounded to
+// nearest, and hand the piece's sums over: operator()(const GemmPiece&, float
+// (&)[kPiece]).  (The tensor cores' additions truncate: each of the 256 that a
+// sum over 4096 takes loses half a unit in the last place of the sum so far,
+// on average.)  (Rows beyond m and columns from `width` on hold
 // nothing of the product.)
 template <class T, bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
@@ -344,11 +358,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       for (int item = pair; ok && item < shape.items; item += pairs, ++tile) {
         int step0;
         const int steps = gemm_steps(shape, item, step0);
-        const int acc = tile & 1;
-        ok = bar_wait(shared_addr(&bars->acc_empty[acc]), (unsigned(tile >> 1) & 1) ^ 1, shape.status);
-        if (!ok) break;
-        fence_after_sync();
+        int acc = 0;
         for (int i = 0; i < steps; ++i) {
+          const bool fresh = Epi::kChunked ? i % shape.chunk == 0 : i == 0;
+          if (fresh) {  // the next accumulator
+            if (i > 0) {
+              commit_pair(shared_addr(&bars->acc_full[acc]));
+              ++tile;
+            }
+            acc = tile & 1;
+            ok = bar_wait(shared_addr(&bars->acc_empty[acc]), (unsigned(tile >> 1) & 1) ^ 1, shape.status);
+            if (!ok) break;
+            fence_after_sync();
+          }
           ok = bar_wait(shared_addr(&bars->full[stage]), parity, shape.status);
           if (!ok) break;
           fence_after_sync();
@@ -356,13 +378,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const uint64_t da = operand_desc<A_MN>(a), db = operand_desc<B_MN>(a + kOperandBytes);
 #pragma unroll
           for (int k = 0; k < kTileK / 16; ++k)
-            mma_pair(tmem + acc * kTileN, da + k * a_step, db + k * b_step, idesc, i > 0 || k > 0);
+            mma_pair(tmem + acc * kTileN, da + k * a_step, db + k * b_step, idesc, !fresh || k > 0);
           commit_pair(shared_addr(&bars->empty[stage]));
           if (++stage == kStages) {
             stage = 0;
             parity ^= 1;
           }
         }
+        if (!ok) break;
         commit_pair(shared_addr(&bars->acc_full[acc]));
       }
     }
@@ -374,21 +397,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     at.tile_row = int(rank) * 128 + quarter * 32;
     at.tile_col = half * half_n;
     int tile = 0;
-    for (int item = pair; item < shape.items; item += pairs, ++tile) {
+    bool ok = true;
+    for (int item = pair; ok && item < shape.items; item += pairs) {
       const GemmItem it = gemm_item(shape, item);
-      const int acc = tile & 1;
-      if (!bar_wait(shared_addr(&bars->acc_full[acc]), unsigned(tile >> 1) & 1, shape.status)) break;
-      fence_after_sync();
       at.row0 = int64_t(it.m0) + at.tile_row;
       at.col = int64_t(it.n0) + at.tile_col;
       at.width = int(min(int64_t(half_n), shape.n - at.col));
       at.slot = it.slot;
-      at.tmem = lanes + acc * kTileN;
-      at.acc_empty = map_rank(shared_addr(&bars->acc_empty[acc]), 0);
-      if (at.row0 < shape.m && at.width > 0)
-        epi(at);
-      else
-        at.release();
+      const bool here = at.row0 < shape.m && at.width > 0;
+      const auto next_acc = [&] {
+        const int acc = tile & 1;
+        ok = bar_wait(shared_addr(&bars->acc_full[acc]), unsigned(tile >> 1) & 1, shape.status);
+        ++tile;
+        fence_after_sync();
+        at.tmem = lanes + acc * kTileN;
+        at.acc_empty = map_rank(shared_addr(&bars->acc_empty[acc]), 0);
+        return ok;
+      };
+      if constexpr (Epi::kChunked) {
+        float v[kPiece];
+#pragma unroll
+        for (int i = 0; i < kPiece; ++i) v[i] = 0.0f;
+        for (int c = 0; c < it.steps && next_acc(); c += shape.chunk) {
+          if (here) {
+#pragma unroll
+            for (int g = 0; g < kPiece; g += 16)
+              if (g < half_n) {
+                float t[16];
+                at.load(g, t);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[g + i] += t[i];
+              }
+          }
+          at.release();
+        }
+        if (here && ok) epi(at, v);
+      } else if (next_acc()) {
+        if (here)
+          epi(at);
+        else
+          at.release();
+      }
     }
   }
   __syncwarp();

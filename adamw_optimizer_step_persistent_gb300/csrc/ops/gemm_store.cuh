@@ -45,6 +45,7 @@ struct StoreEpilogue {
   float* parts;  // fp32 [slots, split_rows(m), tile_n]: sums of split tiles, joined by join_kernel
   int tile_n;
 
+  static constexpr bool kChunked = false;
   __device__ __forceinline__ void begin() const {}
   __device__ __forceinline__ void operator()(const GemmPiece& at) const {
     const int64_t row = at.row0 + threadIdx.x % 32;

@@ -41,41 +41,43 @@ struct LogitEpilogue {
   int64_t pitch;
   Control* control;
 
+  static constexpr bool kChunked = true;  // logits to (nearly) fp32's own accuracy
+
   __device__ __forceinline__ void begin() const { control->finished = 0; }
-  __device__ __forceinline__ void operator()(const GemmPiece& p) const {
+  __device__ __forceinline__ void operator()(const GemmPiece& p, float (&v)[kPiece]) const {
     const int64_t row = p.row0 + threadIdx.x % 32;
     const int64_t at = row < rows ? targets[row] - p.col : -1;
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < p.width; c += 64) {
-      float v[64];
-      load(p, c, v);
-      float m[4] = {v[0], v[1], v[2], v[3]};
+    if (at >= 0 && at < p.width) {
+      float z = 0.0f;
 #pragma unroll
-      for (int i = 4; i < 64; ++i) m[i % 4] = fmaxf(m[i % 4], v[i]);
-      top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-      if (at >= c && at < c + 64 && at < p.width) {
-        float z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) z = c + i == at ? v[i] : z;
-        target_z[row] = z;
-      }
+      for (int i = 0; i < kPiece; ++i) z = i == at ? v[i] : z;
+      target_z[row] = z;
     }
+    if (p.width < kPiece) {  // beyond the vocabulary (or the piece): as if the logit were -inf
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i)
+        if (i >= p.width) v[i] = -INFINITY;
+    }
+    float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 4; i < kPiece; ++i) m[i % 4] = fmaxf(m[i % 4], v[i]);
+    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     const float base = top == -INFINITY ? 0.0f : top;  // nothing above -inf: all terms are 0
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-    for (int c = 0; c < p.width; c += 64) {
-      float v[64];
-      load(p, c, v);
-      if (c + 64 >= p.width) p.release();
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        v[i] = exp2_fast((v[i] - base) * 1.4426950408889634f);
-        sum[i % 4] += v[i];
-      }
-      if (kept)
+    for (int i = 0; i < kPiece; ++i) {
+      v[i] = exp2_fast((v[i] - base) * 1.4426950408889634f);
+      sum[i % 4] += v[i];
+    }
+    if (row < rows)
+      stats[row * pieces + p.col / piece] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (kept) {
+#pragma unroll
+      for (int c = 0; c < kPiece; c += 64) {
+        if (c >= p.width) break;
+        float (&e)[64] = reinterpret_cast<float (&)[64]>(v[c]);
         emit_rows<8>(
-            v, p, c, rows,
+            e, p, c, rows,
             [](const float* e) {
               return make_uint4(pack2<__half>(e[0], e[1]), pack2<__half>(e[2], e[3]),
                                 pack2<__half>(e[4], e[5]), pack2<__half>(e[6], e[7]));
@@ -83,18 +85,8 @@ struct LogitEpilogue {
             [&](int r, int col, uint4 u) {
               *reinterpret_cast<uint4*>(kept + (p.row0 + r) * pitch + p.col + col) = u;
             });
+      }
     }
-    if (row < rows)
-      stats[row * pieces + p.col / piece] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-  }
-
-  // 64 columns, those beyond the vocabulary (or the piece) as if their logits were -inf.
-  static __device__ __forceinline__ void load(const GemmPiece& p, int c, float (&v)[64]) {
-    p.load(c, v);
-    if (p.width - c < 64)
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (c + i >= p.width) v[i] = -INFINITY;
   }
 
   // 2^x for x <= 0; what is below 2^-126 is 0 (its share of a sum that is at
