@@ -358,14 +358,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       for (int item = pair; ok && item < shape.items; item += pairs, ++tile) {
         int step0;
         const int steps = gemm_steps(shape, item, step0);
-        int acc = 0;
-        for (int i = 0; i < steps; ++i) {
-          const bool fresh = Epi::kChunked ? i % shape.chunk == 0 : i == 0;
+        int acc = 0, left = 0;  // left: steps of the accumulator's chunk
+        for (int i = 0; i < steps; ++i, --left) {
+          const bool fresh = left == 0;
           if (fresh) {  // the next accumulator
             if (i > 0) {
               commit_pair(shared_addr(&bars->acc_full[acc]));
               ++tile;
             }
+            left = Epi::kChunked ? shape.chunk : steps;
             acc = tile & 1;
             ok = bar_wait(shared_addr(&bars->acc_empty[acc]), (unsigned(tile >> 1) & 1) ^ 1, shape.status);
             if (!ok) break;
