@@ -66,7 +66,7 @@ def _rows(t: torch.Tensor, what: str):
     """(rows, width, stride) of a tensor taken as a matrix."""
     if t.dim() < 1:
         raise ValueError(f"{what} has no dimension")
-    width = t.shape[-1]
+    width = t.size(-1)
     if t.is_contiguous():
         return (t.numel() // width if width else 0), width, width
     if width > 1 and t.stride(-1) != 1:
@@ -105,7 +105,7 @@ def _like(t: torch.Tensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     there is, but keeps the strides of what is dense in another order)."""
     if t.is_contiguous():
         return torch.empty_like(t, dtype=dtype) if dtype is not None else torch.empty_like(t)
-    return t.new_empty(t.shape, dtype=dtype)
+    return torch.empty((*t.shape,), dtype=dtype or t.dtype, device=t.device)
 
 
 _HERE = contextlib.nullcontext()
@@ -124,7 +124,7 @@ def _workspace(size_of, desc, where: str, like: torch.Tensor):
         _abi.check_ops(status, where)
     if not need.value:
         return None, None, 0
-    ws = like.new_empty(need.value, dtype=torch.uint8)
+    ws = torch.empty(need.value, dtype=torch.uint8, device=like.device)
     return ws, ws.data_ptr(), need.value
 
 
@@ -178,7 +178,7 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
     with _current(index):
         row_loss = torch.empty_like(targets, dtype=torch.float32)
         lse = torch.empty_like(row_loss)
-        loss = x.new_empty((), dtype=torch.float32)
+        loss = torch.empty((), dtype=torch.float32, device=x.device)
         if grads:
             grad_x = _like(x)
             if grad_weight is None:
@@ -204,7 +204,8 @@ def _empty_checkpoint(like: torch.Tensor) -> Checkpoint8:
     shape = like.shape
     groups = -(-shape[-1] // _abi.CHECKPOINT8_GROUP)
     return Checkpoint8(_like(like, torch.int8),
-                       like.new_empty(shape[:-1] + (groups,), dtype=torch.float32), like.dtype)
+                       torch.empty((*shape[:-1], groups), dtype=torch.float32,
+                                   device=like.device), like.dtype)
 
 
 def _kept(c: Optional[Checkpoint8]) -> _abi.Kept8:
@@ -282,7 +283,7 @@ def checkpoint8_weight_grad(grad_y: torch.Tensor, c: Checkpoint8, *,
         raise ValueError(f"out must be [{n}, {width}] of grad_y's dtype or fp32")
     with _current(index):
         if out is None:
-            out = grad_y.new_empty(n, width)
+            out = torch.empty((n, width), dtype=grad_y.dtype, device=grad_y.device)
         desc = _abi.Wgrad(grad_y.data_ptr(), _kept(c), out.data_ptr(), rows, n, width, stride,
                           _rows(out, "out")[2], dtype_code(grad_y.dtype), dtype_code(out.dtype),
                           _abi.WGRAD_ACCUMULATE if accumulate else 0)
@@ -299,17 +300,20 @@ def checkpoint8_weight_grad(grad_y: torch.Tensor, c: Checkpoint8, *,
 
 def _norm_params(width: int, rows: int, block: torch.dtype, pre_weight, post_weight, gate):
     """The parameters' dtype, and how many rows the gate has."""
-    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
-        if w is not None and (w.shape != (width,) or not w.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous [{width}]")
     dtype = pre_weight.dtype
-    if any(t is not None and t.dtype != dtype for t in (post_weight, gate)):
-        raise TypeError("pre_weight, post_weight and gate must have one dtype")
-    if dtype not in (block, torch.float32):
+    if dtype is not block and dtype is not torch.float32:
         raise TypeError(f"the parameters must be {block} or fp32, got {dtype}")
+    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
+        if w is not None:
+            if w.dim() != 1 or w.size(0) != width or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [{width}]")
+            if w.dtype is not dtype:
+                raise TypeError("pre_weight, post_weight and gate must have one dtype")
     if gate is None:
         return dtype, 1
-    if not gate.is_contiguous() or gate.shape[-1] != width:
+    if gate.dtype is not dtype:
+        raise TypeError("pre_weight, post_weight and gate must have one dtype")
+    if gate.dim() < 1 or gate.size(-1) != width or not gate.is_contiguous():
         raise ValueError(f"gate must be a contiguous [..., {width}]")
     gate_rows = gate.numel() // width
     if gate_rows < 1 or rows % gate_rows:
@@ -343,14 +347,15 @@ def block_norm(f: torch.Tensor, h: torch.Tensor, pre_weight: torch.Tensor, *,
     if h.dtype not in (f.dtype, torch.float32):
         raise TypeError(f"h must be {f.dtype} or fp32, got {h.dtype}")
     block = dtype_code(f.dtype)
+    residual = block if h.dtype is f.dtype else dtype_code(h.dtype)
     params, gate_rows = _norm_params(width, rows, f.dtype, pre_weight, post_weight, gate)
     index = _device(f, "f")
     _check_device(index, "f", h, pre_weight, post_weight, gate)
-    h_stride = _rows(h, "h")[2]
+    h_stride = width if h.is_contiguous() else _rows(h, "h")[2]
     with _current(index):
         h_out = _like(h)
         x_out = _like(f)
-        r2 = f.new_empty(f.shape[:-1], dtype=torch.float32)
+        r2 = torch.empty((*f.shape[:-1],), dtype=torch.float32, device=f.device)
         r1 = torch.empty_like(r2) if post_weight is not None else None
         f_kept = _empty_checkpoint(f) if checkpoint else None
         h_kept = _empty_checkpoint(h) if checkpoint else None
@@ -358,7 +363,7 @@ def block_norm(f: torch.Tensor, h: torch.Tensor, pre_weight: torch.Tensor, *,
             f.data_ptr(), h.data_ptr(), _ptr(post_weight), pre_weight.data_ptr(), _ptr(gate),
             h_out.data_ptr(), x_out.data_ptr(), _ptr(r1), r2.data_ptr(), _kept(f_kept),
             _kept(h_kept), rows, width, gate_rows, f_stride, h_stride, float(residual_scale),
-            float(eps), block, dtype_code(h.dtype), dtype_code(params))
+            float(eps), block, residual, block if params is f.dtype else dtype_code(params))
         status = _abi.lib().fadam_block_norm_forward(desc, _stream(index))
     if status:
         _abi.check_ops(status, "fadam_block_norm_forward")
