@@ -81,12 +81,11 @@ inline int norm_ctas_per_sm(int threads) {
   return fit < 8 ? fit : 8;
 }
 
-// Every CTA gets a run, and a gate's rows are cut into as many as that takes.
-// Beyond a CTA per SM each gets four rows at least, or reading the parameters
-// and writing the sums would cost more than the rows.
+// Every CTA that fits gets a run, and a gate's rows are cut into as many as
+// that takes.  (Giving each at least four rows, to read the parameters and
+// write the sums less often, took 13.3 us in place of 9.0 for 512 x 512.)
 inline NormRuns norm_runs(int64_t rows, int64_t gates, int64_t width, int sm_count) {
-  int64_t most = int64_t(sm_count) * norm_ctas_per_sm(row_shape(width).threads);
-  if (most > rows / 4) most = rows / 4 > sm_count ? rows / 4 : sm_count;
+  const int64_t most = int64_t(sm_count) * norm_ctas_per_sm(row_shape(width).threads);
   int64_t slices = most / gates;
   if (slices > rows / gates) slices = rows / gates;
   if (slices < 1) slices = 1;

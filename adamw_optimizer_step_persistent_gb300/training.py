@@ -370,6 +370,19 @@ def block_norm(f: torch.Tensor, h: torch.Tensor, pre_weight: torch.Tensor, *,
     return BlockNorm(h_out, x_out, r1, r2, f_kept, h_kept)
 
 
+def _saved(t: Union[torch.Tensor, Checkpoint8], what: str, shape: torch.Size):
+    """(a tensor on its device, tensor's address or None, kept or not, stride)."""
+    kept = isinstance(t, Checkpoint8)
+    if kept:
+        _check_checkpoint(t, what)
+    data = t.codes if kept else t
+    if data.shape != shape:
+        raise ValueError(f"{what} {tuple(data.shape)} and grad_x_out {tuple(shape)} differ in shape")
+    if kept:
+        return data, None, _kept(t), shape[-1]
+    return data, data.data_ptr(), _NOT_KEPT, _rows(data, what)[2]
+
+
 def block_norm_backward(grad_h_out: Optional[torch.Tensor], grad_x_out: torch.Tensor,
                         f: Union[torch.Tensor, Checkpoint8],
                         h_out: Union[torch.Tensor, Checkpoint8],
@@ -382,49 +395,41 @@ def block_norm_backward(grad_h_out: Optional[torch.Tensor], grad_x_out: torch.Te
     pass left: ``f`` and ``h_out``, each the tensor or its 8-bit checkpoint,
     and the rstds.  The parameters' gradients have the parameters' dtype."""
     rows, width, gx_stride = _rows(grad_x_out, "grad_x_out")
-    block = grad_x_out.dtype
-    saved, strides, dtypes = [], [], []
-    for name, t in (("f", f), ("h_out", h_out)):
-        kept = isinstance(t, Checkpoint8)
-        if kept:
-            _check_checkpoint(t, name)
-        data = t.codes if kept else t
-        if data.shape != grad_x_out.shape:
-            raise ValueError(f"{name} {tuple(data.shape)} and grad_x_out "
-                             f"{tuple(grad_x_out.shape)} differ in shape")
-        saved.append((None, t) if kept else (t, None))
-        strides.append(_rows(data, name)[2])
-        dtypes.append(t.dtype)
-    if dtypes[0] != block or dtypes[1] not in (block, torch.float32):
-        raise TypeError(f"f must be {block} and h_out that or fp32, got {dtypes[0]}, {dtypes[1]}")
-    if grad_h_out is not None and (grad_h_out.shape != grad_x_out.shape
-                                   or grad_h_out.dtype != dtypes[1]):
-        raise ValueError(f"grad_h_out must be {dtypes[1]} of shape {tuple(grad_x_out.shape)}")
+    block, shape = grad_x_out.dtype, grad_x_out.shape
+    f_data, f_at, f_kept, f_stride = _saved(f, "f", shape)
+    h_data, h_at, h_kept, h_stride = _saved(h_out, "h_out", shape)
+    residual = h_out.dtype
+    if f.dtype is not block or residual is not block and residual is not torch.float32:
+        raise TypeError(f"f must be {block} and h_out that or fp32, got {f.dtype}, {residual}")
+    gh_stride = width
+    if grad_h_out is not None:
+        if grad_h_out.shape != shape or grad_h_out.dtype is not residual:
+            raise ValueError(f"grad_h_out must be {residual} of shape {tuple(shape)}")
+        gh_stride = _rows(grad_h_out, "grad_h_out")[2]
     params, gate_rows = _norm_params(width, rows, block, pre_weight, post_weight, gate)
     if (rstd_post is None) != (post_weight is None):
         raise ValueError("rstd_post and post_weight go together")
     for name, r in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
-        if r is not None and (r.dtype != torch.float32 or r.shape != grad_x_out.shape[:-1]
+        if r is not None and (r.dtype is not torch.float32 or r.shape != shape[:-1]
                               or not r.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous fp32 {tuple(grad_x_out.shape[:-1])}")
+            raise ValueError(f"{name} must be a contiguous fp32 {tuple(shape[:-1])}")
     index = _device(grad_x_out, "grad_x_out")
-    _check_device(index, "grad_x_out", grad_h_out, f[0] if isinstance(f, Checkpoint8) else f,
-                  h_out[0] if isinstance(h_out, Checkpoint8) else h_out, rstd_post, rstd_pre,
-                  pre_weight, post_weight, gate)
-    gh_stride = width if grad_h_out is None else _rows(grad_h_out, "grad_h_out")[2]
+    _check_device(index, "grad_x_out", grad_h_out, f_data, h_data, rstd_post, rstd_pre, pre_weight,
+                  post_weight, gate)
     with _current(index):
         grad_f = _like(grad_x_out)
-        grad_h = torch.empty_like(grad_f, dtype=dtypes[1])
+        grad_h = torch.empty_like(grad_f, dtype=residual)
         grad_pre = torch.empty_like(pre_weight)
         grad_post = None if post_weight is None else torch.empty_like(post_weight)
         grad_gate = None if gate is None else torch.empty_like(gate)
+        code = dtype_code(block)
         desc = _abi.BlockNormGrad(
-            _ptr(grad_h_out), grad_x_out.data_ptr(), _ptr(saved[0][0]), _ptr(saved[1][0]),
-            _kept(saved[0][1]), _kept(saved[1][1]), _ptr(rstd_post), rstd_pre.data_ptr(),
-            _ptr(post_weight), pre_weight.data_ptr(), _ptr(gate), grad_f.data_ptr(),
-            grad_h.data_ptr(), _ptr(grad_post), grad_pre.data_ptr(), _ptr(grad_gate), rows, width,
-            gate_rows, gh_stride, gx_stride, strides[0], strides[1], float(residual_scale),
-            dtype_code(block), dtype_code(dtypes[1]), dtype_code(params))
+            _ptr(grad_h_out), grad_x_out.data_ptr(), f_at, h_at, f_kept, h_kept, _ptr(rstd_post),
+            rstd_pre.data_ptr(), _ptr(post_weight), pre_weight.data_ptr(), _ptr(gate),
+            grad_f.data_ptr(), grad_h.data_ptr(), _ptr(grad_post), grad_pre.data_ptr(),
+            _ptr(grad_gate), rows, width, gate_rows, gh_stride, gx_stride, f_stride, h_stride,
+            float(residual_scale), code, code if residual is block else dtype_code(residual),
+            code if params is block else dtype_code(params))
         lib = _abi.lib()
         ws, at, size = _workspace(lib.fadam_block_norm_backward_workspace, desc,
                                   "fadam_block_norm_backward_workspace", grad_x_out)
