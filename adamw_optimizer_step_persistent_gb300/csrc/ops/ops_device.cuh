@@ -80,6 +80,8 @@ __device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.laun
 
 // Wall time after which a wait gives up.
 constexpr unsigned long long kWaitNs = 2000000000ull;
+// How long a waiting thread may sleep before it looks at the clock again.
+constexpr unsigned kSleepNs = 10000000;
 
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -116,10 +118,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, unsigned parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kSleepNs)
       : "memory");
   return done != 0;
 }
