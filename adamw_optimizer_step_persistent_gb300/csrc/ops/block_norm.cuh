@@ -11,7 +11,11 @@
 // registers allow; elsewhere, and when each CTA has one row only, threads load
 // their own columns.  The barrier of a row's reduction also says that its
 // stage has been read.  Up to 4096 columns two and more CTAs share an SM, which
-// hides their reductions' latency in one another.
+// hides their reductions' latency in one another.  Backward, 16384 x 4096 in
+// bf16 from checkpoints: 121 us, 5.3 TB/s; forward, 8192 x 4096 with both
+// checkpoints: 75 us, 4.5 TB/s.  What is left over memory is the issue of some
+// 40 instructions an element (half the slots) by the 16 warps that 128
+// registers a thread leave an SM, and a row's two or one reductions.
 //
 // Backward, with hh = h_out r2, fh = f r1 and, for a row,
 //   g = grad_x_out pre_weight

@@ -11,6 +11,12 @@
 // pair's first CTA).  The accumulators, two of 128 lanes x 256 columns, fill
 // the tensor memory: a tile's epilogue runs under the next tile's products.
 //
+// Bound by the tensor cores, and they by the card's power: 2048 x 4096 x 32000
+// in 280 to 300 us, 1.8 to 1.9 PFLOP/s, with the tensor pipe active 94 to 97%
+// of the time at the 1.7 GHz that the power leaves.  A step of 64 in k takes
+// about 550 cycles where the instructions alone take 512; a tile some 1500 more,
+// which shows when k is short (1037 x 1000 x 50021: 16 steps to a tile, 60%).
+//
 // Either operand may lie in memory with k contiguous ("k-major") or with its
 // own index contiguous (A_MN, B_MN: what a product with a transposed matrix
 // reads), so no operand is ever transposed in memory.  In shared memory a
