@@ -18,6 +18,21 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 DeviceFacts g_facts[kMaxDevices];
 bool g_known[kMaxDevices];
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                            const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                            CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                            CUtensorMapFloatOOBfill);
+Encode find_encode() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return nullptr;
+  }
+  return found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(fn) : nullptr;
+}
 }  // namespace
 
 fadam_status fail(fadam_status st, const char* fmt, ...) {
@@ -59,21 +74,8 @@ fadam_status device_facts(DeviceFacts* out) {
 
 fadam_status matrix_map(CUtensorMap* map, const void* base, int64_t rows, int64_t inner, int64_t ld,
                         int box_rows) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static Encode encode = nullptr;
-  if (!encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                           cudaEnableDefault, &found);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPointByVersion");
-    if (!fn || found != cudaDriverEntryPointSuccess)
-      return fail(FADAM_ECUDA, "the driver has no cuTensorMapEncodeTiled");
-    encode = reinterpret_cast<Encode>(fn);
-  }
+  static const Encode encode = find_encode();
+  if (!encode) return fail(FADAM_ECUDA, "the driver has no cuTensorMapEncodeTiled");
   const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(rows)};
   const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
   const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};

@@ -20,8 +20,8 @@
  *     matching *_workspace function returns and whose contents mean nothing
  *     between calls.  A workspace is 256-byte aligned and must not be used by
  *     another call before this one has run.
- *   - Everything runs on `stream`, without host synchronisation: calls can be
- *     captured in a CUDA graph.  Results are deterministic (the same inputs
+ *   - Everything runs on `stream`, a stream of the current device, without
+ *     host synchronisation: calls can be captured in a CUDA graph.  Results are deterministic (the same inputs
  *     on the same GPU give the same bits).
  *   - Argument checks run on the host before anything is launched; a failing
  *     one returns a status and leaves a message for the calling thread in

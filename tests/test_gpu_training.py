@@ -528,8 +528,121 @@ def test_graph_replays_with_new_inputs():
     assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_the_first_call_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+import adamw_optimizer_step_persistent_gb300 as fadam
+x = torch.randn(300, 72, device="cuda").bfloat16()
+w = torch.randn(500, 72, device="cuda").bfloat16()
+y = torch.randint(0, 500, (300,), device="cuda")
+p = torch.ones(72, device="cuda").bfloat16()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    r = fadam.linear_cross_entropy(x, w, y)
+    n = fadam.block_norm(x, x, p, post_weight=p, checkpoint=True)
+    g = fadam.block_norm_backward(x, x, n.f_checkpoint, n.h_out, n.rstd_post, n.rstd_pre, p, post_weight=p)
+    d = fadam.checkpoint8_weight_grad(x, n.f_checkpoint)
+graph.replay()
+torch.cuda.synchronize()
+s = fadam.linear_cross_entropy(x, w, y)
+assert torch.equal(r.loss, s.loss) and torch.equal(r.grad_weight, s.grad_weight)
+assert torch.equal(d, fadam.checkpoint8_weight_grad(x, fadam.checkpoint8(x)))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=240,
+                   env=dict(os.environ, PYTHONPATH=root))
+
+
+# ---- offsets beyond 32 bits -----------------------------------------------------------------------
+
+def test_xent_beyond_2_to_the_31_logits():
+    T, D, V = 33000, 64, 70001
+    x, w, y = _xent_case(T, D, V, BF16, seed=13, ignored=0.1)
+    r = fadam.linear_cross_entropy(x, w, y, reduction="sum")
+    at = torch.cat([torch.arange(0, T, 997, device="cuda"), torch.arange(T - 40, T, device="cuda")])
+    b = ref.xent_bounds(x[at].double(), w.double(), y[at], BF16, mean=False)
+    b["lse"].holds(r.lse[at], "lse")
+    b["row_loss"].holds(r.row_loss[at], "row_loss")
+    b["grad_x"].holds(r.grad_x[at], "grad_x")
+    # dW of some entries of the vocabulary, over all rows
+    cols = torch.cat([torch.arange(0, V, 1501, device="cuda"), torch.arange(V - 20, V, device="cuda")])
+    p = (x.double() @ w[cols].double().t() - r.lse.double()[:, None]).exp()
+    p -= (y[:, None] == cols).double()
+    p[y == -100] = 0
+    size = p.abs().t() @ x.double().abs()
+    # one rounding of dz, one of the kept exponential, the logits' and the sums' in fp32
+    off = size * (ref.U[BF16] + 2.0 ** -11 + 2.0 ** -14) + 2.0 ** -25 * x.double().abs().sum(0) \
+        + T * ref.E32 * size
+    ref.Bounded(p.t() @ x.double(), off).holds(r.grad_weight[cols], "grad_w")
+
+
+def test_checkpoint_beyond_2_to_the_31_elements():
+    T, D = 270000, 8192
+    x = torch.zeros(T, D, dtype=BF16, device="cuda")
+    x[::9001] = _rand(_gen(1), len(range(0, T, 9001)), D).to(BF16)
+    x[-3:] = _rand(_gen(2), 3, D).to(BF16)
+    k = fadam.checkpoint8(x)
+    back = fadam.checkpoint8_restore(k)
+    for at in (slice(0, T, 9001), slice(T - 4, T)):
+        q, s = ref.codes(x[at])
+        assert torch.equal(k.codes[at].cpu(), q) and torch.equal(k.scales[at].cpu(), s)
+        assert torch.equal(back[at], ref.values(k.codes[at], k.scales[at]).float().to(BF16))
+
+
+@pytest.mark.parametrize("D", [8192, 8191])
+def test_block_norm_beyond_2_to_the_31_elements(D):
+    T = 264000
+    g = _gen(3)
+    f = torch.zeros(T, D, dtype=BF16, device="cuda")
+    at = torch.cat([torch.arange(0, T, 8999, device="cuda"), torch.arange(T - 3, T, device="cuda")])
+    f[at] = _rand(g, len(at), D).to(BF16)
+    w = (1 + 0.2 * _rand(g, D)).to(BF16)
+    n = fadam.block_norm(f, f, w, post_weight=w, checkpoint=True)
+    a = {"f": f[at], "h": f[at], "pre": w, "post": w, "gate": None}
+    want = ref.block_norm_bounds(_d(a["f"]), _d(a["h"]), _d(w), _d(w), None, 1.0, 1e-6)
+    want["h_out"].holds(n.h_out[at], "h_out")
+    want["x_out"].holds(n.x_out[at], "x_out")
+    q, s = ref.codes(n.h_out[at])
+    assert torch.equal(n.h_checkpoint.codes[at].cpu(), q) and torch.equal(n.h_checkpoint.scales[at].cpu(), s)
+    d = fadam.block_norm_backward(f, f, f, n.h_out, n.rstd_post, n.rstd_pre, w, post_weight=w)
+    grad = ref.block_norm_grad(_d(f[at]), _d(f[at]), _d(f[at]), _d(n.h_out[at]), _d(n.rstd_post[at]),
+                               _d(n.rstd_pre[at]), _d(w), _d(w), None, 1.0)
+    grad["h"].holds(d.h[at], "h")
+    grad["f"].holds(d.f[at], "f")
+    # every other row is zero and adds nothing
+    ref.Bounded(grad["pre"].value, grad["pre"].off * (1 + T / len(at))).holds(d.pre_weight, "pre")
+
+
 def test_gradients_land_in_the_optimizer_shard():
     """The example: a model trained through all of the operators."""
     from examples import train_step
     losses = train_step.main(["--steps", "25", "--rows", "512"])
     assert losses[0] > 6.0 and losses[-1] < 0.7 * losses[0]
+
+
+def test_block_norm_in_place_on_the_residual_stream():
+    """h_out may be h (C ABI): the same bits as out of place."""
+    import ctypes
+
+    from adamw_optimizer_step_persistent_gb300 import _abi
+    for rows, D in ((700, 256), (700, 255), (3, 256)):
+        a = _norm_case(rows, D, BF16, F32, BF16, True, 1)
+        n = fadam.block_norm(a["f"], a["h"], a["pre"], post_weight=a["post"], gate=a["gate"], checkpoint=True)
+        h, x = a["h"].clone(), torch.empty_like(a["f"])
+        r1, r2 = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        k = fadam.checkpoint8(a["h"])
+        d = _abi.BlockNorm(f=a["f"].data_ptr(), h=h.data_ptr(), post_weight=a["post"].data_ptr(),
+                           pre_weight=a["pre"].data_ptr(), gate=a["gate"].data_ptr(), h_out=h.data_ptr(),
+                           x_out=x.data_ptr(), rstd_post=r1.data_ptr(), rstd_pre=r2.data_ptr(),
+                           h_kept=_abi.Kept8(k.codes.data_ptr(), k.scales.data_ptr()), rows=rows, width=D,
+                           gate_rows=1, f_stride=D, h_stride=D, residual_scale=1.0, eps=1e-6,
+                           block_dtype=_abi.DT_BF16, residual_dtype=_abi.DT_F32, param_dtype=_abi.DT_BF16)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert _abi.lib().fadam_block_norm_forward(ctypes.byref(d), stream) == _abi.OK
+        torch.cuda.synchronize()
+        assert torch.equal(h, n.h_out) and torch.equal(x, n.x_out) and torch.equal(r2, n.rstd_pre)
+        assert torch.equal(k.codes, n.h_checkpoint.codes) and torch.equal(k.scales, n.h_checkpoint.scales)
