@@ -174,30 +174,37 @@ __device__ __forceinline__ void block_sums(float (&v)[4], float* shared, int thr
 
 // ---- forward -------------------------------------------------------------------------
 
-// A row's vectors kept in 8 bits: from registers where they lie next to each
-// other, else (h_out: after the CTA has written it) from memory, a warp to a
-// group.
-template <class E, int NV, bool kWide>
-__device__ __forceinline__ void keep_row(const Raw<E> (&r)[NV], const E* row, int64_t index,
-                                         int8_t* codes, float* scales, const Columns<NV, kWide>& c) {
-  const int groups = (c.width + kGroup - 1) / kGroup;
-  codes += index * c.width;
-  scales += index * groups;
-  if constexpr (kWide) {
-    int8_t* to[NV];
-    float* scale[NV];
-    bool valid[NV];
+// A row's f and h_out kept in 8 bits, from registers where the vectors lie
+// next to each other.
+template <class F, class H, int NV>
+__device__ __forceinline__ void keep_row(const NormArgs& a, int64_t row, const Columns<NV, true>& c,
+                                         const Raw<F> (&f)[NV], const Raw<H> (&h)[NV]) {
+  const int64_t at = row * c.width, group_at = row * ((c.width + kGroup - 1) / kGroup);
+  float top[2 * NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      to[j] = codes + c.first(j);
-      scale[j] = scales + c.first(j) / kGroup;
-      valid[j] = c.first(j) < c.width;
-    }
-    keep_vectors<E, NV>(r, to, scale, valid);
-  } else {
-    for (int g = c.tid / 32; g < groups; g += c.threads / 32)
-      keep_group(row, g * kGroup, c.width, codes, scales);
+  for (int j = 0; j < NV; ++j) {
+    top[j] = a.f_codes ? from_bits<F>(group_top(f[j])) : 0.0f;
+    top[NV + j] = a.h_codes ? from_bits<H>(group_top(h[j])) : 0.0f;
   }
+  const Scaling shared = share_scaling<2 * NV>(top);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int col = c.first(j), group = col / kGroup;
+    const bool valid = col < c.width, group_valid = group * kGroup < c.width;
+    if (a.f_codes)
+      keep_vector(f[j], shared, j, a.f_codes + at + col, a.f_scales + group_at + group, valid, group_valid);
+    if (a.h_codes)
+      keep_vector(h[j], shared, NV + j, a.h_codes + at + col, a.h_scales + group_at + group, valid,
+                  group_valid);
+  }
+}
+// Else from memory (h_out once the CTA has written it), a warp to a group.
+template <class E, int NV>
+__device__ __forceinline__ void keep_row(const E* row, int64_t index, int8_t* codes, float* scales,
+                                         const Columns<NV, false>& c) {
+  const int groups = (c.width + kGroup - 1) / kGroup;
+  for (int g = c.tid / 32; g < groups; g += c.threads / 32)
+    keep_group(row, g * kGroup, c.width, codes + index * c.width, scales + index * groups);
 }
 
 template <class F, class H, int NV, int MODE>
@@ -278,9 +285,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
           s = fma2(h[j][i], h[j][i], s);
         }
       }
-      if (a.f_codes)
-        keep_row<F, NV, kWide>(f_raw, static_cast<const F*>(a.f) + row * a.f_stride, row, a.f_codes,
-                        a.f_scales, c);
       const float r2 = rsqrtf(block_sum(sum2(s), shared[1], c.threads) * inv_width + a.eps);
       if (c.tid == 0) a.r2[row] = r2;
       if (MODE == kRing) ring.release();
@@ -294,13 +298,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         for (int i = 0; i < 4; ++i) x[i] = mul2(mul2(h[j][i], both(r2)), pre[j][i]);
         store_pairs(static_cast<F*>(a.x_out) + row * width, c, j, x);
       }
-      if (a.h_codes) {
-        if (!kWide) {  // the row is read back
+      if (a.f_codes || a.h_codes) {
+        if constexpr (kWide) {
+          keep_row<F, H, NV>(a, row, c, f_raw, out);
+        } else {
           __threadfence_block();
           sync_rows(c.threads);
+          if (a.f_codes)
+            keep_row(static_cast<const F*>(a.f) + row * a.f_stride, row, a.f_codes, a.f_scales, c);
+          if (a.h_codes) keep_row(static_cast<const H*>(a.h_out) + row * width, row, a.h_codes, a.h_scales, c);
         }
-        keep_row<H, NV, kWide>(out, static_cast<const H*>(a.h_out) + row * width, row, a.h_codes,
-                        a.h_scales, c);
       }
       if (!a.post) sync_rows(c.threads);  // one buffer's barrier guards the other's reuse
     }

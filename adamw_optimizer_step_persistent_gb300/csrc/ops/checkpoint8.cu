@@ -47,18 +47,18 @@ __global__ void __launch_bounds__(kThreads)
   x += row0 * x_stride + col;
   codes += row0 * width + col;
   scales += row0 * groups + col / kGroup;
+  const bool group_here = col / kGroup * kGroup < width;
   Raw<E> v[R];
-  int8_t* to[R];
-  float* scale[R];
-  bool valid[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    valid[r] = r < left && col < width;
-    v[r] = valid[r] ? load_raw(x + r * x_stride) : zero_raw<E>();
-    to[r] = codes + r * int64_t(width);
-    scale[r] = scales + r * groups;
-  }
-  keep_vectors<E, R>(v, to, scale, valid);
+  for (int r = 0; r < R; ++r) v[r] = r < left && col < width ? load_raw(x + r * x_stride) : zero_raw<E>();
+  float top[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) top[r] = from_bits<E>(group_top(v[r]));
+  const Scaling shared = share_scaling<R>(top);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    keep_vector(v[r], shared, r, codes + r * int64_t(width), scales + r * groups, r < left && col < width,
+                r < left && group_here);
 }
 
 template <class E, int R>

@@ -207,11 +207,23 @@ __device__ __forceinline__ float from_bits(uint32_t bits) {
 struct Scaling {
   float scale, inverse;
 };
+// a / 127 rounded towards zero: a times the float below 1/127 is at most that
+// and two units short of it; the exact remainder's sign tells whether the next
+// float still fits.
+__device__ __forceinline__ float over_127(float a) {
+  float q = __fmul_rz(a, 0x1.020408p-7f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float next = __uint_as_float(__float_as_uint(q) + 1);
+    q = __fmaf_rn(-127.0f, next, a) >= 0.0f ? next : q;
+  }
+  return q;
+}
 __device__ __forceinline__ Scaling scaling(float a) {
   const bool finite = a < INFINITY, tiny = a < kTinyGroup;
-  const float inverse = __fdiv_rn(127.0f, tiny ? 1.0f : a);
-  return {finite ? tiny ? 0.0f : __fdiv_rz(a, 127.0f) : __uint_as_float(0x7fffffffu),
-          tiny ? 0.0f : finite ? inverse : 0.0f};
+  const float safe = tiny || !finite ? 1.0f : a;
+  return {finite ? tiny ? 0.0f : over_127(safe) : __uint_as_float(0x7fffffffu),
+          tiny || !finite ? 0.0f : __fdiv_rn(127.0f, safe)};
 }
 
 // Eight codes.  x * inverse, rounded, + 1.5 * 2^23 rounds the product to an
@@ -240,36 +252,36 @@ __device__ __forceinline__ uint2 code8(const Raw<E>& r, float inverse) {
   return make_uint2(word[0], word[1]);
 }
 
-// Keeps vectors of N rows (or N vectors of one row) in 8 bits; half a warp
-// holds a group of each.  Every lane of the warp calls it, lanes beyond the
-// row with zeros and valid = false.  The N divisions of a group are shared out
-// over its lanes.  N is a power of two, at most 16.
-template <class E, int N>
-__device__ __forceinline__ void keep_vectors(const Raw<E> (&r)[N], int8_t* const (&codes)[N],
-                                             float* const (&scales)[N], const bool (&valid)[N]) {
-  uint32_t top[N];
+// Vectors of N rows (or N vectors of one row) in 8 bits; half a warp holds a
+// group of each.  group_top() gives every lane the bits of its group's largest
+// magnitude and share_scaling() shares the N groups' divisions out over their
+// lanes; every lane of the warp calls both, lanes beyond the row with zeros.
+// N is a power of two, at most 16; lane n of a group has the n-th one's scaling.
+template <class E>
+__device__ __forceinline__ uint32_t group_top(const Raw<E>& r) {
+  uint32_t top = top_bits(r);
 #pragma unroll
-  for (int n = 0; n < N; ++n) top[n] = top_bits(r[n]);
+  for (int i = 8; i; i /= 2) top = max(top, __shfl_xor_sync(~0u, top, i));
+  return top;
+}
+template <int N>
+__device__ __forceinline__ Scaling share_scaling(const float (&top)[N]) {
+  // top[lane % N], by the lane's bits (an index would put the array in memory)
+  float mine[N];
 #pragma unroll
-  for (int i = 8; i; i /= 2)
+  for (int n = 0; n < N; ++n) mine[n] = top[n];
 #pragma unroll
-    for (int n = 0; n < N; ++n) top[n] = max(top[n], __shfl_xor_sync(~0u, top[n], i));
-  const int lane = threadIdx.x % 16;
-  uint32_t mine = top[0];
+  for (int bit = 1; bit < N; bit *= 2)
 #pragma unroll
-  for (int n = 1; n < N; ++n) mine = lane % N == n ? top[n] : mine;
-  const Scaling s = scaling(from_bits<E>(mine));
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const float inverse = __shfl_sync(~0u, s.inverse, n, 16);
-    if (valid[n]) *reinterpret_cast<uint2*>(codes[n]) = code8(r[n], inverse);
-  }
-  // lane n of the group has the scale of its n-th vector
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const bool first_valid = __shfl_sync(~0u, int(valid[n]), 0, 16);
-    if (lane == n && first_valid) *scales[n] = s.scale;
-  }
+    for (int n = 0; n < N; n += 2 * bit) mine[n] = threadIdx.x & bit ? mine[n + bit] : mine[n];
+  return scaling(mine[0]);
+}
+template <class E>
+__device__ __forceinline__ void keep_vector(const Raw<E>& r, const Scaling& shared, int n, int8_t* codes,
+                                            float* scale, bool valid, bool group_valid) {
+  const float inverse = __shfl_sync(~0u, shared.inverse, n, 16);
+  if (valid) *reinterpret_cast<uint2*>(codes) = code8(r, inverse);
+  if (threadIdx.x % 16 == n && group_valid) *scale = shared.scale;
 }
 
 // A warp keeps one group [col0, col0 + 128) of a row, element by element.
