@@ -326,6 +326,26 @@ def test_weight_grad_strides_and_leading_dimensions():
     _check_wgrad(fadam.checkpoint8_weight_grad(dy3, k), dy3, k)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,N,D", [(64, 512, 512), (200, 2304, 2064), (1, 300, 4096), (4097, 1000, 1040),
+                                   (1027, 4096, 4112), (2500, 8192, 256), (9000, 257, 400), (640, 256, 16)])
+def test_weight_grad_takes_codes_wherever_they_lie(T, N, D, dtype):
+    """The codes' alignment decides how they are read, not what is computed."""
+    g = _gen(T + N)
+    dy = _rand(g, T, N).to(dtype)
+    k = fadam.checkpoint8(_rand(g, T, D).to(dtype))
+    k.scales[T // 2] *= 37.5
+    moved = torch.empty(T * D + 1, dtype=torch.int8, device="cuda")[1:].view(T, D)
+    moved.copy_(k.codes)
+    other = k._replace(codes=moved)
+    for out in (dtype, F32):
+        a, b = (torch.empty(N, D, dtype=out, device="cuda") for _ in range(2))
+        fadam.checkpoint8_weight_grad(dy, k, out=a)
+        fadam.checkpoint8_weight_grad(dy, other, out=b)
+        assert torch.equal(a, b)
+    _check_wgrad(a, dy, k)
+
+
 def test_weight_grad_no_rows():
     k = fadam.checkpoint8(torch.empty(0, 24, dtype=BF16, device="cuda"))
     dy = torch.empty(0, 16, dtype=BF16, device="cuda")
