@@ -5,7 +5,7 @@
 // CTAs stay and take runs of rows, so that the parameters are read once (and,
 // backward, the sums over rows of their gradients stay with the thread that
 // owns the columns).  A row is spread over the CTA, 16 columns to a thread
-// (32 beyond 8192).  Where rows are whole aligned words, one thread copies the
+// (32 beyond 8192).  Where rows are whole aligned words, a few threads copy the
 // coming rows' tensors into a ring of stages in shared memory with bulk
 // copies, so that the loads in flight do not depend on how many warps the
 // registers allow; elsewhere, and when each CTA has one row only, threads load
@@ -13,7 +13,7 @@
 // stage has been read.  Up to 4096 columns two and more CTAs share an SM, which
 // hides their reductions' latency in one another.  Backward, 16384 x 4096 in
 // bf16 from checkpoints: 121 us, 5.3 TB/s; forward, 8192 x 4096 with both
-// checkpoints: 75 us, 4.5 TB/s.  What is left over memory is the issue of some
+// checkpoints: 66 us, 5.1 TB/s.  What is left over memory is the issue of some
 // 40 instructions an element (half the slots) by the 16 warps that 128
 // registers a thread leave an SM, and a row's two or one reductions.
 //

@@ -20,8 +20,8 @@ struct ChunkGrid {
   unsigned ctas;
 };
 // Four rows to a thread where that still leaves every SM eight CTAs of work,
-// else one: 8192 x 11008 in bf16 are packed in 46.8 us (5.8 TB/s) and restored
-// in 40.7 (6.7 TB/s) with four rows, 70.4 and 51.8 us with one.
+// else one: 8192 x 11008 in bf16 are packed in 43.4 us (6.3 TB/s) and restored
+// in 40.6 (6.7 TB/s) with four rows, 63.8 and 51.7 us with one.
 ChunkGrid chunk_grid(int64_t rows, int64_t width) {
   ChunkGrid g;
   const int64_t vectors = ceil_div(width, 8);
