@@ -6,10 +6,11 @@
 // (256 x fewer where that fills the last wave of tiles better) with
 // tcgen05.mma.cta_group::2: each CTA keeps 128 rows of A and half the tile's
 // rows of B per step of 64 in k, so a step moves 32 KB per SM where a CTA of
-// its own would move 48 KB for 128 x 256.  Warps of a CTA: eight for the epilogue, one
-// that issues the bulk copies, one that issues the tensor-core work (in the
-// pair's first CTA).  The accumulators, two of 128 lanes x 256 columns, fill
-// the tensor memory: a tile's epilogue runs under the next tile's products.
+// its own would move 48 KB for 128 x 256.  Warps of a CTA: eight for the
+// epilogue, one for each operand's bulk copies, one that issues the tensor-core
+// work (in the pair's first CTA).  The accumulators, two of 128 lanes x 256
+// columns, fill the tensor memory: a tile's epilogue runs under the next tile's
+// products.
 //
 // Bound by the tensor cores, and they by the card's power: 2048 x 4096 x 32000
 // in 280 to 300 us, 1.8 to 1.9 PFLOP/s, with the tensor pipe active 94 to 97%
@@ -133,7 +134,7 @@ inline GemmShape gemm_shape(int64_t m, int64_t n, int64_t k, const GemmPlan& pla
   s.b_box = plan.tile_n / 2;
   // Over 4096 of k, lse is off by 1.5e-6 of itself with one chunk, 3.5e-7 with
   // chunks of 16 steps, 6e-8 with four.  One row of tiles waits for memory and
-  // four cost it nothing; 2048 x 32000 logits take 302, 307 and 337 us.
+  // four cost it nothing; 2048 x 32000 logits take 277, 278 and 306 us.
   s.chunk = s.m_tiles == 1 ? 4 : 16;
   s.status = status;
   return s;
