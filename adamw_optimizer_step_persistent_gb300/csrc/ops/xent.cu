@@ -7,11 +7,11 @@
 // logit: a piece of (most often) 128 of a row's logits is reduced in registers to its
 // maximum and its sum of exponentials, and (for the gradients) its
 // exponentials relative to that maximum are kept in 16 bits.  Then a row's
-// pieces are joined to its lse, the kept exponentials are turned into dz in
-// place, and two more products give dx and dW: 6 T V D operations where a
-// second computation of the logits would make it 8.  The kept exponentials
-// are those of a chunk of rows, so the scratch memory is bounded however many
-// rows there are.
+// pieces are joined to its largest logit and its sum of exponentials, the kept
+// ones are turned into dz in place, and two more products give dx and dW:
+// 6 T V D operations where a second computation of the logits would make it 8.
+// The kept exponentials are those of a chunk of rows, so the scratch memory is
+// bounded however many rows there are.
 //
 // Roundings to 16 bits: the exponentials are kept in fp16 whatever the
 // inputs' type (they are in [0, 1]; 2^-12 relative down to 6e-5 of the piece's
@@ -104,6 +104,7 @@ struct RowArgs {
   int64_t first_row, all_rows;   // of this chunk, and of the whole call
   const float2* stats;
   const float* target_z;
+  float2* joined;                // [rows]: the row's largest logit, and its sum of exponentials
   const int64_t* targets;        // of the whole call
   int64_t ignore_index;
   float loss_scale;
@@ -158,12 +159,15 @@ __global__ void __launch_bounds__(kRowThreads) lse_kernel(const __grid_constant_
 #pragma unroll
     for (int i = 16; i; i /= 2) sum += __shfl_xor_sync(~0u, sum, i);
     if (lane == 0) {
-      const float lse = base + logf(sum);
       const int64_t target = a.targets[a.first_row + row];
-      a.lse[a.first_row + row] = lse;
-      // a target outside the vocabulary shows as NaN in the loss and the gradients
+      a.joined[row] = make_float2(base, sum);
+      const float log_sum = logf(sum);
+      a.lse[a.first_row + row] = base + log_sum;
+      // not lse - z: lse is rounded to a unit of its own size (10^-3 at 12800), which
+      // can be more than a confident row's whole loss; dz has base and sum for the
+      // same reason.  A target outside the vocabulary shows as NaN in both.
       a.row_loss[a.first_row + row] = target == a.ignore_index                ? 0.0f
-                                      : target >= 0 && target < a.vocab ? lse - a.target_z[row]
+                                      : target >= 0 && target < a.vocab ? (base - a.target_z[row]) + log_sum
                                                                               : NAN;
       __threadfence();
     }
@@ -246,8 +250,8 @@ __global__ void __launch_bounds__(kRowThreads) dz_kernel(const __grid_constant__
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u)
       if (begin + tid + u * kRowThreads < vectors) raw[u] = dz[begin + tid + u * kRowThreads];
-    const float lse = a.lse[a.first_row + row];
-    const float scale = valid ? a.dz_scale : NAN;
+    const float2 joined = a.joined[row];
+    const float scale = valid ? a.dz_scale / joined.y : NAN;
     const int target_vector = valid ? int(target / 8) : -1;
     // vector c lies in piece c / per_piece; both advance with c
     const int per_piece = a.piece / 8;
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kRowThreads) dz_kernel(const __grid_constant__
       for (int u = 0; u < kRowUnroll; ++u) {
         const int c = first + u * kRowThreads;
         if (c < vectors) {
-          const float f = scale * exp2f((st[piece].x - lse) * 1.4426950408889634f);
+          const float f = scale * exp2f((st[piece].x - joined.x) * 1.4426950408889634f);
           const uint32_t w[4] = {now[u].x, now[u].y, now[u].z, now[u].w};
           uint32_t out[4];
 #pragma unroll
@@ -319,6 +323,7 @@ struct Layout {
   Control* control;
   float2* stats;
   float* target_z;
+  float2* joined;
   void* kept;
   void* kept_x;
   void* x_rows;   // aligned copies, where the caller's rows are not
@@ -358,6 +363,7 @@ Layout layout(const fadam_xent& d, char* base, int sm_count) {
   l.control = static_cast<Control*>(c.take(sizeof(Control)));
   l.stats = static_cast<float2*>(c.take(sizeof(float2) * l.chunk * l.pieces));
   l.target_z = static_cast<float*>(c.take(sizeof(float) * l.chunk));
+  l.joined = static_cast<float2*>(c.take(sizeof(float2) * l.chunk));
   if (grads) l.kept = c.take(2 * l.chunk * l.pitch);
   if (d.grad_w) l.kept_x = c.take(2 * l.chunk * l.width_ld);
   if (!bulk_readable(d.x, d.x_stride)) l.x_rows = c.take(2 * d.rows * l.width_ld);
@@ -426,6 +432,7 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     r.all_rows = d.rows;
     r.stats = l.stats;
     r.target_z = l.target_z;
+    r.joined = l.joined;
     r.targets = d.targets;
     r.ignore_index = d.ignore_index;
     r.loss_scale = d.loss_scale;
