@@ -9,8 +9,16 @@
 // its own would move 48 KB for 128 x 256.  Warps of a CTA: eight for the
 // epilogue, one for each operand's bulk copies, one that issues the tensor-core
 // work (in the pair's first CTA).  The accumulators, two of 128 lanes x 256
-// columns, fill the tensor memory: a tile's epilogue runs under the next tile's
-// products.
+// columns, fill the tensor memory: while one is filled, the epilogue's warps
+// read the other.
+//
+// The tensor cores' fp32 additions truncate: each of the k / 16 of a sum loses
+// half a unit of the sum so far on average, always towards zero.  Whole sums
+// were off by 2.5e-4 of themselves over 40000 terms of one sign and by 5e-4 over
+// 131072.  So they add only a chunk of some 1024 of k, and the epilogue's warps
+// add the chunks in registers, rounded to nearest, under the next chunk's
+// products: 2048 x 4096 x 32000 with both gradients takes 1 to 3% longer, the
+// weight gradient of 8192 x 4096 x 11008 none.
 //
 // Bound by the tensor cores, and they by the card's power: 2048 x 4096 x 32000
 // in 280 to 300 us, 1.8 to 1.9 PFLOP/s, with the tensor pipe active 94 to 97%
@@ -37,7 +45,12 @@ constexpr int kOperandBytes = 128 * kTileK * 2;  // one operand of one stage in 
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpilogueWarps = 8;
 constexpr int kLoadA = kEpilogueWarps, kLoadB = kLoadA + 1, kMultiply = kLoadA + 2;  // the other warps
-constexpr int kGemmThreads = (kEpilogueWarps + 3) * 32;
+constexpr int kGemmThreads = (kEpilogueWarps + 4) * 32;  // whole groups of four warps; one is idle
+// Registers of a thread: 168 as launched (384 threads in 65536); the epilogue's
+// warps, which hold 128 sums each, take over what the other four do without.
+constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 224, kOtherRegisters = 56;
+static_assert(2 * kEpilogueRegisters + kOtherRegisters == 3 * kLaunchRegisters, "no more than launched with");
+static_assert(kEpilogueWarps == 8 && kLaunchRegisters * kGemmThreads <= 65536, "an SM's registers");
 constexpr int kPiece = 128;  // most columns of a tile that one epilogue warp takes
 constexpr int kTmemColumns = 512;
 constexpr int kStagingBytes = 4096;  // of one epilogue warp: 32 rows of 128 bytes
@@ -66,7 +79,7 @@ struct GemmShape {
   int32_t k_steps, steps_per_split;
   int32_t items;
   int32_t a_box, b_box;  // rows of a k-major operand's box
-  int32_t chunk;         // steps of k that a chunked product sums on the tensor cores
+  int32_t chunk;         // steps of k that the tensor cores add up
   int* status;
 };
 
@@ -132,10 +145,9 @@ inline GemmShape gemm_shape(int64_t m, int64_t n, int64_t k, const GemmPlan& pla
   s.items = s.full + (tiles - s.full) * s.splits;
   s.a_box = m < 128 ? int32_t(round_up(m, 8)) : 128;
   s.b_box = plan.tile_n / 2;
-  // Over 4096 of k, lse is off by 1.5e-6 of itself with one chunk, 3.5e-7 with
-  // chunks of 16 steps, 6e-8 with four.  One row of tiles waits for memory and
-  // four cost it nothing; 2048 x 32000 logits take 277, 278 and 306 us.
-  s.chunk = s.m_tiles == 1 ? 4 : 16;
+  // 16 steps, or as many as make even chunks of about that (17 steps are one
+  // chunk, not 16 and one)
+  s.chunk = int32_t(ceil_div(s.steps_per_split, s.steps_per_split < 24 ? 1 : (s.steps_per_split + 8) / 16));
   s.status = status;
   return s;
 }
@@ -252,15 +264,12 @@ struct GemmPiece {
   uint32_t acc_empty;  // the accumulator's barrier, in the pair's first CTA
   uint32_t staging;    // shared address
 
-  // 16, or a multiple of 32, columns from column c of this lane's row.
+  // The columns from column c of this lane's row, those below `columns`.
   template <int N>
-  __device__ __forceinline__ void load(int c, float (&v)[N]) const {
-    if constexpr (N == 16) {
-      tmem_load16(tmem + c, v);
-    } else {
+  __device__ __forceinline__ void load(int c, int columns, float (&v)[N]) const {
 #pragma unroll
-      for (int i = 0; i < N; i += 32) tmem_load32(tmem + c + i, v + i);
-    }
+    for (int i = 0; i < N; i += 32)
+      if (c + i < columns) tmem_load32(tmem + c + i, v + i);
     tmem_wait<N>(v);
   }
   // The accumulator has been read.
@@ -304,14 +313,9 @@ __device__ __forceinline__ void emit_rows(const float (&v)[8 * kPerUnit], const 
 }
 
 // Epi: begin() is called by one thread of the launch at its start.
-// operator()(const GemmPiece&) is called by whole warps, loads the piece, and
-// calls release() once.  With kChunked the tensor cores sum only `chunk` steps
-// of k at a time and the epilogue's warps add the chunks, in fp32 rounded to
-// nearest, and hand the piece's sums over: operator()(const GemmPiece&, float
-// (&)[kPiece]).  (The tensor cores' additions truncate: each of the 256 that a
-// sum over 4096 takes loses half a unit in the last place of the sum so far,
-// on average.)  (Rows beyond m and columns from `width` on hold
-// nothing of the product.)
+// operator()(const GemmPiece&, float (&)[kPiece]) is called by whole warps with
+// a piece's sums, a lane's row each.  (Rows beyond m and columns from `width` on
+// hold nothing of the product.)
 template <class T, bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -345,59 +349,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) epi.begin();
 
-  if (warp == kLoadA) {
-    if (lane == 0) load_loop<A_MN>(shape, &map_a, bars, tiles, true, A_MN ? 128 : shape.a_box, rank);
-  } else if (warp == kLoadB) {
-    if (lane == 0) load_loop<B_MN>(shape, &map_b, bars, tiles + kOperandBytes, false, shape.b_box, rank);
-  } else if (warp == kMultiply) {
-    if (rank == 0 && lane == 0) {
-      constexpr uint32_t kType = T::code == FADAM_DT_BF16 ? 1 : 0;
-      // fp32 result, operand types, which operands are not k-major, the tile
-      const uint32_t idesc = 1u << 4 | kType << 7 | kType << 10 | uint32_t(A_MN) << 15 |
-                             uint32_t(B_MN) << 16 | uint32_t(shape.tile_n / 8) << 17 |
-                             uint32_t(kTileM / 16) << 24;
-      // 16 of k further on: 32 bytes of a row, or 16 rows
-      constexpr uint64_t a_step = A_MN ? (16 * 128) >> 4 : 32 >> 4;
-      constexpr uint64_t b_step = B_MN ? (16 * 128) >> 4 : 32 >> 4;
-      int stage = 0, tile = 0;
-      unsigned parity = 0;
-      bool ok = true;
-      for (int item = pair; ok && item < shape.items; item += pairs, ++tile) {
-        int step0;
-        const int steps = gemm_steps(shape, item, step0);
-        int acc = 0, left = 0;  // left: steps of the accumulator's chunk
-        for (int i = 0; i < steps; ++i, --left) {
-          const bool fresh = left == 0;
-          if (fresh) {  // the next accumulator
-            if (i > 0) {
-              commit_pair(shared_addr(&bars->acc_full[acc]));
-              ++tile;
+  if (warp >= kEpilogueWarps) {
+    keep_registers<kOtherRegisters>();
+    if (warp == kLoadA) {
+      if (lane == 0) load_loop<A_MN>(shape, &map_a, bars, tiles, true, A_MN ? 128 : shape.a_box, rank);
+    } else if (warp == kLoadB) {
+      if (lane == 0) load_loop<B_MN>(shape, &map_b, bars, tiles + kOperandBytes, false, shape.b_box, rank);
+    } else if (warp == kMultiply) {
+      if (rank == 0 && lane == 0) {
+        constexpr uint32_t kType = T::code == FADAM_DT_BF16 ? 1 : 0;
+        // fp32 result, operand types, which operands are not k-major, the tile
+        const uint32_t idesc = 1u << 4 | kType << 7 | kType << 10 | uint32_t(A_MN) << 15 |
+                               uint32_t(B_MN) << 16 | uint32_t(shape.tile_n / 8) << 17 |
+                               uint32_t(kTileM / 16) << 24;
+        // 16 of k further on: 32 bytes of a row, or 16 rows
+        constexpr uint64_t a_step = A_MN ? (16 * 128) >> 4 : 32 >> 4;
+        constexpr uint64_t b_step = B_MN ? (16 * 128) >> 4 : 32 >> 4;
+        int stage = 0, tile = 0;
+        unsigned parity = 0;
+        bool ok = true;
+        for (int item = pair; ok && item < shape.items; item += pairs, ++tile) {
+          int step0;
+          const int steps = gemm_steps(shape, item, step0);
+          int acc = 0, left = 0;  // left: steps of the accumulator's chunk
+          for (int i = 0; i < steps; ++i, --left) {
+            const bool fresh = left == 0;
+            if (fresh) {  // the next accumulator
+              if (i > 0) {
+                commit_pair(shared_addr(&bars->acc_full[acc]));
+                ++tile;
+              }
+              left = shape.chunk;
+              acc = tile & 1;
+              ok = bar_wait(shared_addr(&bars->acc_empty[acc]), (unsigned(tile >> 1) & 1) ^ 1, shape.status);
+              if (!ok) break;
+              fence_after_sync();
             }
-            left = Epi::kChunked ? shape.chunk : steps;
-            acc = tile & 1;
-            ok = bar_wait(shared_addr(&bars->acc_empty[acc]), (unsigned(tile >> 1) & 1) ^ 1, shape.status);
+            ok = bar_wait(shared_addr(&bars->full[stage]), parity, shape.status);
             if (!ok) break;
             fence_after_sync();
-          }
-          ok = bar_wait(shared_addr(&bars->full[stage]), parity, shape.status);
-          if (!ok) break;
-          fence_after_sync();
-          const uint32_t a = tiles + stage * kStageBytes;
-          const uint64_t da = operand_desc<A_MN>(a), db = operand_desc<B_MN>(a + kOperandBytes);
+            const uint32_t a = tiles + stage * kStageBytes;
+            const uint64_t da = operand_desc<A_MN>(a), db = operand_desc<B_MN>(a + kOperandBytes);
 #pragma unroll
-          for (int k = 0; k < kTileK / 16; ++k)
-            mma_pair(tmem + acc * kTileN, da + k * a_step, db + k * b_step, idesc, !fresh || k > 0);
-          commit_pair(shared_addr(&bars->empty[stage]));
-          if (++stage == kStages) {
-            stage = 0;
-            parity ^= 1;
+            for (int k = 0; k < kTileK / 16; ++k)
+              mma_pair(tmem + acc * kTileN, da + k * a_step, db + k * b_step, idesc, !fresh || k > 0);
+            commit_pair(shared_addr(&bars->empty[stage]));
+            if (++stage == kStages) {
+              stage = 0;
+              parity ^= 1;
+            }
           }
+          if (!ok) break;
+          commit_pair(shared_addr(&bars->acc_full[acc]));
         }
-        if (!ok) break;
-        commit_pair(shared_addr(&bars->acc_full[acc]));
       }
     }
   } else {
+    take_registers<kEpilogueRegisters>();
     const int quarter = warp % 4, half = warp / 4, half_n = shape.tile_n / 2;
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + half * half_n;
     GemmPiece at;
@@ -422,30 +430,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         at.acc_empty = map_rank(shared_addr(&bars->acc_empty[acc]), 0);
         return ok;
       };
-      if constexpr (Epi::kChunked) {
-        float v[kPiece];
+      float v[kPiece];
 #pragma unroll
-        for (int i = 0; i < kPiece; ++i) v[i] = 0.0f;
-        for (int c = 0; c < it.steps && next_acc(); c += shape.chunk) {
-          if (here) {
+      for (int i = 0; i < kPiece; ++i) v[i] = 0.0f;
+      next_acc();
+      if (here && ok) at.load(0, half_n, v);
+      at.release();
+      for (int c = shape.chunk; c < it.steps && ok && next_acc(); c += shape.chunk) {
+        if (here) {
 #pragma unroll
-            for (int g = 0; g < kPiece; g += 16)
-              if (g < half_n) {
-                float t[16];
-                at.load(g, t);
+          for (int g = 0; g < kPiece; g += 32)
+            if (g < half_n) {
+              float t[32];
+              at.load(g, half_n, t);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[g + i] += t[i];
-              }
-          }
-          at.release();
+              for (int i = 0; i < 32; ++i) v[g + i] += t[i];
+            }
         }
-        if (here && ok) epi(at, v);
-      } else if (next_acc()) {
-        if (here)
-          epi(at);
-        else
-          at.release();
+        at.release();
       }
+      if (here && ok) epi(at, v);
     }
   }
   __syncwarp();

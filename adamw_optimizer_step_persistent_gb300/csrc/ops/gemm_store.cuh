@@ -45,100 +45,159 @@ struct StoreEpilogue {
   float* parts;  // fp32 [slots, split_rows(m), tile_n]: sums of split tiles, joined by join_kernel
   int tile_n;
 
-  static constexpr bool kChunked = false;
   __device__ __forceinline__ void begin() const {}
-  __device__ __forceinline__ void operator()(const GemmPiece& at) const {
+  __device__ __forceinline__ void operator()(const GemmPiece& at, float (&v)[kPiece]) const {
     const int64_t row = at.row0 + threadIdx.x % 32;
     const bool sums = at.slot >= 0 || s.write_carry;
     const bool zero = !sums && row < s.m && s.masked(row);
     const float f = sums ? 1.0f : s.factor();
     if (sizeof(Out) == 2 && !sums && !s.read_carry && !s.accumulate) {
       Out* out = static_cast<Out*>(s.out) + at.row0 * s.ld + at.col;
-#pragma unroll 1
-      for (int c = 0; c < at.width; c += 64) {
-        float v[64];
-        at.load(c, v);
-        if (c + 64 >= at.width) at.release();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) v[i] = zero ? 0.0f : v[i] * f;
+      for (int c = 0; c < kPiece; c += 64) {
+        if (c >= at.width) break;
+        float (&e)[64] = reinterpret_cast<float (&)[64]>(v[c]);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) e[i] = zero ? 0.0f : e[i] * f;
         if (s.wide && s.n % 8 == 0)
           emit_rows<8>(
-              v, at, c, s.m,
+              e, at, c, s.m,
               [](const float* p) {
                 return make_uint4(pack2<Half>(p[0], p[1]), pack2<Half>(p[2], p[3]),
                                   pack2<Half>(p[4], p[5]), pack2<Half>(p[6], p[7]));
               },
               [&](int r, int col, uint4 u) { *reinterpret_cast<uint4*>(out + r * s.ld + col) = u; });
         else
-          store_elements(v, at, c);
+          store_elements(e, at, c);
       }
       return;
     }
     float* part = at.slot < 0 ? nullptr
                               : parts + at.slot * split_rows(s.m) * tile_n + int64_t(at.tile_row) * tile_n +
                                     at.tile_col;
-#pragma unroll 1
-    for (int c = 0; c < at.width; c += 32) {
-      float v[32];
-      at.load(c, v);
-      if (c + 32 >= at.width) at.release();
+#pragma unroll
+    for (int c = 0; c < kPiece; c += 32) {
+      if (c >= at.width) break;
+      float (&e)[32] = reinterpret_cast<float (&)[32]>(v[c]);
       if (zero)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-      emit_rows<4>(
-          v, at, c, s.m,
-          [](const float* p) {
-            return make_uint4(__float_as_uint(p[0]), __float_as_uint(p[1]), __float_as_uint(p[2]),
-                              __float_as_uint(p[3]));
-          },
-          [&](int r, int col, uint4 u) {
-            if (part)
-              *reinterpret_cast<uint4*>(part + r * tile_n + col) = u;
-            else
-              finish4(at.row0 + r, at.col + col,
-                      make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                  __uint_as_float(u.w)), f);
-          });
+        for (int i = 0; i < 32; ++i) e[i] = 0.0f;
+      finish_rows(e, at, c, f, part);
     }
   }
 
-  // Four columns of a whole sum: add what is carried; carry on, or scale, add
-  // what is there, round, store.
-  __device__ __forceinline__ void finish4(int64_t row, int64_t col, float4 v, float f) const {
-    if (s.read_carry || s.write_carry) {
-      float4* carry = reinterpret_cast<float4*>(s.carry + row * scratch_ld(s.n) + col);
+  // 32 columns of a warp's sums, from column c of its piece: into the split
+  // tile's part, or added to what is carried and carried on, or scaled, added
+  // to what is there, rounded and stored.  Through the staging memory as in
+  // emit_rows.  All old values are on their way before the first is used and
+  // before the first store, which might alias the next load: eight round trips
+  // to memory for a tile in place of 32.
+  __device__ __forceinline__ void finish_rows(const float (&v)[32], const GemmPiece& at, int c, float f,
+                                              float* part) const {
+    const int lane = threadIdx.x % 32, u = lane % 8, r0 = lane / 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      store_shared(at.staging + (lane * 8 + (i ^ (lane & 7))) * 16,
+                   make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                              __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+    __syncwarp();
+    const auto staged = [&](int i) {  // the unit of row 4 i + r0
+      const int r = i * 4 + r0;
+      return at.staging + (r * 8 + (u ^ (r & 7))) * 16;
+    };
+    const int left = c + u * 4 < at.width ? int(min(int64_t(32), s.m - at.row0)) : 0;
+    const int64_t row = at.row0 + r0, col = at.col + c + u * 4;
+    if (part) {
+      part += r0 * tile_n + c + u * 4;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * 4 + r0 < left) *reinterpret_cast<uint4*>(part + i * 4 * tile_n) = load_shared(staged(i));
+    } else {
+      const int64_t carry_ld = scratch_ld(s.n);
+      float4* carry = reinterpret_cast<float4*>(s.carry + row * carry_ld + col);
+      float4 old[8];
       if (s.read_carry) {
-        const float4 o = *carry;
-        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 4 + r0 < left) old[i] = carry[i * carry_ld];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 4 + r0 < left) {
+            const float4 sum = add4(as_float4(load_shared(staged(i))), old[i]);
+            store_shared(staged(i), make_uint4(__float_as_uint(sum.x), __float_as_uint(sum.y),
+                                               __float_as_uint(sum.z), __float_as_uint(sum.w)));
+          }
       }
       if (s.write_carry) {
-        *carry = v;
-        return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 4 + r0 < left) carry[i * carry_ld] = as_float4(load_shared(staged(i)));
+      } else {
+        Out* out = static_cast<Out*>(s.out) + row * s.ld + col;
+        const int columns = int(min(int64_t(4), s.n - col));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          old[i] = s.accumulate && i * 4 + r0 < left ? load4(out + i * 4 * s.ld, columns)
+                                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 4 + r0 < left)
+            store4(out + i * 4 * s.ld, fma4(as_float4(load_shared(staged(i))), f, old[i]), columns);
       }
     }
-    const float e[4] = {v.x, v.y, v.z, v.w};
+    __syncwarp();
+  }
+
+  // The same for four columns of a whole sum.
+  __device__ __forceinline__ void finish4(int64_t row, int64_t col, float4 v, float f) const {
+    float4* carry = reinterpret_cast<float4*>(s.carry + row * scratch_ld(s.n) + col);
+    if (s.read_carry) v = add4(v, *carry);
+    if (s.write_carry) {
+      *carry = v;
+      return;
+    }
     Out* out = static_cast<Out*>(s.out) + row * s.ld + col;
-    const int left = int(min(int64_t(4), s.n - col));
-    if (s.wide && left == 4) {
+    const int columns = int(min(int64_t(4), s.n - col));
+    const float4 old = s.accumulate ? load4(out, columns) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    store4(out, fma4(v, f, old), columns);
+  }
+
+  static __device__ __forceinline__ float4 as_float4(uint4 u) {
+    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+  }
+  static __device__ __forceinline__ float4 fma4(float4 a, float f, float4 b) {
+    return make_float4(fmaf(a.x, f, b.x), fmaf(a.y, f, b.y), fmaf(a.z, f, b.z), fmaf(a.w, f, b.w));
+  }
+  // Up to four neighbouring elements of out.
+  __device__ __forceinline__ float4 load4(const Out* at, int columns) const {
+    if (s.wide && columns == 4) {
       if constexpr (sizeof(Out) == 4) {
-        float4* to = reinterpret_cast<float4*>(out);
-        const float4 o = s.accumulate ? *to : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        *to = make_float4(e[0] * f + o.x, e[1] * f + o.y, e[2] * f + o.z, e[3] * f + o.w);
+        return *reinterpret_cast<const float4*>(at);
       } else {
-        uint2* to = reinterpret_cast<uint2*>(out);
-        float2 a = make_float2(0.0f, 0.0f), b = a;
-        if (s.accumulate) {
-          const uint2 old = *to;
-          a = unpack2<Out>(old.x);
-          b = unpack2<Out>(old.y);
-        }
-        *to = make_uint2(pack2<Out>(e[0] * f + a.x, e[1] * f + a.y),
-                         pack2<Out>(e[2] * f + b.x, e[3] * f + b.y));
+        const uint2 u = *reinterpret_cast<const uint2*>(at);
+        const float2 a = unpack2<Out>(u.x), b = unpack2<Out>(u.y);
+        return make_float4(a.x, a.y, b.x, b.y);
       }
+    }
+    float e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = i < columns ? to_float(at[i]) : 0.0f;
+    return make_float4(e[0], e[1], e[2], e[3]);
+  }
+  __device__ __forceinline__ void store4(Out* at, float4 v, int columns) const {
+    if (s.wide && columns == 4) {
+      if constexpr (sizeof(Out) == 4)
+        *reinterpret_cast<float4*>(at) = v;
+      else
+        *reinterpret_cast<uint2*>(at) = make_uint2(pack2<Out>(v.x, v.y), pack2<Out>(v.z, v.w));
     } else {
+      const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < left) out[i] = from_float<Out>(e[i] * f + (s.accumulate ? to_float(out[i]) : 0.0f));
+        if (i < columns) at[i] = from_float<Out>(e[i]);
     }
   }
 

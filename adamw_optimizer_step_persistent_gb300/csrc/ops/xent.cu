@@ -41,8 +41,6 @@ struct LogitEpilogue {
   int64_t pitch;
   Control* control;
 
-  static constexpr bool kChunked = true;  // logits to (nearly) fp32's own accuracy
-
   __device__ __forceinline__ void begin() const { control->finished = 0; }
   __device__ __forceinline__ void operator()(const GemmPiece& p, float (&v)[kPiece]) const {
     const int64_t row = p.row0 + threadIdx.x % 32;
@@ -413,6 +411,10 @@ fadam_status run(const fadam_xent& d, const Layout& l, const DeviceFacts& dev, c
     const bool last_chunk = first + rows == d.rows;
     CUtensorMap map;
     GemmShape shape = gemm_shape(rows, d.vocab, d.width, l.logits, dev.status);
+    // Over 4096 of k, lse is off by 1.5e-6 of itself with one chunk, 3.5e-7 with
+    // chunks of 16 steps, 6e-8 with four.  One row of tiles waits for memory and
+    // four cost it nothing; 2048 x 32000 logits take 277, 278 and 306 us.
+    shape.chunk = shape.m_tiles == 1 ? 4 : 16;
     if ((st = matrix_map(&map, x + first * x_ld, rows, d.width, x_ld, box_rows(false, shape.a_box))))
       return st;
     LogitEpilogue epi{rows, l.pieces, l.logits.tile_n / 2, d.targets + first, l.stats, l.target_z,

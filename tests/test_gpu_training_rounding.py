@@ -61,3 +61,62 @@ def test_xent_confident_row_at_large_logits(dtype, x0, step):
     limit = p * (2.0 ** -11 + 2.0 ** -18) + 2.0 ** -25 + U[dtype] * want.abs() + 2.0 ** -40
     limit[317] = off + 2.0 ** -24 + U[dtype] * want[317].abs() + 2.0 ** -40
     assert (far <= limit).all(), float((far / limit).max())
+
+
+# ---- long sums of one sign ---------------------------------------------------------------
+
+# A chunk of a sum is at most 23 steps of 64 terms, 92 additions of 16 terms on the
+# tensor cores, each of which may lose two units of the sum so far (the addends'
+# alignment and the result's); the chunks are added in fp32, rounded to nearest.
+def _sum_off(terms):
+    return (2 * 92 + -(-terms // 768) / 2 + 2) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_weight_grad_sums_long_columns(dtype):
+    T, N, D = 40000, 1024, 4864             # 76 whole tiles: no split along the rows
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = (torch.rand(T, N, generator=g, device="cuda") + 0.5).to(dtype)
+    # groups whose largest element is 127: scales of 1, whole numbers
+    x = torch.randint(64, 127, (T, D), generator=g, device="cuda").to(dtype)
+    x[:, ::128] = 127
+    k = fadam.checkpoint8(x)
+    assert torch.equal(k.codes, x.to(torch.int8))
+    out = torch.empty(N, D, dtype=F32, device="cuda")
+    fadam.checkpoint8_weight_grad(dy, k, out=out)
+    want = dy.double().t() @ x.double()
+    far = (out.double() - want).abs() / want
+    assert far.max() <= _sum_off(T), float(far.max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_xent_sums_long_columns(dtype):
+    T, D, V = 16384, 4864, 1024             # dW: 76 whole tiles, 16384 rows
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.exp(2 * torch.randn(T, D, generator=g, device="cuda")).clamp(max=1000).to(dtype)
+    w = torch.zeros(V, D, dtype=dtype, device="cuda")
+    y = torch.zeros(T, dtype=torch.int64, device="cuda")
+    gw = torch.empty(V, D, dtype=F32, device="cuda")
+    fadam.linear_cross_entropy(x, w, y, reduction="sum", grad_weight=gw)
+    # every probability is 2^-10: dz is exact
+    want = x.double().sum(0) * 2.0 ** -10
+    far = (gw[1:].double() - want).abs() / want
+    assert far.max() <= _sum_off(T) + 2.0 ** -23, float(far.max())
+
+
+def test_xent_sums_long_rows():
+    T, D, V = 1024, 4864, 131072            # dx: 76 whole tiles, 131072 entries
+    g = torch.Generator(device="cuda").manual_seed(3)
+    size = torch.rand(D, generator=g, device="cuda") + 1.0
+    w = (torch.rand(V, D, generator=g, device="cuda") * size).to(F16)
+    w[0] = 0.0
+    x = torch.zeros(T, D, dtype=F16, device="cuda")
+    y = torch.zeros(T, dtype=torch.int64, device="cuda")
+    r = fadam.linear_cross_entropy(x, w, y, reduction="sum")
+    want = torch.stack([w[:, i:i + 256].double().mean(0) for i in range(0, D, 256)]).view(-1)
+    far = (r.grad_x.double() - want) / want
+    assert far.abs().max() <= U[F16] + _sum_off(V)
+    # the outputs' own rounding, to nearest, averages out over the columns: 2^-11 in
+    # 4864 independent ones, six standard deviations of a uniform error
+    assert far[0].mean().abs() <= _sum_off(V) + 6 * 2.0 ** -11 / 3 ** 0.5 / D ** 0.5, float(far[0].mean())
+    assert torch.equal(r.grad_x, r.grad_x[:1].expand_as(r.grad_x))
