@@ -103,7 +103,7 @@ SIGNATURES = [
 # ---- the training operators (fadam_ops.h) ----------------------------------------
 
 XENT_MEAN, XENT_ACCUMULATE = 1, 2
-WGRAD_ACCUMULATE = 1
+WGRAD_ACCUMULATE, WGRAD_WIDE_X = 1, 4
 CHECKPOINT8_GROUP = 128
 BLOCK_NORM_MAX_WIDTH = 16384
 

@@ -61,12 +61,39 @@ __global__ void __launch_bounds__(kThreads)
                 r < left && group_here);
 }
 
-template <class E, int R>
-__global__ void __launch_bounds__(kThreads)
-    restore_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
-                   int64_t x_stride, int chunks) {
+// What a checkpoint is divided by, and its product multiplied by, so that fp16
+// can hold the largest element: a power of two, 1 where it can without.
+struct Range {
+  unsigned peak;  // bits of the largest finite scale
+  float undo;     // written by restore_*_kernel
+};
+__global__ void __launch_bounds__(kThreads) peak_kernel(const float* scales, int64_t n, Range* range) {
   chain_wait();
   chain_next();
+  unsigned top = 0;
+  const int64_t step = int64_t(gridDim.x) * kThreads;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += step) {
+    const float s = fabsf(scales[i]);
+    if (s < INFINITY) top = max(top, __float_as_uint(s));
+  }
+  top = __reduce_max_sync(~0u, top);
+  if (threadIdx.x % 32 == 0) atomicMax(&range->peak, top);
+}
+// 2^-e with 127 peak 2^-e below 2^15, at most 1.  (The first thread leaves 2^e.)
+__device__ __forceinline__ float fit_range(Range* range) {
+  const float peak = __uint_as_float(range->peak);
+  const int e = peak < 256.0f ? 0 : ilogbf(peak) - 7;
+  if (blockIdx.x == 0 && threadIdx.x == 0) range->undo = ldexpf(1.0f, e);
+  return ldexpf(1.0f, -e);
+}
+
+template <class E, int R, bool kFit>
+__global__ void __launch_bounds__(kThreads)
+    restore_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
+                   int64_t x_stride, int chunks, Range* range) {
+  chain_wait();
+  chain_next();
+  const float fit = kFit ? fit_range(range) : 1.0f;
   const unsigned block = blockIdx.x / unsigned(chunks);
   const int col = int((blockIdx.x - block * chunks) * blockDim.x + threadIdx.x) * 8;
   if (col >= width) return;
@@ -88,7 +115,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int r = 0; r < R; ++r)
     if (r < left) {
       Pair v[4];
-      codes_pairs(raw[r], scale[r], v);
+      codes_pairs(raw[r], kFit ? scale[r] * fit : scale[r], v);
       store_raw(x + r * x_stride, narrow<E>(v));
     }
 }
@@ -108,18 +135,19 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <class E>
+template <class E, bool kFit>
 __global__ void __launch_bounds__(kThreads)
     restore_any_kernel(const int8_t* codes, const float* scales, int64_t rows, int width, E* x,
-                       int64_t x_stride) {
+                       int64_t x_stride, Range* range) {
   chain_wait();
   chain_next();
+  const float fit = kFit ? fit_range(range) : 1.0f;
   const int groups = (width + kGroup - 1) / kGroup;
   const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
   for (int64_t i = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; i < rows * groups; i += warps) {
     const int64_t row = i / groups;
     const int group = int(i - row * groups);
-    const float scale = scales[i];
+    const float scale = kFit ? scales[i] * fit : scales[i];
 #pragma unroll
     for (int k = 0; k < kGroup / 32; ++k) {
       const int col = group * kGroup + k * 32 + threadIdx.x % 32;
@@ -148,9 +176,9 @@ fadam_status pack(const void* x, int64_t rows, int64_t width, int64_t stride,
                         stream, from, rows, int(width), stride, out.codes, out.scales, g.chunks);
 }
 
-template <class E>
+template <class E, bool kFit = false>
 fadam_status restore(const fadam_checkpoint8& in, int64_t rows, int64_t width, void* x,
-                     int64_t stride, cudaStream_t stream) {
+                     int64_t stride, cudaStream_t stream, Range* range = nullptr) {
   const bool wide = width % 8 == 0 && !misaligned(x, 16) && stride * sizeof(E) % 16 == 0 &&
                     !misaligned(in.codes, 8);
   const char* what = "checkpoint8 restore launch";
@@ -158,11 +186,12 @@ fadam_status restore(const fadam_checkpoint8& in, int64_t rows, int64_t width, v
   const int8_t* codes = in.codes;
   const float* scales = in.scales;
   if (!wide)
-    return launch_chained(what, restore_any_kernel<E>, any_grid(rows, width), kThreads, 0, stream, codes,
-                          scales, rows, int(width), to, stride);
+    return launch_chained(what, restore_any_kernel<E, kFit>, any_grid(rows, width), kThreads, 0, stream,
+                          codes, scales, rows, int(width), to, stride, range);
   const ChunkGrid g = chunk_grid(rows, width);
-  return launch_chained(what, g.unroll == 4 ? restore_kernel<E, 4> : restore_kernel<E, 1>, g.ctas,
-                        g.threads, 0, stream, codes, scales, rows, int(width), to, stride, g.chunks);
+  return launch_chained(what, g.unroll == 4 ? restore_kernel<E, 4, kFit> : restore_kernel<E, 1, kFit>,
+                        g.ctas, g.threads, 0, stream, codes, scales, rows, int(width), to, stride, g.chunks,
+                        range);
 }
 
 fadam_status check_matrix(const void* x, int64_t rows, int64_t width, int64_t stride, int32_t dtype,
@@ -189,6 +218,7 @@ struct Layout {
   int64_t x_ld, dy_ld;
   void* x;        // the restored checkpoint
   void* dy_rows;  // an aligned copy of dy, where its own rows are not
+  Range* range;   // where X may be beyond fp16's range
   float* parts;
   size_t bytes;
 };
@@ -204,6 +234,8 @@ Layout layout(const fadam_wgrad& d, char* base, int sm_count) {
     l.dy_ld = round_up(d.n, 8);
     l.dy_rows = c.take(2 * d.rows * l.dy_ld);
   }
+  if (d.dtype == FADAM_DT_F16 && (d.flags & FADAM_WGRAD_WIDE_X))
+    l.range = static_cast<Range*>(c.take(sizeof(Range)));
   if (const size_t parts = split_bytes(d.n, l.plan)) l.parts = static_cast<float*>(c.take(parts));
   l.bytes = c.used;
   return l;
@@ -230,7 +262,22 @@ fadam_status run(const fadam_wgrad& d, const Layout& l, const DeviceFacts& dev, 
       return st;
     dy = l.dy_rows;
   }
-  if ((st = restore<E>(d.x, d.rows, d.width, l.x, l.x_ld, stream))) return st;
+  if constexpr (T::code == FADAM_DT_F16) {
+    if (d.flags & FADAM_WGRAD_WIDE_X) {
+      const cudaError_t e = cudaMemsetAsync(l.range, 0, sizeof(Range), stream);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+      const int64_t scales = d.rows * ceil_div(d.width, kGroup), ctas = ceil_div(scales, 8 * kThreads);
+      if ((st = launch_chained("peak launch", peak_kernel, ctas < 8 * dev.sm_count ? ctas : 8 * dev.sm_count,
+                               kThreads, 0, stream, static_cast<const float*>(d.x.scales), scales, l.range)))
+        return st;
+      st = restore<E, true>(d.x, d.rows, d.width, l.x, l.x_ld, stream, l.range);
+    } else {
+      st = restore<E>(d.x, d.rows, d.width, l.x, l.x_ld, stream);
+    }
+  } else {
+    st = restore<E>(d.x, d.rows, d.width, l.x, l.x_ld, stream);
+  }
+  if (st) return st;
   CUtensorMap a, b;
   if ((st = matrix_map(&a, dy, d.rows, d.n, l.dy_ld, box_rows(true, 0)))) return st;
   if ((st = matrix_map(&b, l.x, d.rows, d.width, l.x_ld, box_rows(true, 0)))) return st;
@@ -240,6 +287,7 @@ fadam_status run(const fadam_wgrad& d, const Layout& l, const DeviceFacts& dev, 
   s.m = d.n;
   s.n = d.width;
   s.constant = 1.0f;
+  if (l.range) s.scale = &l.range->undo;
   s.accumulate = (d.flags & FADAM_WGRAD_ACCUMULATE) != 0;
   s.wide = wide_stores(d.out, d.out_stride, sizeof(typename Out::type));
   const GemmShape shape = gemm_shape(d.n, d.width, d.rows, l.plan, dev.status);
@@ -251,7 +299,8 @@ fadam_status check(const fadam_wgrad* d) {
   if (!is_16bit(d->dtype)) return fail(FADAM_EDTYPE, "dtype %d is not bf16 or fp16", d->dtype);
   if (d->out_dtype != d->dtype && d->out_dtype != FADAM_DT_F32)
     return fail(FADAM_EDTYPE, "out dtype %d is neither fp32 nor dy's %d", d->out_dtype, d->dtype);
-  if (d->flags & ~FADAM_WGRAD_ACCUMULATE) return fail(FADAM_EINVAL, "unknown flag bits 0x%x", d->flags);
+  if (d->flags & ~(FADAM_WGRAD_ACCUMULATE | FADAM_WGRAD_WIDE_X))
+    return fail(FADAM_EINVAL, "unknown flag bits 0x%x", d->flags);
   const fadam_status st = check_matrix(d->dy, d->rows, d->n, d->dy_stride, d->dtype, &d->x);
   if (st) return st;
   if (d->width < 1 || d->out_stride < d->width)

@@ -278,6 +278,8 @@ def checkpoint8_weight_grad(grad_y: torch.Tensor, c: Checkpoint8, *,
     _check_device(index, "grad_y", c.codes, out)
     rows, n, stride = _rows(grad_y, "grad_y")
     width = c.codes.shape[-1]
+    # fp16 operands end at 65504; what was kept from fp16 is below that
+    wide = grad_y.dtype is torch.float16 and c.dtype is not torch.float16
     if out is not None and (out.shape != (n, width)
                             or out.dtype not in (grad_y.dtype, torch.float32)):
         raise ValueError(f"out must be [{n}, {width}] of grad_y's dtype or fp32")
@@ -286,7 +288,8 @@ def checkpoint8_weight_grad(grad_y: torch.Tensor, c: Checkpoint8, *,
             out = torch.empty((n, width), dtype=grad_y.dtype, device=grad_y.device)
         desc = _abi.Wgrad(grad_y.data_ptr(), _kept(c), out.data_ptr(), rows, n, width, stride,
                           _rows(out, "out")[2], dtype_code(grad_y.dtype), dtype_code(out.dtype),
-                          _abi.WGRAD_ACCUMULATE if accumulate else 0)
+                          (_abi.WGRAD_ACCUMULATE if accumulate else 0)
+                          | (_abi.WGRAD_WIDE_X if wide else 0))
         lib = _abi.lib()
         ws, at, size = _workspace(lib.fadam_checkpoint8_wgrad_workspace, desc,
                                   "fadam_checkpoint8_wgrad_workspace", grad_y)

@@ -118,12 +118,16 @@ fadam_status fadam_checkpoint8_restore(const fadam_checkpoint8* in, int64_t rows
                                        fadam_stream stream);
 
 #define FADAM_WGRAD_ACCUMULATE 1u /* out is added to, else overwritten */
+#define FADAM_WGRAD_WIDE_X 4u     /* X may hold values beyond dy's range */
 
 /* A linear layer's weight gradient out [n, width] (+)= dy^T X from its
  * output's gradient dy [rows, n] (bf16 or fp16) and the 8-bit checkpoint X
  * [rows, width] of its input.  X's elements are rounded to dy's dtype (the
  * tensor cores' operand); sums are fp32, rounded once to out_dtype (dy's, or
- * fp32).  rows may be 0 (a zero gradient). */
+ * fp32).  rows may be 0 (a zero gradient).  An element of magnitude 65504 or
+ * more would be an infinity in fp16: where X was kept from bf16 or fp32 and dy
+ * is fp16, FADAM_WGRAD_WIDE_X divides X by a power of two that brings its
+ * largest element below 2^15 and multiplies the sums by it. */
 typedef struct {
   const void* dy;
   fadam_checkpoint8 x;

@@ -120,3 +120,27 @@ def test_xent_sums_long_rows():
     # 4864 independent ones, six standard deviations of a uniform error
     assert far[0].mean().abs() <= _sum_off(V) + 6 * 2.0 ** -11 / 3 ** 0.5 / D ** 0.5, float(far[0].mean())
     assert torch.equal(r.grad_x, r.grad_x[:1].expand_as(r.grad_x))
+
+
+# ---- kept values beyond fp16's range -------------------------------------------------------
+
+@pytest.mark.parametrize("kept", [BF16, F32])
+@pytest.mark.parametrize("size", [1.0, 1e6, 1e30])
+def test_weight_grad_of_wide_values_from_fp16(kept, size):
+    T, N, D = 300, 130, 264
+    g = torch.Generator(device="cuda").manual_seed(4)
+    dy = (torch.randn(T, N, generator=g, device="cuda") * 1e-3).to(F16)
+    x = (torch.randn(T, D, generator=g, device="cuda") * size).to(kept)
+    k = fadam.checkpoint8(x)
+    out = torch.empty(N, D, dtype=F32, device="cuda")
+    fadam.checkpoint8_weight_grad(dy, k, out=out)
+    v = k.codes.double() * k.scales.double().repeat_interleave(128, 1)[:, :D]
+    each = dy.double().abs().t() @ v.abs()
+    # values rounded to 11 bits (2^-25 of the largest below its 2^-14th), fp32 sums
+    off = each * (2.0 ** -11 + T * 2.0 ** -23) + dy.double().abs().sum(0)[:, None] * v.abs().max() * 2.0 ** -24
+    far = (out.double() - dy.double().t() @ v).abs()
+    assert (far <= off).all(), float((far / off).max())
+    # a group that is not finite is NaN, and only where it belongs
+    k.scales[7, 1] = float("nan")
+    fadam.checkpoint8_weight_grad(dy, k, out=out)
+    assert torch.isnan(out[:, 128:256]).all() and torch.isfinite(out[:, :128]).all()
