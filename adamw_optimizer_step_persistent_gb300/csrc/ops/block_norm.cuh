@@ -529,8 +529,11 @@ template <class Args>
 fadam_status launch_norm(void (*kernel)(Args), const Args& a, int threads, size_t smem,
                          cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024)  // beyond 48 KB, static arrays included, it has to be asked for
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // Beyond 48 KB, static arrays included, it has to be asked for: always as much as
+  // any launch takes, because the limit is the kernel's, and one that another
+  // thread lowered before this launch would refuse it.
+  if (smem > 40 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kNormSharedBytes));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   return launch_chained("block norm launch", kernel, a.runs.ctas, threads, smem, stream, a);
 }

@@ -8,7 +8,7 @@ namespace fadam_ops {
 
 constexpr int kMaxWarps = 16;  // of a CTA: at 128 registers a thread, an SM's worth
 constexpr int kMaxNormStages = 8;
-// Shared memory of an SM that its CTAs' rings and parameters share.
+// Shared memory of an SM that its CTAs' rings and parameters share; no CTA takes more.
 constexpr size_t kNormSharedBytes = 216 * 1024;
 
 // The tensors that a row's stage in shared memory holds, one after the other.
