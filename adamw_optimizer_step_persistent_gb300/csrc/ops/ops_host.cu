@@ -9,6 +9,10 @@
 
 // Set by a kernel whose bounded wait gave up; read by fadam_ops_status.
 static __device__ int g_ops_status;
+// What fadam_ops_status found there.  Read and cleared in one step: what is set
+// in between by a launch of another thread is left for the next call.
+static __device__ int g_ops_status_taken;
+static __global__ void take_status_kernel() { g_ops_status_taken = atomicExch(&g_ops_status, 0); }
 
 namespace fadam_ops {
 
@@ -100,10 +104,13 @@ extern "C" fadam_status fadam_ops_status(int32_t* device_status) {
   clear_error();
   if (!device_status) return fail(FADAM_EINVAL, "device_status is NULL");
   int word = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&word, g_ops_status, sizeof word);
-  if (e == cudaSuccess && word != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_ops_status, &zero, sizeof zero);
+  // all streams of the device: the default one does not wait for non-blocking ones
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    take_status_kernel<<<1, 1>>>();
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, g_ops_status_taken, sizeof word);
   }
   if (e != cudaSuccess) return cuda_fail(e, "fadam_ops_status");
   *device_status = word;

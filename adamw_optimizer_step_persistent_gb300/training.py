@@ -443,8 +443,9 @@ def block_norm_backward(grad_h_out: Optional[torch.Tensor], grad_x_out: torch.Te
 
 
 def ops_status() -> int:
-    """The training operators' device status (synchronises; clears it):
-    ``_abi.OK``, or ``_abi.ETIMEOUT`` when a bounded device wait gave up."""
+    """The current device's status of the training operators (waits for all its
+    streams; clears it, for every thread): ``_abi.OK``, or ``_abi.ETIMEOUT``
+    when a bounded device wait gave up."""
     st = ctypes.c_int32()
     _abi.check_ops(_abi.lib().fadam_ops_status(ctypes.byref(st)), "fadam_ops_status")
     return st.value

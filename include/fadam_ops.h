@@ -232,9 +232,11 @@ fadam_status fadam_block_norm_backward(const fadam_block_norm_grad* desc, void* 
 
 /* ---- errors ------------------------------------------------------------------- */
 
-/* Read (synchronously) and clear the current device's status word of these
- * operators: *device_status = FADAM_OK, or FADAM_ETIMEOUT when a bounded
- * device wait of some launch since the last read gave up. */
+/* Wait for everything that runs on the current device, on any stream, then
+ * read and clear its status word of these operators: *device_status =
+ * FADAM_OK, or FADAM_ETIMEOUT when a bounded device wait of some launch since
+ * the last read gave up.  The word is one for all threads and streams of the
+ * device: whoever reads it first gets it. */
 fadam_status fadam_ops_status(int32_t* device_status);
 
 /* Message of the last failure of these operators in the calling thread (""

@@ -51,3 +51,14 @@ def test_norms_of_two_widths_from_two_threads():
     loops = body(2048, 1300), body(4096, 700)
     torch.cuda.synchronize()
     _in_threads(*loops)
+
+
+def test_status_waits_for_every_stream():
+    """What is still running on another stream may yet give up a wait."""
+    fadam.ops_status()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)        # some 0.2 s
+        done = side.record_event()
+    assert fadam.ops_status() == 0
+    assert done.query()
