@@ -318,7 +318,7 @@ def _norm_params(width: int, rows: int, block: torch.dtype, pre_weight, post_wei
         raise TypeError("pre_weight, post_weight and gate must have one dtype")
     if gate.dim() < 1 or gate.size(-1) != width or not gate.is_contiguous():
         raise ValueError(f"gate must be a contiguous [..., {width}]")
-    gate_rows = gate.numel() // width
+    gate_rows = gate.numel() // width if width else 0
     if gate_rows < 1 or rows % gate_rows:
         raise ValueError(f"{gate_rows} gate rows do not divide {rows} rows")
     return dtype, gate_rows
