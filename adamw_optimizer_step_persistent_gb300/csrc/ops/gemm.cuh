@@ -8,9 +8,9 @@
 // rows of B per step of 64 in k, so a step moves 32 KB per SM where a CTA of
 // its own would move 48 KB for 128 x 256.  Warps of a CTA: eight for the
 // epilogue, one for each operand's bulk copies, one that issues the tensor-core
-// work (in the pair's first CTA).  The accumulators, two of 128 lanes x 256
-// columns, fill the tensor memory: while one is filled, the epilogue's warps
-// read the other.
+// work (in the pair's first CTA), one that is idle.  The accumulators, two of
+// 128 lanes x 256 columns, fill the tensor memory: while one is filled, the
+// epilogue's warps read the other.
 //
 // The tensor cores' fp32 additions truncate: each of the k / 16 of a sum loses
 // half a unit of the sum so far on average, always towards zero.  Whole sums
@@ -21,10 +21,10 @@
 // weight gradient of 8192 x 4096 x 11008 none.
 //
 // Bound by the tensor cores, and they by the card's power: 2048 x 4096 x 32000
-// in 280 to 300 us, 1.8 to 1.9 PFLOP/s, with the tensor pipe active 94 to 97%
-// of the time at the 1.7 GHz that the power leaves.  A step of 64 in k takes
-// about 550 cycles where the instructions alone take 512; a tile some 1500 more,
-// which shows when k is short (1037 x 1000 x 50021: 16 steps to a tile, 60%).
+// in 285 to 300 us, 1.8 to 1.9 PFLOP/s, 4096 x 11008 x 8192 in 385.  A step of
+// 64 in k takes about 550 cycles where the instructions alone take 512; a tile
+// some 1500 more, which shows when k is short (1037 x 1000 x 50021: 16 steps to
+// a tile, 60%).
 //
 // Either operand may lie in memory with k contiguous ("k-major") or with its
 // own index contiguous (A_MN, B_MN: what a product with a transposed matrix

@@ -14,10 +14,13 @@
 // bounded however many rows there are.
 //
 // Roundings to 16 bits: the exponentials are kept in fp16 whatever the
-// inputs' type (they are in [0, 1]; 2^-12 relative down to 6e-5 of the piece's
-// largest, 3e-8 absolute below that), dz once more in the inputs' type,
-// because the tensor cores take it from there.  fp16 dz is held times 2^15
-// (|dz| <= 1 before s), so that a probability of 1e-8 still has all its bits.
+// inputs' type (they are in [0, 1]; 2^-11 relative down to 6e-5 of the piece's
+// largest, 3e-8 of that largest absolute below), dz once more in the inputs'
+// type, because the tensor cores take it from there.  fp16 dz is held times
+// 2^15 (|dz| <= 1 before s), so that this second rounding leaves a probability
+// of 1e-8 all its bits; the first does so only where its piece's largest is not
+// far above it: beside a logit that dominates the piece, a probability 10^8
+// times smaller is 0.
 // Everything else (products' sums, maxima, sums, lse, loss) is fp32; the
 // factor s is applied to the fp32 sums.
 #include "gemm_store.cuh"

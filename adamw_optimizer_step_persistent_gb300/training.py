@@ -10,6 +10,12 @@ can be captured in a CUDA graph.
 Matrices are given as tensors of any number of dimensions whose last one is
 the row; the leading ones are taken together as rows and must be evenly
 strided (no copy is made).
+
+The functions stand outside autograd: they take tensors that require a
+gradient like any others and return tensors that do not, so in the middle of a
+module they would cut the graph.  Gradients are passed on by the caller, e.g.
+``x.backward(linear_cross_entropy(x, w, y).grad_x)``, or from the ``forward``
+and ``backward`` of a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
@@ -139,9 +145,10 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
     ``x`` [..., width] and ``weight`` [vocab, width] are bf16 or fp16, targets
     [...] int64.  The logits are never held: forward alone needs 8 bytes of
     scratch for 128 of them, with gradients a chunk of rows' exponentials is
-    held in 16 bits (``chunk_rows``; 0 chooses).  ``reduction`` is "mean" over
-    the rows whose target is not ``ignore_index`` (0 when there is none) or
-    "sum".  The gradients are those of ``loss_scale * loss``: an optimizer
+    held in 16 bits (``chunk_rows``; 0: as many as fit 4 GiB).  ``reduction``
+    is "mean" over the rows whose target is not ``ignore_index`` (0 when there
+    is none) or "sum".  Products are cut by the sizes, so a row's last bits can
+    change with the number of rows beside it.  The gradients are those of ``loss_scale * loss``: an optimizer
     shard takes it back out with its grad scale.
 
     ``grad_weight`` is a [vocab, width] buffer of the weight's dtype or fp32,
@@ -263,7 +270,9 @@ def checkpoint8_weight_grad(grad_y: torch.Tensor, c: Checkpoint8, *,
                             accumulate: bool = False) -> torch.Tensor:
     """The weight gradient ``grad_y.T @ x`` [n, width] of a linear layer, from
     its output's gradient [..., n] (bf16 or fp16) and the checkpoint of its
-    input [..., width].  ``out`` is a buffer of grad_y's dtype or fp32, such as
+    input [..., width], whose values are rounded to grad_y's dtype for the
+    product (under fp16, those kept from bf16 or fp32 are brought into range by
+    a power of two first).  ``out`` is a buffer of grad_y's dtype or fp32, such as
     a view of an optimizer shard's gradient; with ``accumulate`` the gradient
     is added to it."""
     _check_checkpoint(c, "c")

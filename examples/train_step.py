@@ -11,8 +11,9 @@ products comes from the library:
   checkpoint8_weight_grad            its weight gradients from those
   linear_cross_entropy               the loss, and the gradients of the last
                                      hidden rows and of the vocabulary's weight
-  FusedAdamShard                     the update: every gradient above was
-                                     written where the shard reads it
+  FusedAdamShard                     the update: the matrices' gradients were
+                                     written (or added) where the shard reads
+                                     them, the norms' vectors are copied there
 
     python examples/train_step.py --steps 30
 """

@@ -22,10 +22,15 @@
  *     another call before this one has run.
  *   - Everything runs on `stream`, a stream of the current device, without
  *     host synchronisation: calls can be captured in a CUDA graph.  Results are deterministic (the same inputs
- *     on the same GPU give the same bits).
+ *     of the same sizes on the same GPU give the same bits).
  *   - Argument checks run on the host before anything is launched; a failing
  *     one returns a status and leaves a message for the calling thread in
  *     fadam_ops_last_error().
+ *   - Sums of matrix products are fp32: chunks of up to 1472 terms on the
+ *     tensor cores, whose additions truncate, and the chunks added rounding to
+ *     nearest, so that sums do not drift with their length.  How they are cut
+ *     follows from the sizes: a row's last bits can change with the number of
+ *     rows beside it.
  *   - No entry point traps on the device.  Device-side waits are bounded; one
  *     that gives up ends its kernel, whose outputs are then undefined, and is
  *     reported by fadam_ops_status().
@@ -48,7 +53,8 @@ extern "C" {
 #define FADAM_XENT_ACCUMULATE 2u /* grad_w is added to, else overwritten */
 
 /* With z = x w^T (never written to memory), lse_t = log sum_v exp(z_tv) and
- * row_loss_t = lse_t - z_t,targets[t] (0 where targets[t] == ignore_index):
+ * row_loss_t = lse_t - z_t,targets[t] (0 where targets[t] == ignore_index; taken
+ * from the row's largest logit, so that it keeps its bits where lse is large):
  *   loss   = sum_t row_loss_t, with FADAM_XENT_MEAN divided by the number of
  *            rows that are not ignored (at least 1: the mean over none is 0)
  *   grad_x = loss_scale * dloss/dx,  grad_w (+)= loss_scale * dloss/dw
@@ -62,8 +68,11 @@ extern "C" {
  *   grad_w [vocab, width]              of grad_w_dtype (`dtype` or fp32), or
  *                                      NULL.  Sums are fp32 and rounded once.
  *   chunk_rows                         rows whose exponentials are held at a
- *                                      time (2 bytes each in the workspace);
+ *                                      time (2 bytes each in the workspace, so
+ *                                      as many bytes as 16-bit logits);
  *                                      0: as many as fit 4 GiB
+ * dz = softmax - target is rounded to `dtype` for the products that give the
+ * gradients, after its exponentials were kept in fp16.
  * rows may be 0.  Operands whose rows do not start on 16 bytes are copied to
  * the workspace first. */
 typedef struct {
