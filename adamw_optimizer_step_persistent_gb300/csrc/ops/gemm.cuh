@@ -17,8 +17,9 @@
 // were off by 2.5e-4 of themselves over 40000 terms of one sign and by 5e-4 over
 // 131072.  So they add only a chunk of some 1024 of k, and the epilogue's warps
 // add the chunks in registers, rounded to nearest, under the next chunk's
-// products: 2048 x 4096 x 32000 with both gradients takes 1 to 3% longer, the
-// weight gradient of 8192 x 4096 x 11008 none.
+// products.  Holding a whole piece there costs 1 to 2% (the weight gradient of
+// 8192 x 4096 x 11008 420 us in place of 412), chunks of 16, 32 or all steps
+// the same.
 //
 // Bound by the tensor cores, and they by the card's power: 2048 x 4096 x 32000
 // in 285 to 300 us, 1.8 to 1.9 PFLOP/s, 4096 x 11008 x 8192 in 385.  A step of
@@ -47,8 +48,9 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kLoadA = kEpilogueWarps, kLoadB = kLoadA + 1, kMultiply = kLoadA + 2;  // the other warps
 constexpr int kGemmThreads = (kEpilogueWarps + 4) * 32;  // whole groups of four warps; one is idle
 // Registers of a thread: 168 as launched (384 threads in 65536); the epilogue's
-// warps, which hold 128 sums each, take over what the other four do without.
-constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 224, kOtherRegisters = 56;
+// warps, which hold 128 sums each, take over what the other four do without
+// (with 224 and 56 the 16-bit instances spill 100 bytes).
+constexpr int kLaunchRegisters = 168, kEpilogueRegisters = 232, kOtherRegisters = 40;
 static_assert(2 * kEpilogueRegisters + kOtherRegisters == 3 * kLaunchRegisters, "no more than launched with");
 static_assert(kEpilogueWarps == 8 && kLaunchRegisters * kGemmThreads <= 65536, "an SM's registers");
 constexpr int kPiece = 128;  // most columns of a tile that one epilogue warp takes

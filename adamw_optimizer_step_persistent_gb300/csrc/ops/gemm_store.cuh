@@ -51,12 +51,16 @@ struct StoreEpilogue {
     const bool sums = at.slot >= 0 || s.write_carry;
     const bool zero = !sums && row < s.m && s.masked(row);
     const float f = sums ? 1.0f : s.factor();
-    if (sizeof(Out) == 2 && !sums && !s.read_carry && !s.accumulate) {
+    if (sizeof(Out) == 2 && !sums && !s.read_carry) {
       Out* out = static_cast<Out*>(s.out) + at.row0 * s.ld + at.col;
 #pragma unroll
       for (int c = 0; c < kPiece; c += 64) {
         if (c >= at.width) break;
         float (&e)[64] = reinterpret_cast<float (&)[64]>(v[c]);
+        if (s.accumulate) {
+          if constexpr (sizeof(Out) == 2) add_rows(e, at, c, zero ? 0.0f : f);
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < 64; ++i) e[i] = zero ? 0.0f : e[i] * f;
         if (s.wide && s.n % 8 == 0)
@@ -148,7 +152,61 @@ struct StoreEpilogue {
     __syncwarp();
   }
 
-  // The same for four columns of a whole sum.
+  // 64 columns of a warp's sums, scaled, added to 16-bit rows: 16 rows at a time
+  // through the staging memory, so that eight lanes have a whole line of a row.
+  __device__ __forceinline__ void add_rows(const float (&v)[64], const GemmPiece& at, int c, float f) const {
+    const int lane = threadIdx.x % 32, u = lane % 8, r0 = lane / 8;
+    const int columns = min(8, at.width - c - u * 8), left = int(min(int64_t(32), s.m - at.row0));
+    Out* out = static_cast<Out*>(s.out) + (at.row0 + r0) * s.ld + at.col + c + u * 8;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half, out += 16 * s.ld) {
+      // unit i of a row (four columns): even ones first, exchanged by row
+      if (lane / 16 == half)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          store_shared(at.staging + (lane % 16 * 16 + ((i % 2 * 8 + i / 2) ^ (lane & 7))) * 16,
+                       make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                  __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+      __syncwarp();
+      uint4 old[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (columns > 0 && half * 16 + i * 4 + r0 < left) old[i] = load8(out + i * 4 * s.ld, columns);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (columns > 0 && half * 16 + i * 4 + r0 < left) {
+          const int r = i * 4 + r0;
+          const uint32_t row = at.staging + r * 256;
+          const float2 w0 = unpack2<Out>(old[i].x), w1 = unpack2<Out>(old[i].y);
+          const float2 w2 = unpack2<Out>(old[i].z), w3 = unpack2<Out>(old[i].w);
+          const float4 a = fma4(as_float4(load_shared(row + (u ^ (r & 7)) * 16)), f,
+                                make_float4(w0.x, w0.y, w1.x, w1.y));
+          const float4 b = fma4(as_float4(load_shared(row + ((8 + u) ^ (r & 7)) * 16)), f,
+                                make_float4(w2.x, w2.y, w3.x, w3.y));
+          store8(out + i * 4 * s.ld, a, b, columns);
+        }
+      __syncwarp();
+    }
+  }
+  __device__ __forceinline__ uint4 load8(const Out* at, int columns) const {
+    if (s.wide && columns == 8) return *reinterpret_cast<const uint4*>(at);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < columns) w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(at)[i]) << (i % 2 * 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store8(Out* at, float4 a, float4 b, int columns) const {
+    if (s.wide && columns == 8) {
+      *reinterpret_cast<uint4*>(at) = make_uint4(pack2<Out>(a.x, a.y), pack2<Out>(a.z, a.w),
+                                                 pack2<Out>(b.x, b.y), pack2<Out>(b.z, b.w));
+    } else {
+      store4(at, a, min(4, columns));
+      store4(at + 4, b, columns - 4);
+    }
+  }
+
+  // finish_rows for four columns of a whole sum.
   __device__ __forceinline__ void finish4(int64_t row, int64_t col, float4 v, float f) const {
     float4* carry = reinterpret_cast<float4*>(s.carry + row * scratch_ld(s.n) + col);
     if (s.read_carry) v = add4(v, *carry);
