@@ -467,6 +467,14 @@ template <class T, bool A_MN, bool B_MN, class Epi>
 fadam_status launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const GemmShape& shape,
                          const Epi& epi, int sm_count, cudaStream_t stream) {
   auto* kernel = gemm_kernel<T, A_MN, B_MN, Epi>;
+  // a kernel built with fewer would wait for its share of registers for ever
+  static const int registers = [&] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : -1;
+  }();
+  if (registers != kLaunchRegisters)
+    return fail(FADAM_ECUDA, "the matrix product was built with %d registers a thread, not %d", registers,
+                kLaunchRegisters);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              int(kGemmSmem));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");

@@ -102,3 +102,30 @@ def test_xent_one_gradient_without_the_other(dtype, chunk):
         assert L.fadam_xent_run(d, ws.data_ptr(), need.value, stream) == _abi.OK
         assert torch.equal(out, want.grad_x if wants_x else want.grad_weight)
         assert torch.equal(loss[0], want.loss) and torch.equal(rows, want.row_loss) and torch.equal(lse, want.lse)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D,cols,c0", [(96, 128, 8), (96, 101, 3), (203, 216, 8), (520, 520, 0), (333, 333, 0)])
+def test_gradients_added_to_a_view(D, cols, c0, dtype, wide):
+    """The view's elements are added to, and nothing around it is touched."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    for N in (300, 40):
+        base = torch.randn(N + 9, cols, generator=g, device="cuda").to(F32 if wide else dtype)
+        x, w, y = _xent_case(150, D, N, dtype, seed=D)
+        k = fadam.checkpoint8(x)
+        dy = torch.randn(150, N, generator=g, device="cuda").to(dtype)
+        for chunk in (0, 64, None):
+            room = base.clone()
+            view = room[4:4 + N, c0:c0 + D]
+            old = view.clone()
+            if chunk is None:
+                fadam.checkpoint8_weight_grad(dy, k, out=view, accumulate=True)
+                v = ref.values(*k[:2])
+                want, off = dy.double().t() @ v, dy.double().abs().t() @ v.abs() * (ref.U[dtype] + 150 * ref.E32)
+                ref.Bounded(want + old.double(), off + ref.E32 * old.double().abs()).holds(view, "out")
+            else:
+                r = fadam.linear_cross_entropy(x, w, y, grad_weight=view, accumulate=True, chunk_rows=chunk)
+                _check_xent(r, x, w, y, mean=True, base=old)
+            view.copy_(old)
+            assert torch.equal(room, base)
