@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/fadam.h and include/fadam_ops.h.
+"""ctypes declarations of the C ABI in include/fadam.h, fadam_ops.h and fadam_seq.h.
 
 Argument marshalling only: every step of the update runs in libfadam.so.
 Loading fails loudly when the library has not been built; there is no
@@ -170,6 +170,59 @@ OPS_SIGNATURES = [
     ("fadam_ops_last_error", ctypes.c_char_p, []),
 ]
 
+
+# ---- the sequence operators (fadam_seq.h) -----------------------------------------
+
+EMBED_PADDING, EMBED_ACCUMULATE = 1, 2
+ATTENTION_CAUSAL = 1
+ATTENTION_MAX_WIDTH = 128
+
+
+class Embed(ctypes.Structure):
+    """fadam_embed."""
+    _fields_ = ([(n, _vp) for n in ("tokens", "weight", "out")]
+                + [(n, _i64) for n in ("rows", "width", "vocab", "weight_stride", "out_stride",
+                                       "padding_index")]
+                + [("scale", _f32), ("weight_dtype", _i32), ("out_dtype", _i32), ("flags", _u32)])
+
+
+class EmbedGrad(ctypes.Structure):
+    """fadam_embed_grad."""
+    _fields_ = ([(n, _vp) for n in ("tokens", "grad", "out")]
+                + [(n, _i64) for n in ("rows", "width", "vocab", "grad_stride", "out_stride",
+                                       "padding_index")]
+                + [("scale", _f32), ("grad_dtype", _i32), ("out_dtype", _i32), ("flags", _u32)])
+
+
+class Attention(ctypes.Structure):
+    """fadam_attention."""
+    _fields_ = ([(n, _vp) for n in ("q", "k", "v", "out", "lse", "slopes", "documents", "prefix")]
+                + [(n, _i64) for n in ("tokens", "sequence", "n_documents", "q_stride", "k_stride",
+                                       "v_stride", "q_head_stride", "k_head_stride",
+                                       "v_head_stride")]
+                + [("heads", _i32), ("kv_heads", _i32), ("width", _i32), ("scale", _f32),
+                   ("softcap", _f32), ("dtype", _i32), ("flags", _u32), ("reserved", _u32)])
+
+
+class AttentionGrad(ctypes.Structure):
+    """fadam_attention_grad."""
+    _fields_ = ([("forward", Attention)]
+                + [(n, _vp) for n in ("grad_out", "grad_q", "grad_k", "grad_v")]
+                + [(n, _i64) for n in ("out_stride", "out_head_stride", "grad_out_stride",
+                                       "grad_out_head_stride")])
+
+
+# (name, restype, argtypes) for every function fadam_seq.h declares
+SEQ_SIGNATURES = [
+    ("fadam_embed_forward", _i32, [ctypes.POINTER(Embed), _vp]),
+    ("fadam_embed_grad_workspace", _i32, [ctypes.POINTER(EmbedGrad), _size]),
+    ("fadam_embed_grad_run", _i32, [ctypes.POINTER(EmbedGrad), _vp, ctypes.c_size_t, _vp]),
+    ("fadam_attention_workspace", _i32, [ctypes.POINTER(Attention), _size]),
+    ("fadam_attention_run", _i32, [ctypes.POINTER(Attention), _vp, ctypes.c_size_t, _vp]),
+    ("fadam_attention_backward_workspace", _i32, [ctypes.POINTER(AttentionGrad), _size]),
+    ("fadam_attention_backward", _i32, [ctypes.POINTER(AttentionGrad), _vp, ctypes.c_size_t, _vp]),
+]
+
 _LIB = None
 
 
@@ -195,7 +248,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it first with "
                 "`python -c 'import __graft_entry__ as g; g.build()'` (no fallback path exists)")
         L = ctypes.CDLL(LIB_PATH)
-        for name, res, args in SIGNATURES + OPS_SIGNATURES:
+        for name, res, args in SIGNATURES + OPS_SIGNATURES + SEQ_SIGNATURES:
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args

@@ -30,6 +30,11 @@ OPS_SOURCES = [f"ops/{f}.cu" for f in ("ops_host", "xent", "checkpoint8", "block
 OPS_HEADERS = [f"ops/{f}" for f in ("ops_internal.h", "ops_device.cuh", "gemm.cuh",
                                     "gemm_store.cuh", "rows.cuh", "block_norm.cuh",
                                     "block_norm_internal.h")]
+# the sequence operators (fadam_seq.h), in the same library
+SEQ_SOURCES = [f"ops/{f}.cu" for f in ("attention", "attention_forward_bf16", "attention_forward_f16",
+                                       "attention_backward_bf16", "attention_backward_f16", "embed")]
+SEQ_HEADERS = [f"ops/{f}" for f in ("attention_internal.h", "attention.cuh", "attention_forward.cuh",
+                                    "attention_backward.cuh")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -49,8 +54,9 @@ def _stale(lib: str) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + OPS_SOURCES + OPS_HEADERS]
-    deps += [os.path.join(INCLUDE, f) for f in ("fadam.h", "fadam_ops.h")]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + OPS_SOURCES + OPS_HEADERS
+            + SEQ_SOURCES + SEQ_HEADERS]
+    deps += [os.path.join(INCLUDE, f) for f in ("fadam.h", "fadam_ops.h", "fadam_seq.h")]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -70,7 +76,7 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib: str = LIB
     extra += [f"-D{d}" for d in defines]
     procs = []
     objs = []
-    for src in OPS_SOURCES + SOURCES:
+    for src in SEQ_SOURCES + OPS_SOURCES + SOURCES:
         obj = os.path.join(out_dir, os.path.splitext(os.path.basename(src))[0] + ".o")
         objs.append(obj)
         cmd = [nvcc, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c",

@@ -1,0 +1,243 @@
+// Device helpers of attention: tensor-core and tensor-memory instructions of a
+// single CTA, boxes of a head's rows, scores and masks.
+#pragma once
+
+#include "attention_internal.h"
+#include "ops_device.cuh"
+
+namespace fadam_ops {
+
+// Registers of a thread: 168 as launched (384 threads in 65536); the eight warps
+// that hold scores take over what the other four do without.
+constexpr int kLaunchRegisters = 168, kScoreRegisters = 224, kOtherRegisters = 56;
+static_assert(2 * kScoreRegisters + kOtherRegisters == 3 * kLaunchRegisters, "no more than launched with");
+// A kernel built with fewer would wait for its share of registers for ever.
+template <auto kKernel>
+fadam_status launched_with(const char* what) {
+  static const int registers = [] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, kKernel) == cudaSuccess ? f.numRegs : -1;
+  }();
+  if (registers == kLaunchRegisters) return FADAM_OK;
+  return fail(FADAM_ECUDA, "%s was built with %d registers a thread, not %d", what, registers, kLaunchRegisters);
+}
+
+constexpr int kBoxBytes = kRows * kChunk * 2;  // 128 rows of 128 bytes, 128-byte swizzle
+
+// ---- copies -----------------------------------------------------------------------------
+
+__device__ __forceinline__ void load_head_box(uint32_t dst, const CUtensorMap* map, int x, int head,
+                                              int token, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(head), "r"(token), "r"(bar)
+      : "memory");
+}
+// 128 tokens of one head, C blocks of 64 elements.
+template <int C>
+__device__ __forceinline__ void load_head(uint32_t dst, const CUtensorMap* map, int head, int token,
+                                          uint32_t bar) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) load_head_box(dst + c * kBoxBytes, map, c * kChunk, head, token, bar);
+}
+__device__ __forceinline__ void store_head_box(const CUtensorMap* map, int x, int head, int token,
+                                               uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(head), "r"(token), "r"(src)
+               : "memory");
+}
+// Waits until this thread's stores have been written.
+__device__ __forceinline__ void wait_stores() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+// What this thread wrote to shared memory is there for bulk copies and tensor cores.
+__device__ __forceinline__ void fence_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// A barrier of a group of warps.
+__device__ __forceinline__ void group_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---- tensor cores ----------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_shared, int columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_shared),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, int columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+
+// D (+)= A B, both 16-bit in shared memory.
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      : "memory");
+}
+// The same with A in tensor memory: a lane to a row, two elements to a column.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      : "memory");
+}
+// Arrive at `bar` once the tensor-core work issued so far by this thread is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// 32 columns of this warp's 32 lanes, stored once tmem_stored() returns.
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_stored() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A tile's block as the operand whose k runs along its rows' elements (k-major:
+// scores), or along the rows themselves (MN: products with v, k, q, grad_out,
+// blocks of 64 elements one box apart).
+template <bool MN>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+  const uint64_t lead = MN ? kBoxBytes >> 4 : 1;
+  return uint64_t((addr & 0x3ffff) >> 4) | lead << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+         uint64_t(2) << 61;
+}
+template <class T, bool B_MN>
+__device__ __forceinline__ uint32_t instruction(int n) {
+  constexpr uint32_t kType = T::code == FADAM_DT_BF16 ? 1 : 0;
+  return 1u << 4 | kType << 7 | kType << 10 | uint32_t(B_MN) << 16 | uint32_t(n / 8) << 17 |
+         uint32_t(kRows / 16) << 24;
+}
+
+// D[128, 128] = A B^T over `steps` 16s of a head's elements.
+template <class T>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, int steps) {
+  const uint64_t da = tile_desc<false>(a), db = tile_desc<false>(b);
+  const uint32_t idesc = instruction<T, false>(kRows);
+  for (int k = 0; k < steps; ++k) {
+    const uint64_t at = (k / 4) * (kBoxBytes >> 4) + (k % 4) * 2;  // 16 elements on: 32 bytes, or the next box
+    mma(d, da + at, db + at, idesc, k > 0);
+  }
+}
+
+// D[128, n] (+)= A B over the tile's 128 rows, A in tensor memory: 64 elements
+// from `a`, 64 from `a2`.
+template <class T>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t a2, uint32_t b, int n, bool add) {
+  const uint64_t db = tile_desc<true>(b);
+  const uint32_t idesc = instruction<T, true>(n);
+#pragma unroll
+  for (int k = 0; k < kRows / 16; ++k)  // 16 rows on: 2048 bytes, 8 columns
+    mma_tmem(d, (k < 4 ? a + k * 8 : a2 + (k - 4) * 8), db + k * (2048 >> 4), idesc, add || k > 0);
+}
+
+// Rows [from, to) of a tile, and no others, hold tokens of documents: the rest
+// become zero, so that 0 times what padding holds is 0.  By a whole warp,
+// between the copy's arrival and the first product.
+template <int C>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to) {
+  for (int r = threadIdx.x % 32; r < kRows; r += 32)
+    if (r < from || r >= to)
+#pragma unroll
+      for (int i = 0; i < 8 * C; ++i)
+        store_shared(tile + (i / 8) * kBoxBytes + r * 128 + (i % 8) * 16, make_uint4(0, 0, 0, 0));
+  fence_shared();
+  __syncwarp();
+}
+
+// ---- masks -----------------------------------------------------------------------------
+
+// The spans of token i of the document [a, b) with a prefix of p tokens.
+__host__ __device__ __forceinline__ Spans spans_in(int i, int a, int b, int p, bool causal) {
+  Spans s{a, b, a, b};
+  if (causal) {
+    s.key_hi = i + 1 > a + p ? i + 1 : a + p;
+    s.query_lo = i < a + p ? a : i;
+  }
+  return s;
+}
+__device__ __forceinline__ Spans spans_of(const AttentionArgs& g, int i) {
+  if (g.spans) {
+    const int4 v = __ldg(reinterpret_cast<const int4*>(g.spans) + i);
+    return Spans{v.x, v.y, v.z, v.w};
+  }
+  const int d = i / g.sequence, a = d * g.sequence;
+  const int p = g.prefix ? min(max(__ldg(g.prefix + d), 0), g.sequence) : 0;
+  return spans_in(i, a, a + g.sequence, p, g.causal);
+}
+
+// What a tile's 128 rows need of the other side, from the spans of its rows
+// that see anything: any of it lies in [lo, hi), all rows see [all_lo, all_hi).
+struct Reach {
+  int lo, hi, all_lo, all_hi;
+  __device__ __forceinline__ int first() const { return lo / kRows; }
+  __device__ __forceinline__ int last() const { return hi > lo ? (hi + kRows - 1) / kRows : lo / kRows; }
+  // whether a tile that starts at `at` needs no mask
+  __device__ __forceinline__ bool whole(int at) const { return all_lo <= at && at + kRows <= all_hi; }
+};
+constexpr int kNever = 0x7fffff80;  // a multiple of 128
+// One warp's part of it; rows that do not exist (`here` false) ask for nothing.
+__device__ __forceinline__ Reach reach_of(int lo, int hi, bool here) {
+  const bool sees = here && lo < hi;
+  Reach r;
+  r.lo = __reduce_min_sync(~0u, sees ? lo : kNever);
+  r.hi = __reduce_max_sync(~0u, sees ? hi : 0);
+  r.all_lo = __reduce_max_sync(~0u, here ? lo : 0);
+  r.all_hi = __reduce_min_sync(~0u, here ? hi : kNever);
+  return r;
+}
+__device__ __forceinline__ Reach join(const Reach& a, const Reach& b) {
+  return Reach{min(a.lo, b.lo), max(a.hi, b.hi), max(a.all_lo, b.all_lo), min(a.all_hi, b.all_hi)};
+}
+
+// ---- scores ------------------------------------------------------------------------------
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float inverse_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Scores in units of log 2, from products q . k.  tanh(y) is
+// 1 - 2 / (exp(2 y) + 1), off by 2^-22 at most, times cap log2 e.
+struct Scores {
+  float mul;         // scale log2 e
+  float cap_in;      // 2 log2 e scale / cap
+  float cap;         // cap log2 e; 0: none
+  float slope;       // slope log2 e; 0: none
+  __device__ __forceinline__ Scores(const AttentionArgs& g, int head) {
+    mul = g.scale * kLog2e;
+    cap = g.softcap * kLog2e;
+    cap_in = g.softcap > 0.0f ? 2.0f * kLog2e * (g.scale / g.softcap) : 0.0f;
+    slope = g.slopes ? __ldg(g.slopes + head) * kLog2e : 0.0f;
+  }
+  // 1 / (exp(2 y) + 1); the capped score is cap - 2 cap of it, the cap's
+  // derivative 4 of it times (1 - it)
+  __device__ __forceinline__ float folded(float s) const {
+    return inverse_fast(exp2_fast(s * cap_in) + 1.0f);
+  }
+};
+
+}  // namespace fadam_ops

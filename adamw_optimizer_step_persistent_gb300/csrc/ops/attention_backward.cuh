@@ -1,0 +1,627 @@
+// Attention, backward: with p = exp(s - lse) and
+//   ds = p (grad_out . v - delta) ds/d(q . k),  delta = grad_out . out,
+//   grad_v_j = sum_i p_ij grad_out_i,  grad_k_j = sum_i ds_ij q_i,
+//   grad_q_i = sum_j ds_ij k_j.
+//
+// Two kernels, each of which keeps one side in shared memory, walks over the
+// other and sums in tensor memory, so that every sum has one order and nothing
+// is added to memory: one takes 128 keys and walks over the queries that see
+// them, of all query heads that share the key head (four products a tile: the
+// transposed scores, grad_out . v, grad_v, grad_k); one takes 128 queries
+// (three products).  Computing the scores twice costs seven products in place
+// of five, where grad_q summed in memory would cost fp32 additions to it from
+// every tile, in the order in which they arrive.
+//
+// Both are pipelined in the same way: eight warps turn scores into p and p into
+// ds (a lane to a row, half the columns to four warps) while the tensor cores
+// do the products of the tile before and the scores of the next one.  p and ds
+// go back to tensor memory in 16 bits, as the A operand of their products.
+// (A warp may be a turn ahead of another one when it has written ds, which is
+// why that has a barrier for even and one for odd turns.)
+#pragma once
+
+#include "attention.cuh"
+
+namespace fadam_ops {
+
+constexpr int kBackwardThreads = 384;  // 8 warps for p and ds, one that multiplies, one that loads, two idle
+// Tiles in flight of what a kernel walks over: X is needed by the scores and by
+// the product with ds, Y by grad_out . v (and the product with p).
+constexpr int kRingX = 3, kRingY = 2;
+// fp16: p is held times 2^10 (the smallest normal number is 2^-14), ds times a
+// power of two that brings grad_out's largest element to [1, 2).
+template <class T>
+constexpr float kLiftBits = T::code == FADAM_DT_F16 ? 10.0f : 0.0f;
+
+struct BackwardBarriers {
+  uint64_t own_full, done;
+  uint64_t x_full[kRingX], x_empty[kRingX], y_full[kRingY], y_empty[kRingY];
+  uint64_t scores, dots;        // tensor cores: S, grad_out . v are there
+  uint64_t scores_read, dots_read, weights;          // warps: S and dots read, p written
+  uint64_t slopes[2];                                // ds written, of even and odd turns
+  Reach reach[4];
+  uint32_t tmem;
+};
+struct BackwardExtra {
+  float lse[kRingY][kRows];     // with Y: read for p, before Y is done with
+  float delta[kRingX][kRows];   // with X
+  BackwardBarriers bars;
+};
+template <int C>
+constexpr size_t kBackwardSmem = (2 + kRingX + kRingY) * C * size_t(kBoxBytes) + sizeof(BackwardExtra);
+static_assert(kBackwardSmem<2> <= 227 * 1024, "shared memory of one CTA");
+constexpr int kColumnsS = 0, kColumnsDots = kRows, kColumnsA = 2 * kRows, kColumnsB = 3 * kRows;
+
+// A power of two that brings the largest element of grad_out to [1, 2).
+template <class T>
+__device__ __forceinline__ float ds_factor(const AttentionArgs& g) {
+  if constexpr (T::code != FADAM_DT_F16) return 1.0f;
+  const unsigned bits = *g.peak;
+  if (bits == 0 || bits >= 0x7f800000u) return 1.0f;
+  return ldexpf(1.0f, -ilogbf(__uint_as_float(bits)));
+}
+
+template <class T, int C>
+struct Backward {
+  static constexpr int kTile = C * kBoxBytes;
+  uint32_t own0, own1, x, y;   // shared addresses of the tiles
+  BackwardExtra* extra;
+  BackwardBarriers* bars;
+
+  // Sets up barriers and tensor memory.  False when shared memory does not
+  // start on 1024 bytes, as the swizzle needs.
+  __device__ __forceinline__ bool begin(unsigned char* smem, const AttentionArgs& g) {
+    own0 = shared_addr(smem);
+    if (own0 & 1023) {
+      if (threadIdx.x == 0) atomicExch(g.status, FADAM_ECUDA);
+      return false;
+    }
+    own1 = own0 + kTile;
+    x = own1 + kTile;
+    y = x + kRingX * kTile;
+    extra = reinterpret_cast<BackwardExtra*>(smem + (2 + kRingX + kRingY) * kTile);
+    bars = &extra->bars;
+    if (threadIdx.x == 0) {
+      bar_init(shared_addr(&bars->own_full), 1);
+      bar_init(shared_addr(&bars->done), 1);
+      for (int i = 0; i < kRingX; ++i) {
+        bar_init(shared_addr(&bars->x_full[i]), 1);
+        bar_init(shared_addr(&bars->x_empty[i]), 1);
+      }
+      for (int i = 0; i < kRingY; ++i) {
+        bar_init(shared_addr(&bars->y_full[i]), 1);
+        bar_init(shared_addr(&bars->y_empty[i]), 1);
+      }
+      bar_init(shared_addr(&bars->scores), 1);
+      bar_init(shared_addr(&bars->dots), 1);
+      bar_init(shared_addr(&bars->scores_read), 8);
+      bar_init(shared_addr(&bars->dots_read), 8);
+      bar_init(shared_addr(&bars->weights), 8);
+      bar_init(shared_addr(&bars->slopes[0]), 8);
+      bar_init(shared_addr(&bars->slopes[1]), 8);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x / 32 == 8) tmem_alloc(shared_addr(&bars->tmem), 512);
+    return true;
+  }
+
+  // What the 128 rows of the CTA need: rows are dealt to the first four warps.
+  __device__ __forceinline__ Reach meet(int lo, int hi, bool here) {
+    const int warp = threadIdx.x / 32;
+    if (warp < 4) {
+      const Reach r = reach_of(lo, hi, here);
+      if (threadIdx.x % 32 == 0) bars->reach[warp] = r;
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    return join(join(bars->reach[0], bars->reach[1]), join(bars->reach[2], bars->reach[3]));
+  }
+
+  __device__ __forceinline__ uint32_t x_at(int i) const { return x + i % kRingX * kTile; }
+  __device__ __forceinline__ uint32_t y_at(int i) const { return y + i % kRingY * kTile; }
+  __device__ __forceinline__ bool wait_x(int i, int* status) const {
+    return bar_wait(shared_addr(&bars->x_full[i % kRingX]), unsigned(i / kRingX) & 1, status);
+  }
+  __device__ __forceinline__ bool wait_y(int i, int* status) const {
+    return bar_wait(shared_addr(&bars->y_full[i % kRingY]), unsigned(i / kRingY) & 1, status);
+  }
+
+  // The loading thread: the CTA's own two tiles, then X and Y of n turns in
+  // turn.  load_own(dst0, dst1, bar), load_x(i, dst, slot, bar), load_y(...).
+  template <class Own, class X, class Y>
+  __device__ __forceinline__ void load_loop(int n, int x_extra, int y_extra, int* status, Own load_own,
+                                            X load_x, Y load_y) const {
+    bool ok = true;
+    const uint32_t own = shared_addr(&bars->own_full);
+    bar_expect(own, 2 * kTile);
+    load_own(own0, own1, own);
+    int i = 0;
+    for (; i < n; ++i) {
+      const int sx = i % kRingX, sy = i % kRingY;
+      if (i >= kRingX) ok = bar_wait(shared_addr(&bars->x_empty[sx]), unsigned(i / kRingX - 1) & 1, status);
+      if (!ok) break;
+      uint32_t bar = shared_addr(&bars->x_full[sx]);
+      bar_expect(bar, kTile + x_extra);
+      load_x(i, x_at(i), sx, bar);
+      if (i >= kRingY) ok = bar_wait(shared_addr(&bars->y_empty[sy]), unsigned(i / kRingY - 1) & 1, status);
+      if (!ok) break;
+      bar = shared_addr(&bars->y_full[sy]);
+      bar_expect(bar, kTile + y_extra);
+      load_y(i, y_at(i), sy, bar);
+    }
+    // no copy is in flight when the CTA ends
+    bar_wait(own, 0, status);
+    for (int k = i < kRingX ? 0 : i - kRingX; k < i; ++k) wait_x(k, status);
+    for (int k = i < kRingY ? 0 : i - kRingY; k < i; ++k) wait_y(k, status);
+  }
+};
+
+// 64 columns of scores of a lane's row become p (times 2^lift) and, in place,
+// p times ds/d(q . k).  `apart`: the first column's place less the row's;
+// subtract(c): the column's (or row's) lse in units of log 2.  Columns outside
+// [lo, hi) are not seen.
+template <class E, class Lse>
+__device__ __forceinline__ void weights_of(float (&s)[64], uint32_t (&p)[32], const Scores& f, float apart,
+                                           bool whole, int lo, int hi, Lse lse) {
+  const float mul = f.cap != 0.0f ? 1.0f : f.mul;
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    float w[2], d[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float z = s[c + k];
+      d[k] = 1.0f;
+      if (f.cap != 0.0f) {
+        const float r = f.folded(z);
+        z = fmaf(-2.0f * f.cap, r, f.cap);
+        d[k] = 4.0f * r * (1.0f - r);
+      }
+      z = fmaf(z, mul, -lse(c + k));
+      if (f.slope != 0.0f) z = fmaf(-f.slope, fabsf(apart + float(c + k)), z);
+      w[k] = exp2_fast(z);
+      if (!whole) w[k] = c + k >= lo && c + k < hi ? w[k] : 0.0f;
+    }
+    p[c / 2] = pack2<E>(w[0], w[1]);
+    s[c] = w[0] * d[0];
+    s[c + 1] = w[1] * d[1];
+  }
+}
+
+// ---- grad_k and grad_v: 128 keys, a walk over queries --------------------------------------
+
+struct KeyMaps {
+  CUtensorMap q, k, v, grad_out, grad_k, grad_v;
+};
+
+template <class T, int C>
+__global__ void __launch_bounds__(kBackwardThreads, 1)
+    attention_keys_kernel(const __grid_constant__ KeyMaps maps, const __grid_constant__ AttentionArgs g) {
+  using E = typename T::type;
+  using B = Backward<T, C>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  B b;
+  if (!b.begin(smem, g)) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  BackwardBarriers* bars = b.bars;
+  int* status = g.status;
+  chain_wait();
+
+  // the first keys first: under a causal mask most queries see them
+  const unsigned kv_heads = unsigned(g.heads / g.group), columns = kv_heads * g.splits;
+  const int tile = int(blockIdx.x / columns), rest = int(blockIdx.x % columns);
+  const int kv = rest / g.splits, split = rest % g.splits;
+  const int share = g.group / g.splits, head0 = kv * g.group + split * share;
+  const int key0 = tile * kRows;
+  const int row = threadIdx.x % kRows;  // of the first eight warps: a lane's key
+  Spans span{};
+  if (warp < 8 && key0 + row < g.tokens) span = spans_of(g, key0 + row);
+  const Reach reach = b.meet(span.query_lo, span.query_hi, key0 + row < g.tokens);
+  const uint32_t tmem = bars->tmem;
+  const int first = reach.first(), turns = reach.last() - first, n = turns * share;
+  const auto query_tile = [&](int i) { return first + i % turns; };
+
+  if (warp >= 8) keep_registers<kOtherRegisters>();
+  if (warp >= 10) {
+  } else if (warp == 9) {
+    if (lane == 0 && n > 0) {
+      const int64_t pitch = int64_t(g.tiles) * kRows;
+      const float* lse = g.stats;
+      const float* delta = g.stats + pitch * g.heads;
+      b.load_loop(
+          n, kRows * 4, kRows * 4, status,
+          [&](uint32_t k, uint32_t v, uint32_t bar) {
+            load_head<C>(k, &maps.k, kv, key0, bar);
+            load_head<C>(v, &maps.v, kv, key0, bar);
+          },
+          [&](int i, uint32_t dst, int slot, uint32_t bar) {
+            const int head = head0 + i / turns, at = query_tile(i) * kRows;
+            load_head<C>(dst, &maps.q, head, at, bar);
+            load_bytes(shared_addr(b.extra->delta[slot]), delta + head * pitch + at, kRows * 4, bar);
+          },
+          [&](int i, uint32_t dst, int slot, uint32_t bar) {
+            const int head = head0 + i / turns, at = query_tile(i) * kRows;
+            load_head<C>(dst, &maps.grad_out, head, at, bar);
+            load_bytes(shared_addr(b.extra->lse[slot]), lse + head * pitch + at, kRows * 4, bar);
+          });
+    }
+  } else if (warp == 8) {
+    if (n > 0) {
+      const int steps = (g.width + 15) / 16, width = steps * 16;
+      int inside_lo = 0, inside_hi = g.tiles * kRows;
+      if (g.documents) {
+        inside_lo = __ldg(g.documents);
+        inside_hi = __ldg(g.documents + g.n_documents);
+      }
+      const auto clean = [&](uint32_t at, int i) {
+        const int from = query_tile(i) * kRows;
+        if (from < inside_lo || from + kRows > inside_hi) zero_rows<C>(at, inside_lo - from, inside_hi - from);
+      };
+      const auto scores = [&](int i) {
+        if (!b.wait_x(i, status)) return false;
+        fence_after_sync();
+        clean(b.x_at(i), i);
+        if (lane == 0) {
+          mma_scores<T>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
+          commit(shared_addr(&bars->scores));
+        }
+        return true;
+      };
+      const auto dots = [&](int i) {
+        if (!b.wait_y(i, status)) return false;
+        fence_after_sync();
+        clean(b.y_at(i), i);
+        if (lane == 0) {
+          mma_scores<T>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
+          commit(shared_addr(&bars->dots));
+        }
+        return true;
+      };
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && scores(0) && dots(0);
+      for (int i = 0; ok && i < n; ++i) {
+        ok = bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
+        if (!ok) break;
+        fence_after_sync();
+        if (lane == 0) {
+          mma_rows<T>(tmem + kColumnsA, tmem + kColumnsS, tmem + kColumnsS + 64, b.y_at(i), width, i > 0);
+          commit(shared_addr(&bars->y_empty[i % kRingY]));
+        }
+        if (i + 1 < n && !(ok = scores(i + 1))) break;
+        ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
+        if (!ok) break;
+        fence_after_sync();
+        if (lane == 0) {
+          mma_rows<T>(tmem + kColumnsB, tmem + kColumnsDots, tmem + kColumnsDots + 64, b.x_at(i), width, i > 0);
+          commit(shared_addr(&bars->x_empty[i % kRingX]));
+        }
+        if (i + 1 < n) ok = dots(i + 1);
+      }
+      if (ok && lane == 0) commit(shared_addr(&bars->done));
+    }
+  } else {
+    take_registers<kScoreRegisters>();
+    const int half = warp / 4, quarter = warp % 4;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t at_s = lanes + kColumnsS + half * 64, at_dots = lanes + kColumnsDots + half * 64;
+    const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
+    const uint32_t bar_weights = shared_addr(&bars->weights);
+    const float factor = ds_factor<T>(g) * exp2f(-kLiftBits<T>);
+    bool ok = true;
+    for (int h = 0, i = 0; h < share && ok; ++h) {
+      const Scores f(g, head0 + h);
+      for (int turn = 0; turn < turns; ++turn, ++i) {
+        const int at = (first + turn) * kRows + half * 64;  // the first column's query
+        const bool whole = reach.whole((first + turn) * kRows);
+        const int lo = span.query_lo - at, hi = span.query_hi - at;
+        float s[64];
+        uint32_t p[32];
+        ok = bar_wait(bar_scores, unsigned(i) & 1, status) && b.wait_y(i, status);
+        if (!ok) break;
+        fence_after_sync();
+        tmem_load32(at_s, s);
+        tmem_load32(at_s + 32, s + 32);
+        tmem_wait<64>(s);
+        const float* lse = b.extra->lse[i % kRingY] + half * 64;
+        weights_of<E>(s, p, f, float(at - (key0 + row)), whole, lo, hi, [&](int c) { return lse[c]; });
+        tmem_store32(at_s, p);
+        tmem_stored();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar_weights);
+
+        ok = bar_wait(bar_dots, unsigned(i) & 1, status) && b.wait_x(i, status);
+        if (!ok) break;
+        fence_after_sync();
+        const float* delta = b.extra->delta[i % kRingX] + half * 64;
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          float d[32];
+          tmem_load32(at_dots + c0, d);
+          tmem_wait<32>(d);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float e[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              e[k] = s[c0 + c + k] * (d[c + k] - delta[c0 + c + k]);
+              if (T::code == FADAM_DT_F16) e[k] *= factor;
+              if (!whole) e[k] = c0 + c + k >= lo && c0 + c + k < hi ? e[k] : 0.0f;
+            }
+            p[(c0 + c) / 2] = pack2<E>(e[0], e[1]);
+          }
+        }
+        tmem_store32(at_dots, p);
+        tmem_stored();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) bar_arrive(shared_addr(&bars->slopes[i & 1]));
+      }
+    }
+    // four warps write grad_v (through v's place in shared memory), four grad_k
+    if (n > 0 && ok) ok = bar_wait(shared_addr(&bars->done), 0, status);
+    fence_after_sync();
+    const float scale = half ? g.scale / ds_factor<T>(g) : exp2f(-kLiftBits<T>);
+    const uint32_t from = lanes + (half ? kColumnsB : kColumnsA);
+    const uint32_t tile_at = half ? b.own0 : b.own1;
+    const uint32_t place = tile_at + (quarter * 32 + lane) * 128;
+    float* part = nullptr;
+    if (g.splits > 1)
+      part = g.parts + (((int64_t(split) * 2 + half) * g.tokens + key0 + row) * kv_heads + kv) * g.width;
+#pragma unroll
+    for (int c = 0; c < C * kChunk; c += 32)
+      if (c < g.width) {
+        float o[32];
+        if (n > 0) {
+          tmem_load32(from + c, o);
+          tmem_wait<32>(o);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * scale : 0.0f;
+        if (part) {
+          if (key0 + row < g.tokens)
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              if (c + i < g.width) {
+                reinterpret_cast<float4*>(part + c + i)[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                reinterpret_cast<float4*>(part + c + i)[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+              }
+          continue;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          store_shared(place + c / kChunk * kBoxBytes + (((c % kChunk / 8 + u) ^ (lane & 7)) * 16),
+                       make_uint4(pack2<E>(o[8 * u], o[8 * u + 1]), pack2<E>(o[8 * u + 2], o[8 * u + 3]),
+                                  pack2<E>(o[8 * u + 4], o[8 * u + 5]), pack2<E>(o[8 * u + 6], o[8 * u + 7])));
+      }
+    if (!part) {
+      fence_shared();
+      group_sync(1 + half, 128);
+      if (threadIdx.x % 128 == 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c * kChunk < g.width)
+            store_head_box(half ? &maps.grad_k : &maps.grad_v, c * kChunk, kv, key0, tile_at + c * kBoxBytes);
+        wait_stores();
+      }
+    }
+  }
+  __syncwarp();
+  chain_next();
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+// ---- grad_q: 128 queries, a walk over keys ------------------------------------------------
+
+struct QueryMaps {
+  CUtensorMap q, k, v, grad_out, grad_q;
+};
+
+template <class T, int C>
+__global__ void __launch_bounds__(kBackwardThreads, 1)
+    attention_queries_kernel(const __grid_constant__ QueryMaps maps, const __grid_constant__ AttentionArgs g) {
+  using E = typename T::type;
+  using B = Backward<T, C>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  B b;
+  if (!b.begin(smem, g)) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  BackwardBarriers* bars = b.bars;
+  int* status = g.status;
+  chain_wait();
+
+  const int head = int(blockIdx.x % unsigned(g.heads));
+  const int query0 = (g.tiles - 1 - int(blockIdx.x / unsigned(g.heads))) * kRows;
+  const int row = threadIdx.x % kRows;
+  Spans span{};
+  if (warp < 8 && query0 + row < g.tokens) span = spans_of(g, query0 + row);
+  const Reach reach = b.meet(span.key_lo, span.key_hi, query0 + row < g.tokens);
+  const uint32_t tmem = bars->tmem;
+  const int first = reach.first(), n = reach.last() - first;
+
+  if (warp >= 8) keep_registers<kOtherRegisters>();
+  if (warp >= 10) {
+  } else if (warp == 9) {
+    if (lane == 0 && n > 0) {
+      const int kv = head / g.group;
+      b.load_loop(
+          n, 0, 0, status,
+          [&](uint32_t q, uint32_t go, uint32_t bar) {
+            load_head<C>(q, &maps.q, head, query0, bar);
+            load_head<C>(go, &maps.grad_out, head, query0, bar);
+          },
+          [&](int i, uint32_t dst, int, uint32_t bar) { load_head<C>(dst, &maps.k, kv, (first + i) * kRows, bar); },
+          [&](int i, uint32_t dst, int, uint32_t bar) { load_head<C>(dst, &maps.v, kv, (first + i) * kRows, bar); });
+    }
+  } else if (warp == 8) {
+    if (n > 0) {
+      const int steps = (g.width + 15) / 16, width = steps * 16;
+      int inside_lo = 0, inside_hi = g.tiles * kRows;
+      if (g.documents) {
+        inside_lo = __ldg(g.documents);
+        inside_hi = __ldg(g.documents + g.n_documents);
+      }
+      const auto scores = [&](int i) {
+        if (!b.wait_x(i, status)) return false;
+        fence_after_sync();
+        const int from = (first + i) * kRows;
+        if (from < inside_lo || from + kRows > inside_hi)
+          zero_rows<C>(b.x_at(i), inside_lo - from, inside_hi - from);
+        if (lane == 0) {
+          mma_scores<T>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
+          commit(shared_addr(&bars->scores));
+        }
+        return true;
+      };
+      const auto dots = [&](int i) {
+        if (!b.wait_y(i, status)) return false;
+        fence_after_sync();
+        if (lane == 0) {
+          mma_scores<T>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
+          commit(shared_addr(&bars->dots));
+          commit(shared_addr(&bars->y_empty[i % kRingY]));
+        }
+        return true;
+      };
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && scores(0) && dots(0);
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n) {
+          if (!(ok = bar_wait(shared_addr(&bars->scores_read), unsigned(i) & 1, status))) break;
+          if (!(ok = scores(i + 1))) break;
+          if (!(ok = bar_wait(shared_addr(&bars->dots_read), unsigned(i) & 1, status))) break;
+          if (!(ok = dots(i + 1))) break;
+        }
+        if (!(ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status))) break;
+        fence_after_sync();
+        if (lane == 0) {
+          const uint32_t ds = tmem + kColumnsA + (i & 1) * 64;
+          mma_rows<T>(tmem + kColumnsB, ds, ds + 32, b.x_at(i), width, i > 0);
+          commit(shared_addr(&bars->x_empty[i % kRingX]));
+        }
+      }
+      if (ok && lane == 0) commit(shared_addr(&bars->done));
+    }
+  } else {
+    take_registers<kScoreRegisters>();
+    const int half = warp / 4, quarter = warp % 4;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t at_s = lanes + kColumnsS + half * 64, at_dots = lanes + kColumnsDots + half * 64;
+    const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
+    const uint32_t bar_scores_read = shared_addr(&bars->scores_read);
+    const uint32_t bar_dots_read = shared_addr(&bars->dots_read);
+    const float factor = ds_factor<T>(g) * exp2f(-kLiftBits<T>);
+    const int64_t pitch = int64_t(g.tiles) * kRows;
+    const float lse = g.stats[head * pitch + query0 + row];
+    const float delta = g.stats[(g.heads + head) * pitch + query0 + row];
+    const Scores f(g, head);
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int at = (first + i) * kRows + half * 64;  // the first column's key
+      const bool whole = reach.whole((first + i) * kRows);
+      const int lo = span.key_lo - at, hi = span.key_hi - at;
+      float s[64];
+      uint32_t p[32];
+      ok = bar_wait(bar_scores, unsigned(i) & 1, status);
+      if (!ok) break;
+      fence_after_sync();
+      tmem_load32(at_s, s);
+      tmem_load32(at_s + 32, s + 32);
+      tmem_wait<64>(s);
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar_scores_read);
+      weights_of<E>(s, p, f, float(at - (query0 + row)), whole, lo, hi, [&](int) { return lse; });
+
+      ok = bar_wait(bar_dots, unsigned(i) & 1, status);
+      if (!ok) break;
+      fence_after_sync();
+      float d[64];
+      tmem_load32(at_dots, d);
+      tmem_load32(at_dots + 32, d + 32);
+      tmem_wait<64>(d);
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar_dots_read);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float e[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          e[k] = s[c + k] * (d[c + k] - delta);
+          if (T::code == FADAM_DT_F16) e[k] *= factor;
+          if (!whole) e[k] = c + k >= lo && c + k < hi ? e[k] : 0.0f;
+        }
+        p[c / 2] = pack2<E>(e[0], e[1]);
+      }
+      // (scores of i come behind the product with ds of i - 2: its place is free)
+      tmem_store32(lanes + kColumnsA + (i & 1) * 64 + half * 32, p);
+      tmem_stored();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) bar_arrive(shared_addr(&bars->slopes[i & 1]));
+    }
+    if (n > 0 && ok) ok = bar_wait(shared_addr(&bars->done), 0, status);
+    fence_after_sync();
+    const float scale = g.scale / ds_factor<T>(g);
+    const uint32_t place = b.own0 + (quarter * 32 + lane) * 128;
+#pragma unroll
+    for (int k = 0; k < C; ++k) {  // half the columns to four warps
+      const int c = (half * C + k) * 32;
+      if (c >= g.width) continue;
+      float o[32];
+      if (n > 0) {
+        tmem_load32(lanes + kColumnsB + c, o);
+        tmem_wait<32>(o);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * scale : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        store_shared(place + c / kChunk * kBoxBytes + (((c % kChunk / 8 + u) ^ (lane & 7)) * 16),
+                     make_uint4(pack2<E>(o[8 * u], o[8 * u + 1]), pack2<E>(o[8 * u + 2], o[8 * u + 3]),
+                                pack2<E>(o[8 * u + 4], o[8 * u + 5]), pack2<E>(o[8 * u + 6], o[8 * u + 7])));
+    }
+    fence_shared();
+    group_sync(1, 256);
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (c * kChunk < g.width)
+          store_head_box(&maps.grad_q, c * kChunk, head, query0, b.own0 + c * kBoxBytes);
+      wait_stores();
+    }
+  }
+  __syncwarp();
+  chain_next();
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+template <class T, int C>
+fadam_status launch_backward(const BackwardMaps& m, const AttentionArgs& g, cudaStream_t stream) {
+  auto* keys = attention_keys_kernel<T, C>;
+  auto* queries = attention_queries_kernel<T, C>;
+  fadam_status st;
+  if ((st = launched_with<attention_keys_kernel<T, C>>("attention's backward pass")) ||
+      (st = launched_with<attention_queries_kernel<T, C>>("attention's backward pass")))
+    return st;
+  constexpr int kShared = int(kBackwardSmem<C>);
+  cudaError_t e = cudaFuncSetAttribute(keys, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(queries, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  const KeyMaps km{m.q, m.k, m.v, m.grad_out, m.grad_k, m.grad_v};
+  if ((st = launch_chained("attention keys launch", keys, int64_t(g.tiles) * (g.heads / g.group) * g.splits,
+                           kBackwardThreads, kShared, stream, km, g)))
+    return st;
+  const QueryMaps qm{m.q, m.k, m.v, m.grad_out, m.grad_q};
+  return launch_chained("attention queries launch", queries, int64_t(g.tiles) * g.heads, kBackwardThreads,
+                        kShared, stream, qm, g);
+}
+template <class T>
+fadam_status backward_of(const BackwardMaps& maps, const AttentionArgs& g, cudaStream_t stream) {
+  return g.width <= kChunk ? launch_backward<T, 1>(maps, g, stream) : launch_backward<T, 2>(maps, g, stream);
+}
+
+}  // namespace fadam_ops

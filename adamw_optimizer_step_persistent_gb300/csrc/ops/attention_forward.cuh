@@ -1,0 +1,330 @@
+// Attention, forward.
+//
+// A CTA takes 256 queries of one head in two tiles of 128, and walks over the
+// keys that any of them sees, 128 at a time, once: S = Q K^T on the tensor
+// cores, then a lane to a query takes the row's maximum, exponentials and sum
+// in registers, hands the exponentials in 16 bits back to tensor memory, and
+// O += P V.  The two tiles take turns: while four warps work on one tile's
+// scores, the tensor cores work for the other.  Tensor memory: scores and O of
+// both tiles (4 x 128 columns); P lies over the scores it came from.
+//
+// The running maximum of a row need not be its true maximum: any reference
+// gives the same quotient.  So O (in tensor memory) and the sum are only
+// rescaled when the maximum has grown by more than 2^8, which after the first
+// keys of a row hardly ever happens; exponentials stay below 2^8, in fp16 below
+// 2^15, of which 2^7 keep small ones from its subnormals.
+#pragma once
+
+#include "attention.cuh"
+
+namespace fadam_ops {
+
+constexpr int kForwardThreads = 384;  // 2 x 4 warps for the scores, one that multiplies, one that loads, two idle
+constexpr int kRing = 4;              // tiles of keys or values in flight
+constexpr float kGrowth = 8.0f;
+
+struct ForwardBarriers {
+  uint64_t q_full[2], scores[2], weights[2], done[2];
+  uint64_t full[kRing], empty[kRing];
+  Reach reach[8];
+  uint32_t tmem;
+};
+template <int C>
+constexpr size_t kForwardSmem = 1024 + (2 + kRing) * C * size_t(kBoxBytes) + sizeof(ForwardBarriers);
+
+template <class T, int C>
+__global__ void __launch_bounds__(kForwardThreads, 1)
+    attention_forward_kernel(const __grid_constant__ ForwardMaps maps, const __grid_constant__ AttentionArgs g) {
+  using E = typename T::type;
+  constexpr int kTile = C * kBoxBytes;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t q_tiles = (shared_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t ring = q_tiles + 2 * kTile;
+  ForwardBarriers* bars =
+      reinterpret_cast<ForwardBarriers*>(smem_raw + (ring + kRing * kTile - shared_addr(smem_raw)));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      bar_init(shared_addr(&bars->q_full[t]), 1);
+      bar_init(shared_addr(&bars->scores[t]), 1);
+      bar_init(shared_addr(&bars->weights[t]), 4);
+      bar_init(shared_addr(&bars->done[t]), 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      bar_init(shared_addr(&bars->full[i]), 1);
+      bar_init(shared_addr(&bars->empty[i]), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) tmem_alloc(shared_addr(&bars->tmem), 512);
+  chain_wait();
+
+  // the last queries first: under a causal mask they have the most keys
+  const int head = int(blockIdx.x % unsigned(g.heads));
+  const int pairs = (g.tiles + 1) / 2;
+  const int row0 = (pairs - 1 - int(blockIdx.x / unsigned(g.heads))) * 2 * kRows;
+  const int row = row0 + threadIdx.x;  // of a thread of the first eight warps
+  Spans span{};
+  if (warp < 8) {
+    if (row < g.tokens) span = spans_of(g, row);
+    const Reach r = reach_of(span.key_lo, span.key_hi, row < g.tokens);
+    if (lane == 0) bars->reach[warp] = r;
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = bars->tmem;
+  Reach reach[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    reach[t] = join(join(bars->reach[4 * t], bars->reach[4 * t + 1]),
+                    join(bars->reach[4 * t + 2], bars->reach[4 * t + 3]));
+  const int first = min(reach[0].first(), reach[1].first());
+  const int last = max(reach[0].hi > reach[0].lo ? reach[0].last() : 0,
+                       reach[1].hi > reach[1].lo ? reach[1].last() : 0);
+  const auto sees = [&](int t, int j) { return j >= reach[t].first() && j < reach[t].last(); };
+
+  if (warp >= 8) keep_registers<kOtherRegisters>();
+  if (warp >= 10) {
+  } else if (warp == 9) {
+    // ---- loads: the queries, then keys and values in turn
+    if (lane == 0 && first < last) {
+      prefetch_map(&maps.q);
+      prefetch_map(&maps.k);
+      prefetch_map(&maps.v);
+      const int kv = head / g.group;
+      int n = 0;
+      bool ok = true;
+      const auto queries = [&](int t) {
+        if (reach[t].first() >= reach[t].last()) return;
+        const uint32_t bar = shared_addr(&bars->q_full[t]);
+        bar_expect(bar, kTile);
+        load_head<C>(q_tiles + t * kTile, &maps.q, head, row0 + t * kRows, bar);
+      };
+      const auto next = [&](const CUtensorMap* map, int j) {
+        const int at = n % kRing;
+        if (n >= kRing) ok = bar_wait(shared_addr(&bars->empty[at]), unsigned(n / kRing - 1) & 1, g.status);
+        if (!ok) return;
+        const uint32_t bar = shared_addr(&bars->full[at]);
+        bar_expect(bar, kTile);
+        load_head<C>(ring + at * kTile, map, kv, j * kRows, bar);
+        ++n;
+      };
+      queries(0);
+      for (int j = first; ok && j < last; ++j) {
+        next(&maps.k, j);
+        if (j == first) queries(1);
+        if (ok) next(&maps.v, j);
+      }
+      // no copy is in flight when the CTA ends
+      for (int i = n < kRing ? 0 : n - kRing; i < n; ++i)
+        bar_wait(shared_addr(&bars->full[i % kRing]), unsigned(i / kRing) & 1, g.status);
+    }
+  } else if (warp == 8) {
+    // ---- tensor cores
+    if (first < last) {
+      const int steps = (g.width + 15) / 16, n = (g.width + 15) / 16 * 16;
+      int inside_lo = 0, inside_hi = g.tiles * kRows;
+      if (g.documents) {
+        inside_lo = __ldg(g.documents);
+        inside_hi = __ldg(g.documents + g.n_documents);
+      }
+      bool ok = true;
+      const auto full = [&](int i) {
+        ok = ok && bar_wait(shared_addr(&bars->full[i % kRing]), unsigned(i / kRing) & 1, g.status);
+        fence_after_sync();
+      };
+      const auto scores = [&](int t, int j) {
+        if (!ok || !sees(t, j)) return;
+        if (j == reach[t].first()) {
+          ok = bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
+          if (!ok) return;
+        }
+        if (lane == 0) {
+          mma_scores<T>(tmem + t * kRows, q_tiles + t * kTile, ring + 2 * (j - first) % kRing * kTile, steps);
+          commit(shared_addr(&bars->scores[t]));
+        }
+      };
+      full(0);
+      scores(0, first);
+      scores(1, first);
+      if (ok && lane == 0) commit(shared_addr(&bars->empty[0]));
+      for (int j = first; ok && j < last; ++j) {
+        const int v = 2 * (j - first) + 1;
+        const uint32_t values = ring + v % kRing * kTile;
+        full(v);
+        if (!ok) break;
+        if (j * kRows < inside_lo || (j + 1) * kRows > inside_hi)
+          zero_rows<C>(values, inside_lo - j * kRows, inside_hi - j * kRows);
+        const bool more = j + 1 < last;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (sees(t, j)) {
+            const int turn = j - reach[t].first();
+            ok = ok && bar_wait(shared_addr(&bars->weights[t]), unsigned(turn) & 1, g.status);
+            if (!ok) break;
+            fence_after_sync();
+            if (lane == 0) {
+              const uint32_t p = tmem + t * kRows;
+              mma_rows<T>(tmem + (2 + t) * kRows, p, p + 32, values, n, turn > 0);
+              if (j + 1 == reach[t].last()) commit(shared_addr(&bars->done[t]));
+            }
+          }
+          if (more) {
+            if (t == 0) full(v + 1);
+            scores(t, j + 1);
+          }
+        }
+        if (ok && lane == 0) {
+          commit(shared_addr(&bars->empty[v % kRing]));
+          if (more) commit(shared_addr(&bars->empty[(v + 1) % kRing]));
+        }
+      }
+    }
+  } else {
+    // ---- softmax: a lane to a query
+    take_registers<kScoreRegisters>();
+    const int t = warp / 4, quarter = warp % 4;
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t at_s = lanes + t * kRows, at_o = lanes + (2 + t) * kRows;
+    const uint32_t bar_scores = shared_addr(&bars->scores[t]), bar_weights = shared_addr(&bars->weights[t]);
+    const Scores f(g, head);
+    const bool ready = f.cap != 0.0f || f.slope != 0.0f;  // scores are in units of log 2 before the maximum
+    const float mul = ready ? 1.0f : f.mul;
+    constexpr float kLift = T::code == FADAM_DT_F16 ? 7.0f : 0.0f;
+    float top = -INFINITY, sum = 0.0f;   // top: the reference that exponents are relative to
+    bool ok = true;
+    const Reach mine = t ? reach[1] : reach[0];
+    const int begin = mine.first(), end = mine.last();
+    for (int j = begin; j < end; ++j) {
+      ok = bar_wait(bar_scores, unsigned(j - begin) & 1, g.status);
+      if (!ok) break;
+      fence_after_sync();
+      float s[kRows];
+#pragma unroll
+      for (int c = 0; c < kRows; c += 32) tmem_load32(at_s + c, s + c);
+      tmem_wait<kRows>(s);
+      if (f.cap != 0.0f) {
+#pragma unroll
+        for (int c = 0; c < kRows; ++c) s[c] = fmaf(-2.0f * f.cap, f.folded(s[c]), f.cap);
+      } else if (ready) {
+#pragma unroll
+        for (int c = 0; c < kRows; ++c) s[c] *= f.mul;
+      }
+      if (f.slope != 0.0f) {
+        const float apart = float(j * kRows - row);
+#pragma unroll
+        for (int c = 0; c < kRows; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c]);
+      }
+      if (!mine.whole(j * kRows)) {
+        const int lo = span.key_lo - j * kRows, hi = span.key_hi - j * kRows;
+#pragma unroll
+        for (int c = 0; c < kRows; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
+      }
+      float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kRows; ++c) m[c % 4] = fmaxf(m[c % 4], s[c]);
+      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mul;
+      if (__any_sync(~0u, most > top + kGrowth)) {
+        // (scores of j come behind the product with the values of j - 1: O is at rest)
+        const float now = fmaxf(top, most);
+        const float factor = now == -INFINITY ? 1.0f : exp2_fast(top - now);
+        top = now;
+        sum *= factor;
+        if (j > begin) {
+#pragma unroll
+          for (int c = 0; c < C * kChunk; c += 32)
+            if (c < g.width) {
+              float o[32];
+              tmem_load32(at_o + c, o);
+              tmem_wait<32>(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= factor;
+              tmem_store32(at_o + c, reinterpret_cast<uint32_t*>(o));
+            }
+        }
+      }
+      const float from = top == -INFINITY ? 0.0f : top - kLift;
+      float part[4] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float a = exp2_fast(fmaf(s[h * 64 + c], mul, -from));
+          const float b = exp2_fast(fmaf(s[h * 64 + c + 1], mul, -from));
+          part[c % 4] += a;
+          part[c % 4 + 1] += b;
+          p[c / 2] = pack2<E>(a, b);
+        }
+        tmem_store32(at_s + h * 32, p);
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      tmem_stored();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar_weights);
+    }
+    if (row0 + t * kRows < g.tokens) {
+      // O / sum, through the queries' place in shared memory
+      const bool none = begin >= end || sum == 0.0f;
+      const float inverse = 1.0f / sum;
+      if (begin < end && ok) ok = bar_wait(shared_addr(&bars->done[t]), 0, g.status);
+      fence_after_sync();
+      const uint32_t place = q_tiles + t * kTile + (quarter * 32 + lane) * 128;
+#pragma unroll
+      for (int c = 0; c < C * kChunk; c += 32)
+        if (c < g.width) {
+          float o[32];
+          if (begin < end) {
+            tmem_load32(at_o + c, o);
+            tmem_wait<32>(o);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.0f : o[i] * inverse;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int unit = c % kChunk / 8 + u;
+            store_shared(place + c / kChunk * kBoxBytes + ((unit ^ (lane & 7)) * 16),
+                         make_uint4(pack2<E>(o[8 * u], o[8 * u + 1]), pack2<E>(o[8 * u + 2], o[8 * u + 3]),
+                                    pack2<E>(o[8 * u + 4], o[8 * u + 5]), pack2<E>(o[8 * u + 6], o[8 * u + 7])));
+          }
+        }
+      if (row < g.tokens)
+        g.lse[int64_t(row) * g.heads + head] =
+            none ? -INFINITY : (top - kLift + log2f(sum)) * kLn2;
+      fence_shared();
+      group_sync(1 + t, 128);
+      if (threadIdx.x % 128 == 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c * kChunk < g.width)
+            store_head_box(&maps.out, c * kChunk, head, row0 + t * kRows, q_tiles + t * kTile + c * kBoxBytes);
+        wait_stores();
+      }
+    }
+  }
+  __syncwarp();
+  chain_next();
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+template <class T, int C>
+fadam_status launch_forward(const ForwardMaps& maps, const AttentionArgs& g, cudaStream_t stream) {
+  auto* kernel = attention_forward_kernel<T, C>;
+  if (const fadam_status st = launched_with<attention_forward_kernel<T, C>>("attention")) return st;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kForwardSmem<C>));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  const int64_t items = int64_t((g.tiles + 1) / 2) * g.heads;
+  return launch_chained("attention launch", kernel, items, kForwardThreads, kForwardSmem<C>, stream, maps, g);
+}
+template <class T>
+fadam_status forward_of(const ForwardMaps& maps, const AttentionArgs& g, cudaStream_t stream) {
+  return g.width <= kChunk ? launch_forward<T, 1>(maps, g, stream) : launch_forward<T, 2>(maps, g, stream);
+}
+
+}  // namespace fadam_ops

@@ -1,0 +1,564 @@
+// The token embedding and its weight's gradient.
+//
+// Forward is one pass: a thread takes a vector of eight columns of several
+// rows.  The gradient is a sum over each token's rows: the rows are sorted by
+// token first (stable, so that every sum has one order), then the sorted list
+// is cut into equal pieces whose sums do not depend on how often a token
+// occurs, and what a piece's end cuts is joined.
+#include "fadam_seq.h"
+#include "ops_internal.h"
+#include "rows.cuh"
+
+namespace fadam_ops {
+namespace {
+
+constexpr int kThreads = 256;   // of a CTA that streams rows: 2048 columns
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kRange = 1024;    // most tokens of the vocabulary that one CTA sorts by
+constexpr int kLongest = 64;    // most rows of a piece
+
+// A thread's eight columns of a row: one aligned vector, or (rows that are not
+// whole vectors) every blockDim-th element, so that a warp's accesses coalesce.
+template <bool kWide>
+struct Eight {
+  int col, step, width;
+  __device__ __forceinline__ Eight(int part, int width) : width(width) {
+    const int first = part * int(blockDim.x) * 8;
+    col = kWide ? first + int(threadIdx.x) * 8 : first + int(threadIdx.x);
+    step = kWide ? 1 : int(blockDim.x);
+  }
+  __device__ __forceinline__ bool any() const { return col < width; }
+  __device__ __forceinline__ bool has(int i) const { return kWide || col + i * step < width; }
+
+  template <class E>
+  __device__ __forceinline__ void load(const E* row, Raw<E>& r) const {
+    if constexpr (kWide) {
+      r = load_raw(row + col);
+    } else {
+      E e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = has(i) ? row[col + i * step] : from_float<E>(0.0f);
+      memcpy(&r, e, sizeof r);
+    }
+  }
+  template <class E>
+  __device__ __forceinline__ void store(E* row, const Raw<E>& r) const {
+    if constexpr (kWide) {
+      store_raw(row + col, r);
+    } else {
+      E e[8];
+      memcpy(e, &r, sizeof r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (has(i)) row[col + i * step] = e[i];
+    }
+  }
+};
+
+// How rows are cut into column parts of at most 2048.
+struct Parts {
+  int threads, count;
+};
+Parts parts_of(int64_t width) {
+  Parts p;
+  const int64_t eights = ceil_div(width, 8);
+  p.threads = int(eights < kThreads ? round_up(eights, 32) : kThreads);
+  p.count = int(ceil_div(eights, p.threads));
+  return p;
+}
+
+// ---- forward -----------------------------------------------------------------------
+
+template <class E, class Out, bool kWide, int R>
+__global__ void __launch_bounds__(kThreads)
+    gather_kernel(const int64_t* tokens, const E* weight, int64_t ld, Out* out, int64_t out_ld,
+                  int64_t rows, int width, int64_t vocab, int64_t padding, bool padded, float scale,
+                  int parts) {
+  chain_wait();
+  chain_next();
+  const unsigned block = blockIdx.x / unsigned(parts);
+  const Eight<kWide> at(int(blockIdx.x - block * parts), width);
+  if (!at.any()) return;
+  const int64_t row0 = int64_t(block) * R;
+  int64_t token[R];
+  Raw<E> raw[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) token[r] = row0 + r < rows ? __ldg(tokens + row0 + r) : -1;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    raw[r] = zero_raw<E>();
+    if (token[r] >= 0 && token[r] < vocab) at.load(weight + token[r] * ld, raw[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (row0 + r >= rows) return;
+    // what is neither padding nor in the vocabulary becomes NaN
+    const float bad = token[r] >= 0 && token[r] < vocab ? 0.0f : NAN;
+    const float keep = padded && token[r] == padding ? 0.0f : 1.0f;
+    Pair v[4];
+    widen(raw[r], v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = split(v[i]);
+      v[i] = keep == 0.0f ? make_pair(0.0f, 0.0f)
+             : bad == 0.0f ? make_pair(p.x * scale, p.y * scale)
+                           : make_pair(bad, bad);
+    }
+    at.store(out + (row0 + r) * out_ld, narrow<Out>(v));
+  }
+}
+
+// ---- sorting rows by token -----------------------------------------------------------
+
+struct SortArgs {
+  const int64_t* tokens;
+  int32_t rows;
+  int64_t vocab, padding;
+  bool padded;
+  int32_t range;     // tokens of the vocabulary that a CTA takes
+  int32_t* order;    // [rows] rows sorted by token, those of one token ascending
+  int32_t* starts;   // [vocab + 1] where a token's rows begin in it
+};
+
+// Each CTA takes a range of the vocabulary and reads all tokens twice: first it
+// counts its own (for each of its warps, which have consecutive runs of rows)
+// and those below its range, which says where its part of the order begins;
+// then it places them.  Nothing is exchanged between CTAs, and the order is
+// stable: within a warp's 32 rows a row comes behind those of its token in
+// lower lanes.  Of T rows 152 x 16 T bytes come from L2: 3 us for 16384 rows,
+// while a sort by digits would take three launches or more.
+// Rows of no token are zeroed here, where the counts are (unless kKeep).
+template <class Out, bool kWide, bool kKeep>
+__global__ void __launch_bounds__(kSortThreads)
+    sort_kernel(const SortArgs a, Out* out, int64_t out_ld, int width) {
+  extern __shared__ int counts[];  // [kSortWarps][range], then [range] of all warps
+  __shared__ int warp_sum[kSortWarps];
+  __shared__ int below;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t low = int64_t(blockIdx.x) * a.range;
+  const int mine = int(min(int64_t(a.range), a.vocab - low));
+  int* total = counts + kSortWarps * a.range;
+  for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) counts[i] = 0;
+  if (threadIdx.x == 0) below = 0;
+  __syncthreads();
+  chain_wait();
+  chain_next();
+
+  // rows of a warp: whole groups of 32
+  const int per_warp = int((int64_t(a.rows) + kSortThreads - 1) / kSortThreads) * 32;
+  const int first = warp * per_warp;
+  const int last = int(min(int64_t(a.rows), int64_t(first) + per_warp));
+  int* own = counts + warp * a.range;
+  // the row's token within the range; -1 below it, -2 elsewhere
+  const auto place = [&](int row) {
+    if (row >= last) return -2;
+    const int64_t t = __ldg(a.tokens + row);
+    if (t < 0 || t >= a.vocab || (a.padded && t == a.padding)) return -2;
+    return t < low ? -1 : t < low + mine ? int(t - low) : -2;
+  };
+  int fewer = 0;
+#pragma unroll 4
+  for (int row = first + lane; row - lane < last; row += 32) {
+    const int v = place(row);
+    fewer += v == -1;
+    if (__any_sync(~0u, v >= 0)) {
+      const unsigned peers = __match_any_sync(~0u, v);
+      if (v >= 0 && lane == __ffs(peers) - 1) own[v] += __popc(peers);
+      __syncwarp();
+    }
+  }
+  fewer = __reduce_add_sync(~0u, fewer);
+  if (lane == 0 && fewer) atomicAdd(&below, fewer);
+  __syncthreads();
+
+  // a thread to a token: the warps' shares one after the other, then the tokens
+  const int v = threadIdx.x;
+  int count = 0;
+  if (v < mine)
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int n = counts[w * a.range + v];
+      counts[w * a.range + v] = count;
+      count += n;
+    }
+  int sum = count;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int n = __shfl_up_sync(~0u, sum, d);
+    if (lane >= d) sum += n;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  int base = below;
+  for (int w = 0; w < warp; ++w) base += warp_sum[w];
+  const int start = base + sum - count;
+  if (v < mine) {
+    for (int w = 0; w < kSortWarps; ++w) counts[w * a.range + v] += start;
+    total[v] = count;
+    a.starts[low + v] = start;
+    if (low + v == a.vocab - 1) a.starts[a.vocab] = start + count;
+  }
+  __syncthreads();
+
+#pragma unroll 4
+  for (int row = first + lane; row - lane < last; row += 32) {
+    const int at = place(row);
+    if (!__any_sync(~0u, at >= 0)) continue;
+    const unsigned peers = __match_any_sync(~0u, at);
+    if (at >= 0) a.order[own[at] + __popc(peers & ((1u << lane) - 1))] = row;
+    __syncwarp();
+    if (at >= 0 && lane == __ffs(peers) - 1) own[at] += __popc(peers);
+    __syncwarp();
+  }
+
+  if constexpr (!kKeep) {
+    for (int r = warp; r < mine; r += kSortWarps) {
+      if (total[r]) continue;
+      Out* row = out + (low + r) * out_ld;
+      if constexpr (kWide) {
+        const Raw<Out> zero = zero_raw<Out>();
+        for (int c = lane * 8; c < width; c += 256) store_raw(row + c, zero);
+      } else {
+        for (int c = lane; c < width; c += 32) row[c] = from_float<Out>(0.0f);
+      }
+    }
+  }
+}
+
+// ---- sums over the sorted rows ----------------------------------------------------------
+
+struct SumArgs {
+  const int64_t* tokens;
+  const int32_t* order;
+  const int32_t* starts;
+  int64_t vocab;
+  int32_t width, parts, piece;   // piece: sorted rows of a CTA
+  int64_t grad_ld, out_ld, carry_ld;
+  float* carry;    // [pieces][2][carry_ld]: sums that a piece's begin and end cut
+  float scale;
+};
+
+// The scaled sum of a token's rows, written or added.
+template <class Out, bool kWide, bool kKeep>
+__device__ __forceinline__ void put(const Eight<kWide>& at, Out* row, const float (&sum)[8], float scale) {
+  Pair v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_pair(sum[2 * i] * scale, sum[2 * i + 1] * scale);
+  if constexpr (kKeep) {
+    Raw<Out> old;
+    Pair o[4];
+    at.load(row, old);
+    widen(old, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
+  }
+  at.store(row, narrow<Out>(v));
+}
+
+// A piece's rows, four loads in flight; a token's sum is written when its last
+// row is in the piece and its first one too, else kept for join_kernel.
+template <class E, class Out, bool kWide, bool kKeep>
+__global__ void __launch_bounds__(kThreads)
+    sum_kernel(const SumArgs a, const E* grad, Out* out) {
+  __shared__ int rows[kLongest];
+  __shared__ int ids[kLongest];
+  chain_wait();
+  chain_next();
+  const unsigned piece = blockIdx.x / unsigned(a.parts);
+  const Eight<kWide> at(int(blockIdx.x - piece * a.parts), a.width);
+  const int n = a.starts[a.vocab];  // rows that count
+  const int begin = int(piece) * a.piece;
+  const int many = min(a.piece, n - begin);
+  if (many <= 0) return;
+  for (int i = threadIdx.x; i < many; i += blockDim.x) {
+    rows[i] = a.order[begin + i];
+    ids[i] = int(a.tokens[rows[i]]);
+  }
+  __syncthreads();
+  if (!at.any()) return;
+  const bool cut_begin = a.starts[ids[0]] < begin;
+  const bool cut_end = a.starts[ids[many - 1] + 1] > begin + many;
+  const Eight<true> wide(int(blockIdx.x - piece * a.parts), a.width);
+  const int carry_col = kWide ? at.col : wide.col;  // a thread's eight sums lie together
+  float* carry = a.carry + int64_t(piece) * 2 * a.carry_ld + carry_col;
+
+  float sum[8] = {};
+  int id = ids[0];
+  bool cut = cut_begin;
+  constexpr int kAhead = 4;
+  for (int i = 0; i < many; i += kAhead) {
+    Raw<E> raw[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i + k < many) at.load(grad + rows[i + k] * a.grad_ld, raw[k]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i + k >= many) break;
+      if (ids[i + k] != id) {
+        if (cut) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) carry[c] = sum[c];
+        } else {
+          put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
+        }
+        cut = false;
+        id = ids[i + k];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
+      }
+      Pair v[4];
+      widen(raw[k], v);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 p = split(v[c]);
+        sum[2 * c] += p.x;
+        sum[2 * c + 1] += p.y;
+      }
+    }
+  }
+  if (cut || cut_end) {
+    // the whole piece is one token's middle or end (first place), or its begin (second)
+    float* to = carry + (cut ? 0 : a.carry_ld);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) to[c] = sum[c];
+  } else {
+    put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
+  }
+}
+
+// The pieces' shares of a token that pieces cut, in order: by the piece in
+// which its rows begin.
+template <class Out, bool kWide, bool kKeep>
+__global__ void __launch_bounds__(kThreads) join_kernel(const SumArgs a, Out* out) {
+  chain_wait();
+  chain_next();
+  const unsigned piece = blockIdx.x / unsigned(a.parts);
+  const int part = int(blockIdx.x - piece * a.parts);
+  const Eight<kWide> at(part, a.width);
+  const int n = a.starts[a.vocab];
+  const int begin = int(piece) * a.piece, end = begin + a.piece;
+  if (end >= n || !at.any()) return;
+  const int64_t id = a.tokens[a.order[end - 1]];
+  const int first = a.starts[id], last = a.starts[id + 1];
+  if (first < begin || last <= end) return;
+  const float* carry = a.carry + Eight<true>(part, a.width).col;
+  float sum[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) sum[c] = carry[(int64_t(piece) * 2 + 1) * a.carry_ld + c];
+  const int until = (last + a.piece - 1) / a.piece;
+#pragma unroll 4
+  for (int p = int(piece) + 1; p < until; ++p) {
+    const float4* from = reinterpret_cast<const float4*>(carry + int64_t(p) * 2 * a.carry_ld);
+    const float4 x = from[0], y = from[1];
+    sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+    sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
+  }
+  put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
+}
+
+// ---- host ----------------------------------------------------------------------------
+
+template <class E, class Out>
+fadam_status forward(const fadam_embed& d, cudaStream_t stream) {
+  const bool wide = d.width % 8 == 0 && !misaligned(d.weight, 16) && !misaligned(d.out, 16) &&
+                    d.weight_stride * sizeof(E) % 16 == 0 && d.out_stride * sizeof(Out) % 16 == 0;
+  const Parts p = parts_of(d.width);
+  // four rows to a thread where that leaves every SM four CTAs
+  const bool many = ceil_div(d.rows, 4) * p.count >= 152 * 4;
+  auto* kernel = wide ? (many ? gather_kernel<E, Out, true, 4> : gather_kernel<E, Out, true, 1>)
+                      : (many ? gather_kernel<E, Out, false, 4> : gather_kernel<E, Out, false, 1>);
+  return launch_chained("embedding launch", kernel, ceil_div(d.rows, many ? 4 : 1) * p.count, p.threads, 0,
+                        stream, d.tokens, static_cast<const E*>(d.weight), d.weight_stride,
+                        static_cast<Out*>(d.out), d.out_stride, d.rows, int(d.width), d.vocab,
+                        d.padding_index, (d.flags & FADAM_EMBED_PADDING) != 0, d.scale, p.count);
+}
+
+struct Layout {
+  int32_t* order;
+  int32_t* starts;
+  float* carry;
+  int32_t piece;
+  int64_t pieces, carry_ld;
+  size_t bytes;
+};
+
+Layout layout(const fadam_embed_grad& d, char* base) {
+  Layout l{};
+  Carver c{base};
+  const Parts p = parts_of(d.width);
+  // pieces as long as leave every SM eight CTAs, 4 to 64 rows
+  const int64_t per = d.rows * p.count / (152 * 8);
+  l.piece = int32_t(per < 4 ? 4 : per > kLongest ? kLongest : per);
+  l.pieces = ceil_div(d.rows, l.piece);
+  l.carry_ld = int64_t(p.count) * p.threads * 8;
+  l.order = static_cast<int32_t*>(c.take(4 * d.rows));
+  l.starts = static_cast<int32_t*>(c.take(4 * (d.vocab + 1)));
+  l.carry = static_cast<float*>(c.take(4 * 2 * l.pieces * l.carry_ld));
+  l.bytes = c.used;
+  return l;
+}
+
+template <class E, class Out, bool kWide, bool kKeep>
+fadam_status gradient(const fadam_embed_grad& d, const Layout& l, const DeviceFacts& dev,
+                      cudaStream_t stream) {
+  Out* out = static_cast<Out*>(d.out);
+  SortArgs s{};
+  s.tokens = d.tokens;
+  s.rows = int32_t(d.rows);
+  s.vocab = d.vocab;
+  s.padding = d.padding_index;
+  s.padded = (d.flags & FADAM_EMBED_PADDING) != 0;
+  const int64_t even = ceil_div(d.vocab, dev.sm_count);
+  s.range = int32_t(even < kRange ? even : kRange);
+  s.order = l.order;
+  s.starts = l.starts;
+  auto* sort = sort_kernel<Out, kWide, kKeep>;
+  constexpr int kMostShared = (kSortWarps + 1) * kRange * 4;
+  const cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  fadam_status st = launch_chained("token sort launch", sort, ceil_div(d.vocab, s.range), kSortThreads,
+                                   size_t(kSortWarps + 1) * s.range * 4, stream, s, out, d.out_stride,
+                                   int(d.width));
+  if (st) return st;
+  const Parts p = parts_of(d.width);
+  SumArgs a{};
+  a.tokens = d.tokens;
+  a.order = l.order;
+  a.starts = l.starts;
+  a.vocab = d.vocab;
+  a.width = int32_t(d.width);
+  a.parts = p.count;
+  a.piece = l.piece;
+  a.grad_ld = d.grad_stride;
+  a.out_ld = d.out_stride;
+  a.carry_ld = l.carry_ld;
+  a.carry = l.carry;
+  a.scale = d.scale;
+  st = launch_chained("embedding sums launch", sum_kernel<E, Out, kWide, kKeep>, l.pieces * p.count,
+                      p.threads, 0, stream, a, static_cast<const E*>(d.grad), out);
+  if (st || l.pieces == 1) return st;
+  return launch_chained("embedding join launch", join_kernel<Out, kWide, kKeep>, l.pieces * p.count,
+                        p.threads, 0, stream, a, out);
+}
+
+template <class E, class Out>
+fadam_status gradient(const fadam_embed_grad& d, const Layout& l, const DeviceFacts& dev,
+                      cudaStream_t stream) {
+  const bool wide = d.width % 8 == 0 && !misaligned(d.grad, 16) && !misaligned(d.out, 16) &&
+                    d.grad_stride * sizeof(E) % 16 == 0 && d.out_stride * sizeof(Out) % 16 == 0;
+  const bool keep = (d.flags & FADAM_EMBED_ACCUMULATE) != 0;
+  if (wide)
+    return keep ? gradient<E, Out, true, true>(d, l, dev, stream)
+                : gradient<E, Out, true, false>(d, l, dev, stream);
+  return keep ? gradient<E, Out, false, true>(d, l, dev, stream)
+              : gradient<E, Out, false, false>(d, l, dev, stream);
+}
+
+bool finite(float x) { return x - x == 0.0f; }
+
+// What both directions' descriptors have in common.
+fadam_status check_common(int64_t rows, int64_t width, int64_t vocab, float scale) {
+  if (rows < 0 || width < 1 || vocab < 1)
+    return fail(FADAM_EINVAL, "%lld rows of width %lld over a vocabulary of %lld", (long long)rows,
+                (long long)width, (long long)vocab);
+  const int64_t most = int64_t(1) << 30;
+  if (rows > most || width > most || vocab > most)
+    return fail(FADAM_ELIMIT, "rows, width or vocab beyond 2^30");
+  if (!finite(scale)) return fail(FADAM_EINVAL, "scale is not finite");
+  return FADAM_OK;
+}
+
+fadam_status check(const fadam_embed* d) {
+  if (!d) return fail(FADAM_EINVAL, "the descriptor is NULL");
+  if (!elem_size(d->weight_dtype)) return fail(FADAM_EDTYPE, "dtype %d is not fp32, bf16 or fp16", d->weight_dtype);
+  if (d->out_dtype != d->weight_dtype && d->out_dtype != FADAM_DT_F32)
+    return fail(FADAM_EDTYPE, "out dtype %d is neither fp32 nor the weight's %d", d->out_dtype, d->weight_dtype);
+  if (d->flags & ~FADAM_EMBED_PADDING) return fail(FADAM_EINVAL, "unknown flag bits 0x%x", d->flags);
+  if (const fadam_status st = check_common(d->rows, d->width, d->vocab, d->scale)) return st;
+  if (d->weight_stride < d->width || d->out_stride < d->width)
+    return fail(FADAM_EINVAL, "a row stride is below the width %lld", (long long)d->width);
+  if (!d->weight || (d->rows > 0 && (!d->tokens || !d->out)))
+    return fail(FADAM_EINVAL, "tokens, weight and out must be non-NULL");
+  if (misaligned(d->tokens, 8) || misaligned(d->weight, elem_size(d->weight_dtype)) ||
+      misaligned(d->out, elem_size(d->out_dtype)))
+    return fail(FADAM_EALIGN, "a pointer is not aligned to its element size");
+  return FADAM_OK;
+}
+
+fadam_status check(const fadam_embed_grad* d) {
+  if (!d) return fail(FADAM_EINVAL, "the descriptor is NULL");
+  if (!elem_size(d->grad_dtype)) return fail(FADAM_EDTYPE, "dtype %d is not fp32, bf16 or fp16", d->grad_dtype);
+  if (!elem_size(d->out_dtype) || (d->out_dtype != d->grad_dtype && d->out_dtype != FADAM_DT_F32 &&
+                                   d->grad_dtype != FADAM_DT_F32))
+    return fail(FADAM_EDTYPE, "out dtype %d with gradients of %d", d->out_dtype, d->grad_dtype);
+  if (d->flags & ~(FADAM_EMBED_PADDING | FADAM_EMBED_ACCUMULATE))
+    return fail(FADAM_EINVAL, "unknown flag bits 0x%x", d->flags);
+  if (const fadam_status st = check_common(d->rows, d->width, d->vocab, d->scale)) return st;
+  if (d->grad_stride < d->width || d->out_stride < d->width)
+    return fail(FADAM_EINVAL, "a row stride is below the width %lld", (long long)d->width);
+  if (!d->out || (d->rows > 0 && (!d->tokens || !d->grad)))
+    return fail(FADAM_EINVAL, "tokens, grad and out must be non-NULL");
+  if (misaligned(d->tokens, 8) || misaligned(d->grad, elem_size(d->grad_dtype)) ||
+      misaligned(d->out, elem_size(d->out_dtype)))
+    return fail(FADAM_EALIGN, "a pointer is not aligned to its element size");
+  return FADAM_OK;
+}
+
+}  // namespace
+}  // namespace fadam_ops
+
+using namespace fadam_ops;
+
+extern "C" fadam_status fadam_embed_forward(const fadam_embed* desc, fadam_stream stream_) {
+  clear_error();
+  const fadam_status st = check(desc);
+  if (st || desc->rows == 0) return st;
+  const fadam_embed& d = *desc;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const bool wide = d.out_dtype == FADAM_DT_F32;
+  if (d.weight_dtype == FADAM_DT_BF16)
+    return wide ? forward<__nv_bfloat16, float>(d, stream) : forward<__nv_bfloat16, __nv_bfloat16>(d, stream);
+  if (d.weight_dtype == FADAM_DT_F16)
+    return wide ? forward<__half, float>(d, stream) : forward<__half, __half>(d, stream);
+  return forward<float, float>(d, stream);
+}
+
+extern "C" fadam_status fadam_embed_grad_workspace(const fadam_embed_grad* desc, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(FADAM_EINVAL, "bytes is NULL");
+  const fadam_status st = check(desc);
+  if (st) return st;
+  *bytes = desc->rows == 0 ? 0 : layout(*desc, nullptr).bytes;
+  return FADAM_OK;
+}
+
+extern "C" fadam_status fadam_embed_grad_run(const fadam_embed_grad* desc, void* workspace, size_t bytes,
+                                             fadam_stream stream_) {
+  clear_error();
+  fadam_status st = check(desc);
+  if (st) return st;
+  const fadam_embed_grad& d = *desc;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (d.rows == 0) {
+    if (d.flags & FADAM_EMBED_ACCUMULATE) return FADAM_OK;
+    const int size = elem_size(d.out_dtype);
+    const cudaError_t e = cudaMemset2DAsync(d.out, d.out_stride * size, 0, d.width * size, d.vocab, stream);
+    return e == cudaSuccess ? FADAM_OK : cuda_fail(e, "cudaMemset2DAsync");
+  }
+  DeviceFacts dev;
+  if ((st = device_facts(&dev))) return st;
+  const Layout l = layout(d, static_cast<char*>(workspace));
+  if (!workspace || bytes < l.bytes)
+    return fail(FADAM_EINVAL, "the workspace has %zu bytes, %zu are needed",
+                workspace ? bytes : size_t(0), l.bytes);
+  if (misaligned(workspace, 256)) return fail(FADAM_EALIGN, "the workspace is not 256-byte aligned");
+  if (d.grad_dtype == FADAM_DT_BF16)
+    return d.out_dtype == FADAM_DT_F32 ? gradient<__nv_bfloat16, float>(d, l, dev, stream)
+                                       : gradient<__nv_bfloat16, __nv_bfloat16>(d, l, dev, stream);
+  if (d.grad_dtype == FADAM_DT_F16)
+    return d.out_dtype == FADAM_DT_F32 ? gradient<__half, float>(d, l, dev, stream)
+                                       : gradient<__half, __half>(d, l, dev, stream);
+  if (d.out_dtype == FADAM_DT_BF16) return gradient<float, __nv_bfloat16>(d, l, dev, stream);
+  if (d.out_dtype == FADAM_DT_F16) return gradient<float, __half>(d, l, dev, stream);
+  return gradient<float, float>(d, l, dev, stream);
+}

@@ -5,6 +5,7 @@
 #include <mutex>
 #include <string>
 
+#include "attention_internal.h"
 #include "ops_internal.h"
 
 // Set by a kernel whose bounded wait gave up; read by fadam_ops_status.
@@ -92,6 +93,26 @@ fadam_status matrix_map(CUtensorMap* map, const void* base, int64_t rows, int64_
   if (r != CUDA_SUCCESS)
     return fail(FADAM_ECUDA, "cuTensorMapEncodeTiled: %d for a %lld x %lld matrix of stride %lld",
                 int(r), (long long)rows, (long long)inner, (long long)ld);
+  return FADAM_OK;
+}
+
+fadam_status head_map(CUtensorMap* map, const void* base, int64_t tokens, int heads, int width,
+                      int64_t stride, int64_t head_stride) {
+  static const Encode encode = find_encode();
+  if (!encode) return fail(FADAM_ECUDA, "the driver has no cuTensorMapEncodeTiled");
+  // (strides along a dimension of one are never used, and may be anything)
+  const int64_t token_step = tokens > 1 ? stride : 8, head_step = heads > 1 ? head_stride : 8;
+  const cuuint64_t dims[3] = {cuuint64_t(width), cuuint64_t(heads), cuuint64_t(tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(head_step) * 2, cuuint64_t(token_step) * 2};
+  const cuuint32_t box[3] = {kChunk, 1, kRows};
+  const cuuint32_t step[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(FADAM_ECUDA, "cuTensorMapEncodeTiled: %d for %lld x %d heads of %d, strides %lld and %lld",
+                int(r), (long long)tokens, heads, width, (long long)stride, (long long)head_stride);
   return FADAM_OK;
 }
 
