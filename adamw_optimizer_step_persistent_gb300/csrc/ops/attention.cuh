@@ -70,6 +70,17 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, int columns) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 
+// One lane of a whole warp, always the same one.  (The compiler knows it for
+// one: tensor-core instructions behind it take their operands from uniform
+// registers as they are; behind lane == 0 each cost 85 to 130 cycles.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // D (+)= A B, both 16-bit in shared memory.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -125,13 +136,14 @@ __device__ __forceinline__ uint32_t instruction(int n) {
 }
 
 // D[128, 128] = A B^T over `steps` 16s of a head's elements.
-template <class T>
+template <class T, int C>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, int steps) {
   const uint64_t da = tile_desc<false>(a), db = tile_desc<false>(b);
   const uint32_t idesc = instruction<T, false>(kRows);
-  for (int k = 0; k < steps; ++k) {
+#pragma unroll
+  for (int k = 0; k < C * kChunk / 16; ++k) {
     const uint64_t at = (k / 4) * (kBoxBytes >> 4) + (k % 4) * 2;  // 16 elements on: 32 bytes, or the next box
-    mma(d, da + at, db + at, idesc, k > 0);
+    if (k < steps) mma(d, da + at, db + at, idesc, k > 0);
   }
 }
 

@@ -24,7 +24,7 @@
 
 namespace fadam_ops {
 
-constexpr int kBackwardThreads = 384;  // 8 warps for p and ds, one that multiplies, one that loads, two idle
+constexpr int kBackwardThreads = 384;  // 8 warps for p and ds, two that multiply, one that loads, one idle
 // Tiles in flight of what a kernel walks over: X is needed by the scores and by
 // the product with ds, Y by grad_out . v (and the product with p).
 constexpr int kRingX = 3, kRingY = 2;
@@ -70,7 +70,7 @@ struct Backward {
 
   // Sets up barriers and tensor memory.  False when shared memory does not
   // start on 1024 bytes, as the swizzle needs.
-  __device__ __forceinline__ bool begin(unsigned char* smem, const AttentionArgs& g) {
+  __device__ __forceinline__ bool begin(unsigned char* smem, const AttentionArgs& g, int y_products) {
     own0 = shared_addr(smem);
     if (own0 & 1023) {
       if (threadIdx.x == 0) atomicExch(g.status, FADAM_ECUDA);
@@ -83,14 +83,14 @@ struct Backward {
     bars = &extra->bars;
     if (threadIdx.x == 0) {
       bar_init(shared_addr(&bars->own_full), 1);
-      bar_init(shared_addr(&bars->done), 1);
+      bar_init(shared_addr(&bars->done), 2);  // both multiplying warps
       for (int i = 0; i < kRingX; ++i) {
         bar_init(shared_addr(&bars->x_full[i]), 1);
-        bar_init(shared_addr(&bars->x_empty[i]), 1);
+        bar_init(shared_addr(&bars->x_empty[i]), 2);  // by both of its products
       }
       for (int i = 0; i < kRingY; ++i) {
         bar_init(shared_addr(&bars->y_full[i]), 1);
-        bar_init(shared_addr(&bars->y_empty[i]), 1);
+        bar_init(shared_addr(&bars->y_empty[i]), y_products);
       }
       bar_init(shared_addr(&bars->scores), 1);
       bar_init(shared_addr(&bars->dots), 1);
@@ -150,10 +150,11 @@ struct Backward {
       bar_expect(bar, kTile + y_extra);
       load_y(i, y_at(i), sy, bar);
     }
-    // no copy is in flight when the CTA ends
-    bar_wait(own, 0, status);
-    for (int k = i < kRingX ? 0 : i - kRingX; k < i; ++k) wait_x(k, status);
-    for (int k = i < kRingY ? 0 : i - kRingY; k < i; ++k) wait_y(k, status);
+    // every copy has landed and been used when the CTA ends
+    for (int k = i < kRingX ? 0 : i - kRingX; k < i; ++k)
+      bar_wait(shared_addr(&bars->x_empty[k % kRingX]), unsigned(k / kRingX) & 1, status);
+    for (int k = i < kRingY ? 0 : i - kRingY; k < i; ++k)
+      bar_wait(shared_addr(&bars->y_empty[k % kRingY]), unsigned(k / kRingY) & 1, status);
   }
 };
 
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   using B = Backward<T, C>;
   extern __shared__ __align__(1024) unsigned char smem[];
   B b;
-  if (!b.begin(smem, g)) return;
+  if (!b.begin(smem, g, 2)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   const auto query_tile = [&](int i) { return first + i % turns; };
 
   if (warp >= 8) keep_registers<kOtherRegisters>();
-  if (warp >= 10) {
+  if (warp == 11) {
   } else if (warp == 9) {
     if (lane == 0 && n > 0) {
       const int64_t pitch = int64_t(g.tiles) * kRows;
@@ -245,8 +246,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             load_bytes(shared_addr(b.extra->lse[slot]), lse + head * pitch + at, kRows * 4, bar);
           });
     }
-  } else if (warp == 8) {
+  } else if (warp == 8 || warp == 10) {
+    // scores and grad_v; grad_out . v and grad_k: two warps, two chains
     if (n > 0) {
+      const bool dots = warp == 10;
       const int steps = (g.width + 15) / 16, width = steps * 16;
       int inside_lo = 0, inside_hi = g.tiles * kRows;
       if (g.documents) {
@@ -257,46 +260,37 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         const int from = query_tile(i) * kRows;
         if (from < inside_lo || from + kRows > inside_hi) zero_rows<C>(at, inside_lo - from, inside_hi - from);
       };
-      const auto scores = [&](int i) {
-        if (!b.wait_x(i, status)) return false;
+      const uint32_t at = tmem + (dots ? kColumnsDots : kColumnsS), to = tmem + (dots ? kColumnsB : kColumnsA);
+      const uint32_t own = dots ? b.own1 : b.own0, bar_at = shared_addr(dots ? &bars->dots : &bars->scores);
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status);
+      // (rows outside all documents reach only columns that are masked)
+      const auto inner = [&](int i) {
+        ok = dots ? b.wait_y(i, status) : b.wait_x(i, status);
+        if (!ok) return;
         fence_after_sync();
-        clean(b.x_at(i), i);
-        if (lane == 0) {
-          mma_scores<T>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
-          commit(shared_addr(&bars->scores));
+        if (elect_one()) {
+          mma_scores<T, C>(at, own, dots ? b.y_at(i) : b.x_at(i), steps);
+          commit(bar_at);
+          commit(shared_addr(dots ? &bars->y_empty[i % kRingY] : &bars->x_empty[i % kRingX]));
         }
-        return true;
       };
-      const auto dots = [&](int i) {
-        if (!b.wait_y(i, status)) return false;
-        fence_after_sync();
-        clean(b.y_at(i), i);
-        if (lane == 0) {
-          mma_scores<T>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
-          commit(shared_addr(&bars->dots));
-        }
-        return true;
-      };
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && scores(0) && dots(0);
+      if (ok) inner(0);
       for (int i = 0; ok && i < n; ++i) {
-        ok = bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
+        ok = dots ? b.wait_x(i, status) : b.wait_y(i, status);
+        if (!ok) break;
+        const uint32_t rows = dots ? b.x_at(i) : b.y_at(i);
+        ok = dots ? bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status)
+                  : bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
-        if (lane == 0) {
-          mma_rows<T>(tmem + kColumnsA, tmem + kColumnsS, tmem + kColumnsS + 64, b.y_at(i), width, i > 0);
-          commit(shared_addr(&bars->y_empty[i % kRingY]));
+        clean(rows, i);
+        if (elect_one()) {
+          mma_rows<T>(to, at, at + 64, rows, width, i > 0);
+          commit(shared_addr(dots ? &bars->x_empty[i % kRingX] : &bars->y_empty[i % kRingY]));
         }
-        if (i + 1 < n && !(ok = scores(i + 1))) break;
-        ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
-        if (!ok) break;
-        fence_after_sync();
-        if (lane == 0) {
-          mma_rows<T>(tmem + kColumnsB, tmem + kColumnsDots, tmem + kColumnsDots + 64, b.x_at(i), width, i > 0);
-          commit(shared_addr(&bars->x_empty[i % kRingX]));
-        }
-        if (i + 1 < n) ok = dots(i + 1);
+        if (i + 1 < n) inner(i + 1);
       }
-      if (ok && lane == 0) commit(shared_addr(&bars->done));
+      if (ok && elect_one()) commit(shared_addr(&bars->done));
     }
   } else {
     take_registers<kScoreRegisters>();
@@ -425,7 +419,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   using B = Backward<T, C>;
   extern __shared__ __align__(1024) unsigned char smem[];
   B b;
-  if (!b.begin(smem, g)) return;
+  if (!b.begin(smem, g, 1)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
@@ -441,7 +435,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   const int first = reach.first(), n = reach.last() - first;
 
   if (warp >= 8) keep_registers<kOtherRegisters>();
-  if (warp >= 10) {
+  if (warp == 11) {
   } else if (warp == 9) {
     if (lane == 0 && n > 0) {
       const int kv = head / g.group;
@@ -455,6 +449,25 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
           [&](int i, uint32_t dst, int, uint32_t bar) { load_head<C>(dst, &maps.v, kv, (first + i) * kRows, bar); });
     }
   } else if (warp == 8) {
+    // scores
+    if (n > 0) {
+      const int steps = (g.width + 15) / 16;
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status);
+      for (int i = 0; ok && i < n; ++i) {
+        ok = b.wait_x(i, status) &&
+             (i == 0 || bar_wait(shared_addr(&bars->scores_read), unsigned(i - 1) & 1, status));
+        if (!ok) break;
+        fence_after_sync();
+        if (elect_one()) {
+          mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
+          commit(shared_addr(&bars->scores));
+          commit(shared_addr(&bars->x_empty[i % kRingX]));
+        }
+      }
+      if (ok && elect_one()) commit(shared_addr(&bars->done));
+    }
+  } else if (warp == 10) {
+    // grad_out . v and grad_q
     if (n > 0) {
       const int steps = (g.width + 15) / 16, width = steps * 16;
       int inside_lo = 0, inside_hi = g.tiles * kRows;
@@ -462,45 +475,34 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         inside_lo = __ldg(g.documents);
         inside_hi = __ldg(g.documents + g.n_documents);
       }
-      const auto scores = [&](int i) {
-        if (!b.wait_x(i, status)) return false;
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status);
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i < n) {
+          ok = b.wait_y(i, status) &&
+               (i == 0 || bar_wait(shared_addr(&bars->dots_read), unsigned(i - 1) & 1, status));
+          if (!ok) break;
+          fence_after_sync();
+          if (elect_one()) {
+            mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
+            commit(shared_addr(&bars->dots));
+            commit(shared_addr(&bars->y_empty[i % kRingY]));
+          }
+        }
+        if (i == 0) continue;
+        const int k = i - 1, from = (first + k) * kRows;
+        ok = b.wait_x(k, status) &&
+             bar_wait(shared_addr(&bars->slopes[k & 1]), unsigned(k / 2) & 1, status);
+        if (!ok) break;
         fence_after_sync();
-        const int from = (first + i) * kRows;
         if (from < inside_lo || from + kRows > inside_hi)
-          zero_rows<C>(b.x_at(i), inside_lo - from, inside_hi - from);
-        if (lane == 0) {
-          mma_scores<T>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
-          commit(shared_addr(&bars->scores));
-        }
-        return true;
-      };
-      const auto dots = [&](int i) {
-        if (!b.wait_y(i, status)) return false;
-        fence_after_sync();
-        if (lane == 0) {
-          mma_scores<T>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
-          commit(shared_addr(&bars->dots));
-          commit(shared_addr(&bars->y_empty[i % kRingY]));
-        }
-        return true;
-      };
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && scores(0) && dots(0);
-      for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) {
-          if (!(ok = bar_wait(shared_addr(&bars->scores_read), unsigned(i) & 1, status))) break;
-          if (!(ok = scores(i + 1))) break;
-          if (!(ok = bar_wait(shared_addr(&bars->dots_read), unsigned(i) & 1, status))) break;
-          if (!(ok = dots(i + 1))) break;
-        }
-        if (!(ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status))) break;
-        fence_after_sync();
-        if (lane == 0) {
-          const uint32_t ds = tmem + kColumnsA + (i & 1) * 64;
-          mma_rows<T>(tmem + kColumnsB, ds, ds + 32, b.x_at(i), width, i > 0);
-          commit(shared_addr(&bars->x_empty[i % kRingX]));
+          zero_rows<C>(b.x_at(k), inside_lo - from, inside_hi - from);
+        if (elect_one()) {
+          const uint32_t ds = tmem + kColumnsA + (k & 1) * 64;
+          mma_rows<T>(tmem + kColumnsB, ds, ds + 32, b.x_at(k), width, k > 0);
+          commit(shared_addr(&bars->x_empty[k % kRingX]));
         }
       }
-      if (ok && lane == 0) commit(shared_addr(&bars->done));
+      if (ok && elect_one()) commit(shared_addr(&bars->done));
     }
   } else {
     take_registers<kScoreRegisters>();
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         }
         p[c / 2] = pack2<E>(e[0], e[1]);
       }
-      // (scores of i come behind the product with ds of i - 2: its place is free)
+      // (grad_out . v of i comes behind the product with ds of i - 2: its place is free)
       tmem_store32(lanes + kColumnsA + (i & 1) * 64 + half * 32, p);
       tmem_stored();
       fence_before_sync();

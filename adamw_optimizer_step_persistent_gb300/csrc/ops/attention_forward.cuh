@@ -5,8 +5,11 @@
 // cores, then a lane to a query takes the row's maximum, exponentials and sum
 // in registers, hands the exponentials in 16 bits back to tensor memory, and
 // O += P V.  The two tiles take turns: while four warps work on one tile's
-// scores, the tensor cores work for the other.  Tensor memory: scores and O of
-// both tiles (4 x 128 columns); P lies over the scores it came from.
+// scores, the tensor cores work for the other, each fed by a warp of its own
+// (the tensor cores take no more than two or three instructions ahead, so that
+// one warp for both left them idle during its waits: 4000 cycles a turn of both
+// tiles, of which the products need 2236).  Tensor memory: scores and O of both
+// tiles (4 x 128 columns); P lies over the scores it came from.
 //
 // The running maximum of a row need not be its true maximum: any reference
 // gives the same quotient.  So O (in tensor memory) and the sum are only
@@ -19,7 +22,7 @@
 
 namespace fadam_ops {
 
-constexpr int kForwardThreads = 384;  // 2 x 4 warps for the scores, one that multiplies, one that loads, two idle
+constexpr int kForwardThreads = 384;  // 2 x 4 warps for the scores, two that multiply, one that loads, one idle
 constexpr int kRing = 4;              // tiles of keys or values in flight
 constexpr float kGrowth = 8.0f;
 
@@ -53,7 +56,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       bar_init(shared_addr(&bars->full[i]), 1);
-      bar_init(shared_addr(&bars->empty[i]), 1);
+      bar_init(shared_addr(&bars->empty[i]), 2);  // both multiplying warps
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -83,10 +86,9 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
   const int first = min(reach[0].first(), reach[1].first());
   const int last = max(reach[0].hi > reach[0].lo ? reach[0].last() : 0,
                        reach[1].hi > reach[1].lo ? reach[1].last() : 0);
-  const auto sees = [&](int t, int j) { return j >= reach[t].first() && j < reach[t].last(); };
 
   if (warp >= 8) keep_registers<kOtherRegisters>();
-  if (warp >= 10) {
+  if (warp == 11) {
   } else if (warp == 9) {
     // ---- loads: the queries, then keys and values in turn
     if (lane == 0 && first < last) {
@@ -117,69 +119,65 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
         if (j == first) queries(1);
         if (ok) next(&maps.v, j);
       }
-      // no copy is in flight when the CTA ends
+      // every copy has landed and been used when the CTA ends
       for (int i = n < kRing ? 0 : n - kRing; i < n; ++i)
-        bar_wait(shared_addr(&bars->full[i % kRing]), unsigned(i / kRing) & 1, g.status);
+        bar_wait(shared_addr(&bars->empty[i % kRing]), unsigned(i / kRing) & 1, g.status);
     }
-  } else if (warp == 8) {
-    // ---- tensor cores
+  } else if (warp == 8 || warp == 10) {
+    // ---- tensor cores: a warp to a tile of queries
+    const int t = warp == 8 ? 0 : 1;
+    const Reach mine = t ? reach[1] : reach[0];
     if (first < last) {
-      const int steps = (g.width + 15) / 16, n = (g.width + 15) / 16 * 16;
+      const int steps = (g.width + 15) / 16, n = steps * 16;
       int inside_lo = 0, inside_hi = g.tiles * kRows;
       if (g.documents) {
         inside_lo = __ldg(g.documents);
         inside_hi = __ldg(g.documents + g.n_documents);
       }
+      const uint32_t queries = q_tiles + t * kTile, at_s = tmem + t * kRows, at_o = tmem + (2 + t) * kRows;
+      const uint32_t bar_scores = shared_addr(&bars->scores[t]), bar_weights = shared_addr(&bars->weights[t]);
+      const int begin = mine.first(), end = mine.last();
       bool ok = true;
       const auto full = [&](int i) {
         ok = ok && bar_wait(shared_addr(&bars->full[i % kRing]), unsigned(i / kRing) & 1, g.status);
         fence_after_sync();
       };
-      const auto scores = [&](int t, int j) {
-        if (!ok || !sees(t, j)) return;
-        if (j == reach[t].first()) {
-          ok = bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
-          if (!ok) return;
-        }
-        if (lane == 0) {
-          mma_scores<T>(tmem + t * kRows, q_tiles + t * kTile, ring + 2 * (j - first) % kRing * kTile, steps);
-          commit(shared_addr(&bars->scores[t]));
+      // keys of j: the scores' products, and this warp's part in giving their place back
+      const auto scores = [&](int j) {
+        const int at = 2 * (j - first);
+        full(at);
+        if (ok && j == begin) ok = bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
+        if (!ok) return;
+        if (elect_one()) {
+          if (j >= begin && j < end) {
+            mma_scores<T, C>(at_s, queries, ring + at % kRing * kTile, steps);
+            commit(bar_scores);
+          }
+          commit(shared_addr(&bars->empty[at % kRing]));
         }
       };
-      full(0);
-      scores(0, first);
-      scores(1, first);
-      if (ok && lane == 0) commit(shared_addr(&bars->empty[0]));
+      scores(first);
       for (int j = first; ok && j < last; ++j) {
-        const int v = 2 * (j - first) + 1;
-        const uint32_t values = ring + v % kRing * kTile;
-        full(v);
+        const int at = 2 * (j - first) + 1;
+        const uint32_t values = ring + at % kRing * kTile;
+        full(at);
         if (!ok) break;
-        if (j * kRows < inside_lo || (j + 1) * kRows > inside_hi)
-          zero_rows<C>(values, inside_lo - j * kRows, inside_hi - j * kRows);
-        const bool more = j + 1 < last;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (sees(t, j)) {
-            const int turn = j - reach[t].first();
-            ok = ok && bar_wait(shared_addr(&bars->weights[t]), unsigned(turn) & 1, g.status);
-            if (!ok) break;
-            fence_after_sync();
-            if (lane == 0) {
-              const uint32_t p = tmem + t * kRows;
-              mma_rows<T>(tmem + (2 + t) * kRows, p, p + 32, values, n, turn > 0);
-              if (j + 1 == reach[t].last()) commit(shared_addr(&bars->done[t]));
-            }
-          }
-          if (more) {
-            if (t == 0) full(v + 1);
-            scores(t, j + 1);
-          }
+        const bool here = j >= begin && j < end;
+        if (here) {
+          if (j * kRows < inside_lo || (j + 1) * kRows > inside_hi)
+            zero_rows<C>(values, inside_lo - j * kRows, inside_hi - j * kRows);
+          ok = bar_wait(bar_weights, unsigned(j - begin) & 1, g.status);
+          if (!ok) break;
+          fence_after_sync();
         }
-        if (ok && lane == 0) {
-          commit(shared_addr(&bars->empty[v % kRing]));
-          if (more) commit(shared_addr(&bars->empty[(v + 1) % kRing]));
+        if (elect_one()) {
+          if (here) {
+            mma_rows<T>(at_o, at_s, at_s + 32, values, n, j > begin);
+            if (j + 1 == end) commit(shared_addr(&bars->done[t]));
+          }
+          commit(shared_addr(&bars->empty[at % kRing]));
         }
+        if (j + 1 < last) scores(j + 1);
       }
     }
   } else {
