@@ -1,7 +1,6 @@
 // Attention: argument checks, workspaces, tensor maps, and the small kernels
 // beside the tensor-core ones.
 #include "attention.cuh"
-#include "rows.cuh"
 
 namespace fadam_ops {
 namespace {
@@ -39,9 +38,10 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- the rows' lse and delta for the backward pass -------------------------------------------
 
-// delta = grad_out . out of a token and head, 16 lanes to a row, and lse in
-// units of log 2 less the lift of p's exponent.  Rows that see nothing, and
-// those up to a whole tile, get lse infinity: p is 0.
+// What is added to a row's scores, -lse in units of log 2 and the lift of p's
+// exponent, and to its grad_out . v: -delta = -grad_out . out, 16 lanes to a
+// row.  Rows that see nothing, and those up to a whole tile, get -infinity: p
+// is 0.
 constexpr int kStatRows = 64;  // tokens of a CTA, of one head: 16 at a time
 template <class E, bool kPeak>
 __global__ void __launch_bounds__(kThreads)
@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kThreads)
     }
     const int t = token0 + r * 16 + group;
     if (lane == 0 && t < pitch) {
-      stats[int64_t(head) * pitch + t] = l[r] == -INFINITY ? INFINITY : l[r] * kLog2e - lift;
-      stats[int64_t(heads + head) * pitch + t] = delta;
+      stats[int64_t(head) * pitch + t] = l[r] == -INFINITY ? -INFINITY : lift - l[r] * kLog2e;
+      stats[int64_t(heads + head) * pitch + t] = -delta;
     }
   }
   if (kPeak) {

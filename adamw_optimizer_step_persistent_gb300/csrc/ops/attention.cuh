@@ -4,6 +4,7 @@
 
 #include "attention_internal.h"
 #include "ops_device.cuh"
+#include "rows.cuh"
 
 namespace fadam_ops {
 

@@ -158,34 +158,79 @@ struct Backward {
   }
 };
 
-// 64 columns of scores of a lane's row become p (times 2^lift) and, in place,
-// p times ds/d(q . k).  `apart`: the first column's place less the row's;
-// subtract(c): the column's (or row's) lse in units of log 2.  Columns outside
-// [lo, hi) are not seen.
-template <class E, class Lse>
-__device__ __forceinline__ void weights_of(float (&s)[64], uint32_t (&p)[32], const Scores& f, float apart,
-                                           bool whole, int lo, int hi, Lse lse) {
-  const float mul = f.cap != 0.0f ? 1.0f : f.mul;
+// 64 columns of scores of a lane's row become p (times 2^lift) in 16 bits and,
+// in place, p times ds/d(q . k).  lse(c): what is added to columns c and c + 1.
+// Columns outside [lo, hi) are not seen.
+template <class E, bool kCap, bool kMask, class Lse>
+__device__ __forceinline__ void weights_of(float (&s)[64], uint32_t (&p)[32], const Scores& f, float mul,
+                                           int lo, int hi, Lse lse) {
+  const Pair mul_pair = both(mul);
 #pragma unroll
   for (int c = 0; c < 64; c += 2) {
-    float w[2], d[2];
+    float slope[2] = {1.0f, 1.0f};
+    if constexpr (kCap)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float z = s[c + k];
-      d[k] = 1.0f;
-      if (f.cap != 0.0f) {
-        const float r = f.folded(z);
-        z = fmaf(-2.0f * f.cap, r, f.cap);
-        d[k] = 4.0f * r * (1.0f - r);
-      }
-      z = fmaf(z, mul, -lse(c + k));
-      if (f.slope != 0.0f) z = fmaf(-f.slope, fabsf(apart + float(c + k)), z);
-      w[k] = exp2_fast(z);
-      if (!whole) w[k] = c + k >= lo && c + k < hi ? w[k] : 0.0f;
-    }
+      for (int k = 0; k < 2; ++k) slope[k] = 4.0f * s[c + k] * (1.0f - s[c + k]);
+    Pair z = make_pair(s[c], s[c + 1]);
+    z = kCap ? fma2(z, both(-2.0f * f.cap), add2(both(f.cap), lse(c))) : fma2(z, mul_pair, lse(c));
+    const float2 e = split(z);
+    float w[2] = {exp2_fast(e.x), exp2_fast(e.y)};
+    if constexpr (kMask)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) w[k] = c + k >= lo && c + k < hi ? w[k] : 0.0f;
     p[c / 2] = pack2<E>(w[0], w[1]);
-    s[c] = w[0] * d[0];
-    s[c + 1] = w[1] * d[1];
+    s[c] = kCap ? w[0] * slope[0] : w[0];
+    s[c + 1] = kCap ? w[1] * slope[1] : w[1];
+  }
+}
+// `apart`: the first column's place less the row's.
+template <class E, class Lse>
+__device__ __forceinline__ void weights(float (&s)[64], uint32_t (&p)[32], const Scores& f, float apart,
+                                        bool whole, int lo, int hi, Lse lse) {
+  if (f.cap != 0.0f) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) s[c] = f.folded(s[c]);
+    if (f.slope != 0.0f) {
+      const auto lowered = [&](int c) {
+        const float2 l = split(lse(c));
+        return make_pair(fmaf(-f.slope, fabsf(apart + float(c)), l.x),
+                         fmaf(-f.slope, fabsf(apart + float(c + 1)), l.y));
+      };
+      if (whole) weights_of<E, true, false>(s, p, f, 1.0f, lo, hi, lowered);
+      else weights_of<E, true, true>(s, p, f, 1.0f, lo, hi, lowered);
+    } else if (whole) {
+      weights_of<E, true, false>(s, p, f, 1.0f, lo, hi, lse);
+    } else {
+      weights_of<E, true, true>(s, p, f, 1.0f, lo, hi, lse);
+    }
+    return;
+  }
+  float mul = f.mul;
+  if (f.slope != 0.0f) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c] * f.mul);
+    mul = 1.0f;
+  }
+  if (whole) weights_of<E, false, false>(s, p, f, mul, lo, hi, lse);
+  else weights_of<E, false, true>(s, p, f, mul, lo, hi, lse);
+}
+
+// 32 columns of ds: p (at s) times (grad_out . v - delta), `delta(c)` added to
+// columns c and c + 1; fp16 times `factor`.
+template <class T, bool kMask, class Delta>
+__device__ __forceinline__ void slopes_of(const float* s, const float* d, uint32_t* p, float factor, int lo,
+                                          int hi, Delta delta) {
+  const Pair factor_pair = both(factor);
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    Pair e = mul2(make_pair(s[c], s[c + 1]), add2(make_pair(d[c], d[c + 1]), delta(c)));
+    if constexpr (T::code == FADAM_DT_F16) e = mul2(e, factor_pair);
+    float2 v = split(e);
+    if constexpr (kMask) {
+      v.x = c >= lo && c < hi ? v.x : 0.0f;
+      v.y = c + 1 >= lo && c + 1 < hi ? v.y : 0.0f;
+    }
+    p[c / 2] = pack2<typename T::type>(v.x, v.y);
   }
 }
 
@@ -315,8 +360,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         tmem_load32(at_s, s);
         tmem_load32(at_s + 32, s + 32);
         tmem_wait<64>(s);
-        const float* lse = b.extra->lse[i % kRingY] + half * 64;
-        weights_of<E>(s, p, f, float(at - (key0 + row)), whole, lo, hi, [&](int c) { return lse[c]; });
+        const Pair* lse = reinterpret_cast<const Pair*>(b.extra->lse[i % kRingY] + half * 64);
+        weights<E>(s, p, f, float(at - (key0 + row)), whole, lo, hi, [&](int c) { return lse[c / 2]; });
         tmem_store32(at_s, p);
         tmem_stored();
         fence_before_sync();
@@ -326,23 +371,16 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         ok = bar_wait(bar_dots, unsigned(i) & 1, status) && b.wait_x(i, status);
         if (!ok) break;
         fence_after_sync();
-        const float* delta = b.extra->delta[i % kRingX] + half * 64;
+        const Pair* delta = reinterpret_cast<const Pair*>(b.extra->delta[i % kRingX] + half * 64);
+        float d[64];
+        tmem_load32(at_dots, d);
+        tmem_load32(at_dots + 32, d + 32);
+        tmem_wait<64>(d);
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 32) {
-          float d[32];
-          tmem_load32(at_dots + c0, d);
-          tmem_wait<32>(d);
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float e[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              e[k] = s[c0 + c + k] * (d[c + k] - delta[c0 + c + k]);
-              if (T::code == FADAM_DT_F16) e[k] *= factor;
-              if (!whole) e[k] = c0 + c + k >= lo && c0 + c + k < hi ? e[k] : 0.0f;
-            }
-            p[(c0 + c) / 2] = pack2<E>(e[0], e[1]);
-          }
+          const auto of = [&](int c) { return delta[(c0 + c) / 2]; };
+          if (whole) slopes_of<T, false>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
+          else slopes_of<T, true>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
         }
         tmem_store32(at_dots, p);
         tmem_stored();
@@ -514,8 +552,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     const uint32_t bar_dots_read = shared_addr(&bars->dots_read);
     const float factor = ds_factor<T>(g) * exp2f(-kLiftBits<T>);
     const int64_t pitch = int64_t(g.tiles) * kRows;
-    const float lse = g.stats[head * pitch + query0 + row];
-    const float delta = g.stats[(g.heads + head) * pitch + query0 + row];
+    const Pair lse = both(g.stats[head * pitch + query0 + row]);
+    const Pair delta = both(g.stats[(g.heads + head) * pitch + query0 + row]);
     const Scores f(g, head);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
@@ -533,7 +571,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
       fence_before_sync();
       __syncwarp();
       if (lane == 0) bar_arrive(bar_scores_read);
-      weights_of<E>(s, p, f, float(at - (query0 + row)), whole, lo, hi, [&](int) { return lse; });
+      weights<E>(s, p, f, float(at - (query0 + row)), whole, lo, hi, [&](int) { return lse; });
 
       ok = bar_wait(bar_dots, unsigned(i) & 1, status);
       if (!ok) break;
@@ -546,15 +584,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar_dots_read);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        float e[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          e[k] = s[c + k] * (d[c + k] - delta);
-          if (T::code == FADAM_DT_F16) e[k] *= factor;
-          if (!whole) e[k] = c + k >= lo && c + k < hi ? e[k] : 0.0f;
-        }
-        p[c / 2] = pack2<E>(e[0], e[1]);
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        const auto of = [&](int) { return delta; };
+        if (whole) slopes_of<T, false>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
+        else slopes_of<T, true>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
       }
       // (grad_out . v of i comes behind the product with ds of i - 2: its place is free)
       tmem_store32(lanes + kColumnsA + (i & 1) * 64 + half * 32, p);

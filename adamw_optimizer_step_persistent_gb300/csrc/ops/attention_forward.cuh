@@ -220,9 +220,11 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
 #pragma unroll
         for (int c = 0; c < kRows; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
       }
-      float m[4] = {s[0], s[1], s[2], s[3]};
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 4; c < kRows; ++c) m[c % 4] = fmaxf(m[c % 4], s[c]);
+      for (int c = 0; c < kRows; c += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], s[c + k]), s[c + 4 + k]);
       const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mul;
       if (__any_sync(~0u, most > top + kGrowth)) {
         // (scores of j come behind the product with the values of j - 1: O is at rest)
@@ -244,21 +246,21 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
         }
       }
       const float from = top == -INFINITY ? 0.0f : top - kLift;
-      float part[4] = {};
+      const Pair mul_pair = both(mul), less = both(-from);
+      Pair part[2] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t p[32];
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
-          const float a = exp2_fast(fmaf(s[h * 64 + c], mul, -from));
-          const float b = exp2_fast(fmaf(s[h * 64 + c + 1], mul, -from));
-          part[c % 4] += a;
-          part[c % 4 + 1] += b;
+          const float2 z = split(fma2(make_pair(s[h * 64 + c], s[h * 64 + c + 1]), mul_pair, less));
+          const float a = exp2_fast(z.x), b = exp2_fast(z.y);
+          part[c / 2 % 2] = add2(part[c / 2 % 2], make_pair(a, b));
           p[c / 2] = pack2<E>(a, b);
         }
         tmem_store32(at_s + h * 32, p);
       }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      sum += sum2(add2(part[0], part[1]));
       tmem_stored();
       fence_before_sync();
       __syncwarp();

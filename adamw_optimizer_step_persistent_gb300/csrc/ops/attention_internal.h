@@ -28,7 +28,7 @@ struct AttentionArgs {
   int* status;
 
   // backward
-  float* stats;              // [2][heads][tiles * 128]: lse in units of log 2, then delta
+  float* stats;              // [2][heads][tiles * 128]: -lse in units of log 2, then -delta
   unsigned* peak;            // bits of the largest magnitude in grad_out, the f16 products' scale
   float* parts;              // fp32 sums of grad_k and grad_v by splits of the query heads
   int splits;
