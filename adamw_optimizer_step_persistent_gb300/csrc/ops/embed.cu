@@ -17,6 +17,37 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kRange = 1024;    // most tokens of the vocabulary that one CTA sorts by
 constexpr int kLongest = 64;    // most rows of a piece
+constexpr int kZeroBytes = 16384;  // of a row zeroed by one bulk copy
+
+// Eight elements in one access: 16 bytes, or 32 for fp32 (two of 16 would each
+// touch half of every 32-byte sector).
+template <class E>
+__device__ __forceinline__ Raw<E> load_eight(const E* p) {
+  if constexpr (sizeof(E) == 4) {
+    Raw<E> r;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]),
+                   "=r"(r.w[6]), "=r"(r.w[7])
+                 : "l"(p)
+                 : "memory");
+    return r;
+  } else {
+    return load_raw(p);
+  }
+}
+template <class E>
+__device__ __forceinline__ void store_eight(E* p, const Raw<E>& r) {
+  if constexpr (sizeof(E) == 4)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]),
+                 "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+                 : "memory");
+  else
+    store_raw(p, r);
+}
+// Whether rows of these can be accessed so.
+bool eights(const void* p, int64_t stride, int64_t width, int size) {
+  return width % 8 == 0 && !misaligned(p, 8 * size) && stride % 8 == 0;
+}
 
 // A thread's eight columns of a row: one aligned vector, or (rows that are not
 // whole vectors) every blockDim-th element, so that a warp's accesses coalesce.
@@ -34,7 +65,7 @@ struct Eight {
   template <class E>
   __device__ __forceinline__ void load(const E* row, Raw<E>& r) const {
     if constexpr (kWide) {
-      r = load_raw(row + col);
+      r = load_eight(row + col);
     } else {
       E e[8];
 #pragma unroll
@@ -45,7 +76,7 @@ struct Eight {
   template <class E>
   __device__ __forceinline__ void store(E* row, const Raw<E>& r) const {
     if constexpr (kWide) {
-      store_raw(row + col, r);
+      store_eight(row + col, r);
     } else {
       E e[8];
       memcpy(e, &r, sizeof r);
@@ -132,7 +163,11 @@ struct SortArgs {
 template <class Out, bool kWide, bool kKeep>
 __global__ void __launch_bounds__(kSortThreads)
     sort_kernel(const SortArgs a, Out* out, int64_t out_ld, int width) {
-  extern __shared__ int counts[];  // [kSortWarps][range], then [range] of all warps
+  // kZeroBytes of zeros where rows are written, then counts [kSortWarps][range]
+  // and [range] of all warps
+  extern __shared__ __align__(16) unsigned char sort_smem[];
+  constexpr int kZeros = kKeep || !kWide ? 0 : kZeroBytes;
+  int* counts = reinterpret_cast<int*>(sort_smem + kZeros);
   __shared__ int warp_sum[kSortWarps];
   __shared__ int below;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -140,6 +175,11 @@ __global__ void __launch_bounds__(kSortThreads)
   const int mine = int(min(int64_t(a.range), a.vocab - low));
   int* total = counts + kSortWarps * a.range;
   for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) counts[i] = 0;
+  if (kZeros) {
+    for (int i = threadIdx.x; i < kZeros / 16; i += kSortThreads)
+      reinterpret_cast<uint4*>(sort_smem)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   if (threadIdx.x == 0) below = 0;
   __syncthreads();
   chain_wait();
@@ -216,12 +256,18 @@ __global__ void __launch_bounds__(kSortThreads)
       if (total[r]) continue;
       Out* row = out + (low + r) * out_ld;
       if constexpr (kWide) {
-        const Raw<Out> zero = zero_raw<Out>();
-        for (int c = lane * 8; c < width; c += 256) store_raw(row + c, zero);
+        // bulk copies of zeros, by a lane of its own each
+        const int64_t bytes = int64_t(width) * sizeof(Out);
+        for (int64_t c = int64_t(lane) * kZeroBytes; c < bytes; c += 32 * kZeroBytes)
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                           reinterpret_cast<unsigned char*>(row) + c),
+                       "r"(shared_addr(sort_smem)), "r"(int(min(int64_t(kZeroBytes), bytes - c)))
+                       : "memory");
       } else {
         for (int c = lane; c < width; c += 32) row[c] = from_float<Out>(0.0f);
       }
     }
+    if (kWide) asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
   }
 }
 
@@ -255,10 +301,10 @@ __device__ __forceinline__ void put(const Eight<kWide>& at, Out* row, const floa
   at.store(row, narrow<Out>(v));
 }
 
-// A piece's rows, four loads in flight; a token's sum is written when its last
+// A piece's rows, several loads in flight; a token's sum is written when its last
 // row is in the piece and its first one too, else kept for join_kernel.
 template <class E, class Out, bool kWide, bool kKeep>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kWide ? 4 : 2)
     sum_kernel(const SumArgs a, const E* grad, Out* out) {
   __shared__ int rows[kLongest];
   __shared__ int ids[kLongest];
@@ -285,7 +331,7 @@ __global__ void __launch_bounds__(kThreads)
   float sum[8] = {};
   int id = ids[0];
   bool cut = cut_begin;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = kWide ? 4 : 2;
   for (int i = 0; i < many; i += kAhead) {
     Raw<E> raw[kAhead];
 #pragma unroll
@@ -346,12 +392,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumArgs a, Out* ou
 #pragma unroll
   for (int c = 0; c < 8; ++c) sum[c] = carry[(int64_t(piece) * 2 + 1) * a.carry_ld + c];
   const int until = (last + a.piece - 1) / a.piece;
-#pragma unroll 4
-  for (int p = int(piece) + 1; p < until; ++p) {
-    const float4* from = reinterpret_cast<const float4*>(carry + int64_t(p) * 2 * a.carry_ld);
-    const float4 x = from[0], y = from[1];
-    sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
-    sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
+  constexpr int kAhead = 8;  // loads in flight
+  for (int p = int(piece) + 1; p < until; p += kAhead) {
+    Raw<float> raw[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      raw[k] = p + k < until ? load_eight(carry + int64_t(p + k) * 2 * a.carry_ld) : zero_raw<float>();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] += __uint_as_float(raw[k].w[c]);
   }
   put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
 }
@@ -360,8 +410,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const SumArgs a, Out* ou
 
 template <class E, class Out>
 fadam_status forward(const fadam_embed& d, cudaStream_t stream) {
-  const bool wide = d.width % 8 == 0 && !misaligned(d.weight, 16) && !misaligned(d.out, 16) &&
-                    d.weight_stride * sizeof(E) % 16 == 0 && d.out_stride * sizeof(Out) % 16 == 0;
+  const bool wide = eights(d.weight, d.weight_stride, d.width, sizeof(E)) &&
+                    eights(d.out, d.out_stride, d.width, sizeof(Out));
   const Parts p = parts_of(d.width);
   // four rows to a thread where that leaves every SM four CTAs
   const bool many = ceil_div(d.rows, 4) * p.count >= 152 * 4;
@@ -413,11 +463,12 @@ fadam_status gradient(const fadam_embed_grad& d, const Layout& l, const DeviceFa
   s.order = l.order;
   s.starts = l.starts;
   auto* sort = sort_kernel<Out, kWide, kKeep>;
-  constexpr int kMostShared = (kSortWarps + 1) * kRange * 4;
+  constexpr int kZeros = kKeep || !kWide ? 0 : kZeroBytes;
+  constexpr int kMostShared = kZeros + (kSortWarps + 1) * kRange * 4;
   const cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   fadam_status st = launch_chained("token sort launch", sort, ceil_div(d.vocab, s.range), kSortThreads,
-                                   size_t(kSortWarps + 1) * s.range * 4, stream, s, out, d.out_stride,
+                                   kZeros + size_t(kSortWarps + 1) * s.range * 4, stream, s, out, d.out_stride,
                                    int(d.width));
   if (st) return st;
   const Parts p = parts_of(d.width);
@@ -444,8 +495,8 @@ fadam_status gradient(const fadam_embed_grad& d, const Layout& l, const DeviceFa
 template <class E, class Out>
 fadam_status gradient(const fadam_embed_grad& d, const Layout& l, const DeviceFacts& dev,
                       cudaStream_t stream) {
-  const bool wide = d.width % 8 == 0 && !misaligned(d.grad, 16) && !misaligned(d.out, 16) &&
-                    d.grad_stride * sizeof(E) % 16 == 0 && d.out_stride * sizeof(Out) % 16 == 0;
+  const bool wide = eights(d.grad, d.grad_stride, d.width, sizeof(E)) &&
+                    eights(d.out, d.out_stride, d.width, sizeof(Out));
   const bool keep = (d.flags & FADAM_EMBED_ACCUMULATE) != 0;
   if (wide)
     return keep ? gradient<E, Out, true, true>(d, l, dev, stream)
