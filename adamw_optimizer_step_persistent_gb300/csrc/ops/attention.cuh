@@ -8,10 +8,14 @@
 
 namespace fadam_ops {
 
-// Registers of a thread: 168 as launched (384 threads in 65536); the eight warps
-// that hold scores take over what the other four do without.
-constexpr int kLaunchRegisters = 168, kScoreRegisters = 224, kOtherRegisters = 56;
-static_assert(2 * kScoreRegisters + kOtherRegisters == 3 * kLaunchRegisters, "no more than launched with");
+// Sixteen warps hold scores, four more multiply and load.  A thread's registers
+// are 96 as launched (640 threads in 65536); the sixteen take over what the
+// four do without.
+constexpr int kScoreWarps = 16, kAttentionThreads = (kScoreWarps + 4) * 32;
+constexpr int kMultiply = kScoreWarps, kLoad = kMultiply + 1, kMultiply2 = kMultiply + 2, kIdle = kMultiply + 3;
+constexpr int kLaunchRegisters = 96, kScoreRegisters = 112, kOtherRegisters = 32;
+static_assert(4 * kScoreRegisters + kOtherRegisters == 5 * kLaunchRegisters, "no more than launched with");
+static_assert(kLaunchRegisters * kAttentionThreads <= 65536, "an SM's registers");
 // A kernel built with fewer would wait for its share of registers for ever.
 template <auto kKernel>
 fadam_status launched_with(const char* what) {
@@ -54,9 +58,19 @@ __device__ __forceinline__ void wait_stores() {
 }
 // What this thread wrote to shared memory is there for bulk copies and tensor cores.
 __device__ __forceinline__ void fence_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// A barrier of a group of warps.
+// A barrier of a group of warps; and one that says whether any thread's `x` holds.
 __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool group_any(int id, int threads, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(uint32_t(x))
+      : "memory");
+  return any != 0;
 }
 
 // ---- tensor cores ----------------------------------------------------------------------
@@ -116,6 +130,23 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
       "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -148,15 +179,15 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, i
   }
 }
 
-// D[128, n] (+)= A B over the tile's 128 rows, A in tensor memory: 64 elements
-// from `a`, 64 from `a2`.
-template <class T>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t a2, uint32_t b, int n, bool add) {
+// D[128, n] (+)= A B over the tile's 128 rows, A in tensor memory: kEach
+// elements (half as many columns) in a place, the places `apart`.
+template <class T, int kEach>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, int apart, uint32_t b, int n, bool add) {
   const uint64_t db = tile_desc<true>(b);
   const uint32_t idesc = instruction<T, true>(n);
 #pragma unroll
   for (int k = 0; k < kRows / 16; ++k)  // 16 rows on: 2048 bytes, 8 columns
-    mma_tmem(d, (k < 4 ? a + k * 8 : a2 + (k - 4) * 8), db + k * (2048 >> 4), idesc, add || k > 0);
+    mma_tmem(d, a + k * 16 / kEach * apart + k * 16 % kEach / 2, db + k * (2048 >> 4), idesc, add || k > 0);
 }
 
 // Rows [from, to) of a tile, and no others, hold tokens of documents: the rest
@@ -171,6 +202,29 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to) {
         store_shared(tile + (i / 8) * kBoxBytes + r * 128 + (i % 8) * 16, make_uint4(0, 0, 0, 0));
   fence_shared();
   __syncwarp();
+}
+
+// N elements of a lane's row, from element c of the head, rounded into a tile:
+// `place` is the row's in its first block.
+template <class E, int N>
+__device__ __forceinline__ void store_units(uint32_t place, int c, const float (&o)[N]) {
+#pragma unroll
+  for (int u = 0; u < N / 8; ++u) {
+    const int unit = c % kChunk / 8 + u;
+    store_shared(place + c / kChunk * kBoxBytes + ((unit ^ (threadIdx.x & 7)) * 16),
+                 make_uint4(pack2<E>(o[8 * u], o[8 * u + 1]), pack2<E>(o[8 * u + 2], o[8 * u + 3]),
+                            pack2<E>(o[8 * u + 4], o[8 * u + 5]), pack2<E>(o[8 * u + 6], o[8 * u + 7])));
+  }
+}
+
+// 32 floats of shared memory, the same for all lanes.
+__device__ __forceinline__ void load_pairs(uint32_t at, Pair (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4 u = load_shared(at + i * 16);
+    v[2 * i] = make_pair(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[2 * i + 1] = make_pair(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
 }
 
 // ---- masks -----------------------------------------------------------------------------

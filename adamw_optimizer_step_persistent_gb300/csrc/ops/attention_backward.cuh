@@ -12,10 +12,10 @@
 // of five, where grad_q summed in memory would cost fp32 additions to it from
 // every tile, in the order in which they arrive.
 //
-// Both are pipelined in the same way: eight warps turn scores into p and p into
-// ds (a lane to a row, half the columns to four warps) while the tensor cores
-// do the products of the tile before and the scores of the next one.  p and ds
-// go back to tensor memory in 16 bits, as the A operand of their products.
+// Both are pipelined in the same way: sixteen warps turn scores into p and p
+// into ds (four lanes to a row, 32 columns each) while the tensor cores do the
+// products of the tile before and the scores of the next one.  p and ds go back
+// to tensor memory in 16 bits, as the A operand of their products.
 // (A warp may be a turn ahead of another one when it has written ds, which is
 // why that has a barrier for even and one for odd turns.)
 #pragma once
@@ -24,7 +24,6 @@
 
 namespace fadam_ops {
 
-constexpr int kBackwardThreads = 384;  // 8 warps for p and ds, two that multiply, one that loads, one idle
 // Tiles in flight of what a kernel walks over: X is needed by the scores and by
 // the product with ds, Y by grad_out . v (and the product with p).
 constexpr int kRingX = 3, kRingY = 2;
@@ -68,9 +67,10 @@ struct Backward {
   BackwardExtra* extra;
   BackwardBarriers* bars;
 
-  // Sets up barriers and tensor memory.  False when shared memory does not
+  // Sets up barriers and tensor memory, for one or two multiplying warps (which
+  // both have to be done with an X).  False when shared memory does not
   // start on 1024 bytes, as the swizzle needs.
-  __device__ __forceinline__ bool begin(unsigned char* smem, const AttentionArgs& g, int y_products) {
+  __device__ __forceinline__ bool begin(unsigned char* smem, const AttentionArgs& g, int multiplying) {
     own0 = shared_addr(smem);
     if (own0 & 1023) {
       if (threadIdx.x == 0) atomicExch(g.status, FADAM_ECUDA);
@@ -83,25 +83,25 @@ struct Backward {
     bars = &extra->bars;
     if (threadIdx.x == 0) {
       bar_init(shared_addr(&bars->own_full), 1);
-      bar_init(shared_addr(&bars->done), 2);  // both multiplying warps
+      bar_init(shared_addr(&bars->done), multiplying);
       for (int i = 0; i < kRingX; ++i) {
         bar_init(shared_addr(&bars->x_full[i]), 1);
-        bar_init(shared_addr(&bars->x_empty[i]), 2);  // by both of its products
+        bar_init(shared_addr(&bars->x_empty[i]), multiplying);
       }
       for (int i = 0; i < kRingY; ++i) {
         bar_init(shared_addr(&bars->y_full[i]), 1);
-        bar_init(shared_addr(&bars->y_empty[i]), y_products);
+        bar_init(shared_addr(&bars->y_empty[i]), 1);
       }
       bar_init(shared_addr(&bars->scores), 1);
       bar_init(shared_addr(&bars->dots), 1);
-      bar_init(shared_addr(&bars->scores_read), 8);
-      bar_init(shared_addr(&bars->dots_read), 8);
-      bar_init(shared_addr(&bars->weights), 8);
-      bar_init(shared_addr(&bars->slopes[0]), 8);
-      bar_init(shared_addr(&bars->slopes[1]), 8);
+      bar_init(shared_addr(&bars->scores_read), kScoreWarps);
+      bar_init(shared_addr(&bars->dots_read), kScoreWarps);
+      bar_init(shared_addr(&bars->weights), kScoreWarps);
+      bar_init(shared_addr(&bars->slopes[0]), kScoreWarps);
+      bar_init(shared_addr(&bars->slopes[1]), kScoreWarps);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (threadIdx.x / 32 == 8) tmem_alloc(shared_addr(&bars->tmem), 512);
+    if (threadIdx.x / 32 == kMultiply) tmem_alloc(shared_addr(&bars->tmem), 512);
     return true;
   }
 
@@ -158,15 +158,15 @@ struct Backward {
   }
 };
 
-// 64 columns of scores of a lane's row become p (times 2^lift) in 16 bits and,
+// 32 columns of scores of a lane's row become p (times 2^lift) in 16 bits and,
 // in place, p times ds/d(q . k).  lse(c): what is added to columns c and c + 1.
 // Columns outside [lo, hi) are not seen.
 template <class E, bool kCap, bool kMask, class Lse>
-__device__ __forceinline__ void weights_of(float (&s)[64], uint32_t (&p)[32], const Scores& f, float mul,
+__device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], const Scores& f, float mul,
                                            int lo, int hi, Lse lse) {
   const Pair mul_pair = both(mul);
 #pragma unroll
-  for (int c = 0; c < 64; c += 2) {
+  for (int c = 0; c < 32; c += 2) {
     float slope[2] = {1.0f, 1.0f};
     if constexpr (kCap)
 #pragma unroll
@@ -185,11 +185,11 @@ __device__ __forceinline__ void weights_of(float (&s)[64], uint32_t (&p)[32], co
 }
 // `apart`: the first column's place less the row's.
 template <class E, class Lse>
-__device__ __forceinline__ void weights(float (&s)[64], uint32_t (&p)[32], const Scores& f, float apart,
+__device__ __forceinline__ void weights(float (&s)[32], uint32_t (&p)[16], const Scores& f, float apart,
                                         bool whole, int lo, int hi, Lse lse) {
   if (f.cap != 0.0f) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) s[c] = f.folded(s[c]);
+    for (int c = 0; c < 32; ++c) s[c] = f.folded(s[c]);
     if (f.slope != 0.0f) {
       const auto lowered = [&](int c) {
         const float2 l = split(lse(c));
@@ -208,7 +208,7 @@ __device__ __forceinline__ void weights(float (&s)[64], uint32_t (&p)[32], const
   float mul = f.mul;
   if (f.slope != 0.0f) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c] * f.mul);
+    for (int c = 0; c < 32; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c] * f.mul);
     mul = 1.0f;
   }
   if (whole) weights_of<E, false, false>(s, p, f, mul, lo, hi, lse);
@@ -241,13 +241,13 @@ struct KeyMaps {
 };
 
 template <class T, int C>
-__global__ void __launch_bounds__(kBackwardThreads, 1)
+__global__ void __launch_bounds__(kAttentionThreads, 1)
     attention_keys_kernel(const __grid_constant__ KeyMaps maps, const __grid_constant__ AttentionArgs g) {
   using E = typename T::type;
   using B = Backward<T, C>;
   extern __shared__ __align__(1024) unsigned char smem[];
   B b;
-  if (!b.begin(smem, g, 2)) return;
+  if (!b.begin(smem, g, 1)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
@@ -259,17 +259,17 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   const int kv = rest / g.splits, split = rest % g.splits;
   const int share = g.group / g.splits, head0 = kv * g.group + split * share;
   const int key0 = tile * kRows;
-  const int row = threadIdx.x % kRows;  // of the first eight warps: a lane's key
+  const int row = threadIdx.x % kRows;  // of the first sixteen warps: a lane's key
   Spans span{};
-  if (warp < 8 && key0 + row < g.tokens) span = spans_of(g, key0 + row);
+  if (warp < kScoreWarps && key0 + row < g.tokens) span = spans_of(g, key0 + row);
   const Reach reach = b.meet(span.query_lo, span.query_hi, key0 + row < g.tokens);
   const uint32_t tmem = bars->tmem;
   const int first = reach.first(), turns = reach.last() - first, n = turns * share;
   const auto query_tile = [&](int i) { return first + i % turns; };
 
-  if (warp >= 8) keep_registers<kOtherRegisters>();
-  if (warp == 11) {
-  } else if (warp == 9) {
+  if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();
+  if (warp == kIdle) {
+  } else if (warp == kLoad) {
     if (lane == 0 && n > 0) {
       const int64_t pitch = int64_t(g.tiles) * kRows;
       const float* lse = g.stats;
@@ -291,10 +291,12 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
             load_bytes(shared_addr(b.extra->lse[slot]), lse + head * pitch + at, kRows * 4, bar);
           });
     }
-  } else if (warp == 8 || warp == 10) {
-    // scores and grad_v; grad_out . v and grad_k: two warps, two chains
+  } else if (warp == kMultiply) {
+    // One warp: while the scores' warps work on ds(i), grad_v and the scores of
+    // i + 1 are computed, then, while they work on p(i + 1), grad_k and
+    // grad_out . v.  (Two warps, one for each pair of products, ran them at the
+    // same time, and p(i + 1) waited for both: 3600 cycles a turn.)
     if (n > 0) {
-      const bool dots = warp == 10;
       const int steps = (g.width + 15) / 16, width = steps * 16;
       int inside_lo = 0, inside_hi = g.tiles * kRows;
       if (g.documents) {
@@ -305,43 +307,52 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
         const int from = query_tile(i) * kRows;
         if (from < inside_lo || from + kRows > inside_hi) zero_rows<C>(at, inside_lo - from, inside_hi - from);
       };
-      const uint32_t at = tmem + (dots ? kColumnsDots : kColumnsS), to = tmem + (dots ? kColumnsB : kColumnsA);
-      const uint32_t own = dots ? b.own1 : b.own0, bar_at = shared_addr(dots ? &bars->dots : &bars->scores);
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status);
-      // (rows outside all documents reach only columns that are masked)
-      const auto inner = [&](int i) {
-        ok = dots ? b.wait_y(i, status) : b.wait_x(i, status);
-        if (!ok) return;
+      const auto scores = [&](int i) {
+        if (!b.wait_x(i, status)) return false;
         fence_after_sync();
+        clean(b.x_at(i), i);
         if (elect_one()) {
-          mma_scores<T, C>(at, own, dots ? b.y_at(i) : b.x_at(i), steps);
-          commit(bar_at);
-          commit(shared_addr(dots ? &bars->y_empty[i % kRingY] : &bars->x_empty[i % kRingX]));
+          mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
+          commit(shared_addr(&bars->scores));
         }
+        return true;
       };
-      if (ok) inner(0);
+      const auto dots = [&](int i) {
+        if (!b.wait_y(i, status)) return false;
+        fence_after_sync();
+        clean(b.y_at(i), i);
+        if (elect_one()) {
+          mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
+          commit(shared_addr(&bars->dots));
+        }
+        return true;
+      };
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && scores(0) && dots(0);
       for (int i = 0; ok && i < n; ++i) {
-        ok = dots ? b.wait_x(i, status) : b.wait_y(i, status);
-        if (!ok) break;
-        const uint32_t rows = dots ? b.x_at(i) : b.y_at(i);
-        ok = dots ? bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status)
-                  : bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
+        ok = bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
-        clean(rows, i);
         if (elect_one()) {
-          mma_rows<T>(to, at, at + 64, rows, width, i > 0);
-          commit(shared_addr(dots ? &bars->x_empty[i % kRingX] : &bars->y_empty[i % kRingY]));
+          mma_rows<T, 32>(tmem + kColumnsA, tmem + kColumnsS, 32, b.y_at(i), width, i > 0);
+          commit(shared_addr(&bars->y_empty[i % kRingY]));
         }
-        if (i + 1 < n) inner(i + 1);
+        if (i + 1 < n && !(ok = scores(i + 1))) break;
+        ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
+        if (!ok) break;
+        fence_after_sync();
+        if (elect_one()) {
+          mma_rows<T, 32>(tmem + kColumnsB, tmem + kColumnsDots, 32, b.x_at(i), width, i > 0);
+          commit(shared_addr(&bars->x_empty[i % kRingX]));
+        }
+        if (i + 1 < n) ok = dots(i + 1);
       }
       if (ok && elect_one()) commit(shared_addr(&bars->done));
     }
-  } else {
+  } else if (warp < kScoreWarps) {
     take_registers<kScoreRegisters>();
-    const int half = warp / 4, quarter = warp % 4;
+    const int part = warp / 4, quarter = warp % 4;  // part: of the columns
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
-    const uint32_t at_s = lanes + kColumnsS + half * 64, at_dots = lanes + kColumnsDots + half * 64;
+    const uint32_t at_s = lanes + kColumnsS + part * 32, at_dots = lanes + kColumnsDots + part * 32;
     const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
     const uint32_t bar_weights = shared_addr(&bars->weights);
     const float factor = ds_factor<T>(g) * exp2f(-kLiftBits<T>);
@@ -349,90 +360,89 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     for (int h = 0, i = 0; h < share && ok; ++h) {
       const Scores f(g, head0 + h);
       for (int turn = 0; turn < turns; ++turn, ++i) {
-        const int at = (first + turn) * kRows + half * 64;  // the first column's query
+        const int at = (first + turn) * kRows + part * 32;  // the first column's query
         const bool whole = reach.whole((first + turn) * kRows);
         const int lo = span.query_lo - at, hi = span.query_hi - at;
-        float s[64];
-        uint32_t p[32];
-        ok = bar_wait(bar_scores, unsigned(i) & 1, status) && b.wait_y(i, status);
+        float s[32];
+        uint32_t p[16];
+        Pair of[16];  // the columns' lse, then their delta: read before the tensor cores are waited for
+        ok = b.wait_y(i, status);
+        if (!ok) break;
+        load_pairs(shared_addr(b.extra->lse[i % kRingY] + part * 32), of);
+        ok = bar_wait(bar_scores, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
         tmem_load32(at_s, s);
-        tmem_load32(at_s + 32, s + 32);
-        tmem_wait<64>(s);
-        const Pair* lse = reinterpret_cast<const Pair*>(b.extra->lse[i % kRingY] + half * 64);
-        weights<E>(s, p, f, float(at - (key0 + row)), whole, lo, hi, [&](int c) { return lse[c / 2]; });
-        tmem_store32(at_s, p);
+        tmem_wait<32>(s);
+        weights<E>(s, p, f, float(at - (key0 + row)), whole, lo, hi, [&](int c) { return of[c / 2]; });
+        tmem_store16(at_s, p);
         tmem_stored();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) bar_arrive(bar_weights);
 
-        ok = bar_wait(bar_dots, unsigned(i) & 1, status) && b.wait_x(i, status);
+        ok = b.wait_x(i, status);
+        if (!ok) break;
+        load_pairs(shared_addr(b.extra->delta[i % kRingX] + part * 32), of);
+        ok = bar_wait(bar_dots, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
-        const Pair* delta = reinterpret_cast<const Pair*>(b.extra->delta[i % kRingX] + half * 64);
-        float d[64];
+        float d[32];
         tmem_load32(at_dots, d);
-        tmem_load32(at_dots + 32, d + 32);
-        tmem_wait<64>(d);
-#pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          const auto of = [&](int c) { return delta[(c0 + c) / 2]; };
-          if (whole) slopes_of<T, false>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
-          else slopes_of<T, true>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
-        }
-        tmem_store32(at_dots, p);
+        tmem_wait<32>(d);
+        const auto delta = [&](int c) { return of[c / 2]; };
+        if (whole) slopes_of<T, false>(s, d, p, factor, lo, hi, delta);
+        else slopes_of<T, true>(s, d, p, factor, lo, hi, delta);
+        tmem_store16(at_dots, p);
         tmem_stored();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) bar_arrive(shared_addr(&bars->slopes[i & 1]));
       }
     }
-    // four warps write grad_v (through v's place in shared memory), four grad_k
+    // eight warps write grad_v (through v's place in shared memory), eight
+    // grad_k, half of the elements to four warps
     if (n > 0 && ok) ok = bar_wait(shared_addr(&bars->done), 0, status);
     fence_after_sync();
-    const float scale = half ? g.scale / ds_factor<T>(g) : exp2f(-kLiftBits<T>);
-    const uint32_t from = lanes + (half ? kColumnsB : kColumnsA);
-    const uint32_t tile_at = half ? b.own0 : b.own1;
+    const bool keys = part >= 2;
+    const float scale = keys ? g.scale / ds_factor<T>(g) : exp2f(-kLiftBits<T>);
+    const uint32_t from = lanes + (keys ? kColumnsB : kColumnsA);
+    const uint32_t tile_at = keys ? b.own0 : b.own1;
     const uint32_t place = tile_at + (quarter * 32 + lane) * 128;
-    float* part = nullptr;
+    float* sums = nullptr;
     if (g.splits > 1)
-      part = g.parts + (((int64_t(split) * 2 + half) * g.tokens + key0 + row) * kv_heads + kv) * g.width;
+      sums = g.parts + (((int64_t(split) * 2 + keys) * g.tokens + key0 + row) * kv_heads + kv) * g.width;
 #pragma unroll
-    for (int c = 0; c < C * kChunk; c += 32)
-      if (c < g.width) {
-        float o[32];
-        if (n > 0) {
-          tmem_load32(from + c, o);
-          tmem_wait<32>(o);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * scale : 0.0f;
-        if (part) {
-          if (key0 + row < g.tokens)
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              if (c + i < g.width) {
-                reinterpret_cast<float4*>(part + c + i)[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                reinterpret_cast<float4*>(part + c + i)[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
-              }
-          continue;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          store_shared(place + c / kChunk * kBoxBytes + (((c % kChunk / 8 + u) ^ (lane & 7)) * 16),
-                       make_uint4(pack2<E>(o[8 * u], o[8 * u + 1]), pack2<E>(o[8 * u + 2], o[8 * u + 3]),
-                                  pack2<E>(o[8 * u + 4], o[8 * u + 5]), pack2<E>(o[8 * u + 6], o[8 * u + 7])));
+    for (int k = 0; k < C; ++k) {
+      const int c = (part % 2 * C + k) * 32;
+      if (c >= g.width) continue;
+      float o[32];
+      if (n > 0) {
+        tmem_load32(from + c, o);
+        tmem_wait<32>(o);
       }
-    if (!part) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * scale : 0.0f;
+      if (sums) {
+        if (key0 + row < g.tokens)
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            if (c + i < g.width) {
+              reinterpret_cast<float4*>(sums + c + i)[0] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              reinterpret_cast<float4*>(sums + c + i)[1] = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+            }
+      } else {
+        store_units<E>(place, c, o);
+      }
+    }
+    if (!sums) {
       fence_shared();
-      group_sync(1 + half, 128);
-      if (threadIdx.x % 128 == 0) {
+      group_sync(1 + keys, 256);
+      if (threadIdx.x % 256 == 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (c * kChunk < g.width)
-            store_head_box(half ? &maps.grad_k : &maps.grad_v, c * kChunk, kv, key0, tile_at + c * kBoxBytes);
+            store_head_box(keys ? &maps.grad_k : &maps.grad_v, c * kChunk, kv, key0, tile_at + c * kBoxBytes);
         wait_stores();
       }
     }
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   chain_next();
   fence_before_sync();
   __syncthreads();
-  if (warp == 8) tmem_free(tmem, 512);
+  if (warp == kMultiply) tmem_free(tmem, 512);
 }
 
 // ---- grad_q: 128 queries, a walk over keys ------------------------------------------------
@@ -451,13 +461,13 @@ struct QueryMaps {
 };
 
 template <class T, int C>
-__global__ void __launch_bounds__(kBackwardThreads, 1)
+__global__ void __launch_bounds__(kAttentionThreads, 1)
     attention_queries_kernel(const __grid_constant__ QueryMaps maps, const __grid_constant__ AttentionArgs g) {
   using E = typename T::type;
   using B = Backward<T, C>;
   extern __shared__ __align__(1024) unsigned char smem[];
   B b;
-  if (!b.begin(smem, g, 1)) return;
+  if (!b.begin(smem, g, 2)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
@@ -467,14 +477,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   const int query0 = (g.tiles - 1 - int(blockIdx.x / unsigned(g.heads))) * kRows;
   const int row = threadIdx.x % kRows;
   Spans span{};
-  if (warp < 8 && query0 + row < g.tokens) span = spans_of(g, query0 + row);
+  if (warp < kScoreWarps && query0 + row < g.tokens) span = spans_of(g, query0 + row);
   const Reach reach = b.meet(span.key_lo, span.key_hi, query0 + row < g.tokens);
   const uint32_t tmem = bars->tmem;
   const int first = reach.first(), n = reach.last() - first;
 
-  if (warp >= 8) keep_registers<kOtherRegisters>();
-  if (warp == 11) {
-  } else if (warp == 9) {
+  if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();
+  if (warp == kIdle) {
+  } else if (warp == kLoad) {
     if (lane == 0 && n > 0) {
       const int kv = head / g.group;
       b.load_loop(
@@ -486,7 +496,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
           [&](int i, uint32_t dst, int, uint32_t bar) { load_head<C>(dst, &maps.k, kv, (first + i) * kRows, bar); },
           [&](int i, uint32_t dst, int, uint32_t bar) { load_head<C>(dst, &maps.v, kv, (first + i) * kRows, bar); });
     }
-  } else if (warp == 8) {
+  } else if (warp == kMultiply2) {
     // scores
     if (n > 0) {
       const int steps = (g.width + 15) / 16;
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
       }
       if (ok && elect_one()) commit(shared_addr(&bars->done));
     }
-  } else if (warp == 10) {
+  } else if (warp == kMultiply) {
     // grad_out . v and grad_q
     if (n > 0) {
       const int steps = (g.width + 15) / 16, width = steps * 16;
@@ -536,17 +546,17 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
           zero_rows<C>(b.x_at(k), inside_lo - from, inside_hi - from);
         if (elect_one()) {
           const uint32_t ds = tmem + kColumnsA + (k & 1) * 64;
-          mma_rows<T>(tmem + kColumnsB, ds, ds + 32, b.x_at(k), width, k > 0);
+          mma_rows<T, 128>(tmem + kColumnsB, ds, 0, b.x_at(k), width, k > 0);
           commit(shared_addr(&bars->x_empty[k % kRingX]));
         }
       }
       if (ok && elect_one()) commit(shared_addr(&bars->done));
     }
-  } else {
+  } else if (warp < kScoreWarps) {
     take_registers<kScoreRegisters>();
-    const int half = warp / 4, quarter = warp % 4;
+    const int part = warp / 4, quarter = warp % 4;  // part: of the columns
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
-    const uint32_t at_s = lanes + kColumnsS + half * 64, at_dots = lanes + kColumnsDots + half * 64;
+    const uint32_t at_s = lanes + kColumnsS + part * 32, at_dots = lanes + kColumnsDots + part * 32;
     const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
     const uint32_t bar_scores_read = shared_addr(&bars->scores_read);
     const uint32_t bar_dots_read = shared_addr(&bars->dots_read);
@@ -557,17 +567,16 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     const Scores f(g, head);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int at = (first + i) * kRows + half * 64;  // the first column's key
+      const int at = (first + i) * kRows + part * 32;  // the first column's key
       const bool whole = reach.whole((first + i) * kRows);
       const int lo = span.key_lo - at, hi = span.key_hi - at;
-      float s[64];
-      uint32_t p[32];
+      float s[32];
+      uint32_t p[16];
       ok = bar_wait(bar_scores, unsigned(i) & 1, status);
       if (!ok) break;
       fence_after_sync();
       tmem_load32(at_s, s);
-      tmem_load32(at_s + 32, s + 32);
-      tmem_wait<64>(s);
+      tmem_wait<32>(s);
       fence_before_sync();
       __syncwarp();
       if (lane == 0) bar_arrive(bar_scores_read);
@@ -576,21 +585,17 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
       ok = bar_wait(bar_dots, unsigned(i) & 1, status);
       if (!ok) break;
       fence_after_sync();
-      float d[64];
+      float d[32];
       tmem_load32(at_dots, d);
-      tmem_load32(at_dots + 32, d + 32);
-      tmem_wait<64>(d);
+      tmem_wait<32>(d);
       fence_before_sync();
       __syncwarp();
       if (lane == 0) bar_arrive(bar_dots_read);
-#pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        const auto of = [&](int) { return delta; };
-        if (whole) slopes_of<T, false>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
-        else slopes_of<T, true>(s + c0, d + c0, p + c0 / 2, factor, lo - c0, hi - c0, of);
-      }
+      const auto less = [&](int) { return delta; };
+      if (whole) slopes_of<T, false>(s, d, p, factor, lo, hi, less);
+      else slopes_of<T, true>(s, d, p, factor, lo, hi, less);
       // (grad_out . v of i comes behind the product with ds of i - 2: its place is free)
-      tmem_store32(lanes + kColumnsA + (i & 1) * 64 + half * 32, p);
+      tmem_store16(lanes + kColumnsA + (i & 1) * 64 + part * 16, p);
       tmem_stored();
       fence_before_sync();
       __syncwarp();
@@ -600,25 +605,22 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
     fence_after_sync();
     const float scale = g.scale / ds_factor<T>(g);
     const uint32_t place = b.own0 + (quarter * 32 + lane) * 128;
+    // a quarter of the elements to four warps, C * 16 each
 #pragma unroll
-    for (int k = 0; k < C; ++k) {  // half the columns to four warps
-      const int c = (half * C + k) * 32;
+    for (int k = 0; k < C; ++k) {
+      const int c = (part * C + k) * 16;
       if (c >= g.width) continue;
-      float o[32];
+      float o[16];
       if (n > 0) {
-        tmem_load32(lanes + kColumnsB + c, o);
-        tmem_wait<32>(o);
+        tmem_load16(lanes + kColumnsB + c, o);
+        tmem_wait<16>(o);
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * scale : 0.0f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        store_shared(place + c / kChunk * kBoxBytes + (((c % kChunk / 8 + u) ^ (lane & 7)) * 16),
-                     make_uint4(pack2<E>(o[8 * u], o[8 * u + 1]), pack2<E>(o[8 * u + 2], o[8 * u + 3]),
-                                pack2<E>(o[8 * u + 4], o[8 * u + 5]), pack2<E>(o[8 * u + 6], o[8 * u + 7])));
+      for (int i = 0; i < 16; ++i) o[i] = n > 0 ? o[i] * scale : 0.0f;
+      store_units<E>(place, c, o);
     }
     fence_shared();
-    group_sync(1, 256);
+    group_sync(1, kScoreWarps * 32);
     if (threadIdx.x == 0) {
 #pragma unroll
       for (int c = 0; c < C; ++c)
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1)
   chain_next();
   fence_before_sync();
   __syncthreads();
-  if (warp == 8) tmem_free(tmem, 512);
+  if (warp == kMultiply) tmem_free(tmem, 512);
 }
 
 template <class T, int C>
@@ -648,10 +650,10 @@ fadam_status launch_backward(const BackwardMaps& m, const AttentionArgs& g, cuda
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   const KeyMaps km{m.q, m.k, m.v, m.grad_out, m.grad_k, m.grad_v};
   if ((st = launch_chained("attention keys launch", keys, int64_t(g.tiles) * (g.heads / g.group) * g.splits,
-                           kBackwardThreads, kShared, stream, km, g)))
+                           kAttentionThreads, kShared, stream, km, g)))
     return st;
   const QueryMaps qm{m.q, m.k, m.v, m.grad_out, m.grad_q};
-  return launch_chained("attention queries launch", queries, int64_t(g.tiles) * g.heads, kBackwardThreads,
+  return launch_chained("attention queries launch", queries, int64_t(g.tiles) * g.heads, kAttentionThreads,
                         kShared, stream, qm, g);
 }
 template <class T>

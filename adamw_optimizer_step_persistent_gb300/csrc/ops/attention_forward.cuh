@@ -2,9 +2,9 @@
 //
 // A CTA takes 256 queries of one head in two tiles of 128, and walks over the
 // keys that any of them sees, 128 at a time, once: S = Q K^T on the tensor
-// cores, then a lane to a query takes the row's maximum, exponentials and sum
-// in registers, hands the exponentials in 16 bits back to tensor memory, and
-// O += P V.  The two tiles take turns: while four warps work on one tile's
+// cores, then two lanes to a query (of two warps, 64 columns each) take the
+// row's maximum, exponentials and sum in registers, hand the exponentials in 16
+// bits back to tensor memory, and O += P V.  The two tiles take turns: while four warps work on one tile's
 // scores, the tensor cores work for the other, each fed by a warp of its own
 // (the tensor cores take no more than two or three instructions ahead, so that
 // one warp for both left them idle during its waits: 4000 cycles a turn of both
@@ -22,7 +22,6 @@
 
 namespace fadam_ops {
 
-constexpr int kForwardThreads = 384;  // 2 x 4 warps for the scores, two that multiply, one that loads, one idle
 constexpr int kRing = 4;              // tiles of keys or values in flight
 constexpr float kGrowth = 8.0f;
 
@@ -30,13 +29,14 @@ struct ForwardBarriers {
   uint64_t q_full[2], scores[2], weights[2], done[2];
   uint64_t full[kRing], empty[kRing];
   Reach reach[8];
+  float shared[2][2][kRows];  // what the two lanes of a row tell each other: tile, half, row
   uint32_t tmem;
 };
 template <int C>
 constexpr size_t kForwardSmem = 1024 + (2 + kRing) * C * size_t(kBoxBytes) + sizeof(ForwardBarriers);
 
 template <class T, int C>
-__global__ void __launch_bounds__(kForwardThreads, 1)
+__global__ void __launch_bounds__(kAttentionThreads, 1)
     attention_forward_kernel(const __grid_constant__ ForwardMaps maps, const __grid_constant__ AttentionArgs g) {
   using E = typename T::type;
   constexpr int kTile = C * kBoxBytes;
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     for (int t = 0; t < 2; ++t) {
       bar_init(shared_addr(&bars->q_full[t]), 1);
       bar_init(shared_addr(&bars->scores[t]), 1);
-      bar_init(shared_addr(&bars->weights[t]), 4);
+      bar_init(shared_addr(&bars->weights[t]), 8);
       bar_init(shared_addr(&bars->done[t]), 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -60,19 +60,21 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) tmem_alloc(shared_addr(&bars->tmem), 512);
+  if (warp == kMultiply) tmem_alloc(shared_addr(&bars->tmem), 512);
   chain_wait();
 
   // the last queries first: under a causal mask they have the most keys
   const int head = int(blockIdx.x % unsigned(g.heads));
   const int pairs = (g.tiles + 1) / 2;
   const int row0 = (pairs - 1 - int(blockIdx.x / unsigned(g.heads))) * 2 * kRows;
-  const int row = row0 + threadIdx.x;  // of a thread of the first eight warps
+  // warps of scores: four and four to a tile, each four with half the columns
+  const int tile = warp / 8 & 1, half = warp / 4 & 1, quarter = warp % 4;
+  const int row = row0 + tile * kRows + quarter * 32 + lane;
   Spans span{};
-  if (warp < 8) {
+  if (warp < kScoreWarps) {
     if (row < g.tokens) span = spans_of(g, row);
     const Reach r = reach_of(span.key_lo, span.key_hi, row < g.tokens);
-    if (lane == 0) bars->reach[warp] = r;
+    if (lane == 0 && half == 0) bars->reach[tile * 4 + quarter] = r;
   }
   fence_before_sync();
   __syncthreads();
@@ -87,9 +89,9 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
   const int last = max(reach[0].hi > reach[0].lo ? reach[0].last() : 0,
                        reach[1].hi > reach[1].lo ? reach[1].last() : 0);
 
-  if (warp >= 8) keep_registers<kOtherRegisters>();
-  if (warp == 11) {
-  } else if (warp == 9) {
+  if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();
+  if (warp == kIdle) {
+  } else if (warp == kLoad) {
     // ---- loads: the queries, then keys and values in turn
     if (lane == 0 && first < last) {
       prefetch_map(&maps.q);
@@ -123,9 +125,9 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
       for (int i = n < kRing ? 0 : n - kRing; i < n; ++i)
         bar_wait(shared_addr(&bars->empty[i % kRing]), unsigned(i / kRing) & 1, g.status);
     }
-  } else if (warp == 8 || warp == 10) {
+  } else if (warp == kMultiply || warp == kMultiply2) {
     // ---- tensor cores: a warp to a tile of queries
-    const int t = warp == 8 ? 0 : 1;
+    const int t = warp == kMultiply ? 0 : 1;
     const Reach mine = t ? reach[1] : reach[0];
     if (first < last) {
       const int steps = (g.width + 15) / 16, n = steps * 16;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
         }
         if (elect_one()) {
           if (here) {
-            mma_rows<T>(at_o, at_s, at_s + 32, values, n, j > begin);
+            mma_rows<T, 64>(at_o, at_s, 64, values, n, j > begin);
             if (j + 1 == end) commit(shared_addr(&bars->done[t]));
           }
           commit(shared_addr(&bars->empty[at % kRing]));
@@ -181,12 +183,16 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
       }
     }
   } else {
-    // ---- softmax: a lane to a query
+    // ---- softmax: two lanes to a query, 64 columns each
     take_registers<kScoreRegisters>();
-    const int t = warp / 4, quarter = warp % 4;
+    const int t = tile, pair = 1 + warp / 8 * 4 + quarter;  // pair: their warps' barrier
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
-    const uint32_t at_s = lanes + t * kRows, at_o = lanes + (2 + t) * kRows;
+    const uint32_t at_s = lanes + t * kRows + half * 64;
+    const uint32_t at_o = lanes + (2 + t) * kRows + half * C * 32;  // half of O's columns
+    const int o_width = g.width - half * C * 32;
     const uint32_t bar_scores = shared_addr(&bars->scores[t]), bar_weights = shared_addr(&bars->weights[t]);
+    float* told = &bars->shared[t][half][quarter * 32 + lane];
+    const float* other = &bars->shared[t][half ^ 1][quarter * 32 + lane];
     const Scores f(g, head);
     const bool ready = f.cap != 0.0f || f.slope != 0.0f;  // scores are in units of log 2 before the maximum
     const float mul = ready ? 1.0f : f.mul;
@@ -196,70 +202,72 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     const Reach mine = t ? reach[1] : reach[0];
     const int begin = mine.first(), end = mine.last();
     for (int j = begin; j < end; ++j) {
-      ok = bar_wait(bar_scores, unsigned(j - begin) & 1, g.status);
-      if (!ok) break;
+      // (after a wait that gave up the turns go on without waiting: the two warps
+      // of a pair must meet as often)
+      ok = ok && bar_wait(bar_scores, unsigned(j - begin) & 1, g.status);
       fence_after_sync();
-      float s[kRows];
-#pragma unroll
-      for (int c = 0; c < kRows; c += 32) tmem_load32(at_s + c, s + c);
-      tmem_wait<kRows>(s);
+      float s[64];
+      tmem_load32(at_s, s);
+      tmem_load32(at_s + 32, s + 32);
+      tmem_wait<64>(s);
+      const int at = j * kRows + half * 64;  // the first column's key
       if (f.cap != 0.0f) {
 #pragma unroll
-        for (int c = 0; c < kRows; ++c) s[c] = fmaf(-2.0f * f.cap, f.folded(s[c]), f.cap);
+        for (int c = 0; c < 64; ++c) s[c] = fmaf(-2.0f * f.cap, f.folded(s[c]), f.cap);
       } else if (ready) {
 #pragma unroll
-        for (int c = 0; c < kRows; ++c) s[c] *= f.mul;
+        for (int c = 0; c < 64; ++c) s[c] *= f.mul;
       }
       if (f.slope != 0.0f) {
-        const float apart = float(j * kRows - row);
+        const float apart = float(at - row);
 #pragma unroll
-        for (int c = 0; c < kRows; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c]);
+        for (int c = 0; c < 64; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c]);
       }
       if (!mine.whole(j * kRows)) {
-        const int lo = span.key_lo - j * kRows, hi = span.key_hi - j * kRows;
+        const int lo = span.key_lo - at, hi = span.key_hi - at;
 #pragma unroll
-        for (int c = 0; c < kRows; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
+        for (int c = 0; c < 64; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
       }
       float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < kRows; c += 8)
+      for (int c = 0; c < 64; c += 8)
 #pragma unroll
         for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], s[c + k]), s[c + 4 + k]);
-      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mul;
-      if (__any_sync(~0u, most > top + kGrowth)) {
+      float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mul;
+      if (group_any(pair, 64, most > top + kGrowth)) {
         // (scores of j come behind the product with the values of j - 1: O is at rest)
+        *told = most;
+        group_sync(pair, 64);
+        most = fmaxf(most, *other);
         const float now = fmaxf(top, most);
         const float factor = now == -INFINITY ? 1.0f : exp2_fast(top - now);
         top = now;
         sum *= factor;
         if (j > begin) {
 #pragma unroll
-          for (int c = 0; c < C * kChunk; c += 32)
-            if (c < g.width) {
-              float o[32];
-              tmem_load32(at_o + c, o);
-              tmem_wait<32>(o);
+          for (int c = 0; c < C * 32; c += 16)
+            if (c < o_width) {
+              float o[16];
+              tmem_load16(at_o + c, o);
+              tmem_wait<16>(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= factor;
-              tmem_store32(at_o + c, reinterpret_cast<uint32_t*>(o));
+              for (int i = 0; i < 16; ++i) o[i] *= factor;
+              tmem_store16(at_o + c, reinterpret_cast<uint32_t*>(o));
             }
         }
       }
       const float from = top == -INFINITY ? 0.0f : top - kLift;
       const Pair mul_pair = both(mul), less = both(-from);
       Pair part[2] = {};
+      uint32_t p[32];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const float2 z = split(fma2(make_pair(s[h * 64 + c], s[h * 64 + c + 1]), mul_pair, less));
-          const float a = exp2_fast(z.x), b = exp2_fast(z.y);
-          part[c / 2 % 2] = add2(part[c / 2 % 2], make_pair(a, b));
-          p[c / 2] = pack2<E>(a, b);
-        }
-        tmem_store32(at_s + h * 32, p);
+      for (int c = 0; c < 64; c += 2) {
+        const float2 z = split(fma2(make_pair(s[c], s[c + 1]), mul_pair, less));
+        const float a = exp2_fast(z.x), b = exp2_fast(z.y);
+        part[c / 2 % 2] = add2(part[c / 2 % 2], make_pair(a, b));
+        p[c / 2] = pack2<E>(a, b);
       }
+      tmem_store32(at_s, p);
       sum += sum2(add2(part[0], part[1]));
       tmem_stored();
       fence_before_sync();
@@ -268,35 +276,34 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     }
     if (row0 + t * kRows < g.tokens) {
       // O / sum, through the queries' place in shared memory
+      group_sync(pair, 64);  // what was told has been read
+      *told = sum;
+      group_sync(pair, 64);
+      sum = half ? *other + sum : sum + *other;
       const bool none = begin >= end || sum == 0.0f;
       const float inverse = 1.0f / sum;
       if (begin < end && ok) ok = bar_wait(shared_addr(&bars->done[t]), 0, g.status);
       fence_after_sync();
       const uint32_t place = q_tiles + t * kTile + (quarter * 32 + lane) * 128;
 #pragma unroll
-      for (int c = 0; c < C * kChunk; c += 32)
-        if (c < g.width) {
+      for (int k = 0; k < C * 32; k += 32)
+        if (k < o_width) {
+          const int c = half * C * 32 + k;
           float o[32];
           if (begin < end) {
-            tmem_load32(at_o + c, o);
+            tmem_load32(at_o + k, o);
             tmem_wait<32>(o);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = none ? 0.0f : o[i] * inverse;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int unit = c % kChunk / 8 + u;
-            store_shared(place + c / kChunk * kBoxBytes + ((unit ^ (lane & 7)) * 16),
-                         make_uint4(pack2<E>(o[8 * u], o[8 * u + 1]), pack2<E>(o[8 * u + 2], o[8 * u + 3]),
-                                    pack2<E>(o[8 * u + 4], o[8 * u + 5]), pack2<E>(o[8 * u + 6], o[8 * u + 7])));
-          }
+          store_units<E>(place, c, o);
         }
-      if (row < g.tokens)
+      if (row < g.tokens && half == 0)
         g.lse[int64_t(row) * g.heads + head] =
             none ? -INFINITY : (top - kLift + log2f(sum)) * kLn2;
       fence_shared();
-      group_sync(1 + t, 128);
-      if (threadIdx.x % 128 == 0) {
+      group_sync(9 + t, 256);
+      if (threadIdx.x % 256 == 0) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (c * kChunk < g.width)
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
   chain_next();
   fence_before_sync();
   __syncthreads();
-  if (warp == 8) tmem_free(tmem, 512);
+  if (warp == kMultiply) tmem_free(tmem, 512);
 }
 
 template <class T, int C>
@@ -320,7 +327,7 @@ fadam_status launch_forward(const ForwardMaps& maps, const AttentionArgs& g, cud
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kForwardSmem<C>));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
   const int64_t items = int64_t((g.tiles + 1) / 2) * g.heads;
-  return launch_chained("attention launch", kernel, items, kForwardThreads, kForwardSmem<C>, stream, maps, g);
+  return launch_chained("attention launch", kernel, items, kAttentionThreads, kForwardSmem<C>, stream, maps, g);
 }
 template <class T>
 fadam_status forward_of(const ForwardMaps& maps, const AttentionArgs& g, cudaStream_t stream) {
