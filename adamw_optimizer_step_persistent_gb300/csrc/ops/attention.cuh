@@ -96,6 +96,10 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// A value that is the same in all lanes, so that the compiler knows it.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+
 // D (+)= A B, both 16-bit in shared memory.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -167,15 +171,20 @@ __device__ __forceinline__ uint32_t instruction(int n) {
          uint32_t(kRows / 16) << 24;
 }
 
-// D[128, 128] = A B^T over `steps` 16s of a head's elements.
-template <class T, int C>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, int steps) {
+// D[128, 128] = A B^T over `steps` 16s of a head's elements.  `half` is called
+// half way through.
+struct Nothing {
+  __device__ __forceinline__ void operator()() const {}
+};
+template <class T, int C, class Half = Nothing>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, int steps, Half half = Half()) {
   const uint64_t da = tile_desc<false>(a), db = tile_desc<false>(b);
   const uint32_t idesc = instruction<T, false>(kRows);
 #pragma unroll
   for (int k = 0; k < C * kChunk / 16; ++k) {
     const uint64_t at = (k / 4) * (kBoxBytes >> 4) + (k % 4) * 2;  // 16 elements on: 32 bytes, or the next box
     if (k < steps) mma(d, da + at, db + at, idesc, k > 0);
+    if (k == C * kChunk / 32 - 1) half();
   }
 }
 
@@ -270,6 +279,9 @@ __device__ __forceinline__ Reach reach_of(int lo, int hi, bool here) {
 }
 __device__ __forceinline__ Reach join(const Reach& a, const Reach& b) {
   return Reach{min(a.lo, b.lo), max(a.hi, b.hi), max(a.all_lo, b.all_lo), min(a.all_hi, b.all_hi)};
+}
+__device__ __forceinline__ Reach uniform(const Reach& r) {
+  return Reach{uniform(r.lo), uniform(r.hi), uniform(r.all_lo), uniform(r.all_hi)};
 }
 
 // ---- scores ------------------------------------------------------------------------------

@@ -115,7 +115,7 @@ struct Backward {
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    return join(join(bars->reach[0], bars->reach[1]), join(bars->reach[2], bars->reach[3]));
+    return uniform(join(join(bars->reach[0], bars->reach[1]), join(bars->reach[2], bars->reach[3])));
   }
 
   __device__ __forceinline__ uint32_t x_at(int i) const { return x + i % kRingX * kTile; }
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   B b;
   if (!b.begin(smem, g, 1)) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
   chain_wait();
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   Spans span{};
   if (warp < kScoreWarps && key0 + row < g.tokens) span = spans_of(g, key0 + row);
   const Reach reach = b.meet(span.query_lo, span.query_hi, key0 + row < g.tokens);
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = uniform(bars->tmem);
   const int first = reach.first(), turns = reach.last() - first, n = turns * share;
   const auto query_tile = [&](int i) { return first + i % turns; };
 
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   B b;
   if (!b.begin(smem, g, 2)) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
   chain_wait();
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   Spans span{};
   if (warp < kScoreWarps && query0 + row < g.tokens) span = spans_of(g, query0 + row);
   const Reach reach = b.meet(span.key_lo, span.key_hi, query0 + row < g.tokens);
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = uniform(bars->tmem);
   const int first = reach.first(), n = reach.last() - first;
 
   if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();

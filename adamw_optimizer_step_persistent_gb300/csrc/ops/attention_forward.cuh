@@ -8,7 +8,9 @@
 // scores, the tensor cores work for the other, each fed by a warp of its own
 // (the tensor cores take no more than two or three instructions ahead, so that
 // one warp for both left them idle during its waits: 4000 cycles a turn of both
-// tiles, of which the products need 2236).  Tensor memory: scores and O of both
+// tiles, of which the products need 2236).  The two pass a token: left alone,
+// both tiles' products ran at the same time, and then both tiles' scores were
+// worked on at the same time.  Tensor memory: scores and O of both
 // tiles (4 x 128 columns); P lies over the scores it came from.
 //
 // The running maximum of a row need not be its true maximum: any reference
@@ -27,6 +29,7 @@ constexpr float kGrowth = 8.0f;
 
 struct ForwardBarriers {
   uint64_t q_full[2], scores[2], weights[2], done[2];
+  uint64_t go[2];             // the tensor cores are this tile's
   uint64_t full[kRing], empty[kRing];
   Reach reach[8];
   float shared[2][2][kRows];  // what the two lanes of a row tell each other: tile, half, row
@@ -45,7 +48,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   const uint32_t ring = q_tiles + 2 * kTile;
   ForwardBarriers* bars =
       reinterpret_cast<ForwardBarriers*>(smem_raw + (ring + kRing * kTile - shared_addr(smem_raw)));
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -53,6 +56,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       bar_init(shared_addr(&bars->scores[t]), 1);
       bar_init(shared_addr(&bars->weights[t]), 8);
       bar_init(shared_addr(&bars->done[t]), 1);
+      bar_init(shared_addr(&bars->go[t]), 1);
     }
     for (int i = 0; i < kRing; ++i) {
       bar_init(shared_addr(&bars->full[i]), 1);
@@ -79,12 +83,12 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = uniform(bars->tmem);
   Reach reach[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
-    reach[t] = join(join(bars->reach[4 * t], bars->reach[4 * t + 1]),
-                    join(bars->reach[4 * t + 2], bars->reach[4 * t + 3]));
+    reach[t] = uniform(join(join(bars->reach[4 * t], bars->reach[4 * t + 1]),
+                            join(bars->reach[4 * t + 2], bars->reach[4 * t + 3])));
   const int first = min(reach[0].first(), reach[1].first());
   const int last = max(reach[0].hi > reach[0].lo ? reach[0].last() : 0,
                        reach[1].hi > reach[1].lo ? reach[1].last() : 0);
@@ -145,6 +149,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         fence_after_sync();
       };
       // keys of j: the scores' products, and this warp's part in giving their place back
+      const uint32_t my_go = shared_addr(&bars->go[t]), other_go = shared_addr(&bars->go[t ^ 1]);
       const auto scores = [&](int j) {
         const int at = 2 * (j - first);
         full(at);
@@ -152,13 +157,16 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         if (!ok) return;
         if (elect_one()) {
           if (j >= begin && j < end) {
-            mma_scores<T, C>(at_s, queries, ring + at % kRing * kTile, steps);
+            mma_scores<T, C>(at_s, queries, ring + at % kRing * kTile, steps, [&] { bar_arrive(other_go); });
             commit(bar_scores);
+          } else {
+            bar_arrive(other_go);
           }
           commit(shared_addr(&bars->empty[at % kRing]));
         }
       };
-      scores(first);
+      if (t == 1) ok = bar_wait(my_go, 0, g.status);
+      if (ok) scores(first);
       for (int j = first; ok && j < last; ++j) {
         const int at = 2 * (j - first) + 1;
         const uint32_t values = ring + at % kRing * kTile;
@@ -170,8 +178,12 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
             zero_rows<C>(values, inside_lo - j * kRows, inside_hi - j * kRows);
           ok = bar_wait(bar_weights, unsigned(j - begin) & 1, g.status);
           if (!ok) break;
-          fence_after_sync();
         }
+        // tile 0 of j comes behind tile 1's scores of j, tile 1 behind tile 0's of j + 1
+        const int before = j - first + t;
+        ok = bar_wait(my_go, unsigned(before) & 1, g.status);
+        if (!ok) break;
+        fence_after_sync();
         if (elect_one()) {
           if (here) {
             mma_rows<T, 64>(at_o, at_s, 64, values, n, j > begin);
@@ -179,7 +191,11 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
           }
           commit(shared_addr(&bars->empty[at % kRing]));
         }
-        if (j + 1 < last) scores(j + 1);
+        if (j + 1 < last) {
+          scores(j + 1);
+        } else if (elect_one()) {
+          bar_arrive(other_go);
+        }
       }
     }
   } else {
