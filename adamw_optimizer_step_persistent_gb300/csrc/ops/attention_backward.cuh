@@ -158,29 +158,26 @@ struct Backward {
   }
 };
 
-// 32 columns of scores of a lane's row become p (times 2^lift) in 16 bits and,
-// in place, p times ds/d(q . k).  lse(c): what is added to columns c and c + 1.
-// Columns outside [lo, hi) are not seen.
+// 32 columns of scores of a lane's row, but for a factor `mul`, become p (times
+// 2^lift) in 16 bits and, in place, p times ds/d(q . k).  lse(c): what is added
+// to columns c and c + 1.  Columns outside [lo, hi) are not seen.
 template <class E, bool kCap, bool kMask, class Lse>
-__device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], const Scores& f, float mul,
+__device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], const Pair* slopes, float mul,
                                            int lo, int hi, Lse lse) {
   const Pair mul_pair = both(mul);
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
-    float slope[2] = {1.0f, 1.0f};
-    if constexpr (kCap)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) slope[k] = 4.0f * s[c + k] * (1.0f - s[c + k]);
-    Pair z = make_pair(s[c], s[c + 1]);
-    z = kCap ? fma2(z, both(-2.0f * f.cap), add2(both(f.cap), lse(c))) : fma2(z, mul_pair, lse(c));
-    const float2 e = split(z);
+    const float2 e = split(fma2(make_pair(s[c], s[c + 1]), mul_pair, lse(c)));
     float w[2] = {exp2_fast(e.x), exp2_fast(e.y)};
     if constexpr (kMask)
 #pragma unroll
       for (int k = 0; k < 2; ++k) w[k] = c + k >= lo && c + k < hi ? w[k] : 0.0f;
     p[c / 2] = pack2<E>(w[0], w[1]);
-    s[c] = kCap ? w[0] * slope[0] : w[0];
-    s[c + 1] = kCap ? w[1] * slope[1] : w[1];
+    Pair d = make_pair(w[0], w[1]);
+    if constexpr (kCap) d = mul2(d, slopes[c / 2]);
+    const float2 v = split(d);
+    s[c] = v.x;
+    s[c + 1] = v.y;
   }
 }
 // `apart`: the first column's place less the row's.
@@ -188,31 +185,22 @@ template <class E, class Lse>
 __device__ __forceinline__ void weights(float (&s)[32], uint32_t (&p)[16], const Scores& f, float apart,
                                         bool whole, int lo, int hi, Lse lse) {
   if (f.cap != 0.0f) {
+    f.capped(s);
+    Pair slopes[16];  // 1 - tanh^2
+    const Pair in = both(1.0f / f.cap);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) s[c] = f.folded(s[c]);
-    if (f.slope != 0.0f) {
-      const auto lowered = [&](int c) {
-        const float2 l = split(lse(c));
-        return make_pair(fmaf(-f.slope, fabsf(apart + float(c)), l.x),
-                         fmaf(-f.slope, fabsf(apart + float(c + 1)), l.y));
-      };
-      if (whole) weights_of<E, true, false>(s, p, f, 1.0f, lo, hi, lowered);
-      else weights_of<E, true, true>(s, p, f, 1.0f, lo, hi, lowered);
-    } else if (whole) {
-      weights_of<E, true, false>(s, p, f, 1.0f, lo, hi, lse);
-    } else {
-      weights_of<E, true, true>(s, p, f, 1.0f, lo, hi, lse);
+    for (int c = 0; c < 32; c += 2) {
+      const Pair t = mul2(make_pair(s[c], s[c + 1]), in);
+      slopes[c / 2] = fma2(mul2(t, both(-1.0f)), t, both(1.0f));
     }
+    if (f.slope != 0.0f) f.lowered(s, apart);
+    if (whole) weights_of<E, true, false>(s, p, slopes, 1.0f, lo, hi, lse);
+    else weights_of<E, true, true>(s, p, slopes, 1.0f, lo, hi, lse);
     return;
   }
-  float mul = f.mul;
-  if (f.slope != 0.0f) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c] * f.mul);
-    mul = 1.0f;
-  }
-  if (whole) weights_of<E, false, false>(s, p, f, mul, lo, hi, lse);
-  else weights_of<E, false, true>(s, p, f, mul, lo, hi, lse);
+  const float mul = f.finish(s, apart);
+  if (whole) weights_of<E, false, false>(s, p, nullptr, mul, lo, hi, lse);
+  else weights_of<E, false, true>(s, p, nullptr, mul, lo, hi, lse);
 }
 
 // 32 columns of ds: p (at s) times (grad_out . v - delta), `delta(c)` added to
@@ -308,35 +296,36 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         if (from < inside_lo || from + kRows > inside_hi) zero_rows<C>(at, inside_lo - from, inside_hi - from);
       };
       const auto scores = [&](int i) {
-        if (!b.wait_x(i, status)) return false;
-        fence_after_sync();
-        clean(b.x_at(i), i);
-        if (elect_one()) {
-          mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
-          commit(shared_addr(&bars->scores));
-        }
-        return true;
+        mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
+        commit(shared_addr(&bars->scores));
       };
       const auto dots = [&](int i) {
-        if (!b.wait_y(i, status)) return false;
-        fence_after_sync();
-        clean(b.y_at(i), i);
-        if (elect_one()) {
-          mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
-          commit(shared_addr(&bars->dots));
-        }
-        return true;
+        mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
+        commit(shared_addr(&bars->dots));
       };
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && scores(0) && dots(0);
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && b.wait_x(0, status) && b.wait_y(0, status);
+      if (ok) {
+        clean(b.x_at(0), 0);
+        clean(b.y_at(0), 0);
+        if (elect_one()) {
+          scores(0);
+          dots(0);
+        }
+      }
       for (int i = 0; ok && i < n; ++i) {
-        ok = bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
+        const bool more = i + 1 < n;
+        if (more) {
+          ok = b.wait_x(i + 1, status);
+          if (ok) clean(b.x_at(i + 1), i + 1);
+        }
+        ok = ok && bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
           mma_rows<T, 32>(tmem + kColumnsA, tmem + kColumnsS, 32, b.y_at(i), width, i > 0);
           commit(shared_addr(&bars->y_empty[i % kRingY]));
+          if (more) scores(i + 1);
         }
-        if (i + 1 < n && !(ok = scores(i + 1))) break;
         ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
         if (!ok) break;
         fence_after_sync();
@@ -344,7 +333,14 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
           mma_rows<T, 32>(tmem + kColumnsB, tmem + kColumnsDots, 32, b.x_at(i), width, i > 0);
           commit(shared_addr(&bars->x_empty[i % kRingX]));
         }
-        if (i + 1 < n) ok = dots(i + 1);
+        if (more) {
+          // (not before grad_k's product: Y's place was given back only a turn ago)
+          ok = b.wait_y(i + 1, status);
+          if (!ok) break;
+          fence_after_sync();
+          clean(b.y_at(i + 1), i + 1);
+          if (elect_one()) dots(i + 1);
+        }
       }
       if (ok && elect_one()) commit(shared_addr(&bars->done));
     }

@@ -143,45 +143,41 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       const uint32_t queries = q_tiles + t * kTile, at_s = tmem + t * kRows, at_o = tmem + (2 + t) * kRows;
       const uint32_t bar_scores = shared_addr(&bars->scores[t]), bar_weights = shared_addr(&bars->weights[t]);
       const int begin = mine.first(), end = mine.last();
+      const uint32_t my_go = shared_addr(&bars->go[t]), other_go = shared_addr(&bars->go[t ^ 1]);
       bool ok = true;
       const auto full = [&](int i) {
         ok = ok && bar_wait(shared_addr(&bars->full[i % kRing]), unsigned(i / kRing) & 1, g.status);
-        fence_after_sync();
       };
-      // keys of j: the scores' products, and this warp's part in giving their place back
-      const uint32_t my_go = shared_addr(&bars->go[t]), other_go = shared_addr(&bars->go[t ^ 1]);
+      // the scores of j, and this warp's part in giving the keys' place back; the
+      // other tile's products may follow from half way through
       const auto scores = [&](int j) {
-        const int at = 2 * (j - first);
-        full(at);
-        if (ok && j == begin) ok = bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
-        if (!ok) return;
-        if (elect_one()) {
-          if (j >= begin && j < end) {
-            mma_scores<T, C>(at_s, queries, ring + at % kRing * kTile, steps, [&] { bar_arrive(other_go); });
-            commit(bar_scores);
-          } else {
-            bar_arrive(other_go);
-          }
-          commit(shared_addr(&bars->empty[at % kRing]));
+        const int at = 2 * (j - first) % kRing;
+        if (j >= begin && j < end) {
+          mma_scores<T, C>(at_s, queries, ring + at * kTile, steps, [&] { bar_arrive(other_go); });
+          commit(bar_scores);
+        } else {
+          bar_arrive(other_go);
         }
+        commit(shared_addr(&bars->empty[at]));
       };
-      if (t == 1) ok = bar_wait(my_go, 0, g.status);
-      if (ok) scores(first);
+      full(0);
+      if (ok && begin < end) ok = bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
+      if (ok && t == 1) ok = bar_wait(my_go, 0, g.status);
+      fence_after_sync();
+      if (ok && elect_one()) scores(first);
       for (int j = first; ok && j < last; ++j) {
         const int at = 2 * (j - first) + 1;
         const uint32_t values = ring + at % kRing * kTile;
+        const bool here = j >= begin && j < end, more = j + 1 < last;
         full(at);
-        if (!ok) break;
-        const bool here = j >= begin && j < end;
-        if (here) {
+        if (more) full(at + 1);
+        if (ok && here) {
           if (j * kRows < inside_lo || (j + 1) * kRows > inside_hi)
             zero_rows<C>(values, inside_lo - j * kRows, inside_hi - j * kRows);
           ok = bar_wait(bar_weights, unsigned(j - begin) & 1, g.status);
-          if (!ok) break;
         }
         // tile 0 of j comes behind tile 1's scores of j, tile 1 behind tile 0's of j + 1
-        const int before = j - first + t;
-        ok = bar_wait(my_go, unsigned(before) & 1, g.status);
+        ok = ok && bar_wait(my_go, unsigned(j - first + t) & 1, g.status);
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
@@ -190,11 +186,11 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
             if (j + 1 == end) commit(shared_addr(&bars->done[t]));
           }
           commit(shared_addr(&bars->empty[at % kRing]));
-        }
-        if (j + 1 < last) {
-          scores(j + 1);
-        } else if (elect_one()) {
-          bar_arrive(other_go);
+          if (more) {
+            scores(j + 1);
+          } else {
+            bar_arrive(other_go);
+          }
         }
       }
     }
@@ -210,8 +206,6 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     float* told = &bars->shared[t][half][quarter * 32 + lane];
     const float* other = &bars->shared[t][half ^ 1][quarter * 32 + lane];
     const Scores f(g, head);
-    const bool ready = f.cap != 0.0f || f.slope != 0.0f;  // scores are in units of log 2 before the maximum
-    const float mul = ready ? 1.0f : f.mul;
     constexpr float kLift = T::code == FADAM_DT_F16 ? 7.0f : 0.0f;
     float top = -INFINITY, sum = 0.0f;   // top: the reference that exponents are relative to
     bool ok = true;
@@ -227,18 +221,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       tmem_load32(at_s + 32, s + 32);
       tmem_wait<64>(s);
       const int at = j * kRows + half * 64;  // the first column's key
-      if (f.cap != 0.0f) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = fmaf(-2.0f * f.cap, f.folded(s[c]), f.cap);
-      } else if (ready) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] *= f.mul;
-      }
-      if (f.slope != 0.0f) {
-        const float apart = float(at - row);
-#pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = fmaf(-f.slope, fabsf(apart + float(c)), s[c]);
-      }
+      const float mul = f.finish(s, float(at - row));
       if (!mine.whole(j * kRows)) {
         const int lo = span.key_lo - at, hi = span.key_hi - at;
 #pragma unroll
