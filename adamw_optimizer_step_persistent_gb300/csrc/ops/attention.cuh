@@ -29,6 +29,21 @@ fadam_status launched_with(const char* what) {
 
 constexpr int kBoxBytes = kRows * kChunk * 2;  // 128 rows of 128 bytes, 128-byte swizzle
 
+// A place in a ring of N and the parity of its barrier's phase.  (Kept from turn
+// to turn: a quotient and a remainder a turn cost the multiplying warps, whose
+// instructions wait among those of twenty warps, some 300 cycles.)
+template <int N>
+struct Place {
+  int at = 0;
+  unsigned parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // ---- copies -----------------------------------------------------------------------------
 
 __device__ __forceinline__ void load_head_box(uint32_t dst, const CUtensorMap* map, int x, int head,
@@ -199,11 +214,13 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, int apart, uint
     mma_tmem(d, a + k * 16 / kEach * apart + k * 16 % kEach / 2, db + k * (2048 >> 4), idesc, add || k > 0);
 }
 
-// Rows [from, to) of a tile, and no others, hold tokens of documents: the rest
+// Rows of a tile (its first one is token `at`) that lie outside all documents
 // become zero, so that 0 times what padding holds is 0.  By a whole warp,
-// between the copy's arrival and the first product.
+// between the copy's arrival and the product over the tile's rows.
 template <int C>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to) {
+__device__ __forceinline__ void clean_rows(uint32_t tile, int at, const AttentionArgs& g) {
+  const int from = __ldg(g.documents) - at, to = __ldg(g.documents + g.n_documents) - at;
+  if (from <= 0 && to >= kRows) return;
   for (int r = threadIdx.x % 32; r < kRows; r += 32)
     if (r < from || r >= to)
 #pragma unroll

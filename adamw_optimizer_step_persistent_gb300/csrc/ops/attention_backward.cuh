@@ -118,13 +118,13 @@ struct Backward {
     return uniform(join(join(bars->reach[0], bars->reach[1]), join(bars->reach[2], bars->reach[3])));
   }
 
-  __device__ __forceinline__ uint32_t x_at(int i) const { return x + i % kRingX * kTile; }
-  __device__ __forceinline__ uint32_t y_at(int i) const { return y + i % kRingY * kTile; }
-  __device__ __forceinline__ bool wait_x(int i, int* status) const {
-    return bar_wait(shared_addr(&bars->x_full[i % kRingX]), unsigned(i / kRingX) & 1, status);
+  __device__ __forceinline__ uint32_t x_at(int at) const { return x + at * kTile; }
+  __device__ __forceinline__ uint32_t y_at(int at) const { return y + at * kTile; }
+  __device__ __forceinline__ bool wait_x(const Place<kRingX>& p, int* status) const {
+    return bar_wait(shared_addr(&bars->x_full[p.at]), p.parity, status);
   }
-  __device__ __forceinline__ bool wait_y(int i, int* status) const {
-    return bar_wait(shared_addr(&bars->y_full[i % kRingY]), unsigned(i / kRingY) & 1, status);
+  __device__ __forceinline__ bool wait_y(const Place<kRingY>& p, int* status) const {
+    return bar_wait(shared_addr(&bars->y_full[p.at]), p.parity, status);
   }
 
   // The loading thread: the CTA's own two tiles, then X and Y of n turns in
@@ -136,25 +136,25 @@ struct Backward {
     const uint32_t own = shared_addr(&bars->own_full);
     bar_expect(own, 2 * kTile);
     load_own(own0, own1, own);
-    int i = 0;
-    for (; i < n; ++i) {
-      const int sx = i % kRingX, sy = i % kRingY;
-      if (i >= kRingX) ok = bar_wait(shared_addr(&bars->x_empty[sx]), unsigned(i / kRingX - 1) & 1, status);
+    Place<kRingX> px;  // an empty place passes for the parity before the first phase's
+    Place<kRingY> py;
+    for (int i = 0; i < n; ++i, px.next(), py.next()) {
+      ok = bar_wait(shared_addr(&bars->x_empty[px.at]), px.parity ^ 1, status);
       if (!ok) break;
-      uint32_t bar = shared_addr(&bars->x_full[sx]);
+      uint32_t bar = shared_addr(&bars->x_full[px.at]);
       bar_expect(bar, kTile + x_extra);
-      load_x(i, x_at(i), sx, bar);
-      if (i >= kRingY) ok = bar_wait(shared_addr(&bars->y_empty[sy]), unsigned(i / kRingY - 1) & 1, status);
+      load_x(i, x_at(px.at), px.at, bar);
+      ok = bar_wait(shared_addr(&bars->y_empty[py.at]), py.parity ^ 1, status);
       if (!ok) break;
-      bar = shared_addr(&bars->y_full[sy]);
+      bar = shared_addr(&bars->y_full[py.at]);
       bar_expect(bar, kTile + y_extra);
-      load_y(i, y_at(i), sy, bar);
+      load_y(i, y_at(py.at), py.at, bar);
     }
     // every copy has landed and been used when the CTA ends
-    for (int k = i < kRingX ? 0 : i - kRingX; k < i; ++k)
-      bar_wait(shared_addr(&bars->x_empty[k % kRingX]), unsigned(k / kRingX) & 1, status);
-    for (int k = i < kRingY ? 0 : i - kRingY; k < i; ++k)
-      bar_wait(shared_addr(&bars->y_empty[k % kRingY]), unsigned(k / kRingY) & 1, status);
+    for (int i = 0; i < kRingX; ++i, px.next())
+      bar_wait(shared_addr(&bars->x_empty[px.at]), px.parity ^ 1, status);
+    for (int i = 0; i < kRingY; ++i, py.next())
+      bar_wait(shared_addr(&bars->y_empty[py.at]), py.parity ^ 1, status);
   }
 };
 
@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   const Reach reach = b.meet(span.query_lo, span.query_hi, key0 + row < g.tokens);
   const uint32_t tmem = uniform(bars->tmem);
   const int first = reach.first(), turns = reach.last() - first, n = turns * share;
-  const auto query_tile = [&](int i) { return first + i % turns; };
 
   if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();
   if (warp == kIdle) {
@@ -262,21 +261,24 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       const int64_t pitch = int64_t(g.tiles) * kRows;
       const float* lse = g.stats;
       const float* delta = g.stats + pitch * g.heads;
+      int head = head0, at = first;  // of the turn: a tile of queries
       b.load_loop(
           n, kRows * 4, kRows * 4, status,
           [&](uint32_t k, uint32_t v, uint32_t bar) {
             load_head<C>(k, &maps.k, kv, key0, bar);
             load_head<C>(v, &maps.v, kv, key0, bar);
           },
-          [&](int i, uint32_t dst, int slot, uint32_t bar) {
-            const int head = head0 + i / turns, at = query_tile(i) * kRows;
-            load_head<C>(dst, &maps.q, head, at, bar);
-            load_bytes(shared_addr(b.extra->delta[slot]), delta + head * pitch + at, kRows * 4, bar);
+          [&](int, uint32_t dst, int slot, uint32_t bar) {
+            load_head<C>(dst, &maps.q, head, at * kRows, bar);
+            load_bytes(shared_addr(b.extra->delta[slot]), delta + head * pitch + at * kRows, kRows * 4, bar);
           },
-          [&](int i, uint32_t dst, int slot, uint32_t bar) {
-            const int head = head0 + i / turns, at = query_tile(i) * kRows;
-            load_head<C>(dst, &maps.grad_out, head, at, bar);
-            load_bytes(shared_addr(b.extra->lse[slot]), lse + head * pitch + at, kRows * 4, bar);
+          [&](int, uint32_t dst, int slot, uint32_t bar) {
+            load_head<C>(dst, &maps.grad_out, head, at * kRows, bar);
+            load_bytes(shared_addr(b.extra->lse[slot]), lse + head * pitch + at * kRows, kRows * 4, bar);
+            if (++at == first + turns) {
+              at = first;
+              ++head;
+            }
           });
     }
   } else if (warp == kMultiply) {
@@ -286,27 +288,26 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     // same time, and p(i + 1) waited for both: 3600 cycles a turn.)
     if (n > 0) {
       const int steps = (g.width + 15) / 16, width = steps * 16;
-      int inside_lo = 0, inside_hi = g.tiles * kRows;
-      if (g.documents) {
-        inside_lo = __ldg(g.documents);
-        inside_hi = __ldg(g.documents + g.n_documents);
-      }
-      const auto clean = [&](uint32_t at, int i) {
-        const int from = query_tile(i) * kRows;
-        if (from < inside_lo || from + kRows > inside_hi) zero_rows<C>(at, inside_lo - from, inside_hi - from);
-      };
-      const auto scores = [&](int i) {
-        mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
+      const uint32_t bar_weights = shared_addr(&bars->weights);
+      const auto scores = [&](int at) {
+        mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(at), steps);
         commit(shared_addr(&bars->scores));
       };
-      const auto dots = [&](int i) {
-        mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
+      const auto dots = [&](int at) {
+        mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(at), steps);
         commit(shared_addr(&bars->dots));
       };
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && b.wait_x(0, status) && b.wait_y(0, status);
+      Place<kRingX> x, next_x;
+      Place<kRingY> y, next_y;
+      int query = first;  // the tile of next_x and next_y
+      const auto clean = [&](uint32_t at) {
+        if (g.documents) clean_rows<C>(at, query * kRows, g);
+      };
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && b.wait_x(x, status) && b.wait_y(y, status);
       if (ok) {
-        clean(b.x_at(0), 0);
-        clean(b.y_at(0), 0);
+        clean(b.x_at(0));
+        clean(b.y_at(0));
+        fence_after_sync();
         if (elect_one()) {
           scores(0);
           dots(0);
@@ -314,33 +315,38 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       }
       for (int i = 0; ok && i < n; ++i) {
         const bool more = i + 1 < n;
+        next_x.next();
+        next_y.next();
+        if (++query == first + turns) query = first;
         if (more) {
-          ok = b.wait_x(i + 1, status);
-          if (ok) clean(b.x_at(i + 1), i + 1);
+          ok = b.wait_x(next_x, status);
+          if (ok) clean(b.x_at(next_x.at));
         }
-        ok = ok && bar_wait(shared_addr(&bars->weights), unsigned(i) & 1, status);
+        ok = ok && bar_wait(bar_weights, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
-          mma_rows<T, 32>(tmem + kColumnsA, tmem + kColumnsS, 32, b.y_at(i), width, i > 0);
-          commit(shared_addr(&bars->y_empty[i % kRingY]));
-          if (more) scores(i + 1);
+          mma_rows<T, 32>(tmem + kColumnsA, tmem + kColumnsS, 32, b.y_at(y.at), width, i > 0);
+          commit(shared_addr(&bars->y_empty[y.at]));
+          if (more) scores(next_x.at);
         }
         ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
-          mma_rows<T, 32>(tmem + kColumnsB, tmem + kColumnsDots, 32, b.x_at(i), width, i > 0);
-          commit(shared_addr(&bars->x_empty[i % kRingX]));
+          mma_rows<T, 32>(tmem + kColumnsB, tmem + kColumnsDots, 32, b.x_at(x.at), width, i > 0);
+          commit(shared_addr(&bars->x_empty[x.at]));
         }
         if (more) {
           // (not before grad_k's product: Y's place was given back only a turn ago)
-          ok = b.wait_y(i + 1, status);
+          ok = b.wait_y(next_y, status);
           if (!ok) break;
+          clean(b.y_at(next_y.at));
           fence_after_sync();
-          clean(b.y_at(i + 1), i + 1);
-          if (elect_one()) dots(i + 1);
+          if (elect_one()) dots(next_y.at);
         }
+        x = next_x;
+        y = next_y;
       }
       if (ok && elect_one()) commit(shared_addr(&bars->done));
     }
@@ -353,18 +359,20 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     const uint32_t bar_weights = shared_addr(&bars->weights);
     const float factor = ds_factor<T>(g) * exp2f(-kLiftBits<T>);
     bool ok = true;
+    Place<kRingX> x;
+    Place<kRingY> y;
     for (int h = 0, i = 0; h < share && ok; ++h) {
       const Scores f(g, head0 + h);
-      for (int turn = 0; turn < turns; ++turn, ++i) {
+      for (int turn = 0; turn < turns; ++turn, ++i, x.next(), y.next()) {
         const int at = (first + turn) * kRows + part * 32;  // the first column's query
         const bool whole = reach.whole((first + turn) * kRows);
         const int lo = span.query_lo - at, hi = span.query_hi - at;
         float s[32];
         uint32_t p[16];
         Pair of[16];  // the columns' lse, then their delta: read before the tensor cores are waited for
-        ok = b.wait_y(i, status);
+        ok = b.wait_y(y, status);
         if (!ok) break;
-        load_pairs(shared_addr(b.extra->lse[i % kRingY] + part * 32), of);
+        load_pairs(shared_addr(b.extra->lse[y.at] + part * 32), of);
         ok = bar_wait(bar_scores, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
@@ -377,9 +385,9 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(bar_weights);
 
-        ok = b.wait_x(i, status);
+        ok = b.wait_x(x, status);
         if (!ok) break;
-        load_pairs(shared_addr(b.extra->delta[i % kRingX] + part * 32), of);
+        load_pairs(shared_addr(b.extra->delta[x.at] + part * 32), of);
         ok = bar_wait(bar_dots, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
@@ -496,54 +504,51 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     // scores
     if (n > 0) {
       const int steps = (g.width + 15) / 16;
+      const uint32_t bar_read = shared_addr(&bars->scores_read);
+      Place<kRingX> x;
       bool ok = bar_wait(shared_addr(&bars->own_full), 0, status);
-      for (int i = 0; ok && i < n; ++i) {
-        ok = b.wait_x(i, status) &&
-             (i == 0 || bar_wait(shared_addr(&bars->scores_read), unsigned(i - 1) & 1, status));
+      for (int i = 0; ok && i < n; ++i, x.next()) {
+        ok = b.wait_x(x, status) && (i == 0 || bar_wait(bar_read, unsigned(i - 1) & 1, status));
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
-          mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(i), steps);
+          mma_scores<T, C>(tmem + kColumnsS, b.own0, b.x_at(x.at), steps);
           commit(shared_addr(&bars->scores));
-          commit(shared_addr(&bars->x_empty[i % kRingX]));
+          commit(shared_addr(&bars->x_empty[x.at]));
         }
       }
       if (ok && elect_one()) commit(shared_addr(&bars->done));
     }
   } else if (warp == kMultiply) {
-    // grad_out . v and grad_q
+    // grad_out . v of a turn, then grad_q of the one before
     if (n > 0) {
       const int steps = (g.width + 15) / 16, width = steps * 16;
-      int inside_lo = 0, inside_hi = g.tiles * kRows;
-      if (g.documents) {
-        inside_lo = __ldg(g.documents);
-        inside_hi = __ldg(g.documents + g.n_documents);
-      }
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status);
-      for (int i = 0; ok && i <= n; ++i) {
-        if (i < n) {
-          ok = b.wait_y(i, status) &&
-               (i == 0 || bar_wait(shared_addr(&bars->dots_read), unsigned(i - 1) & 1, status));
+      const uint32_t bar_read = shared_addr(&bars->dots_read);
+      Place<kRingX> x;
+      Place<kRingY> y;
+      const auto dots = [&] {
+        mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(y.at), steps);
+        commit(shared_addr(&bars->dots));
+        commit(shared_addr(&bars->y_empty[y.at]));
+      };
+      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && b.wait_y(y, status);
+      fence_after_sync();
+      if (ok && elect_one()) dots();
+      for (int i = 0; ok && i < n; ++i, x.next()) {
+        if (i + 1 < n) {
+          y.next();
+          ok = b.wait_y(y, status) && bar_wait(bar_read, unsigned(i) & 1, status);
           if (!ok) break;
           fence_after_sync();
-          if (elect_one()) {
-            mma_scores<T, C>(tmem + kColumnsDots, b.own1, b.y_at(i), steps);
-            commit(shared_addr(&bars->dots));
-            commit(shared_addr(&bars->y_empty[i % kRingY]));
-          }
+          if (elect_one()) dots();
         }
-        if (i == 0) continue;
-        const int k = i - 1, from = (first + k) * kRows;
-        ok = b.wait_x(k, status) &&
-             bar_wait(shared_addr(&bars->slopes[k & 1]), unsigned(k / 2) & 1, status);
+        ok = b.wait_x(x, status) && bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
         if (!ok) break;
+        if (g.documents) clean_rows<C>(b.x_at(x.at), (first + i) * kRows, g);
         fence_after_sync();
-        if (from < inside_lo || from + kRows > inside_hi)
-          zero_rows<C>(b.x_at(k), inside_lo - from, inside_hi - from);
         if (elect_one()) {
-          const uint32_t ds = tmem + kColumnsA + (k & 1) * 64;
-          mma_rows<T, 128>(tmem + kColumnsB, ds, 0, b.x_at(k), width, k > 0);
-          commit(shared_addr(&bars->x_empty[k % kRingX]));
+          mma_rows<T, 128>(tmem + kColumnsB, tmem + kColumnsA + (i & 1) * 64, 0, b.x_at(x.at), width, i > 0);
+          commit(shared_addr(&bars->x_empty[x.at]));
         }
       }
       if (ok && elect_one()) commit(shared_addr(&bars->done));

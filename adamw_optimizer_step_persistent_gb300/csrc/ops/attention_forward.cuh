@@ -24,19 +24,19 @@
 
 namespace fadam_ops {
 
-constexpr int kRing = 4;              // tiles of keys or values in flight
+constexpr int kRing = 2;              // pairs of a tile of keys and one of values in flight
 constexpr float kGrowth = 8.0f;
 
 struct ForwardBarriers {
   uint64_t q_full[2], scores[2], weights[2], done[2];
   uint64_t go[2];             // the tensor cores are this tile's
-  uint64_t full[kRing], empty[kRing];
+  uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
   Reach reach[8];
   float shared[2][2][kRows];  // what the two lanes of a row tell each other: tile, half, row
   uint32_t tmem;
 };
 template <int C>
-constexpr size_t kForwardSmem = 1024 + (2 + kRing) * C * size_t(kBoxBytes) + sizeof(ForwardBarriers);
+constexpr size_t kForwardSmem = 1024 + (2 + 2 * kRing) * C * size_t(kBoxBytes) + sizeof(ForwardBarriers);
 
 template <class T, int C>
 __global__ void __launch_bounds__(kAttentionThreads, 1)
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   const uint32_t q_tiles = (shared_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t ring = q_tiles + 2 * kTile;
   ForwardBarriers* bars =
-      reinterpret_cast<ForwardBarriers*>(smem_raw + (ring + kRing * kTile - shared_addr(smem_raw)));
+      reinterpret_cast<ForwardBarriers*>(smem_raw + (ring + 2 * kRing * kTile - shared_addr(smem_raw)));
   const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -59,8 +59,10 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       bar_init(shared_addr(&bars->go[t]), 1);
     }
     for (int i = 0; i < kRing; ++i) {
-      bar_init(shared_addr(&bars->full[i]), 1);
-      bar_init(shared_addr(&bars->empty[i]), 2);  // both multiplying warps
+      bar_init(shared_addr(&bars->k_full[i]), 1);
+      bar_init(shared_addr(&bars->v_full[i]), 1);
+      bar_init(shared_addr(&bars->k_empty[i]), 2);  // both multiplying warps
+      bar_init(shared_addr(&bars->v_empty[i]), 2);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -102,7 +104,6 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       prefetch_map(&maps.k);
       prefetch_map(&maps.v);
       const int kv = head / g.group;
-      int n = 0;
       bool ok = true;
       const auto queries = [&](int t) {
         if (reach[t].first() >= reach[t].last()) return;
@@ -110,24 +111,25 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         bar_expect(bar, kTile);
         load_head<C>(q_tiles + t * kTile, &maps.q, head, row0 + t * kRows, bar);
       };
-      const auto next = [&](const CUtensorMap* map, int j) {
-        const int at = n % kRing;
-        if (n >= kRing) ok = bar_wait(shared_addr(&bars->empty[at]), unsigned(n / kRing - 1) & 1, g.status);
-        if (!ok) return;
-        const uint32_t bar = shared_addr(&bars->full[at]);
-        bar_expect(bar, kTile);
-        load_head<C>(ring + at * kTile, map, kv, j * kRows, bar);
-        ++n;
-      };
+      Place<kRing> place;  // an empty place passes for the parity before the first phase's
       queries(0);
-      for (int j = first; ok && j < last; ++j) {
-        next(&maps.k, j);
+      for (int j = first; j < last; ++j, place.next()) {
+        ok = bar_wait(shared_addr(&bars->k_empty[place.at]), place.parity ^ 1, g.status);
+        if (!ok) break;
+        const uint32_t k_bar = shared_addr(&bars->k_full[place.at]), v_bar = shared_addr(&bars->v_full[place.at]);
+        bar_expect(k_bar, kTile);
+        load_head<C>(ring + 2 * place.at * kTile, &maps.k, kv, j * kRows, k_bar);
         if (j == first) queries(1);
-        if (ok) next(&maps.v, j);
+        ok = bar_wait(shared_addr(&bars->v_empty[place.at]), place.parity ^ 1, g.status);
+        if (!ok) break;
+        bar_expect(v_bar, kTile);
+        load_head<C>(ring + (2 * place.at + 1) * kTile, &maps.v, kv, j * kRows, v_bar);
       }
       // every copy has landed and been used when the CTA ends
-      for (int i = n < kRing ? 0 : n - kRing; i < n; ++i)
-        bar_wait(shared_addr(&bars->empty[i % kRing]), unsigned(i / kRing) & 1, g.status);
+      for (int i = 0; i < kRing; ++i, place.next()) {
+        bar_wait(shared_addr(&bars->k_empty[place.at]), place.parity ^ 1, g.status);
+        bar_wait(shared_addr(&bars->v_empty[place.at]), place.parity ^ 1, g.status);
+      }
     }
   } else if (warp == kMultiply || warp == kMultiply2) {
     // ---- tensor cores: a warp to a tile of queries
@@ -135,63 +137,57 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     const Reach mine = t ? reach[1] : reach[0];
     if (first < last) {
       const int steps = (g.width + 15) / 16, n = steps * 16;
-      int inside_lo = 0, inside_hi = g.tiles * kRows;
-      if (g.documents) {
-        inside_lo = __ldg(g.documents);
-        inside_hi = __ldg(g.documents + g.n_documents);
-      }
       const uint32_t queries = q_tiles + t * kTile, at_s = tmem + t * kRows, at_o = tmem + (2 + t) * kRows;
       const uint32_t bar_scores = shared_addr(&bars->scores[t]), bar_weights = shared_addr(&bars->weights[t]);
       const int begin = mine.first(), end = mine.last();
       const uint32_t my_go = shared_addr(&bars->go[t]), other_go = shared_addr(&bars->go[t ^ 1]);
-      bool ok = true;
-      const auto full = [&](int i) {
-        ok = ok && bar_wait(shared_addr(&bars->full[i % kRing]), unsigned(i / kRing) & 1, g.status);
-      };
       // the scores of j, and this warp's part in giving the keys' place back; the
       // other tile's products may follow from half way through
-      const auto scores = [&](int j) {
-        const int at = 2 * (j - first) % kRing;
+      const auto scores = [&](int j, int at) {
         if (j >= begin && j < end) {
-          mma_scores<T, C>(at_s, queries, ring + at * kTile, steps, [&] { bar_arrive(other_go); });
+          mma_scores<T, C>(at_s, queries, ring + 2 * at * kTile, steps, [&] { bar_arrive(other_go); });
           commit(bar_scores);
         } else {
           bar_arrive(other_go);
         }
-        commit(shared_addr(&bars->empty[at]));
+        commit(shared_addr(&bars->k_empty[at]));
       };
-      full(0);
+      Place<kRing> keys, values;
+      bool ok = bar_wait(shared_addr(&bars->k_full[0]), 0, g.status);
       if (ok && begin < end) ok = bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
       if (ok && t == 1) ok = bar_wait(my_go, 0, g.status);
       fence_after_sync();
-      if (ok && elect_one()) scores(first);
+      if (ok && elect_one()) scores(first, 0);
+      keys.next();
+      unsigned turn = 0, go = t;  // tile 0 of j comes behind tile 1's scores of j, tile 1 behind tile 0's of j + 1
       for (int j = first; ok && j < last; ++j) {
-        const int at = 2 * (j - first) + 1;
-        const uint32_t values = ring + at % kRing * kTile;
         const bool here = j >= begin && j < end, more = j + 1 < last;
-        full(at);
-        if (more) full(at + 1);
+        const uint32_t v_at = ring + (2 * values.at + 1) * kTile;
+        ok = bar_wait(shared_addr(&bars->v_full[values.at]), values.parity, g.status);
+        if (ok && more) ok = bar_wait(shared_addr(&bars->k_full[keys.at]), keys.parity, g.status);
         if (ok && here) {
-          if (j * kRows < inside_lo || (j + 1) * kRows > inside_hi)
-            zero_rows<C>(values, inside_lo - j * kRows, inside_hi - j * kRows);
-          ok = bar_wait(bar_weights, unsigned(j - begin) & 1, g.status);
+          if (g.documents) clean_rows<C>(v_at, j * kRows, g);
+          ok = bar_wait(bar_weights, turn, g.status);
+          turn ^= 1;
         }
-        // tile 0 of j comes behind tile 1's scores of j, tile 1 behind tile 0's of j + 1
-        ok = ok && bar_wait(my_go, unsigned(j - first + t) & 1, g.status);
+        ok = ok && bar_wait(my_go, go, g.status);
+        go ^= 1;
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
           if (here) {
-            mma_rows<T, 64>(at_o, at_s, 64, values, n, j > begin);
+            mma_rows<T, 64>(at_o, at_s, 64, v_at, n, j > begin);
             if (j + 1 == end) commit(shared_addr(&bars->done[t]));
           }
-          commit(shared_addr(&bars->empty[at % kRing]));
+          commit(shared_addr(&bars->v_empty[values.at]));
           if (more) {
-            scores(j + 1);
+            scores(j + 1, keys.at);
           } else {
             bar_arrive(other_go);
           }
         }
+        keys.next();
+        values.next();
       }
     }
   } else {
