@@ -141,7 +141,8 @@ fadam_status check_rows(const char* name, const void* p, int64_t stride, int64_t
 fadam_status check(const fadam_attention* d) {
   if (!d) return fail(FADAM_EINVAL, "the descriptor is NULL");
   if (!is_16bit(d->dtype)) return fail(FADAM_EDTYPE, "dtype %d is not bf16 or fp16", d->dtype);
-  if (d->flags & ~FADAM_ATTENTION_CAUSAL) return fail(FADAM_EINVAL, "unknown flag bits 0x%x", d->flags);
+  if (d->flags & ~FADAM_ATTENTION_CAUSAL || d->reserved)
+    return fail(FADAM_EINVAL, "unknown flag bits 0x%x, reserved %u", d->flags, d->reserved);
   if (d->tokens < 0 || d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads || d->width < 8 ||
       d->width % 8)
     return fail(FADAM_EINVAL, "%lld tokens, %d heads over %d, width %d (a multiple of 8)",
@@ -156,6 +157,8 @@ fadam_status check(const fadam_attention* d) {
     return fail(FADAM_EINVAL, "%lld documents", (long long)d->n_documents);
   if (!(d->scale > 0.0f) || !finite(d->scale)) return fail(FADAM_EINVAL, "scale is not finite and above 0");
   if (!(d->softcap >= 0.0f) || !finite(d->softcap)) return fail(FADAM_EINVAL, "softcap is not finite and at least 0");
+  if (d->softcap > 0.0f && !finite(d->scale / d->softcap))
+    return fail(FADAM_EINVAL, "scale %g over softcap %g is not finite", d->scale, d->softcap);
   fadam_status st;
   if ((st = check_rows("q", d->q, d->q_stride, d->q_head_stride, *d, d->heads)) ||
       (st = check_rows("k", d->k, d->k_stride, d->k_head_stride, *d, d->kv_heads)) ||
