@@ -7,33 +7,102 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// ---- spans of documents ------------------------------------------------------------------
+// ---- plans: the spans of documents, and the order of the tiles -----------------------------------
 
-// A thread to a token: its document by bisection, and what that makes it see.
-// A token outside all documents (or offsets that decrease) sees nothing.
-__global__ void __launch_bounds__(kThreads)
-    spans_kernel(const int32_t* documents, int64_t n, const int32_t* prefix, int tokens, bool causal,
-                 Spans* spans) {
-  chain_wait();
-  chain_next();
-  const int i = int(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= tokens) return;
-  int64_t lo = 0, hi = n + 1;  // the last offset that is not beyond i lies in [lo - 1, hi - 1]
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (__ldg(documents + mid) <= i) lo = mid + 1;
-    else hi = mid;
+struct PlanArgs {
+  const int32_t* documents;
+  const int32_t* prefix;
+  int64_t n_documents;
+  int tokens, sequence;
+  bool causal;
+  Spans* spans;        // [tokens], written where there are documents
+  int span_blocks;
+  // orders of tiles of `rows`, most work first: by the keys of their queries, or
+  // by the queries of their keys
+  struct Order {
+    int* to;
+    int rows, tiles;
+    bool keys;
+  } orders[2];
+};
+
+// What token i sees: by its document, found by bisection, or its sequence.  A
+// token outside all documents (or with offsets that decrease) sees nothing.
+__device__ __forceinline__ Spans find_spans(const PlanArgs& p, int i) {
+  int64_t d;
+  int a, b;
+  if (p.documents) {
+    int64_t lo = 0, hi = p.n_documents + 1;  // the last offset that is not beyond i lies in [lo - 1, hi - 1]
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (__ldg(p.documents + mid) <= i) lo = mid + 1;
+      else hi = mid;
+    }
+    d = lo - 1;
+    if (d < 0 || d >= p.n_documents) return Spans{};
+    a = max(__ldg(p.documents + d), 0);
+    b = min(__ldg(p.documents + d + 1), p.tokens);
+    if (i < a || i >= b) return Spans{};
+  } else {
+    d = i / p.sequence;
+    a = int(d) * p.sequence;
+    b = a + p.sequence;
   }
-  Spans s{};
-  const int64_t d = lo - 1;
-  if (d >= 0 && d < n) {
-    const int a = max(__ldg(documents + d), 0), b = min(__ldg(documents + d + 1), tokens);
-    if (a <= i && i < b) {
-      const int p = prefix ? min(max(__ldg(prefix + d), 0), b - a) : 0;
-      s = spans_in(i, a, b, p, causal);
+  return spans_in(i, a, b, p.prefix ? min(max(__ldg(p.prefix + d), 0), b - a) : 0, p.causal);
+}
+
+// One block to an order: the tiles sorted by how many tiles of the other side
+// their first and last rows reach, longest first, so that no long one is left
+// for the end.  (Equal ones in any order: it decides nothing but who is first.)
+__device__ void sort_tiles(const PlanArgs& p, const PlanArgs::Order& o) {
+  constexpr int kBuckets = 1024;
+  __shared__ int count[kBuckets];
+  int lo = 0, hi = p.tokens;
+  if (p.documents) {
+    lo = min(max(__ldg(p.documents), 0), p.tokens);
+    hi = min(max(__ldg(p.documents + p.n_documents), 0), p.tokens);
+  }
+  int shift = 0;
+  while ((p.tokens / kRows) >> shift >= kBuckets) ++shift;
+  const auto bucket = [&](int tile) {
+    const int first = max(tile * o.rows, lo), last = min((tile + 1) * o.rows, hi) - 1;
+    int work = 0;
+    if (first <= last) {
+      const Spans a = find_spans(p, first), b = find_spans(p, last);
+      work = o.keys ? b.query_hi - a.query_lo : b.key_hi - a.key_lo;
+    }
+    return kBuckets - 1 - min(max(work / kRows >> shift, 0), kBuckets - 1);
+  };
+  for (int i = threadIdx.x; i < kBuckets; i += kThreads) count[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < o.tiles; i += kThreads) atomicAdd(&count[bucket(i)], 1);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int sum = 0;
+    for (int i = 0; i < kBuckets; i += 32) {
+      const int n = count[i + threadIdx.x];
+      int upto = n;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int other = __shfl_up_sync(~0u, upto, d);
+        if (int(threadIdx.x) >= d) upto += other;
+      }
+      count[i + threadIdx.x] = sum + upto - n;
+      sum += __shfl_sync(~0u, upto, 31);
     }
   }
-  spans[i] = s;
+  __syncthreads();
+  for (int i = threadIdx.x; i < o.tiles; i += kThreads) o.to[atomicAdd(&count[bucket(i)], 1)] = i;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
+  chain_wait();
+  chain_next();
+  // (the orders first: they take longest)
+  const int orders = int(gridDim.x) - p.span_blocks, block = int(blockIdx.x) - orders;
+  if (block < 0) return sort_tiles(p, p.orders[blockIdx.x]);
+  const int i = block * kThreads + threadIdx.x;
+  if (i < p.tokens) p.spans[i] = find_spans(p, i);
 }
 
 // ---- the rows' lse and delta for the backward pass -------------------------------------------
@@ -188,36 +257,47 @@ fadam_status check(const fadam_attention_grad* d) {
 
 struct Layout {
   Spans* spans;
+  int* order;      // of tiles (pairs of them, forward) of queries
+  int* key_order;  // of tiles of keys
   float* stats;
   unsigned* peak;
   float* parts;
   int splits;
   size_t bytes;
 };
+// One sequence needs no plan: its last queries and first keys have most work.
+bool planned(const fadam_attention& d) { return d.documents || d.tokens > d.sequence; }
 Layout layout(const fadam_attention& d, char* base) {
   Layout l{};
   Carver c{base};
   if (d.documents) l.spans = static_cast<Spans*>(c.take(sizeof(Spans) * d.tokens));
+  if (planned(d)) l.order = static_cast<int*>(c.take(sizeof(int) * ceil_div(d.tokens, 2 * kRows)));
   l.bytes = c.used;
   return l;
 }
 
 // Over how many CTAs the query heads that share a key head are split, for
-// grad_k and grad_v: as few as give two CTAs to an SM.  (Under a causal mask
-// the first keys' CTA does twice the average's work.)
+// grad_k and grad_v: where there are fewer CTAs than SMs, and one that all
+// queries see would take more than eight turns.
 int splits_of(const fadam_attention& d, int sm_count) {
   const int group = d.heads / d.kv_heads;
-  const int64_t ctas = ceil_div(d.tokens, kRows) * d.kv_heads;
+  const int64_t tiles = ceil_div(d.tokens, kRows);
+  if (group * tiles <= 8) return 1;
   for (int s = 1; s < group; ++s)
-    if (group % s == 0 && ctas * s >= 2 * sm_count) return s;
+    if (group % s == 0 && tiles * d.kv_heads * s >= sm_count) return s;
   return group;
 }
 Layout layout(const fadam_attention_grad& desc, char* base, int sm_count) {
   const fadam_attention& d = desc.forward;
+  const int64_t tiles = ceil_div(d.tokens, kRows);
   Layout l{};
   Carver c{base};
   if (d.documents) l.spans = static_cast<Spans*>(c.take(sizeof(Spans) * d.tokens));
-  l.stats = static_cast<float*>(c.take(sizeof(float) * 2 * d.heads * round_up(d.tokens, kRows)));
+  if (planned(d)) {
+    l.order = static_cast<int*>(c.take(sizeof(int) * tiles));
+    l.key_order = static_cast<int*>(c.take(sizeof(int) * tiles));
+  }
+  l.stats = static_cast<float*>(c.take(sizeof(float) * 2 * d.heads * tiles * kRows));
   l.peak = static_cast<unsigned*>(c.take(sizeof(unsigned)));
   l.splits = splits_of(d, sm_count);
   if (l.splits > 1)
@@ -226,7 +306,7 @@ Layout layout(const fadam_attention_grad& desc, char* base, int sm_count) {
   return l;
 }
 
-AttentionArgs arguments(const fadam_attention& d, const Spans* spans, const DeviceFacts& dev) {
+AttentionArgs arguments(const fadam_attention& d, const Layout& l, const DeviceFacts& dev) {
   AttentionArgs g{};
   g.tokens = int(d.tokens);
   g.sequence = d.documents ? 0 : int(d.sequence);
@@ -238,7 +318,9 @@ AttentionArgs arguments(const fadam_attention& d, const Spans* spans, const Devi
   g.scale = d.scale;
   g.softcap = d.softcap;
   g.slopes = d.slopes;
-  g.spans = spans;
+  g.spans = l.spans;
+  g.order = l.order;
+  g.key_order = l.key_order;
   g.prefix = d.documents ? nullptr : d.prefix;
   g.documents = d.documents;
   g.n_documents = d.n_documents;
@@ -247,11 +329,22 @@ AttentionArgs arguments(const fadam_attention& d, const Spans* spans, const Devi
   return g;
 }
 
-fadam_status find_spans(const fadam_attention& d, Spans* spans, cudaStream_t stream) {
-  if (!d.documents) return FADAM_OK;
-  return launch_chained("document spans launch", spans_kernel, ceil_div(d.tokens, kThreads), kThreads, 0,
-                        stream, d.documents, d.n_documents, d.prefix, int(d.tokens),
-                        (d.flags & FADAM_ATTENTION_CAUSAL) != 0, spans);
+fadam_status plan(const fadam_attention& d, const Layout& l, cudaStream_t stream) {
+  if (!planned(d)) return FADAM_OK;
+  PlanArgs p{};
+  p.documents = d.documents;
+  p.prefix = d.prefix;
+  p.n_documents = d.n_documents;
+  p.tokens = int(d.tokens);
+  p.sequence = d.documents ? 0 : int(d.sequence);
+  p.causal = (d.flags & FADAM_ATTENTION_CAUSAL) != 0;
+  p.spans = l.spans;
+  p.span_blocks = l.spans ? int(ceil_div(d.tokens, kThreads)) : 0;
+  int orders = 0;
+  const int rows = l.key_order ? kRows : 2 * kRows, tiles = int(ceil_div(d.tokens, rows));
+  p.orders[orders++] = {l.order, rows, tiles, false};
+  if (l.key_order) p.orders[orders++] = {l.key_order, rows, tiles, true};
+  return launch_chained("attention plan launch", plan_kernel, orders + p.span_blocks, kThreads, 0, stream, p);
 }
 
 fadam_status check_workspace(const void* workspace, size_t bytes, size_t need) {
@@ -267,7 +360,7 @@ fadam_status backward(const fadam_attention_grad& desc, const Layout& l, const B
   using E = typename T::type;
   constexpr bool kPeak = T::code == FADAM_DT_F16;
   const fadam_attention& d = desc.forward;
-  AttentionArgs g = arguments(d, l.spans, dev);
+  AttentionArgs g = arguments(d, l, dev);
   g.stats = l.stats;
   g.peak = l.peak;
   g.parts = l.parts;
@@ -277,7 +370,7 @@ fadam_status backward(const fadam_attention_grad& desc, const Layout& l, const B
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   }
   fadam_status st;
-  if ((st = find_spans(d, l.spans, stream))) return st;
+  if ((st = plan(d, l, stream))) return st;
   const int pitch = g.tiles * kRows;
   if ((st = launch_chained("attention stats launch", stats_kernel<E, kPeak>,
                            int64_t(pitch / kStatRows) * d.heads, kThreads, 0, stream,
@@ -326,8 +419,8 @@ extern "C" fadam_status fadam_attention_run(const fadam_attention* desc, void* w
       (st = head_map(&maps.v, d.v, d.tokens, d.kv_heads, d.width, d.v_stride, d.v_head_stride)) ||
       (st = head_map(&maps.out, d.out, d.tokens, d.heads, d.width, int64_t(d.heads) * d.width, d.width)))
     return st;
-  if ((st = find_spans(d, l.spans, stream))) return st;
-  const AttentionArgs g = arguments(d, l.spans, dev);
+  if ((st = plan(d, l, stream))) return st;
+  const AttentionArgs g = arguments(d, l, dev);
   return d.dtype == FADAM_DT_BF16 ? attention_forward_bf16(maps, g, stream)
                                   : attention_forward_f16(maps, g, stream);
 }

@@ -240,10 +240,11 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
   chain_wait();
+  chain_next();  // (the queries' kernel reads nothing of this one)
 
-  // the first keys first: under a causal mask most queries see them
   const unsigned kv_heads = unsigned(g.heads / g.group), columns = kv_heads * g.splits;
-  const int tile = int(blockIdx.x / columns), rest = int(blockIdx.x % columns);
+  const int place = int(blockIdx.x / columns), tile = g.key_order ? g.key_order[place] : place;
+  const int rest = int(blockIdx.x % columns);
   const int kv = rest / g.splits, split = rest % g.splits;
   const int share = g.group / g.splits, head0 = kv * g.group + split * share;
   const int key0 = tile * kRows;
@@ -452,7 +453,6 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     }
   }
   __syncwarp();
-  chain_next();
   fence_before_sync();
   __syncthreads();
   if (warp == kMultiply) tmem_free(tmem, 512);
@@ -475,10 +475,14 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
-  chain_wait();
+  // No wait at the start: the keys' kernel, whose CTAs let this one's come once
+  // all of them run, waited for what comes before both, and neither reads what
+  // the other writes.  This one's CTAs take the SMs that the last of those
+  // leave; its own last CTA waits for them, so that what follows finds both done.
 
   const int head = int(blockIdx.x % unsigned(g.heads));
-  const int query0 = (g.tiles - 1 - int(blockIdx.x / unsigned(g.heads))) * kRows;
+  const int place = int(blockIdx.x / unsigned(g.heads));
+  const int query0 = (g.order ? g.order[place] : g.tiles - 1 - place) * kRows;
   const int row = threadIdx.x % kRows;
   Spans span{};
   if (warp < kScoreWarps && query0 + row < g.tokens) span = spans_of(g, query0 + row);
@@ -631,6 +635,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     }
   }
   __syncwarp();
+  if (blockIdx.x == gridDim.x - 1) chain_wait();
   chain_next();
   fence_before_sync();
   __syncthreads();

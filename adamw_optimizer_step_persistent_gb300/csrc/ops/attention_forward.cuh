@@ -69,10 +69,10 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   if (warp == kMultiply) tmem_alloc(shared_addr(&bars->tmem), 512);
   chain_wait();
 
-  // the last queries first: under a causal mask they have the most keys
   const int head = int(blockIdx.x % unsigned(g.heads));
   const int pairs = (g.tiles + 1) / 2;
-  const int row0 = (pairs - 1 - int(blockIdx.x / unsigned(g.heads))) * 2 * kRows;
+  const int place = int(blockIdx.x / unsigned(g.heads));
+  const int row0 = (g.order ? g.order[place] : pairs - 1 - place) * 2 * kRows;
   // warps of scores: four and four to a tile, each four with half the columns
   const int tile = warp / 8 & 1, half = warp / 4 & 1, quarter = warp % 4;
   const int row = row0 + tile * kRows + quarter * 32 + lane;

@@ -21,6 +21,8 @@ struct AttentionArgs {
   float scale, softcap;
   const float* slopes;
   const Spans* spans;        // [tokens] where there are documents
+  const int* order;          // of tiles of queries (forward: of pairs of them), or NULL: last ones first
+  const int* key_order;      // of tiles of keys, or NULL: first ones first
   const int32_t* prefix;     // of the sequences, where there are none
   const int32_t* documents;  // the first and the last offset say what is padding
   int64_t n_documents;

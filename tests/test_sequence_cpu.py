@@ -161,9 +161,9 @@ def test_attention_backward_refuses(at, value, want):
 
 def test_attention_workspace():
     size = ctypes.c_size_t(3)
-    assert L.fadam_attention_workspace(_attention(), size) == _abi.OK and size.value == 0
+    assert L.fadam_attention_workspace(_attention(sequence=64), size) == _abi.OK and size.value == 0
     packed = _attention(documents=FAKE, n_documents=3)
-    assert L.fadam_attention_workspace(packed, size) == _abi.OK and size.value == 16 * 64
+    assert L.fadam_attention_workspace(packed, size) == _abi.OK and size.value >= 16 * 64
     none = _attention(tokens=0, q=None, k=None, v=None, out=None, lse=None)
     assert L.fadam_attention_run(none, None, 0, None) == _abi.OK
     # a head or token dimension of one has no stride
