@@ -9,6 +9,7 @@ constexpr int kThreads = 256;
 
 // ---- plans: the spans of documents, and the order of the tiles -----------------------------------
 
+constexpr int kNearOffsets = 4096;  // most that are kept in shared memory
 struct PlanArgs {
   const int32_t* documents;
   const int32_t* prefix;
@@ -28,20 +29,21 @@ struct PlanArgs {
 
 // What token i sees: by its document, found by bisection, or its sequence.  A
 // token outside all documents (or with offsets that decrease) sees nothing.
-__device__ __forceinline__ Spans find_spans(const PlanArgs& p, int i) {
+// `offsets` are the documents', in shared memory where they fit.
+__device__ __forceinline__ Spans find_spans(const PlanArgs& p, const int32_t* offsets, int i) {
   int64_t d;
   int a, b;
   if (p.documents) {
     int64_t lo = 0, hi = p.n_documents + 1;  // the last offset that is not beyond i lies in [lo - 1, hi - 1]
     while (lo < hi) {
       const int64_t mid = (lo + hi) / 2;
-      if (__ldg(p.documents + mid) <= i) lo = mid + 1;
+      if (offsets[mid] <= i) lo = mid + 1;
       else hi = mid;
     }
     d = lo - 1;
     if (d < 0 || d >= p.n_documents) return Spans{};
-    a = max(__ldg(p.documents + d), 0);
-    b = min(__ldg(p.documents + d + 1), p.tokens);
+    a = max(offsets[d], 0);
+    b = min(offsets[d + 1], p.tokens);
     if (i < a || i >= b) return Spans{};
   } else {
     d = i / p.sequence;
@@ -54,13 +56,13 @@ __device__ __forceinline__ Spans find_spans(const PlanArgs& p, int i) {
 // One block to an order: the tiles sorted by how many tiles of the other side
 // their first and last rows reach, longest first, so that no long one is left
 // for the end.  (Equal ones in any order: it decides nothing but who is first.)
-__device__ void sort_tiles(const PlanArgs& p, const PlanArgs::Order& o) {
+__device__ __forceinline__ void sort_tiles(const PlanArgs& p, const PlanArgs::Order& o, const int32_t* offsets) {
   constexpr int kBuckets = 1024;
   __shared__ int count[kBuckets];
   int lo = 0, hi = p.tokens;
   if (p.documents) {
-    lo = min(max(__ldg(p.documents), 0), p.tokens);
-    hi = min(max(__ldg(p.documents + p.n_documents), 0), p.tokens);
+    lo = min(max(offsets[0], 0), p.tokens);
+    hi = min(max(offsets[p.n_documents], 0), p.tokens);
   }
   int shift = 0;
   while ((p.tokens / kRows) >> shift >= kBuckets) ++shift;
@@ -68,7 +70,7 @@ __device__ void sort_tiles(const PlanArgs& p, const PlanArgs::Order& o) {
     const int first = max(tile * o.rows, lo), last = min((tile + 1) * o.rows, hi) - 1;
     int work = 0;
     if (first <= last) {
-      const Spans a = find_spans(p, first), b = find_spans(p, last);
+      const Spans a = find_spans(p, offsets, first), b = find_spans(p, offsets, last);
       work = o.keys ? b.query_hi - a.query_lo : b.key_hi - a.key_lo;
     }
     return kBuckets - 1 - min(max(work / kRows >> shift, 0), kBuckets - 1);
@@ -98,11 +100,20 @@ __device__ void sort_tiles(const PlanArgs& p, const PlanArgs::Order& o) {
 __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
   chain_wait();
   chain_next();
+  // the offsets, next to the threads that bisect them (each step in global memory
+  // would wait for L2)
+  __shared__ int32_t near[kNearOffsets];
+  const int32_t* offsets = p.documents;
+  if (offsets && p.n_documents < kNearOffsets) {
+    for (int i = threadIdx.x; i <= p.n_documents; i += kThreads) near[i] = offsets[i];
+    __syncthreads();
+    offsets = near;
+  }
   // (the orders first: they take longest)
   const int orders = int(gridDim.x) - p.span_blocks, block = int(blockIdx.x) - orders;
-  if (block < 0) return sort_tiles(p, p.orders[blockIdx.x]);
+  if (block < 0) return sort_tiles(p, p.orders[blockIdx.x], offsets);
   const int i = block * kThreads + threadIdx.x;
-  if (i < p.tokens) p.spans[i] = find_spans(p, i);
+  if (i < p.tokens) p.spans[i] = find_spans(p, offsets, i);
 }
 
 // ---- the rows' lse and delta for the backward pass -------------------------------------------

@@ -67,9 +67,10 @@ __device__ __forceinline__ void store_head_box(const CUtensorMap* map, int x, in
                "r"(x), "r"(head), "r"(token), "r"(src)
                : "memory");
 }
-// Waits until this thread's stores have been written.
+// Waits until this thread's stores have read shared memory (they are written
+// by the time that the kernel ends).
 __device__ __forceinline__ void wait_stores() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 // What this thread wrote to shared memory is there for bulk copies and tensor cores.
 __device__ __forceinline__ void fence_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kSortThreads)
         for (int c = lane; c < width; c += 32) row[c] = from_float<Out>(0.0f);
       }
     }
-    if (kWide) asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+    if (kWide) asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 }
 
