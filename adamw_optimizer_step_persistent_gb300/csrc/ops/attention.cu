@@ -282,7 +282,7 @@ Layout layout(const fadam_attention& d, char* base) {
   Layout l{};
   Carver c{base};
   if (d.documents) l.spans = static_cast<Spans*>(c.take(sizeof(Spans) * d.tokens));
-  if (planned(d)) l.order = static_cast<int*>(c.take(sizeof(int) * ceil_div(d.tokens, 2 * kRows)));
+  if (planned(d)) l.order = static_cast<int*>(c.take(sizeof(int) * ceil_div(d.tokens, kRows)));
   l.bytes = c.used;
   return l;
 }
@@ -326,6 +326,7 @@ AttentionArgs arguments(const fadam_attention& d, const Layout& l, const DeviceF
   g.width = d.width;
   g.tiles = int(ceil_div(d.tokens, kRows));
   g.causal = (d.flags & FADAM_ATTENTION_CAUSAL) != 0;
+  g.pair_heads = g.group % 2 == 0;
   g.scale = d.scale;
   g.softcap = d.softcap;
   g.slopes = d.slopes;
@@ -352,7 +353,8 @@ fadam_status plan(const fadam_attention& d, const Layout& l, cudaStream_t stream
   p.spans = l.spans;
   p.span_blocks = l.spans ? int(ceil_div(d.tokens, kThreads)) : 0;
   int orders = 0;
-  const int rows = l.key_order ? kRows : 2 * kRows, tiles = int(ceil_div(d.tokens, rows));
+  const bool pairs = !l.key_order && d.heads / d.kv_heads % 2 != 0;  // forward: 256 consecutive rows
+  const int rows = pairs ? 2 * kRows : kRows, tiles = int(ceil_div(d.tokens, rows));
   p.orders[orders++] = {l.order, rows, tiles, false};
   if (l.key_order) p.orders[orders++] = {l.key_order, rows, tiles, true};
   return launch_chained("attention plan launch", plan_kernel, orders + p.span_blocks, kThreads, 0, stream, p);

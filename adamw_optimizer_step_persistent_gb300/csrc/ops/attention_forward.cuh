@@ -1,7 +1,9 @@
 // Attention, forward.
 //
-// A CTA takes 256 queries of one head in two tiles of 128, and walks over the
-// keys that any of them sees, 128 at a time, once: S = Q K^T on the tensor
+// A CTA takes two tiles of 128 queries and walks over the keys that any of them
+// sees, 128 at a time, once.  The tiles are the same rows of two query heads that
+// share their keys, where an even number of heads does (they see the same keys:
+// no turn is one tile's alone), else 256 consecutive rows of one head.  A turn: S = Q K^T on the tensor
 // cores, then two lanes to a query (of two warps, 64 columns each) take the
 // row's maximum, exponentials and sum in registers, hand the exponentials in 16
 // bits back to tensor memory, and O += P V.  The two tiles take turns: while four warps work on one tile's
@@ -69,13 +71,15 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   if (warp == kMultiply) tmem_alloc(shared_addr(&bars->tmem), 512);
   chain_wait();
 
-  const int head = int(blockIdx.x % unsigned(g.heads));
-  const int pairs = (g.tiles + 1) / 2;
-  const int place = int(blockIdx.x / unsigned(g.heads));
-  const int row0 = (g.order ? g.order[place] : pairs - 1 - place) * 2 * kRows;
+  const unsigned columns = unsigned(g.pair_heads ? g.heads / 2 : g.heads);
+  const int items = g.pair_heads ? g.tiles : (g.tiles + 1) / 2;
+  const int place = int(blockIdx.x / columns), item = g.order ? g.order[place] : items - 1 - place;
+  const int head0 = int(blockIdx.x % columns) << g.pair_heads, row0 = item * kRows << (g.pair_heads ^ 1);
+  const auto head_of = [&](int t) { return head0 + (t & g.pair_heads); };
+  const auto row_of = [&](int t) { return row0 + (g.pair_heads ? 0 : t * kRows); };
   // warps of scores: four and four to a tile, each four with half the columns
   const int tile = warp / 8 & 1, half = warp / 4 & 1, quarter = warp % 4;
-  const int row = row0 + tile * kRows + quarter * 32 + lane;
+  const int row = row_of(tile) + quarter * 32 + lane;
   Spans span{};
   if (warp < kScoreWarps) {
     if (row < g.tokens) span = spans_of(g, row);
@@ -103,13 +107,13 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       prefetch_map(&maps.q);
       prefetch_map(&maps.k);
       prefetch_map(&maps.v);
-      const int kv = head / g.group;
+      const int kv = head0 / g.group;
       bool ok = true;
       const auto queries = [&](int t) {
         if (reach[t].first() >= reach[t].last()) return;
         const uint32_t bar = shared_addr(&bars->q_full[t]);
         bar_expect(bar, kTile);
-        load_head<C>(q_tiles + t * kTile, &maps.q, head, row0 + t * kRows, bar);
+        load_head<C>(q_tiles + t * kTile, &maps.q, head_of(t), row_of(t), bar);
       };
       Place<kRing> place;  // an empty place passes for the parity before the first phase's
       queries(0);
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   } else {
     // ---- softmax: two lanes to a query, 64 columns each
     take_registers<kScoreRegisters>();
-    const int t = tile, pair = 1 + warp / 8 * 4 + quarter;  // pair: their warps' barrier
+    const int t = tile, head = head_of(t), pair = 1 + warp / 8 * 4 + quarter;  // pair: their warps' barrier
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
     const uint32_t at_s = lanes + t * kRows + half * 64;
     const uint32_t at_o = lanes + (2 + t) * kRows + half * C * 32;  // half of O's columns
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar_weights);
     }
-    if (row0 + t * kRows < g.tokens) {
+    if (row_of(t) < g.tokens) {
       // O / sum, through the queries' place in shared memory
       group_sync(pair, 64);  // what was told has been read
       *told = sum;
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (c * kChunk < g.width)
-            store_head_box(&maps.out, c * kChunk, head, row0 + t * kRows, q_tiles + t * kTile + c * kBoxBytes);
+            store_head_box(&maps.out, c * kChunk, head, row_of(t), q_tiles + t * kTile + c * kBoxBytes);
         wait_stores();
       }
     }
@@ -321,7 +325,7 @@ fadam_status launch_forward(const ForwardMaps& maps, const AttentionArgs& g, cud
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kForwardSmem<C>));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  const int64_t items = int64_t((g.tiles + 1) / 2) * g.heads;
+  const int64_t items = g.pair_heads ? int64_t(g.tiles) * (g.heads / 2) : int64_t((g.tiles + 1) / 2) * g.heads;
   return launch_chained("attention launch", kernel, items, kAttentionThreads, kForwardSmem<C>, stream, maps, g);
 }
 template <class T>

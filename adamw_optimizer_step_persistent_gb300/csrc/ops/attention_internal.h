@@ -18,10 +18,11 @@ struct AttentionArgs {
   int tokens, sequence, heads, group, width;   // group: query heads to a key head
   int tiles;                                   // of 128 tokens
   int causal;
+  int pair_heads;                              // forward: a CTA's two tiles are the same rows of two heads
   float scale, softcap;
   const float* slopes;
   const Spans* spans;        // [tokens] where there are documents
-  const int* order;          // of tiles of queries (forward: of pairs of them), or NULL: last ones first
+  const int* order;          // of tiles of queries (forward: of what a CTA takes), or NULL: last ones first
   const int* key_order;      // of tiles of keys, or NULL: first ones first
   const int32_t* prefix;     // of the sequences, where there are none
   const int32_t* documents;  // the first and the last offset say what is padding
