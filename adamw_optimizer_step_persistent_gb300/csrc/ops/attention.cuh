@@ -13,7 +13,7 @@ namespace fadam_ops {
 // four do without.
 constexpr int kScoreWarps = 16, kAttentionThreads = (kScoreWarps + 4) * 32;
 constexpr int kMultiply = kScoreWarps, kLoad = kMultiply + 1, kMultiply2 = kMultiply + 2, kIdle = kMultiply + 3;
-constexpr int kLaunchRegisters = 96, kScoreRegisters = 112, kOtherRegisters = 32;
+constexpr int kLaunchRegisters = 96, kScoreRegisters = 104, kOtherRegisters = 64;
 static_assert(4 * kScoreRegisters + kOtherRegisters == 5 * kLaunchRegisters, "no more than launched with");
 static_assert(kLaunchRegisters * kAttentionThreads <= 65536, "an SM's registers");
 // A kernel built with fewer would wait for its share of registers for ever.

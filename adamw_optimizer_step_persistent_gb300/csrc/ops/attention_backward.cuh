@@ -81,7 +81,7 @@ struct Backward {
     y = x + kRingX * kTile;
     extra = reinterpret_cast<BackwardExtra*>(smem + (2 + kRingX + kRingY) * kTile);
     bars = &extra->bars;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kLoad * 32) {
       bar_init(shared_addr(&bars->own_full), 1);
       bar_init(shared_addr(&bars->done), multiplying);
       for (int i = 0; i < kRingX; ++i) {
@@ -127,15 +127,20 @@ struct Backward {
     return bar_wait(shared_addr(&bars->y_full[p.at]), p.parity, status);
   }
 
-  // The loading thread: the CTA's own two tiles, then X and Y of n turns in
-  // turn.  load_own(dst0, dst1, bar), load_x(i, dst, slot, bar), load_y(...).
-  template <class Own, class X, class Y>
-  __device__ __forceinline__ void load_loop(int n, int x_extra, int y_extra, int* status, Own load_own,
-                                            X load_x, Y load_y) const {
+  // The loading thread: the CTA's own two tiles, while the others find out what
+  // they need, then X and Y of n turns in turn.  load_x(dst, slot, bar).
+  __device__ __forceinline__ void load_own(const CUtensorMap* map0, const CUtensorMap* map1, int head,
+                                           int token) const {
+    if (threadIdx.x != kLoad * 32) return;
+    const uint32_t bar = shared_addr(&bars->own_full);
+    bar_expect(bar, 2 * kTile);
+    load_head<C>(own0, map0, head, token, bar);
+    load_head<C>(own1, map1, head, token, bar);
+  }
+  template <class X, class Y>
+  __device__ __forceinline__ void load_loop(int n, int x_extra, int y_extra, int* status, X load_x,
+                                            Y load_y) const {
     bool ok = true;
-    const uint32_t own = shared_addr(&bars->own_full);
-    bar_expect(own, 2 * kTile);
-    load_own(own0, own1, own);
     Place<kRingX> px;  // an empty place passes for the parity before the first phase's
     Place<kRingY> py;
     for (int i = 0; i < n; ++i, px.next(), py.next()) {
@@ -143,14 +148,15 @@ struct Backward {
       if (!ok) break;
       uint32_t bar = shared_addr(&bars->x_full[px.at]);
       bar_expect(bar, kTile + x_extra);
-      load_x(i, x_at(px.at), px.at, bar);
+      load_x(x_at(px.at), px.at, bar);
       ok = bar_wait(shared_addr(&bars->y_empty[py.at]), py.parity ^ 1, status);
       if (!ok) break;
       bar = shared_addr(&bars->y_full[py.at]);
       bar_expect(bar, kTile + y_extra);
-      load_y(i, y_at(py.at), py.at, bar);
+      load_y(y_at(py.at), py.at, bar);
     }
     // every copy has landed and been used when the CTA ends
+    bar_wait(shared_addr(&bars->own_full), 0, status);
     for (int i = 0; i < kRingX; ++i, px.next())
       bar_wait(shared_addr(&bars->x_empty[px.at]), px.parity ^ 1, status);
     for (int i = 0; i < kRingY; ++i, py.next())
@@ -251,6 +257,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   const int row = threadIdx.x % kRows;  // of the first sixteen warps: a lane's key
   Spans span{};
   if (warp < kScoreWarps && key0 + row < g.tokens) span = spans_of(g, key0 + row);
+  b.load_own(&maps.k, &maps.v, kv, key0);
   const Reach reach = b.meet(span.query_lo, span.query_hi, key0 + row < g.tokens);
   const uint32_t tmem = uniform(bars->tmem);
   const int first = reach.first(), turns = reach.last() - first, n = turns * share;
@@ -258,22 +265,18 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();
   if (warp == kIdle) {
   } else if (warp == kLoad) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       const int64_t pitch = int64_t(g.tiles) * kRows;
       const float* lse = g.stats;
       const float* delta = g.stats + pitch * g.heads;
       int head = head0, at = first;  // of the turn: a tile of queries
       b.load_loop(
           n, kRows * 4, kRows * 4, status,
-          [&](uint32_t k, uint32_t v, uint32_t bar) {
-            load_head<C>(k, &maps.k, kv, key0, bar);
-            load_head<C>(v, &maps.v, kv, key0, bar);
-          },
-          [&](int, uint32_t dst, int slot, uint32_t bar) {
+          [&](uint32_t dst, int slot, uint32_t bar) {
             load_head<C>(dst, &maps.q, head, at * kRows, bar);
             load_bytes(shared_addr(b.extra->delta[slot]), delta + head * pitch + at * kRows, kRows * 4, bar);
           },
-          [&](int, uint32_t dst, int slot, uint32_t bar) {
+          [&](uint32_t dst, int slot, uint32_t bar) {
             load_head<C>(dst, &maps.grad_out, head, at * kRows, bar);
             load_bytes(shared_addr(b.extra->lse[slot]), lse + head * pitch + at * kRows, kRows * 4, bar);
             if (++at == first + turns) {
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     }
     // eight warps write grad_v (through v's place in shared memory), eight
     // grad_k, half of the elements to four warps
-    if (n > 0 && ok) ok = bar_wait(shared_addr(&bars->done), 0, status);
+    if (ok) ok = bar_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
     fence_after_sync();
     const bool keys = part >= 2;
     const float scale = keys ? g.scale / ds_factor<T>(g) : exp2f(-kLiftBits<T>);
@@ -486,6 +489,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   const int row = threadIdx.x % kRows;
   Spans span{};
   if (warp < kScoreWarps && query0 + row < g.tokens) span = spans_of(g, query0 + row);
+  b.load_own(&maps.q, &maps.grad_out, head, query0);
   const Reach reach = b.meet(span.key_lo, span.key_hi, query0 + row < g.tokens);
   const uint32_t tmem = uniform(bars->tmem);
   const int first = reach.first(), n = reach.last() - first;
@@ -493,16 +497,18 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();
   if (warp == kIdle) {
   } else if (warp == kLoad) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       const int kv = head / g.group;
-      b.load_loop(
-          n, 0, 0, status,
-          [&](uint32_t q, uint32_t go, uint32_t bar) {
-            load_head<C>(q, &maps.q, head, query0, bar);
-            load_head<C>(go, &maps.grad_out, head, query0, bar);
-          },
-          [&](int i, uint32_t dst, int, uint32_t bar) { load_head<C>(dst, &maps.k, kv, (first + i) * kRows, bar); },
-          [&](int i, uint32_t dst, int, uint32_t bar) { load_head<C>(dst, &maps.v, kv, (first + i) * kRows, bar); });
+      int x_key = first * kRows, y_key = x_key;
+      const auto keys = [&](uint32_t dst, int, uint32_t bar) {
+        load_head<C>(dst, &maps.k, kv, x_key, bar);
+        x_key += kRows;
+      };
+      const auto values = [&](uint32_t dst, int, uint32_t bar) {
+        load_head<C>(dst, &maps.v, kv, y_key, bar);
+        y_key += kRows;
+      };
+      b.load_loop(n, 0, 0, status, keys, values);
     }
   } else if (warp == kMultiply2) {
     // scores
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(shared_addr(&bars->slopes[i & 1]));
     }
-    if (n > 0 && ok) ok = bar_wait(shared_addr(&bars->done), 0, status);
+    if (ok) ok = bar_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
     fence_after_sync();
     const float scale = g.scale / ds_factor<T>(g);
     const uint32_t place = b.own0 + (quarter * 32 + lane) * 128;

@@ -52,7 +52,10 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       reinterpret_cast<ForwardBarriers*>(smem_raw + (ring + 2 * kRing * kTile - shared_addr(smem_raw)));
   const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
 
-  if (threadIdx.x == 0) {
+  if (warp == kMultiply) tmem_alloc(shared_addr(&bars->tmem), 512);
+  const unsigned columns = unsigned(g.pair_heads ? g.heads / 2 : g.heads);
+  const int items = g.pair_heads ? g.tiles : (g.tiles + 1) / 2;
+  if (warp == kLoad && lane == 0) {
     for (int t = 0; t < 2; ++t) {
       bar_init(shared_addr(&bars->q_full[t]), 1);
       bar_init(shared_addr(&bars->scores[t]), 1);
@@ -68,15 +71,19 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMultiply) tmem_alloc(shared_addr(&bars->tmem), 512);
   chain_wait();
-
-  const unsigned columns = unsigned(g.pair_heads ? g.heads / 2 : g.heads);
-  const int items = g.pair_heads ? g.tiles : (g.tiles + 1) / 2;
   const int place = int(blockIdx.x / columns), item = g.order ? g.order[place] : items - 1 - place;
   const int head0 = int(blockIdx.x % columns) << g.pair_heads, row0 = item * kRows << (g.pair_heads ^ 1);
   const auto head_of = [&](int t) { return head0 + (t & g.pair_heads); };
   const auto row_of = [&](int t) { return row0 + (g.pair_heads ? 0 : t * kRows); };
+  if (warp == kLoad && lane == 0) {
+    // the queries, while the others find out which keys they see
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t bar = shared_addr(&bars->q_full[t]);
+      bar_expect(bar, kTile);
+      load_head<C>(q_tiles + t * kTile, &maps.q, head_of(t), row_of(t), bar);
+    }
+  }
   // warps of scores: four and four to a tile, each four with half the columns
   const int tile = warp / 8 & 1, half = warp / 4 & 1, quarter = warp % 4;
   const int row = row_of(tile) + quarter * 32 + lane;
@@ -102,38 +109,28 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   if (warp >= kScoreWarps) keep_registers<kOtherRegisters>();
   if (warp == kIdle) {
   } else if (warp == kLoad) {
-    // ---- loads: the queries, then keys and values in turn
-    if (lane == 0 && first < last) {
-      prefetch_map(&maps.q);
-      prefetch_map(&maps.k);
-      prefetch_map(&maps.v);
+    // ---- loads: keys and values in turn
+    if (lane == 0) {
       const int kv = head0 / g.group;
       bool ok = true;
-      const auto queries = [&](int t) {
-        if (reach[t].first() >= reach[t].last()) return;
-        const uint32_t bar = shared_addr(&bars->q_full[t]);
-        bar_expect(bar, kTile);
-        load_head<C>(q_tiles + t * kTile, &maps.q, head_of(t), row_of(t), bar);
-      };
-      Place<kRing> place;  // an empty place passes for the parity before the first phase's
-      queries(0);
-      for (int j = first; j < last; ++j, place.next()) {
-        ok = bar_wait(shared_addr(&bars->k_empty[place.at]), place.parity ^ 1, g.status);
+      Place<kRing> pair;  // an empty place passes for the parity before the first phase's
+      for (int j = first; j < last; ++j, pair.next()) {
+        ok = bar_wait(shared_addr(&bars->k_empty[pair.at]), pair.parity ^ 1, g.status);
         if (!ok) break;
-        const uint32_t k_bar = shared_addr(&bars->k_full[place.at]), v_bar = shared_addr(&bars->v_full[place.at]);
+        const uint32_t k_bar = shared_addr(&bars->k_full[pair.at]), v_bar = shared_addr(&bars->v_full[pair.at]);
         bar_expect(k_bar, kTile);
-        load_head<C>(ring + 2 * place.at * kTile, &maps.k, kv, j * kRows, k_bar);
-        if (j == first) queries(1);
-        ok = bar_wait(shared_addr(&bars->v_empty[place.at]), place.parity ^ 1, g.status);
+        load_head<C>(ring + 2 * pair.at * kTile, &maps.k, kv, j * kRows, k_bar);
+        ok = bar_wait(shared_addr(&bars->v_empty[pair.at]), pair.parity ^ 1, g.status);
         if (!ok) break;
         bar_expect(v_bar, kTile);
-        load_head<C>(ring + (2 * place.at + 1) * kTile, &maps.v, kv, j * kRows, v_bar);
+        load_head<C>(ring + (2 * pair.at + 1) * kTile, &maps.v, kv, j * kRows, v_bar);
       }
       // every copy has landed and been used when the CTA ends
-      for (int i = 0; i < kRing; ++i, place.next()) {
-        bar_wait(shared_addr(&bars->k_empty[place.at]), place.parity ^ 1, g.status);
-        bar_wait(shared_addr(&bars->v_empty[place.at]), place.parity ^ 1, g.status);
+      for (int i = 0; i < kRing; ++i, pair.next()) {
+        bar_wait(shared_addr(&bars->k_empty[pair.at]), pair.parity ^ 1, g.status);
+        bar_wait(shared_addr(&bars->v_empty[pair.at]), pair.parity ^ 1, g.status);
       }
+      for (int t = 0; t < 2; ++t) bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
     }
   } else if (warp == kMultiply || warp == kMultiply2) {
     // ---- tensor cores: a warp to a tile of queries
@@ -258,15 +255,18 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       const float from = top == -INFINITY ? 0.0f : top - kLift;
       const Pair mul_pair = both(mul), less = both(-from);
       Pair part[2] = {};
-      uint32_t p[32];
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        const float2 z = split(fma2(make_pair(s[c], s[c + 1]), mul_pair, less));
-        const float a = exp2_fast(z.x), b = exp2_fast(z.y);
-        part[c / 2 % 2] = add2(part[c / 2 % 2], make_pair(a, b));
-        p[c / 2] = pack2<E>(a, b);
+      for (int h = 0; h < 64; h += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float2 z = split(fma2(make_pair(s[h + c], s[h + c + 1]), mul_pair, less));
+          const float a = exp2_fast(z.x), b = exp2_fast(z.y);
+          part[c / 2 % 2] = add2(part[c / 2 % 2], make_pair(a, b));
+          p[c / 2] = pack2<E>(a, b);
+        }
+        tmem_store16(at_s + h / 2, p);
       }
-      tmem_store32(at_s, p);
       sum += sum2(add2(part[0], part[1]));
       tmem_stored();
       fence_before_sync();
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       sum = half ? *other + sum : sum + *other;
       const bool none = begin >= end || sum == 0.0f;
       const float inverse = 1.0f / sum;
-      if (begin < end && ok) ok = bar_wait(shared_addr(&bars->done[t]), 0, g.status);
+      if (ok) ok = bar_wait(shared_addr(begin < end ? &bars->done[t] : &bars->q_full[t]), 0, g.status);
       fence_after_sync();
       const uint32_t place = q_tiles + t * kTile + (quarter * 32 + lane) * 128;
 #pragma unroll
