@@ -219,10 +219,16 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       tmem_wait<64>(s);
       const int at = j * kRows + half * 64;  // the first column's key
       const float mul = f.finish(s, float(at - row));
-      if (!mine.whole(j * kRows)) {
-        const int lo = span.key_lo - at, hi = span.key_hi - at;
+      // (most tiles that need a mask are cut on one side)
+      if (mine.all_hi < (j + 1) * kRows) {
+        const int hi = span.key_hi - at;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = c >= lo && c < hi ? s[c] : -INFINITY;
+        for (int c = 0; c < 64; ++c) s[c] = c < hi ? s[c] : -INFINITY;
+      }
+      if (mine.all_lo > j * kRows) {
+        const int lo = span.key_lo - at;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = c >= lo ? s[c] : -INFINITY;
       }
       float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll

@@ -114,39 +114,37 @@ def embedding_weight_grad(grad: torch.Tensor, tokens: torch.Tensor, vocab: Optio
 
 # ---- attention ---------------------------------------------------------------------------
 
-def _heads(t: torch.Tensor, what: str):
+def _heads(t: torch.Tensor, shape: tuple, what: str):
     """(token stride, head stride) of [..., tokens, heads, width]."""
-    if t.dim() < 3:
-        raise ValueError(f"{what} must be [..., tokens, heads, width], got {tuple(t.shape)}")
-    *lead, heads, width = t.shape
-    if t.is_contiguous():
-        return heads * width, width
-    if width > 1 and t.stride(-1) != 1:
+    step, width = t.stride(), shape[-1]
+    if step[-1] != 1 and width > 1:
         raise ValueError(f"the last dimension of {what} is not contiguous")
     # tokens: the dimensions before the heads, evenly strided
-    step = None
-    for n, s in reversed(list(zip(lead, t.stride()))):
+    token, many = step[-3], shape[-3]
+    for n, s in zip(shape[-4::-1], step[-4::-1]):
         if n == 1:
             continue
-        if step is None:
-            step, many = s, n
-        elif s == step * many:
-            many *= n
-        else:
+        if many == 1:
+            token = s
+        elif s != token * many and n and many:
             raise ValueError(f"the leading dimensions of {what} are not evenly strided")
-    return (heads * width if step is None else step), (t.stride(-2) if heads > 1 else width)
+        many *= n
+    return (token if many > 1 else shape[-2] * width), (step[-2] if shape[-2] > 1 else width)
 
 
 def _attention(q, k, v, causal, scale, softcap, slopes, documents, prefix):
     """The descriptor but for out and lse, and the device."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype not in _16BIT or t.dtype is not q.dtype:
-            raise TypeError(f"q, k and v must all be bf16 or fp16, got {name} {t.dtype}")
-    qs, ks, vs = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
-    heads, width = q.shape[-2:]
-    kv_heads = k.shape[-2]
-    if k.shape != v.shape or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != width:
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
+    dtype = q.dtype
+    if dtype not in _16BIT or k.dtype is not dtype or v.dtype is not dtype:
+        raise TypeError(f"q, k and v must all be bf16 or fp16, got {dtype}, {k.dtype} and {v.dtype}")
+    of_q, of_k = tuple(q.shape), tuple(k.shape)
+    if len(of_q) < 3:
+        raise ValueError(f"q must be [..., tokens, heads, width], got {of_q}")
+    if of_k != tuple(v.shape) or of_k[:-2] != of_q[:-2] or of_k[-1] != of_q[-1]:
+        raise ValueError(f"q {of_q}, k {of_k} and v {tuple(v.shape)} do not fit")
+    qs, ks, vs = _heads(q, of_q, "q"), _heads(k, of_k, "k"), _heads(v, of_k, "v")
+    sequence, heads, width = of_q[-3:]
+    kv_heads = of_k[-2]
     if not kv_heads or not heads or heads % kv_heads:
         raise ValueError(f"{kv_heads} heads of k and v do not divide {heads} of q")
     if width % 8 or not 0 < width <= _abi.ATTENTION_MAX_WIDTH:
@@ -157,7 +155,6 @@ def _attention(q, k, v, causal, scale, softcap, slopes, documents, prefix):
     if slopes is not None and (slopes.dtype is not torch.float32 or slopes.shape != (heads,)
                                or not slopes.is_contiguous()):
         raise ValueError(f"slopes must be a contiguous fp32 [{heads}]")
-    sequence = q.shape[-3]
     tokens = q.numel() // (heads * width)
     count = tokens // sequence if sequence else 0
     if documents is not None:
@@ -174,7 +171,7 @@ def _attention(q, k, v, causal, scale, softcap, slopes, documents, prefix):
         q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, _ptr(slopes), _ptr(documents),
         _ptr(prefix), tokens, max(sequence, 1), count, qs[0], ks[0], vs[0], qs[1], ks[1], vs[1],
         heads, kv_heads, width, float(width ** -0.5 if scale is None else scale), float(softcap),
-        dtype_code(q.dtype), _abi.ATTENTION_CAUSAL if causal else 0, 0)
+        dtype_code(dtype), _abi.ATTENTION_CAUSAL if causal else 0, 0)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = True,
@@ -222,12 +219,13 @@ def attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     The gradients of k and v are sums over the query heads that share them, in
     one fixed order."""
     index, desc = _attention(q, k, v, causal, scale, softcap, slopes, documents, prefix)
+    shape = tuple(q.shape)
     for name, t in (("out", out), ("grad_out", grad_out)):
-        if t.shape != q.shape or t.dtype is not q.dtype:
-            raise ValueError(f"{name} must be {q.dtype} of shape {tuple(q.shape)}")
-    if lse.shape != q.shape[:-1] or lse.dtype is not torch.float32 or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous fp32 {tuple(q.shape[:-1])}")
-    strides = *_heads(out, "out"), *_heads(grad_out, "grad_out")
+        if tuple(t.shape) != shape or t.dtype is not q.dtype:
+            raise ValueError(f"{name} must be {q.dtype} of shape {shape}")
+    if tuple(lse.shape) != shape[:-1] or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 {shape[:-1]}")
+    strides = *_heads(out, shape, "out"), *_heads(grad_out, shape, "grad_out")
     _check_device(index, "q", grad_out, out, lse)
     with _current(index):
         grads = AttentionGrads(_like(q), _like(k), _like(v))
