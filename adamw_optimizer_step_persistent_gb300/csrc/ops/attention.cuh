@@ -281,8 +281,6 @@ struct Reach {
   int lo, hi, all_lo, all_hi;
   __device__ __forceinline__ int first() const { return lo / kRows; }
   __device__ __forceinline__ int last() const { return hi > lo ? (hi + kRows - 1) / kRows : lo / kRows; }
-  // whether a tile that starts at `at` needs no mask
-  __device__ __forceinline__ bool whole(int at) const { return all_lo <= at && at + kRows <= all_hi; }
 };
 constexpr int kNever = 0x7fffff80;  // a multiple of 128
 // One warp's part of it; rows that do not exist (`here` false) ask for nothing.

@@ -164,68 +164,81 @@ struct Backward {
   }
 };
 
+// Which of 32 columns a lane's row does not see: those below lo, where a row
+// of the tile is cut there, and those from hi on.
+struct Cut {
+  bool below, above;
+  int lo, hi;
+  __device__ __forceinline__ Cut(const Reach& r, int tile, int column, int span_lo, int span_hi)
+      : below(r.all_lo > tile), above(r.all_hi < tile + kRows), lo(span_lo - column), hi(span_hi - column) {}
+  // (one side at a time: most tiles that need a mask are cut on one)
+  __device__ __forceinline__ void set(float (&v)[32], float to) const {
+    if (below)
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = c >= lo ? v[c] : to;
+    if (above)
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = c < hi ? v[c] : to;
+  }
+};
+
 // 32 columns of scores of a lane's row, but for a factor `mul`, become p (times
-// 2^lift) in 16 bits and, in place, p times ds/d(q . k).  lse(c): what is added
-// to columns c and c + 1.  Columns outside [lo, hi) are not seen.
-template <class E, bool kCap, bool kMask, class Lse>
-__device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], const Pair* slopes, float mul,
-                                           int lo, int hi, Lse lse) {
-  const Pair mul_pair = both(mul);
+// 2^lift), in 16 bits, and p times ds/d(q . k) in place: with a cap 1 - tanh^2,
+// from the capped scores, without their bias by distance (kBias).
+template <class E, bool kCap, bool kBias, class Lse>
+__device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], const Scores& f, float mul,
+                                           float apart, Lse lse) {
+  const Pair mul_pair = both(mul), in = both(kCap ? 1.0f / f.cap : 0.0f);
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
-    const float2 e = split(fma2(make_pair(s[c], s[c + 1]), mul_pair, lse(c)));
-    float w[2] = {exp2_fast(e.x), exp2_fast(e.y)};
-    if constexpr (kMask)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) w[k] = c + k >= lo && c + k < hi ? w[k] : 0.0f;
-    p[c / 2] = pack2<E>(w[0], w[1]);
-    Pair d = make_pair(w[0], w[1]);
-    if constexpr (kCap) d = mul2(d, slopes[c / 2]);
-    const float2 v = split(d);
+    const Pair z = make_pair(s[c], s[c + 1]);
+    const float2 e = split(fma2(z, mul_pair, lse(c)));
+    Pair w = make_pair(exp2_fast(e.x), exp2_fast(e.y));
+    float2 v = split(w);
+    p[c / 2] = pack2<E>(v.x, v.y);
+    if constexpr (kCap) {
+      Pair capped = z;
+      if constexpr (kBias)
+        capped = make_pair(fmaf(f.slope, fabsf(apart + float(c)), s[c]),
+                           fmaf(f.slope, fabsf(apart + float(c + 1)), s[c + 1]));
+      const Pair t = mul2(capped, in);
+      w = mul2(w, fma2(mul2(t, both(-1.0f)), t, both(1.0f)));
+      v = split(w);
+    }
     s[c] = v.x;
     s[c + 1] = v.y;
   }
 }
-// `apart`: the first column's place less the row's.
+// From products q . k.  lse(c): what is added to columns c and c + 1; `apart`:
+// the first column's place less the row's.  (What is not seen becomes p = 0, and
+// any value in place.)
 template <class E, class Lse>
 __device__ __forceinline__ void weights(float (&s)[32], uint32_t (&p)[16], const Scores& f, float apart,
-                                        bool whole, int lo, int hi, Lse lse) {
-  if (f.cap != 0.0f) {
-    f.capped(s);
-    Pair slopes[16];  // 1 - tanh^2
-    const Pair in = both(1.0f / f.cap);
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const Pair t = mul2(make_pair(s[c], s[c + 1]), in);
-      slopes[c / 2] = fma2(mul2(t, both(-1.0f)), t, both(1.0f));
-    }
-    if (f.slope != 0.0f) f.lowered(s, apart);
-    if (whole) weights_of<E, true, false>(s, p, slopes, 1.0f, lo, hi, lse);
-    else weights_of<E, true, true>(s, p, slopes, 1.0f, lo, hi, lse);
-    return;
-  }
+                                        const Cut& cut, Lse lse) {
   const float mul = f.finish(s, apart);
-  if (whole) weights_of<E, false, false>(s, p, nullptr, mul, lo, hi, lse);
-  else weights_of<E, false, true>(s, p, nullptr, mul, lo, hi, lse);
+  cut.set(s, -INFINITY);
+  if (f.cap == 0.0f) weights_of<E, false, false>(s, p, f, mul, apart, lse);
+  else if (f.slope == 0.0f) weights_of<E, true, false>(s, p, f, mul, apart, lse);
+  else weights_of<E, true, true>(s, p, f, mul, apart, lse);
 }
 
 // 32 columns of ds: p (at s) times (grad_out . v - delta), `delta(c)` added to
-// columns c and c + 1; fp16 times `factor`.
-template <class T, bool kMask, class Delta>
-__device__ __forceinline__ void slopes_of(const float* s, const float* d, uint32_t* p, float factor, int lo,
-                                          int hi, Delta delta) {
+// columns c and c + 1; fp16 times `factor`.  What is not seen is set to 0.
+template <class T, class Delta>
+__device__ __forceinline__ void slopes_of(float (&s)[32], const float (&d)[32], uint32_t (&p)[16], float factor,
+                                          const Cut& cut, Delta delta) {
   const Pair factor_pair = both(factor);
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     Pair e = mul2(make_pair(s[c], s[c + 1]), add2(make_pair(d[c], d[c + 1]), delta(c)));
     if constexpr (T::code == FADAM_DT_F16) e = mul2(e, factor_pair);
-    float2 v = split(e);
-    if constexpr (kMask) {
-      v.x = c >= lo && c < hi ? v.x : 0.0f;
-      v.y = c + 1 >= lo && c + 1 < hi ? v.y : 0.0f;
-    }
-    p[c / 2] = pack2<typename T::type>(v.x, v.y);
+    const float2 v = split(e);
+    s[c] = v.x;
+    s[c + 1] = v.y;
   }
+  cut.set(s, 0.0f);
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) p[c / 2] = pack2<typename T::type>(s[c], s[c + 1]);
 }
 
 // ---- grad_k and grad_v: 128 keys, a walk over queries --------------------------------------
@@ -368,9 +381,8 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     for (int h = 0, i = 0; h < share && ok; ++h) {
       const Scores f(g, head0 + h);
       for (int turn = 0; turn < turns; ++turn, ++i, x.next(), y.next()) {
-        const int at = (first + turn) * kRows + part * 32;  // the first column's query
-        const bool whole = reach.whole((first + turn) * kRows);
-        const int lo = span.query_lo - at, hi = span.query_hi - at;
+        const int tile_at = (first + turn) * kRows, at = tile_at + part * 32;  // the first column's query
+        const Cut cut(reach, tile_at, at, span.query_lo, span.query_hi);
         float s[32];
         uint32_t p[16];
         Pair of[16];  // the columns' lse, then their delta: read before the tensor cores are waited for
@@ -382,7 +394,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         fence_after_sync();
         tmem_load32(at_s, s);
         tmem_wait<32>(s);
-        weights<E>(s, p, f, float(at - (key0 + row)), whole, lo, hi, [&](int c) { return of[c / 2]; });
+        weights<E>(s, p, f, float(at - (key0 + row)), cut, [&](int c) { return of[c / 2]; });
         tmem_store16(at_s, p);
         tmem_stored();
         fence_before_sync();
@@ -399,8 +411,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         tmem_load32(at_dots, d);
         tmem_wait<32>(d);
         const auto delta = [&](int c) { return of[c / 2]; };
-        if (whole) slopes_of<T, false>(s, d, p, factor, lo, hi, delta);
-        else slopes_of<T, true>(s, d, p, factor, lo, hi, delta);
+        slopes_of<T>(s, d, p, factor, cut, delta);
         tmem_store16(at_dots, p);
         tmem_stored();
         fence_before_sync();
@@ -578,9 +589,8 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     const Scores f(g, head);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int at = (first + i) * kRows + part * 32;  // the first column's key
-      const bool whole = reach.whole((first + i) * kRows);
-      const int lo = span.key_lo - at, hi = span.key_hi - at;
+      const int tile_at = (first + i) * kRows, at = tile_at + part * 32;  // the first column's key
+      const Cut cut(reach, tile_at, at, span.key_lo, span.key_hi);
       float s[32];
       uint32_t p[16];
       ok = bar_wait(bar_scores, unsigned(i) & 1, status);
@@ -591,7 +601,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       fence_before_sync();
       __syncwarp();
       if (lane == 0) bar_arrive(bar_scores_read);
-      weights<E>(s, p, f, float(at - (query0 + row)), whole, lo, hi, [&](int) { return lse; });
+      weights<E>(s, p, f, float(at - (query0 + row)), cut, [&](int) { return lse; });
 
       ok = bar_wait(bar_dots, unsigned(i) & 1, status);
       if (!ok) break;
@@ -603,8 +613,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar_dots_read);
       const auto less = [&](int) { return delta; };
-      if (whole) slopes_of<T, false>(s, d, p, factor, lo, hi, less);
-      else slopes_of<T, true>(s, d, p, factor, lo, hi, less);
+      slopes_of<T>(s, d, p, factor, cut, less);
       // (grad_out . v of i comes behind the product with ds of i - 2: its place is free)
       tmem_store16(lanes + kColumnsA + (i & 1) * 64 + part * 16, p);
       tmem_stored();
