@@ -4,7 +4,10 @@
 // rows.  The gradient is a sum over each token's rows: the rows are sorted by
 // token first (stable, so that every sum has one order), then the sorted list
 // is cut into equal pieces whose sums do not depend on how often a token
-// occurs, and what a piece's end cuts is joined.
+// occurs, and what pieces' ends cut is joined by the last piece that has a part
+// of it.  Rows of no token are zeroed by the sort, which knows them.  (By other
+// CTAs of the sums' launch it took longer, 37 us for 50021 x 1000 in place of 29:
+// the sums are a chain of loads, each of which then waits behind the zeros.)
 #include "fadam_seq.h"
 #include "ops_internal.h"
 #include "rows.cuh"
@@ -150,6 +153,8 @@ struct SortArgs {
   int32_t range;     // tokens of the vocabulary that a CTA takes
   int32_t* order;    // [rows] rows sorted by token, those of one token ascending
   int32_t* starts;   // [vocab + 1] where a token's rows begin in it
+  int32_t* arrived;  // [marks] set to zero
+  int32_t marks;
 };
 
 // Each CTA takes a range of the vocabulary and reads all tokens twice: first it
@@ -158,22 +163,21 @@ struct SortArgs {
 // then it places them.  Nothing is exchanged between CTAs, and the order is
 // stable: within a warp's 32 rows a row comes behind those of its token in
 // lower lanes.  Of T rows 152 x 16 T bytes come from L2: 3 us for 16384 rows,
-// while a sort by digits would take three launches or more.
-// Rows of no token are zeroed here, where the counts are (unless kKeep).
+// while a sort by digits would take three launches or more.  At the end
+// (unless kKeep) rows of no token are zeroed, by bulk copies where they allow it.
 template <class Out, bool kWide, bool kKeep>
 __global__ void __launch_bounds__(kSortThreads)
     sort_kernel(const SortArgs a, Out* out, int64_t out_ld, int width) {
   // kZeroBytes of zeros where rows are written, then counts [kSortWarps][range]
-  // and [range] of all warps
   extern __shared__ __align__(16) unsigned char sort_smem[];
   constexpr int kZeros = kKeep || !kWide ? 0 : kZeroBytes;
   int* counts = reinterpret_cast<int*>(sort_smem + kZeros);
   __shared__ int warp_sum[kSortWarps];
+  __shared__ bool unused[kKeep ? 1 : kRange];
   __shared__ int below;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t low = int64_t(blockIdx.x) * a.range;
   const int mine = int(min(int64_t(a.range), a.vocab - low));
-  int* total = counts + kSortWarps * a.range;
   for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) counts[i] = 0;
   if (kZeros) {
     for (int i = threadIdx.x; i < kZeros / 16; i += kSortThreads)
@@ -185,6 +189,8 @@ __global__ void __launch_bounds__(kSortThreads)
   chain_wait();
   chain_next();
 
+  for (int64_t i = int64_t(blockIdx.x) * kSortThreads + threadIdx.x; i < a.marks; i += int64_t(gridDim.x) * kSortThreads)
+    a.arrived[i] = 0;
   // rows of a warp: whole groups of 32
   const int per_warp = int((int64_t(a.rows) + kSortThreads - 1) / kSortThreads) * 32;
   const int first = warp * per_warp;
@@ -197,14 +203,18 @@ __global__ void __launch_bounds__(kSortThreads)
     if (t < 0 || t >= a.vocab || (a.padded && t == a.padding)) return -2;
     return t < low ? -1 : t < low + mine ? int(t - low) : -2;
   };
+  constexpr int kAhead = 8;  // loads in flight
   int fewer = 0;
-#pragma unroll 4
-  for (int row = first + lane; row - lane < last; row += 32) {
-    const int v = place(row);
-    fewer += v == -1;
-    if (__any_sync(~0u, v >= 0)) {
-      const unsigned peers = __match_any_sync(~0u, v);
-      if (v >= 0 && lane == __ffs(peers) - 1) own[v] += __popc(peers);
+  for (int row = first; row < last; row += 32 * kAhead) {
+    int at[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) at[k] = place(row + 32 * k + lane);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      fewer += at[k] == -1;
+      if (!__any_sync(~0u, at[k] >= 0)) continue;
+      const unsigned peers = __match_any_sync(~0u, at[k]);
+      if (at[k] >= 0 && lane == __ffs(peers) - 1) own[at[k]] += __popc(peers);
       __syncwarp();
     }
   }
@@ -212,15 +222,12 @@ __global__ void __launch_bounds__(kSortThreads)
   if (lane == 0 && fewer) atomicAdd(&below, fewer);
   __syncthreads();
 
-  // a thread to a token: the warps' shares one after the other, then the tokens
-  const int v = threadIdx.x;
+  // a thread to a token: where its rows begin, then each warp's share of them
+  const int v = threadIdx.x, used = per_warp ? (a.rows + per_warp - 1) / per_warp : 0;
   int count = 0;
   if (v < mine)
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int n = counts[w * a.range + v];
-      counts[w * a.range + v] = count;
-      count += n;
-    }
+#pragma unroll 8
+    for (int w = 0; w < used; ++w) count += counts[w * a.range + v];
   int sum = count;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -233,27 +240,42 @@ __global__ void __launch_bounds__(kSortThreads)
   for (int w = 0; w < warp; ++w) base += warp_sum[w];
   const int start = base + sum - count;
   if (v < mine) {
-    for (int w = 0; w < kSortWarps; ++w) counts[w * a.range + v] += start;
-    total[v] = count;
+    int next = start;
+    for (int w0 = 0; w0 < used; w0 += 8) {
+      int n[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) n[w] = w0 + w < used ? counts[(w0 + w) * a.range + v] : 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        if (w0 + w < used) {
+          counts[(w0 + w) * a.range + v] = next;
+          next += n[w];
+        }
+    }
+    if (!kKeep) unused[v] = count == 0;
     a.starts[low + v] = start;
     if (low + v == a.vocab - 1) a.starts[a.vocab] = start + count;
   }
   __syncthreads();
 
-#pragma unroll 4
-  for (int row = first + lane; row - lane < last; row += 32) {
-    const int at = place(row);
-    if (!__any_sync(~0u, at >= 0)) continue;
-    const unsigned peers = __match_any_sync(~0u, at);
-    if (at >= 0) a.order[own[at] + __popc(peers & ((1u << lane) - 1))] = row;
-    __syncwarp();
-    if (at >= 0 && lane == __ffs(peers) - 1) own[at] += __popc(peers);
-    __syncwarp();
+  for (int row = first; row < last; row += 32 * kAhead) {
+    int at[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) at[k] = place(row + 32 * k + lane);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (!__any_sync(~0u, at[k] >= 0)) continue;
+      const unsigned peers = __match_any_sync(~0u, at[k]);
+      if (at[k] >= 0) a.order[own[at[k]] + __popc(peers & ((1u << lane) - 1))] = row + 32 * k + lane;
+      __syncwarp();
+      if (at[k] >= 0 && lane == __ffs(peers) - 1) own[at[k]] += __popc(peers);
+      __syncwarp();
+    }
   }
 
   if constexpr (!kKeep) {
     for (int r = warp; r < mine; r += kSortWarps) {
-      if (total[r]) continue;
+      if (!unused[r]) continue;
       Out* row = out + (low + r) * out_ld;
       if constexpr (kWide) {
         // bulk copies of zeros, by a lane of its own each
@@ -281,6 +303,8 @@ struct SumArgs {
   int32_t width, parts, piece;   // piece: sorted rows of a CTA
   int64_t grad_ld, out_ld, carry_ld;
   float* carry;    // [pieces][2][carry_ld]: sums that a piece's begin and end cut
+  int32_t* arrived;  // [pieces][parts]: of a token whose rows begin in the piece and end in another, the
+                     // pieces that have left their part
   float scale;
 };
 
@@ -301,8 +325,44 @@ __device__ __forceinline__ void put(const Eight<kWide>& at, Out* row, const floa
   at.store(row, narrow<Out>(v));
 }
 
-// A piece's rows, several loads in flight; a token's sum is written when its last
-// row is in the piece and its first one too, else kept for join_kernel.
+// The sum of the token `id`, whose rows are cut by pieces: the last of them to
+// leave its part (in `carry`) adds all parts, in order.
+template <class Out, bool kWide, bool kKeep>
+__device__ __forceinline__ void join_parts(const SumArgs& a, const Eight<kWide>& at, int64_t id, unsigned part,
+                                           int carry_col, Out* out) {
+  __shared__ int before;
+  const int begin = a.starts[id], end = a.starts[id + 1];
+  const int first = begin / a.piece, last = (end - 1) / a.piece;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) before = atomicAdd(&a.arrived[int64_t(first) * a.parts + part], 1);
+  __syncthreads();
+  const bool mine = before == last - first;
+  __syncthreads();  // (a CTA may come here twice)
+  if (!mine || !at.any()) return;
+  __threadfence();
+  const float* carry = a.carry + carry_col;
+  // a token that begins where its piece does has left its part as one that was cut there
+  float sum[8] = {};
+  constexpr int kAhead = 4;  // loads in flight
+  for (int p = first; p <= last; p += kAhead) {
+    Raw<float> raw[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      raw[k] = p + k > last ? zero_raw<float>()
+                            : load_eight(carry + (int64_t(p + k) * 2 + (p + k == first && begin % a.piece)) * a.carry_ld);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] += __uint_as_float(raw[k].w[c]);
+  }
+  put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
+}
+
+// A piece's rows, several loads in flight; a token's sum is written when its
+// first and its last row are in the piece, else its part is left for
+// join_parts: in the piece's first place when the token's rows begin before
+// the piece or with it, else in the second.
 template <class E, class Out, bool kWide, bool kKeep>
 __global__ void __launch_bounds__(kThreads, kWide ? 4 : 2)
     sum_kernel(const SumArgs a, const E* grad, Out* out) {
@@ -310,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, kWide ? 4 : 2)
   __shared__ int ids[kLongest];
   chain_wait();
   chain_next();
-  const unsigned piece = blockIdx.x / unsigned(a.parts);
-  const Eight<kWide> at(int(blockIdx.x - piece * a.parts), a.width);
+  const unsigned piece = blockIdx.x / unsigned(a.parts), part = blockIdx.x - piece * a.parts;
+  const Eight<kWide> at(int(part), a.width);
   const int n = a.starts[a.vocab];  // rows that count
   const int begin = int(piece) * a.piece;
   const int many = min(a.piece, n - begin);
@@ -321,89 +381,51 @@ __global__ void __launch_bounds__(kThreads, kWide ? 4 : 2)
     ids[i] = int(a.tokens[rows[i]]);
   }
   __syncthreads();
-  if (!at.any()) return;
-  const bool cut_begin = a.starts[ids[0]] < begin;
-  const bool cut_end = a.starts[ids[many - 1] + 1] > begin + many;
-  const Eight<true> wide(int(blockIdx.x - piece * a.parts), a.width);
-  const int carry_col = kWide ? at.col : wide.col;  // a thread's eight sums lie together
+  const int head = ids[0], tail = ids[many - 1];
+  const bool cut_begin = a.starts[head] < begin, cut_end = a.starts[tail + 1] > begin + many;
+  const int carry_col = Eight<true>(int(part), a.width).col;  // a thread's eight sums lie together
   float* carry = a.carry + int64_t(piece) * 2 * a.carry_ld + carry_col;
+  const auto keep = [&](int place, const float(&sum)[8]) {
+    Raw<float> raw;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) raw.w[c] = __float_as_uint(sum[c]);
+    store_eight(carry + place * a.carry_ld, raw);
+  };
 
-  float sum[8] = {};
-  int id = ids[0];
-  bool cut = cut_begin;
-  constexpr int kAhead = kWide ? 4 : 2;
-  for (int i = 0; i < many; i += kAhead) {
-    Raw<E> raw[kAhead];
+  if (at.any()) {
+    float sum[8] = {};
+    int id = head;
+    constexpr int kAhead = kWide ? 4 : 2;
+    for (int i = 0; i < many; i += kAhead) {
+      Raw<E> raw[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (i + k < many) at.load(grad + rows[i + k] * a.grad_ld, raw[k]);
+      for (int k = 0; k < kAhead; ++k)
+        if (i + k < many) at.load(grad + rows[i + k] * a.grad_ld, raw[k]);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (i + k >= many) break;
-      if (ids[i + k] != id) {
-        if (cut) {
+      for (int k = 0; k < kAhead; ++k) {
+        if (i + k >= many) break;
+        if (ids[i + k] != id) {
+          if (cut_begin && id == head) keep(0, sum);
+          else put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
+          id = ids[i + k];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) carry[c] = sum[c];
-        } else {
-          put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
+          for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
         }
-        cut = false;
-        id = ids[i + k];
+        Pair v[4];
+        widen(raw[k], v);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) sum[c] = 0.0f;
-      }
-      Pair v[4];
-      widen(raw[k], v);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 p = split(v[c]);
-        sum[2 * c] += p.x;
-        sum[2 * c + 1] += p.y;
+        for (int c = 0; c < 4; ++c) {
+          const float2 p = split(v[c]);
+          sum[2 * c] += p.x;
+          sum[2 * c + 1] += p.y;
+        }
       }
     }
+    if (cut_end || (cut_begin && tail == head)) keep(tail == head ? 0 : 1, sum);
+    else put<Out, kWide, kKeep>(at, out + tail * a.out_ld, sum, a.scale);
   }
-  if (cut || cut_end) {
-    // the whole piece is one token's middle or end (first place), or its begin (second)
-    float* to = carry + (cut ? 0 : a.carry_ld);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) to[c] = sum[c];
-  } else {
-    put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
-  }
-}
-
-// The pieces' shares of a token that pieces cut, in order: by the piece in
-// which its rows begin.
-template <class Out, bool kWide, bool kKeep>
-__global__ void __launch_bounds__(kThreads) join_kernel(const SumArgs a, Out* out) {
-  chain_wait();
-  chain_next();
-  const unsigned piece = blockIdx.x / unsigned(a.parts);
-  const int part = int(blockIdx.x - piece * a.parts);
-  const Eight<kWide> at(part, a.width);
-  const int n = a.starts[a.vocab];
-  const int begin = int(piece) * a.piece, end = begin + a.piece;
-  if (end >= n || !at.any()) return;
-  const int64_t id = a.tokens[a.order[end - 1]];
-  const int first = a.starts[id], last = a.starts[id + 1];
-  if (first < begin || last <= end) return;
-  const float* carry = a.carry + Eight<true>(part, a.width).col;
-  float sum[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) sum[c] = carry[(int64_t(piece) * 2 + 1) * a.carry_ld + c];
-  const int until = (last + a.piece - 1) / a.piece;
-  constexpr int kAhead = 8;  // loads in flight
-  for (int p = int(piece) + 1; p < until; p += kAhead) {
-    Raw<float> raw[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      raw[k] = p + k < until ? load_eight(carry + int64_t(p + k) * 2 * a.carry_ld) : zero_raw<float>();
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] += __uint_as_float(raw[k].w[c]);
-  }
-  put<Out, kWide, kKeep>(at, out + id * a.out_ld, sum, a.scale);
+  if (cut_begin || (cut_end && tail == head)) join_parts<Out, kWide, kKeep>(a, at, head, part, carry_col, out);
+  if (cut_end && tail != head) join_parts<Out, kWide, kKeep>(a, at, tail, part, carry_col, out);
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -427,6 +449,7 @@ struct Layout {
   int32_t* order;
   int32_t* starts;
   float* carry;
+  int32_t* arrived;
   int32_t piece;
   int64_t pieces, carry_ld;
   size_t bytes;
@@ -444,6 +467,7 @@ Layout layout(const fadam_embed_grad& d, char* base) {
   l.order = static_cast<int32_t*>(c.take(4 * d.rows));
   l.starts = static_cast<int32_t*>(c.take(4 * (d.vocab + 1)));
   l.carry = static_cast<float*>(c.take(4 * 2 * l.pieces * l.carry_ld));
+  l.arrived = static_cast<int32_t*>(c.take(4 * l.pieces * p.count));
   l.bytes = c.used;
   return l;
 }
@@ -462,16 +486,19 @@ fadam_status gradient(const fadam_embed_grad& d, const Layout& l, const DeviceFa
   s.range = int32_t(even < kRange ? even : kRange);
   s.order = l.order;
   s.starts = l.starts;
+  const Parts p = parts_of(d.width);
+  s.arrived = l.arrived;
+  s.marks = int32_t(l.pieces * p.count);
   auto* sort = sort_kernel<Out, kWide, kKeep>;
   constexpr int kZeros = kKeep || !kWide ? 0 : kZeroBytes;
-  constexpr int kMostShared = kZeros + (kSortWarps + 1) * kRange * 4;
-  const cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+  const cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kZeros + kSortWarps * kRange * 4);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  fadam_status st = launch_chained("token sort launch", sort, ceil_div(d.vocab, s.range), kSortThreads,
-                                   kZeros + size_t(kSortWarps + 1) * s.range * 4, stream, s, out, d.out_stride,
-                                   int(d.width));
+  const fadam_status st =
+      launch_chained("token sort launch", sort, ceil_div(d.vocab, s.range), kSortThreads,
+                     kZeros + size_t(kSortWarps) * s.range * 4, stream, s, static_cast<Out*>(d.out), d.out_stride,
+                     int(d.width));
   if (st) return st;
-  const Parts p = parts_of(d.width);
   SumArgs a{};
   a.tokens = d.tokens;
   a.order = l.order;
@@ -484,12 +511,10 @@ fadam_status gradient(const fadam_embed_grad& d, const Layout& l, const DeviceFa
   a.out_ld = d.out_stride;
   a.carry_ld = l.carry_ld;
   a.carry = l.carry;
+  a.arrived = l.arrived;
   a.scale = d.scale;
-  st = launch_chained("embedding sums launch", sum_kernel<E, Out, kWide, kKeep>, l.pieces * p.count,
-                      p.threads, 0, stream, a, static_cast<const E*>(d.grad), out);
-  if (st || l.pieces == 1) return st;
-  return launch_chained("embedding join launch", join_kernel<Out, kWide, kKeep>, l.pieces * p.count,
-                        p.threads, 0, stream, a, out);
+  return launch_chained("embedding sums launch", sum_kernel<E, Out, kWide, kKeep>, l.pieces * p.count, p.threads, 0,
+                        stream, a, static_cast<const E*>(d.grad), out);
 }
 
 template <class E, class Out>
