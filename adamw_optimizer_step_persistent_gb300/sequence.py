@@ -49,19 +49,21 @@ def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0,
     it the shard's screen or norm."""
     if weight.dim() != 2:
         raise ValueError(f"weight must be [vocab, width], got {tuple(weight.shape)}")
-    dtype = weight.dtype if dtype is None else dtype
-    if dtype not in (weight.dtype, torch.float32):
-        raise TypeError(f"dtype must be {weight.dtype} or fp32, got {dtype}")
-    code = dtype_code(weight.dtype)
+    kind = weight.dtype
+    code = out_code = dtype_code(kind)
+    if dtype is not None and dtype is not kind:
+        if dtype is not torch.float32:
+            raise TypeError(f"dtype must be {kind} or fp32, got {dtype}")
+        kind, out_code = dtype, _abi.DT_F32
     tokens = _tokens(tokens)
     index = _device(tokens, "tokens")
     _check_device(index, "tokens", weight)
     vocab, width, stride = _rows(weight, "weight")
     with _current(index):
-        out = torch.empty((*tokens.shape, width), dtype=dtype, device=tokens.device)
+        out = tokens.new_empty((*tokens.shape, width), dtype=kind)
         desc = _abi.Embed(tokens.data_ptr(), weight.data_ptr(), out.data_ptr(), tokens.numel(),
                           width, vocab, stride, width, int(padding_index or 0), float(scale), code,
-                          dtype_code(dtype), 0 if padding_index is None else _abi.EMBED_PADDING)
+                          out_code, 0 if padding_index is None else _abi.EMBED_PADDING)
         status = _abi.lib().fadam_embed_forward(desc, _stream(index))
     if status:
         _abi.check_ops(status, "fadam_embed_forward")
@@ -196,8 +198,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool
     """
     index, desc = _attention(q, k, v, causal, scale, softcap, slopes, documents, prefix)
     with _current(index):
-        out = _like(q)
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        shape = q.shape
+        out = q.new_empty(shape)
+        lse = q.new_empty(shape[:-1], dtype=torch.float32)
         desc.out, desc.lse = out.data_ptr(), lse.data_ptr()
         lib = _abi.lib()
         ws, at, size = _workspace(lib.fadam_attention_workspace, desc, "fadam_attention_workspace", q)
@@ -228,7 +231,7 @@ def attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     strides = *_heads(out, shape, "out"), *_heads(grad_out, shape, "grad_out")
     _check_device(index, "q", grad_out, out, lse)
     with _current(index):
-        grads = AttentionGrads(_like(q), _like(k), _like(v))
+        grads = AttentionGrads(*(t.new_empty(t.shape) for t in (q, k, v)))
         desc.out, desc.lse = out.data_ptr(), lse.data_ptr()
         desc = _abi.AttentionGrad(desc, grad_out.data_ptr(), *(t.data_ptr() for t in grads), *strides)
         lib = _abi.lib()
