@@ -230,6 +230,8 @@ fadam_status check(const fadam_attention* d) {
   if (d->tokens > int64_t(1) << 24 || d->heads > 1 << 14 || d->width > FADAM_ATTENTION_MAX_WIDTH)
     return fail(FADAM_ELIMIT, "%lld tokens (2^24), %d heads (2^14), width %d (%d)", (long long)d->tokens,
                 d->heads, d->width, FADAM_ATTENTION_MAX_WIDTH);
+  if (ceil_div(d->tokens, kRows) * d->heads > int64_t(1) << 30)
+    return fail(FADAM_ELIMIT, "%lld tokens of %d heads", (long long)d->tokens, d->heads);
   if (!d->documents && (d->sequence < 1 || d->tokens % d->sequence))
     return fail(FADAM_EINVAL, "%lld tokens are not whole sequences of %lld", (long long)d->tokens,
                 (long long)d->sequence);

@@ -105,7 +105,8 @@ fadam_status fadam_embed_grad_run(const fadam_embed_grad* desc, void* workspace,
  *   prefix [n_documents]            int32 (one for each sequence where
  *                                   documents is NULL), or NULL: none
  * q, k, v (and grad_out) start on 16 bytes, and their token and head strides
- * are multiples of 8 elements.  tokens up to 2^24.
+ * are multiples of 8 elements.  tokens up to 2^24, heads up to 2^14, and tokens
+ * / 128 times heads up to 2^30.
  * Scores and sums are fp32; exp(s - m), for a running m, is rounded to dtype
  * for the product with v.  Documents that share 128 consecutive tokens (from a
  * multiple of 128) share tensor-core operands: an infinity or a NaN in a k or

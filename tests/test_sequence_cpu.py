@@ -121,7 +121,7 @@ BAD_ATTENTION = [
     ({"tokens": -1}, _abi.EINVAL), ({"heads": 0}, _abi.EINVAL), ({"kv_heads": 0}, _abi.EINVAL),
     ({"kv_heads": 3}, _abi.EINVAL), ({"kv_heads": -2}, _abi.EINVAL), ({"width": 0}, _abi.EINVAL),
     ({"width": 60}, _abi.EINVAL), ({"width": 136}, _abi.ELIMIT), ({"tokens": 2**25}, _abi.ELIMIT),
-    ({"heads": 2**15}, _abi.ELIMIT), ({"sequence": 0}, _abi.EINVAL), ({"sequence": 48}, _abi.EINVAL),
+    ({"heads": 2**15}, _abi.ELIMIT), ({"tokens": 2**24, "heads": 2**14, "sequence": 1}, _abi.ELIMIT), ({"sequence": 0}, _abi.EINVAL), ({"sequence": 48}, _abi.EINVAL),
     ({"documents": FAKE, "n_documents": -1}, _abi.EINVAL), ({"scale": 0.0}, _abi.EINVAL),
     ({"scale": -1.0}, _abi.EINVAL), ({"scale": NAN}, _abi.EINVAL), ({"scale": INF}, _abi.EINVAL),
     ({"softcap": -1.0}, _abi.EINVAL), ({"softcap": NAN}, _abi.EINVAL), ({"softcap": INF}, _abi.EINVAL),
