@@ -239,8 +239,12 @@ fadam_status check(const fadam_attention* d) {
     return fail(FADAM_EINVAL, "%lld documents", (long long)d->n_documents);
   if (!(d->scale > 0.0f) || !finite(d->scale)) return fail(FADAM_EINVAL, "scale is not finite and above 0");
   if (!(d->softcap >= 0.0f) || !finite(d->softcap)) return fail(FADAM_EINVAL, "softcap is not finite and at least 0");
-  if (d->softcap > 0.0f && !finite(d->scale / d->softcap))
-    return fail(FADAM_EINVAL, "scale %g over softcap %g is not finite", d->scale, d->softcap);
+  if (d->softcap > 0.0f) {
+    // (the square of the cap, and the last factor of tanh's series, in fp32)
+    const double y = double(d->scale) / d->softcap;
+    if (d->softcap < 1e-15f || d->softcap > 1e15f || d->softcap * y * y * y * y * y * y * y > 1e37)
+      return fail(FADAM_EINVAL, "softcap %g with scale %g", d->softcap, d->scale);
+  }
   fadam_status st;
   if ((st = check_rows("q", d->q, d->q_stride, d->q_head_stride, *d, d->heads)) ||
       (st = check_rows("k", d->k, d->k_stride, d->k_head_stride, *d, d->kv_heads)) ||
@@ -331,6 +335,13 @@ AttentionArgs arguments(const fadam_attention& d, const Layout& l, const DeviceF
   g.pair_heads = g.group % 2 == 0;
   g.scale = d.scale;
   g.softcap = d.softcap;
+  if (d.softcap > 0.0f) {
+    // cap tanh(y), y = x scale / cap: tanh's Taylor series
+    const double y = double(d.scale) / d.softcap;
+    double c = double(d.softcap) * y * 1.4426950408889634;
+    const double taylor[4] = {1.0, -1.0 / 3.0, 2.0 / 15.0, -17.0 / 315.0};
+    for (int i = 0; i < 4; ++i, c *= y * y) g.series[i].x = g.series[i].y = float(c * taylor[i]);
+  }
   g.slopes = d.slopes;
   g.spans = l.spans;
   g.order = l.order;

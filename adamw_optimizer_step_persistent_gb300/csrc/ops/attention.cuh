@@ -321,18 +321,18 @@ struct Scores {
   float cap;         // cap log2 e; 0: none
   float inverse;     // 1 / cap: scores to multiples of the cap
   float slope;       // slope log2 e; 0: none
-  __device__ __forceinline__ Scores(const AttentionArgs& g, int head) {
+  const float2 (&series)[4];
+  __device__ __forceinline__ Scores(const AttentionArgs& g, int head) : series(g.series) {
     mul = g.scale * kLog2e;
     cap = g.softcap * kLog2e;
     inverse = g.softcap > 0.0f ? g.scale / g.softcap : 0.0f;
     slope = g.slopes ? __ldg(g.slopes + head) * kLog2e : 0.0f;
   }
   // Products become capped scores, cap tanh(s / cap).  Where no score of a
-  // warp's is beyond 0.35 caps, by tanh's Taylor series (off by 9e-8 there):
-  // eight multiplications for two scores.  Else tanh(y) is 1 - 2 / (exp(2 y) +
-  // 1), whose exponential and reciprocal take three times the time of the
-  // softmax's own exponential (packed documents of 4096 tokens: 78 us with it,
-  // 64 with the series).
+  // warp's is beyond a quarter of the cap, by tanh's Taylor series to the seventh
+  // power (off by 9e-8 of the cap there): five multiplications for two scores.
+  // Else tanh(y) is 1 - 2 / (exp(2 y) + 1), whose exponential and reciprocal take
+  // three times the time of the softmax's own exponential.
   template <int N>
   __device__ __forceinline__ void capped(float (&s)[N]) const {
     float far[2] = {0.0f, 0.0f};
@@ -341,7 +341,7 @@ struct Scores {
 #pragma unroll
       for (int k = 0; k < 2; ++k) far[k] = fmaxf(fmaxf(far[k], fabsf(s[c + k])), fabsf(s[c + 2 + k]));
     // (a NaN is far from anything, and keeps the others' way)
-    if (__any_sync(~0u, fmaxf(far[0], far[1]) * inverse > 0.35f)) {
+    if (__any_sync(~0u, fmaxf(far[0], far[1]) * inverse > 0.25f)) {
 #pragma unroll
       for (int c = 0; c < N; ++c) {
         const float e = exp2_fast(s[c] * (2.0f * kLog2e * inverse));
@@ -349,15 +349,13 @@ struct Scores {
       }
       return;
     }
-    const Pair in = both(inverse), by = both(mul);
+    Pair of[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) of[i] = make_pair(series[i].x, series[i].y);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const Pair x = make_pair(s[c], s[c + 1]), y = mul2(x, in), u = mul2(y, y);
-      Pair p = fma2(u, both(62.0f / 2835.0f), both(-17.0f / 315.0f));
-      p = fma2(u, p, both(2.0f / 15.0f));
-      p = fma2(u, p, both(-1.0f / 3.0f));
-      p = fma2(u, p, both(1.0f));
-      const float2 v = split(mul2(mul2(x, by), p));
+      const Pair x = make_pair(s[c], s[c + 1]), u = mul2(x, x);
+      const float2 v = split(mul2(x, fma2(u, fma2(u, fma2(u, of[3], of[2]), of[1]), of[0])));
       s[c] = v.x;
       s[c + 1] = v.y;
     }

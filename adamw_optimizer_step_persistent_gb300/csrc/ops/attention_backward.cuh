@@ -188,7 +188,7 @@ struct Cut {
 template <class E, bool kCap, bool kBias, class Lse>
 __device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], const Scores& f, float mul,
                                            float apart, Lse lse) {
-  const Pair mul_pair = both(mul), in = both(kCap ? 1.0f / f.cap : 0.0f);
+  const Pair mul_pair = both(mul), less = both(kCap ? -1.0f / (f.cap * f.cap) : 0.0f);
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     const Pair z = make_pair(s[c], s[c + 1]);
@@ -201,8 +201,7 @@ __device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], co
       if constexpr (kBias)
         capped = make_pair(fmaf(f.slope, fabsf(apart + float(c)), s[c]),
                            fmaf(f.slope, fabsf(apart + float(c + 1)), s[c + 1]));
-      const Pair t = mul2(capped, in);
-      w = mul2(w, fma2(mul2(t, both(-1.0f)), t, both(1.0f)));
+      w = mul2(w, fma2(mul2(capped, capped), less, both(1.0f)));
       v = split(w);
     }
     s[c] = v.x;

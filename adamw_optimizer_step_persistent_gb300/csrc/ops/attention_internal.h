@@ -20,6 +20,7 @@ struct AttentionArgs {
   int causal;
   int pair_heads;                              // forward: a CTA's two tiles are the same rows of two heads
   float scale, softcap;
+  float2 series[4];          // capped scores in units of log 2 near zero: of x, x^3, x^5, x^7, twice each
   const float* slopes;
   const Spans* spans;        // [tokens] where there are documents
   const int* order;          // of tiles of queries (forward: of what a CTA takes), or NULL: last ones first

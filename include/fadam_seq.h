@@ -127,7 +127,7 @@ typedef struct {
   int64_t q_head_stride, k_head_stride, v_head_stride; /* head to head */
   int32_t heads, kv_heads, width;
   float scale;   /* finite, > 0 */
-  float softcap; /* finite, >= 0; 0: none */
+  float softcap; /* 0: none; else 1e-15 to 1e15, and scale^7 / softcap^6 at most 1e37 */
   int32_t dtype;
   uint32_t flags;
   uint32_t reserved; /* set to 0 */

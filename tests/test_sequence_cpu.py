@@ -125,7 +125,7 @@ BAD_ATTENTION = [
     ({"documents": FAKE, "n_documents": -1}, _abi.EINVAL), ({"scale": 0.0}, _abi.EINVAL),
     ({"scale": -1.0}, _abi.EINVAL), ({"scale": NAN}, _abi.EINVAL), ({"scale": INF}, _abi.EINVAL),
     ({"softcap": -1.0}, _abi.EINVAL), ({"softcap": NAN}, _abi.EINVAL), ({"softcap": INF}, _abi.EINVAL),
-    ({"softcap": 1e-45}, _abi.EINVAL), ({"q": None}, _abi.EINVAL), ({"k": None}, _abi.EINVAL),
+    ({"softcap": 1e-45}, _abi.EINVAL), ({"softcap": 1e16}, _abi.EINVAL), ({"softcap": 1e-9}, _abi.EINVAL), ({"q": None}, _abi.EINVAL), ({"k": None}, _abi.EINVAL),
     ({"v": None}, _abi.EINVAL), ({"out": None}, _abi.EINVAL), ({"lse": None}, _abi.EINVAL),
     ({"q": FAKE + 8}, _abi.EALIGN), ({"k": FAKE + 2}, _abi.EALIGN), ({"v": FAKE + 4}, _abi.EALIGN),
     ({"out": FAKE + 8}, _abi.EALIGN), ({"lse": FAKE + 2}, _abi.EALIGN), ({"slopes": FAKE + 2}, _abi.EALIGN),
