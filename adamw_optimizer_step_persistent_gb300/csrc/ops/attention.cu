@@ -55,9 +55,11 @@ __device__ __forceinline__ Spans find_spans(const PlanArgs& p, const int32_t* of
 
 // One block to an order: the tiles sorted by how many tiles of the other side
 // their first and last rows reach, longest first, so that no long one is left
-// for the end.  (Equal ones in any order: it decides nothing but who is first.)
+// for the end.  (Equal ones in any order: it decides nothing but who is first.
+// 256 classes of length: with 1024 the scan below made a call of 4096 packed
+// tokens 63.0 us in place of 61.8.)
 __device__ __forceinline__ void sort_tiles(const PlanArgs& p, const PlanArgs::Order& o, const int32_t* offsets) {
-  constexpr int kBuckets = 1024;
+  constexpr int kBuckets = 256;
   __shared__ int count[kBuckets];
   int lo = 0, hi = p.tokens;
   if (p.documents) {
