@@ -332,7 +332,10 @@ struct Scores {
   // warp's is beyond a quarter of the cap, by tanh's Taylor series to the seventh
   // power (off by 9e-8 of the cap there): five multiplications for two scores.
   // Else tanh(y) is 1 - 2 / (exp(2 y) + 1), whose exponential and reciprocal take
-  // three times the time of the softmax's own exponential.
+  // three times the time of the softmax's own exponential.  (4096 packed tokens,
+  // 32 heads of 128: with the exponentials alone forward 78 us and backward 254,
+  // with five terms up to 0.35 caps 74 and 244; in the kernels as they are five
+  // terms take 68 and 169, these four 63 and 158.)
   template <int N>
   __device__ __forceinline__ void capped(float (&s)[N]) const {
     float far[2] = {0.0f, 0.0f};

@@ -3,9 +3,9 @@
 They stand next to the training operators (``training.py``) and follow the same
 rules: the token embedding with its weight's gradient, and attention over packed
 documents, forward and backward.  Matrices are tensors whose leading dimensions
-are taken together and must be evenly strided; nothing is copied, nothing
-synchronises, calls can be captured in a CUDA graph, and the functions stand
-outside autograd.
+are taken together and must be evenly strided; no matrix is copied, nothing
+synchronises, calls can be captured in a CUDA graph (the tensors they are given
+have to live as long as it does), and the functions stand outside autograd.
 """
 from __future__ import annotations
 
@@ -185,7 +185,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool
     ``q`` [..., tokens, heads, width], ``k`` and ``v`` [..., tokens, kv_heads,
     width] are bf16 or fp16, ``kv_heads`` divides ``heads`` (query heads next to
     each other share one), the width is a multiple of 8 up to 128; views of one
-    projection's output are taken as they are.  Each run of ``tokens`` is one
+    projection's output are taken as they are, where they start on 16 bytes and
+    their strides are multiples of 8.  Each run of ``tokens`` is one
     document, or (``documents``, int32 [n + 1] on the device) all tokens
     together are cut into documents at these offsets, and tokens outside them
     see nothing: their rows are 0 and their lse -infinity.

@@ -147,7 +147,9 @@ fadam_status fadam_attention_run(const fadam_attention* desc, void* workspace, s
  * grad_k and grad_v are summed over the query heads that share a head, in fp32
  * and in a fixed order.  p = exp(s - lse) and its product with (grad_out . v -
  * grad_out . out) are rounded to dtype for the products; in fp16 after
- * multiplication by powers of two that keep them within its range. */
+ * multiplication by powers of two, p by 2^10 and the product by one that brings
+ * grad_out's largest element to [1, 2): elements of v below 128 in magnitude keep
+ * it finite.  Nothing is summed by atomics: results are deterministic. */
 typedef struct {
   fadam_attention forward;
   const void* grad_out;

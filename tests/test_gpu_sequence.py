@@ -364,6 +364,67 @@ def test_attention_bad_documents_stay_in_bounds():
     torch.cuda.synchronize()
 
 
+def test_attention_over_thousands_of_documents():
+    """More documents than a block keeps the offsets of; each a few tokens long."""
+    T, H, D = 11_000, 2, 16
+    g = _gen(7)
+    lengths = torch.randint(0, 4, (7000,), generator=torch.Generator().manual_seed(1)).tolist()
+    offsets = [0]
+    for n in lengths:
+        if offsets[-1] + n <= T - 17:
+            offsets.append(offsets[-1] + n)
+    assert len(offsets) > 4096
+    q, k, v, go = (_rand(g, T, H, D).to(BF16) for _ in range(4))
+    docs = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    prefix = torch.ones(len(offsets) - 1, dtype=torch.int32, device="cuda")
+    r = fadam.attention(q, k, v, documents=docs, prefix=prefix)
+    d = fadam.attention_backward(go, q, k, v, r.out, r.lse, documents=docs, prefix=prefix)
+    for first in (0, 3000, len(offsets) - 200):      # a stretch of documents, as tokens of their own
+        part = offsets[first:first + 190]
+        rows = slice(part[0], part[-1])
+        c = ref.Case(*(t[rows] for t in (q, k, v)), D ** -0.5, offsets=[o - part[0] for o in part])
+        out, lse, _ = ref.attention(c)
+        out.holds(r.out[rows], "out")
+        lse.holds(r.lse[rows], "lse")
+        want = ref.attention_grad(c, go[rows], r.out[rows], r.lse[rows])
+        for name in "qkv":
+            want[name].holds(getattr(d, name)[rows], "grad_" + name)
+    assert (r.out[offsets[-1]:] == 0).all() and all((t[offsets[-1]:] == 0).all() for t in d)
+
+
+def test_two_threads_two_streams():
+    """Two shapes from two host threads at once: the same bits as alone."""
+    import threading
+    cases = [_case(900, 4, 2, 128, BF16, seed=1, offsets=[0, 300, 870]), _case(650, 6, 3, 64, F16, seed=2, bias=True)]
+    work = []
+    for c in cases:
+        shaped = [_shaped(c, t) for t in (c.q, c.k, c.v)]
+        kw = _options(c)
+        r = fadam.attention(*shaped, **kw)
+        work.append((shaped, kw, r, fadam.attention_backward(r.out, *shaped, r.out, r.lse, **kw)))
+    torch.cuda.synchronize()
+    errors = []
+
+    def body(shaped, kw, r, d):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(200):
+                    s = fadam.attention(*shaped, **kw)
+                    e = fadam.attention_backward(s.out, *shaped, s.out, s.lse, **kw)
+                stream.synchronize()
+            for a, b in zip((*r, *d), (*s, *e)):
+                assert torch.equal(a, b)
+        except BaseException as e:      # reported by the test's own thread
+            errors.append(e)
+    threads = [threading.Thread(target=body, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
+
+
 def test_attention_against_differences():
     """The gradients against differences of the 64-bit form's loss along one
     direction: the two formulas, not the roundings (a few percent of bf16's)."""
