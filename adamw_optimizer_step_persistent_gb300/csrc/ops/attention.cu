@@ -18,13 +18,8 @@ struct PlanArgs {
   bool causal;
   Spans* spans;        // [tokens], written where there are documents
   int span_blocks;
-  // orders of tiles of `rows`, most work first: by the keys of their queries, or
-  // by the queries of their keys
-  struct Order {
-    int* to;
-    int rows, tiles;
-    bool keys;
-  } orders[2];
+  int* order;          // of `tiles` of `rows` queries, or NULL: not asked for
+  int rows, tiles;
 };
 
 // What token i sees: by its document, found by bisection, or its sequence.  A
@@ -53,12 +48,10 @@ __device__ __forceinline__ Spans find_spans(const PlanArgs& p, const int32_t* of
   return spans_in(i, a, b, p.prefix ? min(max(__ldg(p.prefix + d), 0), b - a) : 0, p.causal);
 }
 
-// One block to an order: the tiles sorted by how many tiles of the other side
-// their first and last rows reach, longest first, so that no long one is left
-// for the end.  (Equal ones in any order: it decides nothing but who is first.
-// 256 classes of length: with 1024 the scan below made a call of 4096 packed
-// tokens 63.0 us in place of 61.8.)
-__device__ __forceinline__ void sort_tiles(const PlanArgs& p, const PlanArgs::Order& o, const int32_t* offsets) {
+// One block: the tiles sorted by how many tiles of keys their first and last
+// rows reach (256 classes of length), longest first, so that no long one is left
+// for the end.  (Equal ones in any order: it decides nothing but who is first.)
+__device__ __forceinline__ void sort_tiles(const PlanArgs& p, const int32_t* offsets) {
   constexpr int kBuckets = 256;
   __shared__ int count[kBuckets];
   int lo = 0, hi = p.tokens;
@@ -69,17 +62,17 @@ __device__ __forceinline__ void sort_tiles(const PlanArgs& p, const PlanArgs::Or
   int shift = 0;
   while ((p.tokens / kRows) >> shift >= kBuckets) ++shift;
   const auto bucket = [&](int tile) {
-    const int first = max(tile * o.rows, lo), last = min((tile + 1) * o.rows, hi) - 1;
+    const int first = max(tile * p.rows, lo), last = min((tile + 1) * p.rows, hi) - 1;
     int work = 0;
     if (first <= last) {
       const Spans a = find_spans(p, offsets, first), b = find_spans(p, offsets, last);
-      work = o.keys ? b.query_hi - a.query_lo : b.key_hi - a.key_lo;
+      work = b.key_hi - a.key_lo;
     }
     return kBuckets - 1 - min(max(work / kRows >> shift, 0), kBuckets - 1);
   };
   for (int i = threadIdx.x; i < kBuckets; i += kThreads) count[i] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < o.tiles; i += kThreads) atomicAdd(&count[bucket(i)], 1);
+  for (int i = threadIdx.x; i < p.tiles; i += kThreads) atomicAdd(&count[bucket(i)], 1);
   __syncthreads();
   if (threadIdx.x < 32) {
     int sum = 0;
@@ -96,7 +89,7 @@ __device__ __forceinline__ void sort_tiles(const PlanArgs& p, const PlanArgs::Or
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < o.tiles; i += kThreads) o.to[atomicAdd(&count[bucket(i)], 1)] = i;
+  for (int i = threadIdx.x; i < p.tiles; i += kThreads) p.order[atomicAdd(&count[bucket(i)], 1)] = i;
 }
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
@@ -111,9 +104,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     __syncthreads();
     offsets = near;
   }
-  // (the orders first: they take longest)
-  const int orders = int(gridDim.x) - p.span_blocks, block = int(blockIdx.x) - orders;
-  if (block < 0) return sort_tiles(p, p.orders[blockIdx.x], offsets);
+  // (the order first: it takes longest)
+  const int block = int(blockIdx.x) - (p.order != nullptr);
+  if (block < 0) return sort_tiles(p, offsets);
   const int i = block * kThreads + threadIdx.x;
   if (i < p.tokens) p.spans[i] = find_spans(p, offsets, i);
 }
@@ -276,21 +269,31 @@ fadam_status check(const fadam_attention_grad* d) {
 
 struct Layout {
   Spans* spans;
-  int* order;      // of tiles (pairs of them, forward) of queries
-  int* key_order;  // of tiles of keys
+  int* order;  // forward: of what a CTA takes
   float* stats;
   unsigned* peak;
   float* parts;
   int splits;
   size_t bytes;
 };
-// One sequence needs no plan: its last queries and first keys have most work.
-bool planned(const fadam_attention& d) { return d.documents || d.tokens > d.sequence; }
+bool several(const fadam_attention& d) { return d.documents || d.tokens > d.sequence; }
+// Whether the forward pass takes its tiles in order of their work, longest first,
+// rather than from the last one back (which is that order for one sequence): for
+// several sequences that give no more than two CTAs to an SM, so that a long one
+// at the end shows.  5 of 777 with 12 heads of 64 (192 CTAs) take 23.6 us so and
+// 26.0 from the last one back; with more CTAs the order's launch and sequences
+// that take turns in L2 cost more than it gives: 4 of 1024 (512 CTAs) 48.2 and
+// 46.7, 8 of 2048 (1024) 141 and 137, 11 documents in 4096 tokens (512) 56.5 and
+// 53.2, though 13 in 16384 (1024) 159 and 164.
+bool ordered(const fadam_attention& d, int sm_count) {
+  const int64_t ctas = ceil_div(d.tokens, 2 * kRows) * d.heads;
+  return several(d) && ctas <= 2 * int64_t(sm_count);
+}
 Layout layout(const fadam_attention& d, char* base) {
   Layout l{};
   Carver c{base};
   if (d.documents) l.spans = static_cast<Spans*>(c.take(sizeof(Spans) * d.tokens));
-  if (planned(d)) l.order = static_cast<int*>(c.take(sizeof(int) * ceil_div(d.tokens, kRows)));
+  if (several(d)) l.order = static_cast<int*>(c.take(sizeof(int) * ceil_div(d.tokens, kRows)));
   l.bytes = c.used;
   return l;
 }
@@ -312,10 +315,6 @@ Layout layout(const fadam_attention_grad& desc, char* base, int sm_count) {
   Layout l{};
   Carver c{base};
   if (d.documents) l.spans = static_cast<Spans*>(c.take(sizeof(Spans) * d.tokens));
-  if (planned(d)) {
-    l.order = static_cast<int*>(c.take(sizeof(int) * tiles));
-    l.key_order = static_cast<int*>(c.take(sizeof(int) * tiles));
-  }
   l.stats = static_cast<float*>(c.take(sizeof(float) * 2 * d.heads * tiles * kRows));
   l.peak = static_cast<unsigned*>(c.take(sizeof(unsigned)));
   l.splits = splits_of(d, sm_count);
@@ -347,7 +346,6 @@ AttentionArgs arguments(const fadam_attention& d, const Layout& l, const DeviceF
   g.slopes = d.slopes;
   g.spans = l.spans;
   g.order = l.order;
-  g.key_order = l.key_order;
   g.prefix = d.documents ? nullptr : d.prefix;
   g.documents = d.documents;
   g.n_documents = d.n_documents;
@@ -357,7 +355,7 @@ AttentionArgs arguments(const fadam_attention& d, const Layout& l, const DeviceF
 }
 
 fadam_status plan(const fadam_attention& d, const Layout& l, cudaStream_t stream) {
-  if (!planned(d)) return FADAM_OK;
+  if (!l.spans && !l.order) return FADAM_OK;
   PlanArgs p{};
   p.documents = d.documents;
   p.prefix = d.prefix;
@@ -367,12 +365,11 @@ fadam_status plan(const fadam_attention& d, const Layout& l, cudaStream_t stream
   p.causal = (d.flags & FADAM_ATTENTION_CAUSAL) != 0;
   p.spans = l.spans;
   p.span_blocks = l.spans ? int(ceil_div(d.tokens, kThreads)) : 0;
-  int orders = 0;
-  const bool pairs = !l.key_order && d.heads / d.kv_heads % 2 != 0;  // forward: 256 consecutive rows
-  const int rows = pairs ? 2 * kRows : kRows, tiles = int(ceil_div(d.tokens, rows));
-  p.orders[orders++] = {l.order, rows, tiles, false};
-  if (l.key_order) p.orders[orders++] = {l.key_order, rows, tiles, true};
-  return launch_chained("attention plan launch", plan_kernel, orders + p.span_blocks, kThreads, 0, stream, p);
+  p.order = l.order;
+  p.rows = d.heads / d.kv_heads % 2 ? 2 * kRows : kRows;  // (an odd group: 256 rows of one head to a CTA)
+  p.tiles = int(ceil_div(d.tokens, p.rows));
+  return launch_chained("attention plan launch", plan_kernel, (p.order != nullptr) + p.span_blocks, kThreads, 0,
+                        stream, p);
 }
 
 fadam_status check_workspace(const void* workspace, size_t bytes, size_t need) {
@@ -439,8 +436,9 @@ extern "C" fadam_status fadam_attention_run(const fadam_attention* desc, void* w
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   DeviceFacts dev;
   if ((st = device_facts(&dev))) return st;
-  const Layout l = layout(d, static_cast<char*>(workspace));
+  Layout l = layout(d, static_cast<char*>(workspace));
   if ((st = check_workspace(workspace, bytes, l.bytes))) return st;
+  if (!ordered(d, dev.sm_count)) l.order = nullptr;
   ForwardMaps maps;
   if ((st = head_map(&maps.q, d.q, d.tokens, d.heads, d.width, d.q_stride, d.q_head_stride)) ||
       (st = head_map(&maps.k, d.k, d.tokens, d.kv_heads, d.width, d.k_stride, d.k_head_stride)) ||

@@ -23,8 +23,7 @@ struct AttentionArgs {
   float2 series[4];          // capped scores in units of log 2 near zero: of x, x^3, x^5, x^7, twice each
   const float* slopes;
   const Spans* spans;        // [tokens] where there are documents
-  const int* order;          // of tiles of queries (forward: of what a CTA takes), or NULL: last ones first
-  const int* key_order;      // of tiles of keys, or NULL: first ones first
+  const int* order;          // forward: of what a CTA takes, or NULL: last ones first
   const int32_t* prefix;     // of the sequences, where there are none
   const int32_t* documents;  // the first and the last offset say what is padding
   int64_t n_documents;
