@@ -238,6 +238,15 @@ def test_attention_prefixes(offsets, prefix):
         _check(_case(600, 2, 1, D, dtype, seed=3, offsets=offsets, prefix=prefix, sequence=200))
 
 
+@pytest.mark.parametrize("H,Hk", [(65, 65), (66, 33)])
+def test_attention_tiles_as_they_come(H, Hk):
+    """Several sequences and documents of more than two CTAs to an SM, whose
+    tiles are not sorted by their work: one head or two to a CTA."""
+    for kw in (dict(sequence=200), dict(sequence=200, prefix=[0, 30, 200, 1, 128, 77]),
+               dict(offsets=[10, 40, 700, 701, 1190])):
+        _check(_case(1200, H, Hk, 16, BF16, seed=H, **kw))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_attention_padding_may_hold_anything(dtype):
     """Rows outside all documents, before and behind them, of q, k, v, grad_out
