@@ -334,8 +334,8 @@ struct Scores {
   // Else tanh(y) is 1 - 2 / (exp(2 y) + 1), whose exponential and reciprocal take
   // three times the time of the softmax's own exponential.  (4096 packed tokens,
   // 32 heads of 128: with the exponentials alone forward 78 us and backward 254,
-  // with five terms up to 0.35 caps 74 and 244; in the kernels as they are five
-  // terms take 68 and 169, these four 63 and 158.)
+  // with five terms up to 0.35 caps 74 and 244; in later kernels five terms took
+  // 68 and 169, these four 63 and 158.)
   template <int N>
   __device__ __forceinline__ void capped(float (&s)[N]) const {
     float far[2] = {0.0f, 0.0f};
