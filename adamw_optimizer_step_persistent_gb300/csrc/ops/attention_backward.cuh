@@ -3,7 +3,7 @@
 //   grad_v_j = sum_i p_ij grad_out_i,  grad_k_j = sum_i ds_ij q_i,
 //   grad_q_i = sum_j ds_ij k_j.
 //
-// Two kernels, each of which keeps one side in shared memory, walks over the
+// Two kinds of CTAs, each of which keeps one side in shared memory, walks over the
 // other and sums in tensor memory, so that every sum has one order and nothing
 // is added to memory: one takes 128 keys and walks over the queries that see
 // them, of all query heads that share the key head (four products a tile: the
@@ -117,7 +117,7 @@ struct Backward {
   }
 
   // What the 128 rows of the CTA need: rows are dealt to the first four warps.
-  __device__ __forceinline__ Reach meet(int lo, int hi, bool here) {
+  __device__ __forceinline__ Reach meet(int lo, int hi, bool here) const {
     const int warp = threadIdx.x / 32;
     if (warp < 4) {
       const Reach r = reach_of(lo, hi, here);
@@ -253,27 +253,20 @@ __device__ __forceinline__ void slopes_of(float (&s)[32], const float (&d)[32], 
 
 // ---- grad_k and grad_v: 128 keys, a walk over queries --------------------------------------
 
-struct KeyMaps {
-  CUtensorMap q, k, v, grad_out, grad_k, grad_v;
-};
-
 template <class T, int C>
-__global__ void __launch_bounds__(kAttentionThreads, 1)
-    attention_keys_kernel(const __grid_constant__ KeyMaps maps, const __grid_constant__ AttentionArgs g) {
+__device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps& maps, const AttentionArgs& g,
+                                         unsigned item) {
   using E = typename T::type;
-  using B = Backward<T, C>;
-  extern __shared__ __align__(1024) unsigned char smem[];
-  B b;
+  Backward<T, C> b;
   if (!b.begin(smem, g, 1)) return;
   const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
   chain_wait();
-  chain_next();  // (the queries' kernel reads nothing of this one)
 
   const unsigned kv_heads = unsigned(g.heads / g.group), columns = kv_heads * g.splits;
-  const int tile = int(blockIdx.x / columns);
-  const int rest = int(blockIdx.x % columns);
+  const int tile = int(item / columns);
+  const int rest = int(item % columns);
   const int kv = rest / g.splits, split = rest % g.splits;
   const int share = g.group / g.splits, head0 = kv * g.group + split * share;
   const int key0 = tile * kRows;
@@ -477,6 +470,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     }
   }
   __syncwarp();
+  chain_next();
   fence_before_sync();
   __syncthreads();
   if (warp == kMultiply) tmem_free(tmem, 512);
@@ -484,28 +478,19 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
 
 // ---- grad_q: 128 queries, a walk over keys ------------------------------------------------
 
-struct QueryMaps {
-  CUtensorMap q, k, v, grad_out, grad_q;
-};
-
 template <class T, int C>
-__global__ void __launch_bounds__(kAttentionThreads, 1)
-    attention_queries_kernel(const __grid_constant__ QueryMaps maps, const __grid_constant__ AttentionArgs g) {
+__device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardMaps& maps, const AttentionArgs& g,
+                                            unsigned item) {
   using E = typename T::type;
-  using B = Backward<T, C>;
-  extern __shared__ __align__(1024) unsigned char smem[];
-  B b;
+  Backward<T, C> b;
   if (!b.begin(smem, g, 2)) return;
   const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
   BackwardBarriers* bars = b.bars;
   int* status = g.status;
-  // No wait at the start: the keys' kernel, whose CTAs let this one's come once
-  // all of them run, waited for what comes before both, and neither reads what
-  // the other writes.  This one's CTAs take the SMs that the last of those
-  // leave; its own last CTA waits for them, so that what follows finds both done.
+  chain_wait();
 
-  const int head = int(blockIdx.x % unsigned(g.heads));
-  const int query0 = (g.tiles - 1 - int(blockIdx.x / unsigned(g.heads))) * kRows;
+  const int head = int(item % unsigned(g.heads));
+  const int query0 = (g.tiles - 1 - int(item / unsigned(g.heads))) * kRows;
   const int row = threadIdx.x % kRows;
   Spans span{};
   if (warp < kScoreWarps && query0 + row < g.tokens) span = spans_of(g, query0 + row);
@@ -659,32 +644,37 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     }
   }
   __syncwarp();
-  if (blockIdx.x == gridDim.x - 1) chain_wait();
   chain_next();
   fence_before_sync();
   __syncthreads();
   if (warp == kMultiply) tmem_free(tmem, 512);
 }
 
+// ---- both, in one launch -------------------------------------------------------------------
+
+// The first CTAs take keys, the others queries, which get the SMs that the last
+// of those leave.  (Two launches, of which the second one's CTAs started under
+// the first one's end without a wait of their own, read what the launches
+// before both had written, and nothing but their own wait makes that visible.)
 template <class T, int C>
-fadam_status launch_backward(const BackwardMaps& m, const AttentionArgs& g, cudaStream_t stream) {
-  auto* keys = attention_keys_kernel<T, C>;
-  auto* queries = attention_queries_kernel<T, C>;
-  fadam_status st;
-  if ((st = launched_with<attention_keys_kernel<T, C>>("attention's backward pass")) ||
-      (st = launched_with<attention_queries_kernel<T, C>>("attention's backward pass")))
-    return st;
+__global__ void __launch_bounds__(kAttentionThreads, 1)
+    attention_backward_kernel(const __grid_constant__ BackwardMaps maps, const __grid_constant__ AttentionArgs g) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (blockIdx.x < g.key_items) keys_cta<T, C>(smem, maps, g, blockIdx.x);
+  else queries_cta<T, C>(smem, maps, g, blockIdx.x - g.key_items);
+}
+
+template <class T, int C>
+fadam_status launch_backward(const BackwardMaps& maps, AttentionArgs g, cudaStream_t stream) {
+  auto* kernel = attention_backward_kernel<T, C>;
+  if (const fadam_status st = launched_with<attention_backward_kernel<T, C>>("attention's backward pass")) return st;
   constexpr int kShared = int(kBackwardSmem<C>);
-  cudaError_t e = cudaFuncSetAttribute(keys, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(queries, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  const KeyMaps km{m.q, m.k, m.v, m.grad_out, m.grad_k, m.grad_v};
-  if ((st = launch_chained("attention keys launch", keys, int64_t(g.tiles) * (g.heads / g.group) * g.splits,
-                           kAttentionThreads, kShared, stream, km, g)))
-    return st;
-  const QueryMaps qm{m.q, m.k, m.v, m.grad_out, m.grad_q};
-  return launch_chained("attention queries launch", queries, int64_t(g.tiles) * g.heads, kAttentionThreads,
-                        kShared, stream, qm, g);
+  // (tiles times heads are at most 2^30, and the key heads' splits no more than the heads: unsigned holds both)
+  g.key_items = unsigned(int64_t(g.tiles) * (g.heads / g.group) * g.splits);
+  return launch_chained("attention backward launch", kernel, g.key_items + int64_t(g.tiles) * g.heads,
+                        kAttentionThreads, kShared, stream, maps, g);
 }
 template <class T>
 fadam_status backward_of(const BackwardMaps& maps, const AttentionArgs& g, cudaStream_t stream) {

@@ -35,6 +35,7 @@ struct AttentionArgs {
   unsigned* peak;            // bits of the largest magnitude in grad_out, the f16 products' scale
   float* parts;              // fp32 sums of grad_k and grad_v by splits of the query heads
   int splits;
+  unsigned key_items;        // CTAs of the first kind, which take keys
 };
 
 // One matrix [tokens, heads, width] of 16-bit elements for boxes of 128 tokens

@@ -1,0 +1,65 @@
+"""Launches that may begin under the end of the one before them: what the
+operators' sources have to keep to, by reading them (no GPU)."""
+import glob
+import os
+import re
+
+import pytest
+
+OPS = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                   "adamw_optimizer_step_persistent_gb300", "csrc", "ops")
+
+
+def _close(text, at, pair):
+    """Behind the bracket that closes the one before `at`."""
+    depth = 1
+    while depth:
+        depth += {pair[0]: 1, pair[1]: -1}.get(text[at], 0)
+        at += 1
+    return at
+
+
+def _functions():
+    """{(file, name): (is a kernel, body)} of the kernels, and of the functions
+    that are one kind of their CTAs."""
+    found = {}
+    for path in sorted(glob.glob(os.path.join(OPS, "*.cu*"))):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for m in re.finditer(r"\bvoid\s+", text):
+            at = m.end()
+            while attribute := re.compile(r"__\w+__\(").match(text, at):
+                at = re.compile(r"\s*").match(text, _close(text, attribute.end(), "()")).end()
+            name = re.compile(r"(\w+)\(").match(text, at)
+            if not name:
+                continue
+            at = re.compile(r"[\s\w]*").match(text, _close(text, name.end(), "()")).end()
+            kernel = text[:m.start()].rstrip().endswith("__global__")
+            if text[at] == "{" and (kernel or name[1].endswith("_cta")):
+                found[os.path.basename(path), name[1]] = (kernel, text[at:_close(text, at + 1, "{}")])
+    return found
+
+
+FUNCTIONS = _functions()
+KERNELS = sorted(k for k, (kernel, _) in FUNCTIONS.items() if kernel and k[1] != "take_status_kernel")
+
+
+def _waits(at):
+    body = FUNCTIONS[at][1]
+    if re.search(r"\n  chain_wait\(\);", body):
+        return True
+    # a kernel of several kinds of CTAs: each of them
+    kinds = re.findall(r"\b(\w+_cta)\b", body)
+    return bool(kinds) and all(_waits((at[0], k)) for k in kinds)
+
+
+def test_kernels_are_found():
+    sources = "".join(re.sub(r"//[^\n]*", "", open(p).read()) for p in glob.glob(os.path.join(OPS, "*.cu*")))
+    assert len(KERNELS) == sources.count("__global__") - 1
+
+
+@pytest.mark.parametrize("at", KERNELS, ids=lambda at: at[1])
+def test_every_thread_waits_for_the_launch_before(at):
+    """What earlier launches wrote is visible behind a kernel's own wait only:
+    it stands in the kernel's (or its CTAs') outermost block, behind no condition."""
+    assert _waits(at)
+    assert not re.search(r"if \([^\n]*\)\s*chain_wait\(\)", FUNCTIONS[at][1])
