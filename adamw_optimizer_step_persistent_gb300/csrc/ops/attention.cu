@@ -116,32 +116,92 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 // What is added to a row's scores, -lse in units of log 2 and the lift of p's
 // exponent, and to its grad_out . v: -delta = -grad_out . out, 16 lanes to a
 // row.  Rows that see nothing, and those up to a whole tile, get -infinity: p
-// is 0.
+// is 0.  For fp16 (kPeak) also the row's largest |grad_out|, and the documents'
+// peaks (their largest finite ones: atomics of a maximum, whose order changes
+// nothing); blocks behind those of the rows take the sums of v's magnitudes.
 constexpr int kStatRows = 64;  // tokens of a CTA, of one head: 16 at a time
+template <class E>
+struct StatRows {
+  const E* base;
+  int64_t ld, head_ld;
+  __device__ __forceinline__ Raw<E> load(int token, int head, int col) const {
+    return load_raw(base + token * ld + head * head_ld + col);
+  }
+};
+
+// A row's peak, counted with its CTA's first document's, or at its own place.
+__device__ __forceinline__ void count_peak(unsigned* shared, int base, unsigned* peaks, int entry, float x) {
+  if (!(x > 0.0f && x < INFINITY)) return;
+  atomicMax(entry == base ? shared : peaks + entry, __float_as_uint(x));
+}
+
 template <class E, bool kPeak>
 __global__ void __launch_bounds__(kThreads)
-    stats_kernel(const E* out, int64_t out_ld, int64_t out_head_ld, const E* grad, int64_t grad_ld,
-                 int64_t grad_head_ld, const float* lse,
-                 int tokens, int heads, int width, int pitch, float lift, float* stats, unsigned* peak) {
+    stats_kernel(const StatRows<E> out, const StatRows<E> grad, const StatRows<E> values, float lift,
+                 const __grid_constant__ AttentionArgs g) {
   chain_wait();
   chain_next();
-  const int head = int(blockIdx.x % unsigned(heads)), token0 = int(blockIdx.x / unsigned(heads)) * kStatRows;
-  const int group = threadIdx.x / 16, lane = threadIdx.x % 16;
+  __shared__ unsigned shared[2];
+  const unsigned row_blocks = unsigned(g.tiles) * (kRows / kStatRows) * g.heads;
+  const bool of_v = kPeak && blockIdx.x >= row_blocks;
+  const int kv_heads = g.heads / g.group, heads = of_v ? kv_heads : g.heads;
+  const unsigned block = of_v ? blockIdx.x - row_blocks : blockIdx.x;
+  const int head = int(block % unsigned(heads)), token0 = int(block / unsigned(heads)) * kStatRows;
+  const int group = threadIdx.x / 16, lane = threadIdx.x % 16, width = g.width;
   constexpr int kTurns = kStatRows / 16;
+  int base = 0;
+  unsigned* peaks = nullptr;
+  const int64_t apart = int64_t(kv_heads) * g.entries;
+  if constexpr (kPeak) {
+    if (threadIdx.x < 2) shared[threadIdx.x] = 0;
+    base = entry_of(g, token0).at;
+    peaks = g.peaks + int64_t(of_v ? head : head / g.group) * g.entries;
+    __syncthreads();
+  }
   Raw<E> a[kTurns], b[kTurns];
+  if (kPeak && of_v) {
+    Entry entry[kTurns];
+#pragma unroll
+    for (int r = 0; r < kTurns; ++r) {
+      const int t = token0 + r * 16 + group;
+      entry[r] = entry_of(g, t);
+      a[r] = zero_raw<E>();
+      if (entry[r].lives && lane * 8 < width) a[r] = values.load(t, head, lane * 8);
+    }
+#pragma unroll
+    for (int r = 0; r < kTurns; ++r) {
+      Pair x[4];
+      widen(a[r], x);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = split(x[i]);
+        sum += fabsf(v.x) < INFINITY ? fabsf(v.x) : 0.0f;
+        sum += fabsf(v.y) < INFINITY ? fabsf(v.y) : 0.0f;
+      }
+#pragma unroll
+      for (int d = 8; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+      if (lane == 0 && entry[r].lives) count_peak(&shared[0], base, peaks + 2 * apart, entry[r].at, sum);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && shared[0]) atomicMax(peaks + 2 * apart + base, shared[0]);
+    return;
+  }
   float l[kTurns];
+  int entry[kTurns];
 #pragma unroll
   for (int r = 0; r < kTurns; ++r) {
     const int t = token0 + r * 16 + group;
+    if (kPeak) entry[r] = entry_of(g, t).at;
     a[r] = zero_raw<E>();
     b[r] = zero_raw<E>();
-    l[r] = t < tokens ? lse[int64_t(t) * heads + head] : -INFINITY;
+    l[r] = t < g.tokens ? g.lse[int64_t(t) * heads + head] : -INFINITY;
     if (l[r] != -INFINITY && lane * 8 < width) {
-      a[r] = load_raw(out + t * out_ld + head * out_head_ld + lane * 8);
-      b[r] = load_raw(grad + t * grad_ld + head * grad_head_ld + lane * 8);
+      a[r] = out.load(t, head, lane * 8);
+      b[r] = grad.load(t, head, lane * 8);
     }
   }
-  float top = 0.0f;
+  const int64_t pitch = int64_t(g.tiles) * kRows;
 #pragma unroll
   for (int r = 0; r < kTurns; ++r) {
     Pair x[4], y[4];
@@ -150,27 +210,35 @@ __global__ void __launch_bounds__(kThreads)
     Pair sum = mul2(x[0], y[0]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) sum = fma2(x[i], y[i], sum);
-    float delta = sum2(sum);
+    float delta = sum2(sum), top = 0.0f;
 #pragma unroll
     for (int d = 8; d > 0; d /= 2) delta += __shfl_xor_sync(~0u, delta, d);
     if (kPeak) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 v = split(y[i]);
-        // (a NaN counts as an infinity: the gradients are not finite anyway)
-        top = fmaxf(top, v.x == v.x ? fabsf(v.x) : INFINITY);
-        top = fmaxf(top, v.y == v.y ? fabsf(v.y) : INFINITY);
+        top = fmaxf(top, fabsf(v.x) < INFINITY ? fabsf(v.x) : 0.0f);
+        top = fmaxf(top, fabsf(v.y) < INFINITY ? fabsf(v.y) : 0.0f);
       }
+#pragma unroll
+      for (int d = 8; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     }
     const int t = token0 + r * 16 + group;
-    if (lane == 0 && t < pitch) {
-      stats[int64_t(head) * pitch + t] = l[r] == -INFINITY ? -INFINITY : lift - l[r] * kLog2e;
-      stats[int64_t(heads + head) * pitch + t] = -delta;
+    if (lane == 0) {  // (there is a place for every row of a tile)
+      g.stats[head * pitch + t] = l[r] == -INFINITY ? -INFINITY : lift - l[r] * kLog2e;
+      g.stats[(int64_t(heads) + head) * pitch + t] = -delta;
+      if constexpr (kPeak) {
+        g.stats[(2 * int64_t(heads) + head) * pitch + t] = top;
+        if (l[r] != -INFINITY) {
+          count_peak(&shared[0], base, peaks, entry[r], top);
+          count_peak(&shared[1], base, peaks + apart, entry[r], fabsf(delta));
+        }
+      }
     }
   }
-  if (kPeak) {
-    const unsigned bits = __reduce_max_sync(~0u, __float_as_uint(top));
-    if (threadIdx.x % 32 == 0 && bits) atomicMax(peak, bits);
+  if constexpr (kPeak) {
+    __syncthreads();
+    if (threadIdx.x < 2 && shared[threadIdx.x]) atomicMax(peaks + threadIdx.x * apart + base, shared[threadIdx.x]);
   }
 }
 
@@ -271,7 +339,8 @@ struct Layout {
   Spans* spans;
   int* order;  // forward: of what a CTA takes
   float* stats;
-  unsigned* peak;
+  unsigned* peaks;
+  int entries;
   float* parts;
   int splits;
   size_t bytes;
@@ -309,14 +378,19 @@ int splits_of(const fadam_attention& d, int sm_count) {
     if (group % s == 0 && tiles * d.kv_heads * s >= sm_count) return s;
   return group;
 }
+size_t peaks_bytes(const fadam_attention& d, const Layout& l) {
+  return sizeof(unsigned) * 3 * d.kv_heads * l.entries;
+}
 Layout layout(const fadam_attention_grad& desc, char* base, int sm_count) {
   const fadam_attention& d = desc.forward;
   const int64_t tiles = ceil_div(d.tokens, kRows);
   Layout l{};
   Carver c{base};
   if (d.documents) l.spans = static_cast<Spans*>(c.take(sizeof(Spans) * d.tokens));
-  l.stats = static_cast<float*>(c.take(sizeof(float) * 2 * d.heads * tiles * kRows));
-  l.peak = static_cast<unsigned*>(c.take(sizeof(unsigned)));
+  const bool f16 = d.dtype == FADAM_DT_F16;
+  l.stats = static_cast<float*>(c.take(sizeof(float) * (f16 ? 3 : 2) * d.heads * tiles * kRows));
+  l.entries = int(d.documents ? d.tokens : d.tokens / d.sequence);
+  if (f16) l.peaks = static_cast<unsigned*>(c.take(peaks_bytes(d, l)));
   l.splits = splits_of(d, sm_count);
   if (l.splits > 1)
     l.parts = static_cast<float*>(c.take(sizeof(float) * 2 * l.splits * d.tokens * d.kv_heads * d.width));
@@ -387,23 +461,22 @@ fadam_status backward(const fadam_attention_grad& desc, const Layout& l, const B
   const fadam_attention& d = desc.forward;
   AttentionArgs g = arguments(d, l, dev);
   g.stats = l.stats;
-  g.peak = l.peak;
+  g.peaks = l.peaks;
+  g.entries = l.entries;
   g.parts = l.parts;
   g.splits = l.splits;
   if (kPeak) {
-    const cudaError_t e = cudaMemsetAsync(l.peak, 0, sizeof(unsigned), stream);
+    const cudaError_t e = cudaMemsetAsync(l.peaks, 0, peaks_bytes(d, l), stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   }
   fadam_status st;
   if ((st = plan(d, l, stream))) return st;
-  const int pitch = g.tiles * kRows;
-  if ((st = launch_chained("attention stats launch", stats_kernel<E, kPeak>,
-                           int64_t(pitch / kStatRows) * d.heads, kThreads, 0, stream,
-                           static_cast<const E*>(d.out), desc.out_stride, desc.out_head_stride,
-                           static_cast<const E*>(desc.grad_out),
-                           desc.grad_out_stride, desc.grad_out_head_stride,
-                           static_cast<const float*>(d.lse), int(d.tokens), int(d.heads), int(d.width), pitch,
-                           kPeak ? 10.0f : 0.0f, l.stats, l.peak)))
+  const StatRows<E> out{static_cast<const E*>(d.out), desc.out_stride, desc.out_head_stride};
+  const StatRows<E> grad{static_cast<const E*>(desc.grad_out), desc.grad_out_stride, desc.grad_out_head_stride};
+  const StatRows<E> values{static_cast<const E*>(d.v), d.v_stride, d.v_head_stride};
+  const int64_t blocks = int64_t(g.tiles) * (kRows / kStatRows) * (d.heads + (kPeak ? d.kv_heads : 0));
+  if ((st = launch_chained("attention stats launch", stats_kernel<E, kPeak>, blocks, kThreads, 0, stream, out,
+                           grad, values, kPeak ? 10.0f : 0.0f, g)))
     return st;
   st = kPeak ? attention_backward_f16(maps, g, stream) : attention_backward_bf16(maps, g, stream);
   if (st || l.splits == 1) return st;

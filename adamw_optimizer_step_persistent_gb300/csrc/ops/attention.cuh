@@ -275,6 +275,18 @@ __device__ __forceinline__ Spans spans_of(const AttentionArgs& g, int i) {
   return spans_in(i, a, a + g.sequence, p, g.causal);
 }
 
+// Where in `peaks` a token's document has its place; whether it is in one.
+struct Entry {
+  int at;
+  bool lives;
+};
+__device__ __forceinline__ Entry entry_of(const AttentionArgs& g, int i) {
+  if (i >= g.tokens) return Entry{0, false};
+  if (!g.spans) return Entry{i / g.sequence, true};
+  const int2 keys = __ldg(reinterpret_cast<const int2*>(g.spans + i));
+  return Entry{keys.x, keys.x < keys.y};
+}
+
 // What a tile's 128 rows need of the other side, from the spans of its rows
 // that see anything: any of it lies in [lo, hi), all rows see [all_lo, all_hi).
 struct Reach {

@@ -39,9 +39,10 @@ namespace fadam_ops {
 // the product with ds, Y by grad_out . v (and the product with p).
 constexpr int kRingX = 3, kRingY = 2;
 // fp16: p is held times 2^10 (the smallest normal number is 2^-14), ds times a
-// power of two that brings grad_out's largest element to [1, 2).
+// power of two for each row, a query's where grad_q is summed, a key's where
+// grad_k is: see ds_exponent().
 template <class T>
-constexpr float kLiftBits = T::code == FADAM_DT_F16 ? 10.0f : 0.0f;
+constexpr int kLiftBits = T::code == FADAM_DT_F16 ? 10 : 0;
 
 struct BackwardBarriers {
   uint64_t own_full, done;
@@ -55,6 +56,7 @@ struct BackwardBarriers {
 struct BackwardExtra {
   float lse[kRingY][kRows];     // with Y: read for p, before Y is done with
   float delta[kRingX][kRows];   // with X
+  int8_t exponent[kRows];       // fp16: of the rows' ds, for the end
   BackwardBarriers bars;
 };
 template <int C>
@@ -62,14 +64,33 @@ constexpr size_t kBackwardSmem = (2 + kRingX + kRingY) * C * size_t(kBoxBytes) +
 static_assert(kBackwardSmem<2> <= 227 * 1024, "shared memory of one CTA");
 constexpr int kColumnsS = 0, kColumnsDots = kRows, kColumnsA = 2 * kRows, kColumnsB = 3 * kRows;
 
-// A power of two that brings the largest element of grad_out to [1, 2).
+// A bound of a row's ds: |p (go . v - delta)| is at most go's largest magnitude
+// times the sum of v's, and |delta|.  Of the key `token` of a key head by what
+// its document holds, so that one of small gradients keeps its bits beside one of
+// large ones; of the query `token` of a head by its own grad_out and delta.
 template <class T>
-__device__ __forceinline__ float ds_factor(const AttentionArgs& g) {
-  if constexpr (T::code != FADAM_DT_F16) return 1.0f;
-  const unsigned bits = *g.peak;
-  if (bits == 0 || bits >= 0x7f800000u) return 1.0f;
-  return ldexpf(1.0f, -ilogbf(__uint_as_float(bits)));
+__device__ __forceinline__ float key_bound(const AttentionArgs& g, int kv, int token) {
+  if constexpr (T::code != FADAM_DT_F16) return 0.0f;
+  const int64_t kv_heads = g.heads / g.group, apart = kv_heads * g.entries;
+  const unsigned* at = g.peaks + int64_t(kv) * g.entries + entry_of(g, token).at;
+  return fmaf(__uint_as_float(at[0]), __uint_as_float(at[2 * apart]), __uint_as_float(at[apart]));
 }
+template <class T>
+__device__ __forceinline__ float query_bound(const AttentionArgs& g, int head, int token) {
+  if constexpr (T::code != FADAM_DT_F16) return 0.0f;
+  const int64_t kv_heads = g.heads / g.group, pitch = int64_t(g.tiles) * kRows;
+  const unsigned v = g.peaks[(2 * kv_heads + head / g.group) * g.entries + entry_of(g, token).at];
+  const float delta = fabsf(g.stats[(g.heads + head) * pitch + token]);
+  return fmaf(g.stats[(2 * int64_t(g.heads) + head) * pitch + token], __uint_as_float(v),
+              delta < INFINITY ? delta : 0.0f);
+}
+// The exponent of a power of two that brings the bound to [2^14, 2^15): no ds is
+// then infinite in fp16, whatever v holds, and one of 2^-28 of the bound is
+// still a normal number.  (A bound is 0 or between 2^-48 and 2^42.)
+__device__ __forceinline__ int ds_exponent(float bound) {
+  return bound > 0.0f ? 14 + 127 - int(__float_as_uint(bound) >> 23) : 0;
+}
+__device__ __forceinline__ float power_of_two(int exponent) { return __uint_as_float(unsigned(127 + exponent) << 23); }
 
 template <class T, int C>
 struct Backward {
@@ -114,6 +135,19 @@ struct Backward {
     }
     if (threadIdx.x / 32 == kMultiply) tmem_alloc(shared_addr(&bars->tmem), 512);
     return true;
+  }
+
+  // What a row's ds (2^10 of it, fp16) is multiplied by, and its sums at the end.
+  // (The four lanes of a row write the same: each reads what it wrote itself.)
+  __device__ __forceinline__ float keep_factor(int row, float bound) const {
+    if constexpr (T::code != FADAM_DT_F16) return 1.0f;
+    const int exponent = ds_exponent(bound);
+    extra->exponent[row] = int8_t(exponent);
+    return power_of_two(exponent - kLiftBits<T>);
+  }
+  __device__ __forceinline__ float inverse_factor(int row) const {
+    if constexpr (T::code != FADAM_DT_F16) return 1.0f;
+    return power_of_two(-int(extra->exponent[row]));
   }
 
   // What the 128 rows of the CTA need: rows are dealt to the first four warps.
@@ -233,7 +267,7 @@ __device__ __forceinline__ void weights(float (&s)[32], uint32_t (&p)[16], const
 }
 
 // 32 columns of ds: p (at s) times (grad_out . v - delta), `delta(c)` added to
-// columns c and c + 1; fp16 times `factor`.  What is not seen is set to 0.
+// columns c and c + 1; fp16 times the row's `factor`.  What is not seen is set to 0.
 template <class T, class Delta>
 __device__ __forceinline__ void slopes_of(float (&s)[32], const float (&d)[32], uint32_t (&p)[16], float factor,
                                           const Cut& cut, Delta delta) {
@@ -273,6 +307,8 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
   const int row = threadIdx.x % kRows;  // of the first sixteen warps: a lane's key
   Spans span{};
   if (warp < kScoreWarps && key0 + row < g.tokens) span = spans_of(g, key0 + row);
+  float bound = 0.0f;
+  if (warp < kScoreWarps) bound = key_bound<T>(g, kv, key0 + row);  // (on its way while the CTA meets)
   b.load_own(&maps.k, &maps.v, kv, key0);
   const Reach reach = b.meet(span.query_lo, span.query_hi, key0 + row < g.tokens);
   const uint32_t tmem = uniform(bars->tmem);
@@ -377,7 +413,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
     const uint32_t at_s = lanes + kColumnsS + part * 32, at_dots = lanes + kColumnsDots + part * 32;
     const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
     const uint32_t bar_weights = shared_addr(&bars->weights);
-    const float factor = ds_factor<T>(g) * exp2f(-kLiftBits<T>);
+    const float factor = b.keep_factor(row, bound);
     bool ok = true;
     Place<kRingX> x;
     Place<kRingY> y;
@@ -427,7 +463,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
     if (ok) ok = bar_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
     fence_after_sync();
     const bool keys = part >= 2;
-    const float scale = keys ? g.scale / ds_factor<T>(g) : exp2f(-kLiftBits<T>);
+    const float scale = keys ? g.scale * b.inverse_factor(row) : power_of_two(-kLiftBits<T>);
     const uint32_t from = lanes + (keys ? kColumnsB : kColumnsA);
     const uint32_t tile_at = keys ? b.own0 : b.own1;
     const uint32_t place = tile_at + (quarter * 32 + lane) * 128;
@@ -494,6 +530,8 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
   const int row = threadIdx.x % kRows;
   Spans span{};
   if (warp < kScoreWarps && query0 + row < g.tokens) span = spans_of(g, query0 + row);
+  float bound = 0.0f;
+  if (warp < kScoreWarps) bound = query_bound<T>(g, head, query0 + row);
   b.load_own(&maps.q, &maps.grad_out, head, query0);
   const Reach reach = b.meet(span.key_lo, span.key_hi, query0 + row < g.tokens);
   const uint32_t tmem = uniform(bars->tmem);
@@ -576,7 +614,7 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
     const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
     const uint32_t bar_scores_read = shared_addr(&bars->scores_read);
     const uint32_t bar_dots_read = shared_addr(&bars->dots_read);
-    const float factor = ds_factor<T>(g) * exp2f(-kLiftBits<T>);
+    const float factor = b.keep_factor(row, bound);
     const int64_t pitch = int64_t(g.tiles) * kRows;
     const Pair lse = both(g.stats[head * pitch + query0 + row]);
     const Pair delta = both(g.stats[(g.heads + head) * pitch + query0 + row]);
@@ -617,7 +655,7 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
     }
     if (ok) ok = bar_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
     fence_after_sync();
-    const float scale = g.scale / ds_factor<T>(g);
+    const float scale = g.scale * b.inverse_factor(row);
     const uint32_t place = b.own0 + (quarter * 32 + lane) * 128;
     // a quarter of the elements to four warps, C * 16 each
 #pragma unroll

@@ -31,8 +31,11 @@ struct AttentionArgs {
   int* status;
 
   // backward
-  float* stats;              // [2][heads][tiles * 128]: -lse in units of log 2, then -delta
-  unsigned* peak;            // bits of the largest magnitude in grad_out, the f16 products' scale
+  float* stats;              // [2][heads][tiles * 128]: -lse in units of log 2, then -delta; f16: a third,
+                             // a grad_out row's largest magnitude
+  unsigned* peaks;           // f16: [3][kv_heads][entries], bits of a key head's largest in a document:
+                             // grad_out's magnitudes, delta's, sums of a v row's magnitudes
+  int entries;               // one for each sequence, or one for each token, of which a document's first counts
   float* parts;              // fp32 sums of grad_k and grad_v by splits of the query heads
   int splits;
   unsigned key_items;        // CTAs of the first kind, which take keys

@@ -145,11 +145,15 @@ fadam_status fadam_attention_run(const fadam_attention* desc, void* workspace, s
  *   grad_q [tokens, heads, width], grad_k, grad_v [tokens, kv_heads, width]
  *                                        of dtype, contiguous
  * grad_k and grad_v are summed over the query heads that share a head, in fp32
- * and in a fixed order.  p = exp(s - lse) and its product with (grad_out . v -
- * grad_out . out) are rounded to dtype for the products; in fp16 after
- * multiplication by powers of two, p by 2^10 and the product by one that brings
- * grad_out's largest element to [1, 2): elements of v below 128 in magnitude keep
- * it finite.  Nothing is summed by atomics: results are deterministic. */
+ * and in a fixed order.  p = exp(s - lse) and ds, its product with (grad_out . v
+ * - grad_out . out), are rounded to dtype for the products; in fp16 after
+ * multiplication by powers of two: p by 2^10, ds by one of its row.  That brings a
+ * bound of the row's ds (max |grad_out| times the largest sum of a |v| row, and
+ * |grad_out . out|) to [2^14, 2^15), so that no ds overflows, and those of 2^-28 of
+ * the bound and more keep fp16's precision.  The bound is the query's own for
+ * grad_q; for grad_k it is that of the key head's queries in the key's document:
+ * other documents do not matter.  Nothing is summed by atomics: results are
+ * deterministic. */
 typedef struct {
   fadam_attention forward;
   const void* grad_out;
