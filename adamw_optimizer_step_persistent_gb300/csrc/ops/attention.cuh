@@ -340,14 +340,15 @@ struct Scores {
     inverse = g.softcap > 0.0f ? g.scale / g.softcap : 0.0f;
     slope = g.slopes ? __ldg(g.slopes + head) * kLog2e : 0.0f;
   }
-  // Products become capped scores, cap tanh(s / cap).  Where no score of a
-  // warp's is beyond a quarter of the cap, by tanh's Taylor series to the seventh
-  // power (off by 9e-8 of the cap there): five multiplications for two scores.
-  // Else tanh(y) is 1 - 2 / (exp(2 y) + 1), whose exponential and reciprocal take
-  // three times the time of the softmax's own exponential.  (4096 packed tokens,
-  // 32 heads of 128: with the exponentials alone forward 78 us and backward 254,
-  // with five terms up to 0.35 caps 74 and 244; in later kernels five terms took
-  // 68 and 169, these four 63 and 158.)
+  // Products become capped scores, cap tanh(s / cap).  Those up to a quarter of the
+  // cap by tanh's Taylor series to the seventh power (off by 9e-8 of the cap there):
+  // five multiplications for two scores.  Those beyond it by 1 - 2 / (exp(2 y) + 1),
+  // whose exponential and reciprocal take three times the time of the softmax's own
+  // exponential, and which a warp without any leaves out.  Each score's form is its
+  // own: what lies beside it, seen or not, changes no bit of it.  (4096 packed
+  // tokens, 32 heads of 128, in a graph: with a cap of 50, which no score comes near, forward 58 us
+  // and backward 154; with one of 2, where every warp has scores beyond, 91 and 197,
+  // and 68 and 171 as long as these warps took the second form for all of theirs.)
   template <int N>
   __device__ __forceinline__ void capped(float (&s)[N]) const {
     float far[2] = {0.0f, 0.0f};
@@ -355,12 +356,21 @@ struct Scores {
     for (int c = 0; c < N; c += 4)
 #pragma unroll
       for (int k = 0; k < 2; ++k) far[k] = fmaxf(fmaxf(far[k], fabsf(s[c + k])), fabsf(s[c + 2 + k]));
-    // (a NaN is far from anything, and keeps the others' way)
     if (__any_sync(~0u, fmaxf(far[0], far[1]) * inverse > 0.25f)) {
+      // (two passes in place: both forms of a score at a time would not fit the registers)
+      unsigned done[N / 32] = {};
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        if (fabsf(s[c]) * inverse > 0.25f) {
+          const float e = exp2_fast(s[c] * (2.0f * kLog2e * inverse));
+          s[c] = fmaf(-2.0f * cap, inverse_fast(e + 1.0f), cap);
+          done[c / 32] |= 1u << c % 32;
+        }
 #pragma unroll
       for (int c = 0; c < N; ++c) {
-        const float e = exp2_fast(s[c] * (2.0f * kLog2e * inverse));
-        s[c] = fmaf(-2.0f * cap, inverse_fast(e + 1.0f), cap);
+        const float x = s[c], u = x * x;
+        const float near = x * fmaf(u, fmaf(u, fmaf(u, series[3].x, series[2].x), series[1].x), series[0].x);
+        if (!(done[c / 32] >> c % 32 & 1)) s[c] = near;
       }
       return;
     }
@@ -381,10 +391,11 @@ struct Scores {
 #pragma unroll
     for (int c = 0; c < N; ++c) s[c] = fmaf(-slope, fabsf(apart + float(c)), s[c]);
   }
-  // Products become scores, but for a factor that is returned.
-  template <int N>
+  // Products become scores, but for a factor that is returned.  (Without kCap there
+  // is none.)
+  template <bool kCap, int N>
   __device__ __forceinline__ float finish(float (&s)[N], float apart) const {
-    if (cap != 0.0f) {
+    if (kCap && cap != 0.0f) {
       capped(s);
     } else if (slope != 0.0f) {
 #pragma unroll

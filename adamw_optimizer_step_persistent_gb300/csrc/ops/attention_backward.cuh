@@ -259,7 +259,7 @@ __device__ __forceinline__ void weights_of(float (&s)[32], uint32_t (&p)[16], co
 template <class E, class Lse>
 __device__ __forceinline__ void weights(float (&s)[32], uint32_t (&p)[16], const Scores& f, float apart,
                                         const Cut& cut, Lse lse) {
-  const float mul = f.finish(s, apart);
+  const float mul = f.finish<true>(s, apart);
   cut.set(s, -INFINITY);
   if (f.cap == 0.0f) weights_of<E, false, false>(s, p, f, mul, apart, lse);
   else if (f.slope == 0.0f) weights_of<E, true, false>(s, p, f, mul, apart, lse);

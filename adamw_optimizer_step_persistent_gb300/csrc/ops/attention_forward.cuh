@@ -50,7 +50,9 @@ struct ForwardBarriers {
 template <int C>
 constexpr size_t kForwardSmem = 1024 + (2 + 2 * kRing) * C * size_t(kBoxBytes) + sizeof(ForwardBarriers);
 
-template <class T, int C>
+// (Capped scores have an instance of their own: with what they take in its loop the
+// others' 8192 tokens took 405 us in a graph in place of 390.)
+template <class T, int C, bool kCap>
 __global__ void __launch_bounds__(kAttentionThreads, 1)
     attention_forward_kernel(const __grid_constant__ ForwardMaps maps, const __grid_constant__ AttentionArgs g) {
   using E = typename T::type;
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       tmem_load32(at_s + 32, s + 32);
       tmem_wait<64>(s);
       const int at = j * kRows + half * 64;  // the first column's key
-      const float mul = f.finish(s, float(at - row));
+      const float mul = f.finish<kCap>(s, float(at - row));
       // (most tiles that need a mask are cut on one side)
       if (mine.all_hi < (j + 1) * kRows) {
         const int hi = span.key_hi - at;
@@ -334,10 +336,10 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
   if (warp == kMultiply) tmem_free(tmem, 512);
 }
 
-template <class T, int C>
+template <class T, int C, bool kCap>
 fadam_status launch_forward(const ForwardMaps& maps, const AttentionArgs& g, cudaStream_t stream) {
-  auto* kernel = attention_forward_kernel<T, C>;
-  if (const fadam_status st = launched_with<attention_forward_kernel<T, C>>("attention")) return st;
+  auto* kernel = attention_forward_kernel<T, C, kCap>;
+  if (const fadam_status st = launched_with<attention_forward_kernel<T, C, kCap>>("attention")) return st;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kForwardSmem<C>));
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
@@ -346,7 +348,9 @@ fadam_status launch_forward(const ForwardMaps& maps, const AttentionArgs& g, cud
 }
 template <class T>
 fadam_status forward_of(const ForwardMaps& maps, const AttentionArgs& g, cudaStream_t stream) {
-  return g.width <= kChunk ? launch_forward<T, 1>(maps, g, stream) : launch_forward<T, 2>(maps, g, stream);
+  if (g.softcap > 0.0f)
+    return g.width <= kChunk ? launch_forward<T, 1, true>(maps, g, stream) : launch_forward<T, 2, true>(maps, g, stream);
+  return g.width <= kChunk ? launch_forward<T, 1, false>(maps, g, stream) : launch_forward<T, 2, false>(maps, g, stream);
 }
 
 }  // namespace fadam_ops

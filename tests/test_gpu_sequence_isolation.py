@@ -39,3 +39,51 @@ def test_back_to_back_calls_in_the_same_workspace(dtype):
             for a, b in zip(alone[i], g):
                 wrong += (a.view(torch.uint8) != b.view(torch.uint8)).sum()
     assert int(wrong) == 0
+
+
+def _all(c, go):
+    kw = _options(c)
+    r = fadam.attention(c.q, c.k, c.v, **kw)
+    return (*r, *fadam.attention_backward(go, c.q, c.k, c.v, r.out, r.lse, **kw))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("bias", [False, True])
+def test_capped_scores_have_their_bits_whatever_lies_beside_them(dtype, bias):
+    """Small scores of a row that sees few of its tile; beside it, not seen, what
+    is far beyond the cap.  (The cap is below the growth at which a row's
+    reference maximum is raised.)"""
+    def case(offsets):
+        return _case(400, 4, 2, 64, dtype, seed=5, size=0.3, softcap=2.0, offsets=offsets, bias=bias)
+
+    def large(n, seed):
+        return [(_rand(_gen(seed + i), n, h, 64) * 40).to(dtype) for i, h in enumerate((4, 2, 2))]
+
+    go = (_rand(_gen(4), 400, 4, 64) * 1e-2).to(dtype)
+    # padding, of finite numbers and of any
+    c = case([40, 130, 333])
+    want = _all(c, go)
+    live = slice(40, 333)
+    for fill in (None, float("inf"), float("nan")):
+        for rows in (slice(0, 40), slice(333, 400)):
+            n = rows.stop - rows.start
+            for t, x in zip((c.q, c.k, c.v), large(n, 7)):
+                t[rows] = x if fill is None else fill
+        for a, b in zip(want, _all(c, go)):
+            assert torch.equal(a[live], b[live])
+    # a document in the same tiles
+    c = case([0, 70, 200, 400])
+    want = _all(c, go)
+    for t, x in zip((c.q, c.k, c.v), large(130, 9)):
+        t[70:200] = x
+    for a, b in zip(want, _all(c, go)):
+        for rows in (slice(0, 70), slice(200, 400)):
+            assert torch.equal(a[rows], b[rows])
+    # later tokens of the same document
+    c = case([0, 400])
+    kw = _options(c)
+    want = fadam.attention(c.q, c.k, c.v, **kw)
+    for t, x in zip((c.q, c.k, c.v), large(250, 11)):
+        t[150:] = x
+    for a, b in zip(want, fadam.attention(c.q, c.k, c.v, **kw)):
+        assert torch.equal(a[:150], b[:150])
