@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         *told = most;
         group_sync(pair, 64);
         most = fmaxf(most, *other);
-        const float now = fmaxf(top, most);
+        // (a row that has not grown itself keeps its reference, and with it its bits)
+        const float now = most > top + kGrowth ? most : top;
         const float factor = now == -INFINITY ? 1.0f : exp2_fast(top - now);
         top = now;
         sum *= factor;

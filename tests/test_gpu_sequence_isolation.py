@@ -87,3 +87,27 @@ def test_capped_scores_have_their_bits_whatever_lies_beside_them(dtype, bias):
         t[150:] = x
     for a, b in zip(want, fadam.attention(c.q, c.k, c.v, **kw)):
         assert torch.equal(a[:150], b[:150])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("kw", [{}, dict(bias=True), dict(softcap=60.0)])
+def test_rows_have_their_bits_whatever_their_neighbours_grow_to(dtype, kw):
+    """Rows whose scores grow a little from tile to tile, beside rows whose scores
+    grow by much: those of another document, and later ones of their own."""
+    c = _case(700, 4, 2, 64, dtype, seed=6, size=0.8, offsets=[0, 300, 330, 700], **kw)
+    along = _rand(_gen(9), 64)
+    small = c.k.float() + along * (torch.arange(700, device="cuda")[:, None, None] // 128) * 0.1
+    c = c._replace(k=small.to(dtype), q=(c.q.float() + 0.3 * along).to(dtype))
+    kw = _options(c)
+    want = fadam.attention(c.q, c.k, c.v, **kw)
+    # a document of 30 tokens whose tile holds the others' rows
+    large = c._replace(k=c.k.clone(), q=c.q.clone())
+    large.k[300:330] *= 6
+    large.q[300:330] *= 6
+    for a, b in zip(want, fadam.attention(large.q, large.k, large.v, **kw)):
+        assert torch.equal(a[:300], b[:300]) and torch.equal(a[330:], b[330:])
+    # later tokens of a document: they see the tiles that earlier ones see, with larger scores
+    large = c._replace(q=c.q.clone())
+    large.q[600:] *= 5
+    for a, b in zip(want, fadam.attention(large.q, large.k, large.v, **kw)):
+        assert torch.equal(a[:600], b[:600])
