@@ -303,7 +303,7 @@ fadam_status check(const fadam_attention* d) {
   if (!(d->scale > 0.0f) || !finite(d->scale)) return fail(FADAM_EINVAL, "scale is not finite and above 0");
   if (!(d->softcap >= 0.0f) || !finite(d->softcap)) return fail(FADAM_EINVAL, "softcap is not finite and at least 0");
   if (d->softcap > 0.0f) {
-    // (the square of the cap, and the last factor of tanh's series, in fp32)
+    // (the square of the cap in fp32, and no cap that has nothing to do with the scores)
     const double y = double(d->scale) / d->softcap;
     if (d->softcap < 1e-15f || d->softcap > 1e15f || d->softcap * y * y * y * y * y * y * y > 1e37)
       return fail(FADAM_EINVAL, "softcap %g with scale %g", d->softcap, d->scale);
@@ -411,11 +411,10 @@ AttentionArgs arguments(const fadam_attention& d, const Layout& l, const DeviceF
   g.scale = d.scale;
   g.softcap = d.softcap;
   if (d.softcap > 0.0f) {
-    // cap tanh(y), y = x scale / cap: tanh's Taylor series
-    const double y = double(d.scale) / d.softcap;
-    double c = double(d.softcap) * y * 1.4426950408889634;
+    // cap tanh(y), y = x scale / cap: x scale tanh(y) / y by tanh's Taylor series
     const double taylor[4] = {1.0, -1.0 / 3.0, 2.0 / 15.0, -17.0 / 315.0};
-    for (int i = 0; i < 4; ++i, c *= y * y) g.series[i].x = g.series[i].y = float(c * taylor[i]);
+    for (int i = 0; i < 4; ++i)
+      g.series[i].x = g.series[i].y = float(double(d.scale) * 1.4426950408889634 * taylor[i]);
   }
   g.slopes = d.slopes;
   g.spans = l.spans;

@@ -342,12 +342,14 @@ struct Scores {
   }
   // Products become capped scores, cap tanh(s / cap).  Those up to a quarter of the
   // cap by tanh's Taylor series to the seventh power (off by 9e-8 of the cap there):
-  // five multiplications for two scores.  Those beyond it by 1 - 2 / (exp(2 y) + 1),
+  // six multiplications for two scores.  (In powers of the product itself they are
+  // five, but the factors of a wide cap's higher powers are then below fp32's
+  // numbers.)  Those beyond it by 1 - 2 / (exp(2 y) + 1),
   // whose exponential and reciprocal take three times the time of the softmax's own
   // exponential, and which a warp without any leaves out.  Each score's form is its
   // own: what lies beside it, seen or not, changes no bit of it.  (4096 packed
-  // tokens, 32 heads of 128, in a graph: with a cap of 50, which no score comes near, forward 58 us
-  // and backward 154; with one of 2, where every warp has scores beyond, 91 and 197,
+  // tokens, 32 heads of 128, in a graph: with a cap of 50, which no score comes near, forward 60 us
+  // and backward 158; with one of 2, where every warp has scores beyond, 93 and 201,
   // and 68 and 171 as long as these warps took the second form for all of theirs.)
   template <int N>
   __device__ __forceinline__ void capped(float (&s)[N]) const {
@@ -368,7 +370,7 @@ struct Scores {
         }
 #pragma unroll
       for (int c = 0; c < N; ++c) {
-        const float x = s[c], u = x * x;
+        const float x = s[c], y = x * inverse, u = y * y;
         const float near = x * fmaf(u, fmaf(u, fmaf(u, series[3].x, series[2].x), series[1].x), series[0].x);
         if (!(done[c / 32] >> c % 32 & 1)) s[c] = near;
       }
@@ -379,7 +381,7 @@ struct Scores {
     for (int i = 0; i < 4; ++i) of[i] = make_pair(series[i].x, series[i].y);
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const Pair x = make_pair(s[c], s[c + 1]), u = mul2(x, x);
+      const Pair x = make_pair(s[c], s[c + 1]), y = mul2(x, both(inverse)), u = mul2(y, y);
       const float2 v = split(mul2(x, fma2(u, fma2(u, fma2(u, of[3], of[2]), of[1]), of[0])));
       s[c] = v.x;
       s[c + 1] = v.y;

@@ -20,7 +20,8 @@ struct AttentionArgs {
   int causal;
   int pair_heads;                              // forward: a CTA's two tiles are the same rows of two heads
   float scale, softcap;
-  float2 series[4];          // capped scores in units of log 2 near zero: of x, x^3, x^5, x^7, twice each
+  float2 series[4];          // capped scores in units of log 2 near zero, for products x that are y caps: of x, x y^2,
+                             // x y^4, x y^6, twice each
   const float* slopes;
   const Spans* spans;        // [tokens] where there are documents
   const int* order;          // forward: of what a CTA takes, or NULL: last ones first

@@ -1,0 +1,35 @@
+"""Attention at the ends of what its arguments allow, against the 64-bit forms."""
+import math
+
+import pytest
+import torch
+
+import adamw_optimizer_step_persistent_gb300 as fadam
+from tests import sequence_reference as ref
+from tests.test_gpu_sequence import BF16, F16, _case, _check, _gen, _no_wait_gave_up, _options, _rand, _shaped  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("softcap", [1e4, 1e9, 1e12, 1e15])
+def test_attention_wide_caps(softcap):
+    """Caps far beyond the scores, which then are what they are without one, and
+    products that come near such a cap."""
+    c = _case(300, 4, 2, 64, BF16, seed=1, softcap=softcap)
+    shaped = [_shaped(c, t) for t in (c.q, c.k, c.v)]
+    r = fadam.attention(*shaped, **_options(c))
+    # tanh(y) is y but for y^3 / 3, and y is below 1e-2
+    out, lse, _ = ref.attention(c._replace(softcap=0.0))
+    cubes = float((c.scale * torch.einsum("ihd,jhd->hij", c.q.double(), c.k.double().repeat_interleave(2, 1))).abs()
+                  .max()) ** 3 / 3 / softcap ** 2
+    ref.Bounded(lse.value, lse.off + cubes).holds(r.lse.view(300, 4), "lse")
+    ref.Bounded(out.value, out.off + 2 * cubes * c.v.double().abs().max()).holds(r.out.view(c.q.shape), "out")
+    # up to about a quarter of the cap and beyond it
+    for top in (0.2, 1.0):
+        big = math.sqrt(top * softcap / 32.0)
+        c = ref.Case(*((_rand(_gen(i), 200, h, 64) * s).to(BF16) for i, (h, s) in enumerate(((4, big), (2, big), (2, 1.0)))),
+                     1.0, softcap=softcap, sequence=200)
+        shaped = [_shaped(c, t) for t in (c.q, c.k, c.v)]
+        r = fadam.attention(*shaped, **_options(c))
+        _, lse, _ = ref.attention(c)
+        lse.holds(r.lse.view(200, 4), f"lse of scores up to {top} caps")
