@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 // What is added to a row's scores, -lse in units of log 2 and the lift of p's
 // exponent, and to its grad_out . v: -delta = -grad_out . out, 16 lanes to a
 // row.  Rows that see nothing, and those up to a whole tile, get -infinity: p
-// is 0.  For fp16 (kPeak) also the row's largest |grad_out|, and the documents'
+// is 0.  (Their lse is -infinity, but so is that of a row that sees keys whose
+// scores all are: its gradients are NaN.)  For fp16 (kPeak) also the row's largest |grad_out|, and the documents'
 // peaks (their largest finite ones: atomics of a maximum, whose order changes
 // nothing); blocks behind those of the rows take the sums of v's magnitudes.
 constexpr int kStatRows = 64;  // tokens of a CTA, of one head: 16 at a time
@@ -189,14 +190,17 @@ __global__ void __launch_bounds__(kThreads)
   }
   float l[kTurns];
   int entry[kTurns];
+  bool lives[kTurns];
 #pragma unroll
   for (int r = 0; r < kTurns; ++r) {
     const int t = token0 + r * 16 + group;
-    if (kPeak) entry[r] = entry_of(g, t).at;
+    const Entry e = entry_of(g, t);
+    entry[r] = e.at;
     a[r] = zero_raw<E>();
     b[r] = zero_raw<E>();
-    l[r] = t < g.tokens ? g.lse[int64_t(t) * heads + head] : -INFINITY;
-    if (l[r] != -INFINITY && lane * 8 < width) {
+    lives[r] = e.lives;
+    l[r] = e.lives ? g.lse[int64_t(t) * heads + head] : 0.0f;
+    if (e.lives && lane * 8 < width) {
       a[r] = out.load(t, head, lane * 8);
       b[r] = grad.load(t, head, lane * 8);
     }
@@ -225,11 +229,11 @@ __global__ void __launch_bounds__(kThreads)
     }
     const int t = token0 + r * 16 + group;
     if (lane == 0) {  // (there is a place for every row of a tile)
-      g.stats[head * pitch + t] = l[r] == -INFINITY ? -INFINITY : lift - l[r] * kLog2e;
+      g.stats[head * pitch + t] = lives[r] ? lift - l[r] * kLog2e : -INFINITY;
       g.stats[(int64_t(heads) + head) * pitch + t] = -delta;
       if constexpr (kPeak) {
         g.stats[(2 * int64_t(heads) + head) * pitch + t] = top;
-        if (l[r] != -INFINITY) {
+        if (lives[r]) {
           count_peak(&shared[0], base, peaks, entry[r], top);
           count_peak(&shared[1], base, peaks + apart, entry[r], fabsf(delta));
         }

@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       *told = sum;
       group_sync(pair, 64);
       sum = half ? *other + sum : sum + *other;
-      const bool none = begin >= end || sum == 0.0f;
+      // (a row that sees keys whose scores are all -infinity is NaN, 0 times infinity,
+      // as an infinity elsewhere makes it)
+      const bool none = span.key_lo >= span.key_hi;
       const float inverse = 1.0f / sum;
       if (ok) ok = bar_wait(shared_addr(begin < end ? &bars->done[t] : &bars->q_full[t]), 0, g.status);
       fence_after_sync();

@@ -33,3 +33,30 @@ def test_attention_wide_caps(softcap):
         r = fadam.attention(*shaped, **_options(c))
         _, lse, _ = ref.attention(c)
         lse.holds(r.lse.view(200, 4), f"lse of scores up to {top} caps")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_a_row_of_scores_that_are_all_minus_infinity_is_not_an_empty_one(dtype):
+    """exp(s - lse) of the formula is then exp(-inf + inf): NaN, out and its
+    gradients, as with a score of +infinity; not the zeros of a row that sees
+    nothing."""
+    for offsets in (None, [0, 300]):
+        c = _case(300, 2, 1, 64, dtype, seed=4, offsets=offsets)
+        c.k[:6, 0, 3] = -1.5
+        c.q[5, 1, 3] = math.inf
+        shaped = [_shaped(c, t) for t in (c.q, c.k, c.v)]
+        kw = _options(c)
+        r = fadam.attention(*shaped, **kw)
+        out, lse = r.out.view(c.q.shape), r.lse.view(300, 2)
+        assert torch.isnan(out[5, 1]).all() and float(lse[5, 1]) == -math.inf
+        assert torch.isfinite(out[:5]).all() and torch.isfinite(out[5, 0]).all() and torch.isfinite(out[6:]).all()
+        go = torch.full_like(r.out, 1e-2)
+        d = fadam.attention_backward(go, *shaped, r.out, r.lse, **kw)
+        assert torch.isnan(d.q.view(c.q.shape)[5, 1]).all()
+        assert not torch.isfinite(d.k).all() and not torch.isfinite(d.v).all()
+    # a row of no document beside them keeps its zeros
+    c = _case(300, 2, 1, 64, dtype, seed=4, offsets=[10, 290])
+    c.k[10:16, 0, 3] = -1.5
+    c.q[15, 1, 3] = math.inf
+    r = fadam.attention(c.q, c.k, c.v, **_options(c))
+    assert torch.isnan(r.out[15, 1]).all() and (r.out[:10] == 0).all() and (r.lse[:10] == -math.inf).all()
