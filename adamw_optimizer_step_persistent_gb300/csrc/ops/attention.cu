@@ -352,16 +352,23 @@ struct Layout {
 bool several(const fadam_attention& d) { return d.documents || d.tokens > d.sequence; }
 // Whether the forward pass takes its tiles in order of their work, longest first,
 // rather than from the last one back (which is that order for one sequence): for
-// several sequences that give no more than two CTAs to an SM, so that a long one
-// at the end shows.  5 of 777 with 12 heads of 64 (192 CTAs) take 23.6 us so and
-// 26.0 from the last one back; with more CTAs the order's launch and sequences
-// that take turns in L2 cost more than it gives: 4 of 1024 (512 CTAs) 48.2 and
-// 46.7, 8 of 2048 (1024) 141 and 137, 11 documents in 4096 tokens (512) 56.5 and
-// 53.2, though 13 in 16384 (1024) 159 and 164.
+// several sequences whose CTAs come to some SMs twice, so that a long one at the
+// end shows.  With up to one CTA to an SM all start at once and the order's launch
+// is lost: 3 of 400 with 16 heads (80 CTAs) take 13.7 us sorted and 11.6 as they
+// come, 5 of 777 with 8 (128) 20.7 and 18.6, 4 documents in 1500 tokens (144) 18.7
+// and 17.5.  Up to two: 5 of 777 with 12 heads (192) 24.4 and 27.3, over 4 key
+// heads 26.1 and 29.5, 11 documents in 4096 tokens (192, 256) 22.5 and 23.8, 26.4
+// and 32.9, 4 of 1024 (256) 28.3 and 29.3, 3 of 700 (288) 29.3 both; but 2 of 1024
+// (256) 25.8 and 23.4.  Beyond, sequences that take turns in L2 cost more than the
+// order gives: 4 of 600 (320) 28.4 and 27.6, 3 of 1000 (384) 41.5 and 39.3, 4 of
+// 1024 (512) 48.2 and 46.7, 8 of 2048 (1024) 141 and 137, 11 documents in 4096
+// tokens (512) 56.5 and 53.2, though 13 in 16384 (1024) 159 and 164.
 bool ordered(const fadam_attention& d, int sm_count) {
   const int64_t ctas = ceil_div(d.tokens, 2 * kRows) * d.heads;
-  return several(d) && ctas <= 2 * int64_t(sm_count);
+  return several(d) && ctas > sm_count && ctas <= 2 * int64_t(sm_count);
 }
+// (The order has its place whether or not it is asked for: how large a workspace
+// is depends on no device.)
 Layout layout(const fadam_attention& d, char* base) {
   Layout l{};
   Carver c{base};

@@ -60,3 +60,12 @@ def test_a_row_of_scores_that_are_all_minus_infinity_is_not_an_empty_one(dtype):
     c.q[15, 1, 3] = math.inf
     r = fadam.attention(c.q, c.k, c.v, **_options(c))
     assert torch.isnan(r.out[15, 1]).all() and (r.out[:10] == 0).all() and (r.lse[:10] == -math.inf).all()
+
+
+@pytest.mark.parametrize("H,Hk", [(35, 35), (36, 18), (56, 56)])
+def test_attention_tiles_in_order_of_their_work(H, Hk):
+    """Several sequences and documents of one to two CTAs to an SM, whose tiles
+    are sorted by their work: one head or two to a CTA."""
+    for kw in (dict(sequence=200), dict(sequence=200, prefix=[0, 30, 200, 1, 128, 77]),
+               dict(offsets=[10, 40, 700, 701, 1190]), dict(offsets=[0, 0, 300, 1200]), dict(offsets=[600, 650])):
+        _check(_case(1200, H, Hk, 16, BF16, seed=H, **kw))
