@@ -111,3 +111,62 @@ def test_rows_have_their_bits_whatever_their_neighbours_grow_to(dtype, kw):
     large.q[600:] *= 5
     for a, b in zip(want, fadam.attention(large.q, large.k, large.v, **kw)):
         assert torch.equal(a[:600], b[:600])
+
+
+@pytest.mark.parametrize("many", [1, 700, 3000])
+def test_an_embedding_sum_does_not_change_with_the_tokens_between_its_rows(many):
+    """A token's rows are added in their order, by groups that the sorted list is
+    cut into: other tokens' rows between them, whose places in that list lie
+    behind, change no bit."""
+    T, D, V = 4096, 72, 50
+    rows = _rand(_gen(3), T, D)
+    together = torch.full((T,), 31, dtype=torch.int64, device="cuda")
+    together[:many] = 4
+    want = fadam.embedding_weight_grad(rows, together, V)
+    for seed in range(4):
+        at = torch.randperm(T, generator=torch.Generator().manual_seed(seed))
+        first = at[:many].sort().values.cuda()
+        rest = at[many:].sort().values.cuda()
+        tokens, spread = torch.empty_like(together), torch.empty_like(rows)
+        tokens[first], tokens[rest] = 4, 5 + torch.arange(T - many, device="cuda") % 45
+        spread[first], spread[rest] = rows[:many], rows[many:]
+        got = fadam.embedding_weight_grad(spread, tokens, V)
+        assert torch.equal(got[4], want[4])
+
+
+def test_calls_of_two_threads_have_their_bits_every_time():
+    """Two shapes from two host threads at once: every call's results, not the
+    last one's alone."""
+    import threading
+    cases = [_case(900, 4, 2, 128, BF16, seed=1, offsets=[0, 300, 870], softcap=9.0),
+             _case(650, 6, 3, 64, F16, seed=2, offsets=[20, 600], bias=True)]
+    tokens = torch.randint(0, 40, (650,), generator=_gen(4), device="cuda")
+
+    def run(c, kw):
+        r = fadam.attention(c.q, c.k, c.v, **kw)
+        d = fadam.attention_backward(r.out, c.q, c.k, c.v, r.out, r.lse, **kw)
+        return (*r, *d, fadam.embedding_weight_grad(d.q[:650].flatten(1), tokens, 40))
+
+    work = [(c, _options(c)) for c in cases]
+    alone = [run(*w) for w in work]
+    wrong = [torch.zeros((), dtype=torch.int64, device="cuda") for _ in work]
+    torch.cuda.synchronize()
+    errors = []
+
+    def body(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(150):
+                    for a, b in zip(alone[i], run(*work[i])):
+                        wrong[i] += (a.view(torch.uint8) != b.view(torch.uint8)).sum()
+                stream.synchronize()
+        except BaseException as e:      # reported by the test's own thread
+            errors.append(e)
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
+    assert [int(w) for w in wrong] == [0, 0]

@@ -69,3 +69,12 @@ def test_attention_tiles_in_order_of_their_work(H, Hk):
     for kw in (dict(sequence=200), dict(sequence=200, prefix=[0, 30, 200, 1, 128, 77]),
                dict(offsets=[10, 40, 700, 701, 1190]), dict(offsets=[0, 0, 300, 1200]), dict(offsets=[600, 650])):
         _check(_case(1200, H, Hk, 16, BF16, seed=H, **kw))
+
+
+@pytest.mark.parametrize("T,H,Hk,D,dtype,kw", [
+    (8192, 2, 1, 128, BF16, {}), (8192, 1, 1, 64, F16, dict(softcap=30.0)), (8100, 1, 1, 128, F16, dict(bias=True)),
+    (6000, 2, 2, 72, BF16, dict(causal=False)), (8192, 2, 1, 64, BF16, dict(offsets=[5, 900, 8190], prefix=[400, 5000]))])
+def test_attention_walks_over_many_tiles(T, H, Hk, D, dtype, kw):
+    """Up to 64 tiles of keys or queries, and twice as many where heads share
+    their keys: rings and barriers go round many times."""
+    _check(_case(T, H, Hk, D, dtype, seed=T, **kw))
