@@ -90,10 +90,10 @@ class Model:
         self._add(first, **{"post" + name: d.post_weight, "pre" + name: d.pre_weight, "gate" + name: d.gate})
         return d
 
-    def step(self, tokens, targets, documents, first=True):
+    def step(self, tokens, targets, documents=None, first=True):
         """Forward and backward of one micro-batch of packed documents, which
-        start at the offsets `documents`.  Gradients are added to those of the
-        step's earlier micro-batches unless it is the first."""
+        start at the offsets `documents` (none: the tokens are one).  Gradients are
+        added to those of the step's earlier micro-batches unless it is the first."""
         w, g, add = self.w, self.grads, not first
         masks = dict(documents=documents, slopes=self.slopes, softcap=30.0)
         shut = torch.zeros_like(w["norm0"]).view(1, -1)
