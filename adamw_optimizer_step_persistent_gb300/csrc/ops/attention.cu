@@ -17,7 +17,6 @@ struct PlanArgs {
   int tokens, sequence;
   bool causal;
   Spans* spans;        // [tokens], written where there are documents
-  int span_blocks;
   int* order;          // of `tiles` of `rows` queries, or NULL: not asked for
   int rows, tiles;
 };
@@ -448,11 +447,11 @@ fadam_status plan(const fadam_attention& d, const Layout& l, cudaStream_t stream
   p.sequence = d.documents ? 0 : int(d.sequence);
   p.causal = (d.flags & FADAM_ATTENTION_CAUSAL) != 0;
   p.spans = l.spans;
-  p.span_blocks = l.spans ? int(ceil_div(d.tokens, kThreads)) : 0;
   p.order = l.order;
   p.rows = d.heads / d.kv_heads % 2 ? 2 * kRows : kRows;  // (an odd group: 256 rows of one head to a CTA)
   p.tiles = int(ceil_div(d.tokens, p.rows));
-  return launch_chained("attention plan launch", plan_kernel, (p.order != nullptr) + p.span_blocks, kThreads, 0,
+  const int64_t span_blocks = l.spans ? ceil_div(d.tokens, kThreads) : 0;
+  return launch_chained("attention plan launch", plan_kernel, (p.order != nullptr) + span_blocks, kThreads, 0,
                         stream, p);
 }
 

@@ -5,7 +5,9 @@
 // token first (stable, so that every sum has one order), then the sorted list
 // is cut into equal pieces whose sums do not depend on how often a token
 // occurs, and what pieces' ends cut is joined by the last piece that has a part
-// of it.  Rows of no token are zeroed by the sort, which knows them.  (By other
+// of it.  (That one adds a token's parts in turn: 16384 rows of 4096 in bf16 that
+// are all one token are added into fp32 in 135 us, rows of a token each in 116;
+// 2^20 rows of 512 in 3738 and 946.)  Rows of no token are zeroed by the sort, which knows them.  (By other
 // CTAs of the sums' launch it took longer, 37 us for 50021 x 1000 in place of 29:
 // the sums are a chain of loads, each of which then waits behind the zeros.)
 #include "fadam_seq.h"
@@ -21,6 +23,9 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kRange = 1024;    // most tokens of the vocabulary that one CTA sorts by
 constexpr int kLongest = 64;    // most rows of a piece
 constexpr int kZeroBytes = 16384;  // of a row zeroed by one bulk copy
+// GB300's.  (What depends on it, and with it a sum's groups and the size of the
+// workspace, depends on no device that is asked.)
+constexpr int kSms = 152;
 
 // Eight elements in one access: 16 bytes, or 32 for fp32 (two of 16 would each
 // touch half of every 32-byte sector).
@@ -163,8 +168,10 @@ struct SortArgs {
 // and those below its range, which says where its part of the order begins;
 // then it places them.  Nothing is exchanged between CTAs, and the order is
 // stable: within a warp's 32 rows a row comes behind those of its token in
-// lower lanes.  Of T rows 152 x 16 T bytes come from L2, where a sort by digits
-// would take three launches or more (1037 rows over 50021: some 8000 cycles).
+// lower lanes.  Of T rows every CTA reads 16 T bytes, from L2 mostly: there is one
+// to an SM for vocabularies up to 1024 tokens an SM, and one for each 1024 tokens
+// beyond.  A sort by digits would take three launches or more (1037 rows over
+// 50021: some 8000 cycles).
 // At the end (unless kKeep) rows of no token are zeroed, by bulk copies where
 // they allow it: 131072 x 4096 in fp32 from 16384 rows 320 us, 6.1 TB/s.
 template <class Out, bool kWide, bool kKeep>
@@ -441,7 +448,7 @@ fadam_status forward(const fadam_embed& d, cudaStream_t stream) {
                     eights(d.out, d.out_stride, d.width, sizeof(Out));
   const Parts p = parts_of(d.width);
   // four rows to a thread where that leaves every SM four CTAs
-  const bool many = ceil_div(d.rows, 4) * p.count >= 152 * 4;
+  const bool many = ceil_div(d.rows, 4) * p.count >= kSms * 4;
   auto* kernel = wide ? (many ? gather_kernel<E, Out, true, 4> : gather_kernel<E, Out, true, 1>)
                       : (many ? gather_kernel<E, Out, false, 4> : gather_kernel<E, Out, false, 1>);
   return launch_chained("embedding launch", kernel, ceil_div(d.rows, many ? 4 : 1) * p.count, p.threads, 0,
@@ -465,7 +472,7 @@ Layout layout(const fadam_embed_grad& d, char* base) {
   Carver c{base};
   const Parts p = parts_of(d.width);
   // pieces as long as leave every SM eight CTAs, 4 to 64 rows
-  const int64_t per = d.rows * p.count / (152 * 8);
+  const int64_t per = d.rows * p.count / (kSms * 8);
   l.piece = int32_t(per < 4 ? 4 : per > kLongest ? kLongest : per);
   l.pieces = ceil_div(d.rows, l.piece);
   l.carry_ld = int64_t(p.count) * p.threads * 8;

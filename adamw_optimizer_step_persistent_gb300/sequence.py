@@ -15,7 +15,7 @@ import torch
 
 from . import _abi
 from .optimizer import _ptr, dtype_code
-from .training import (_16BIT, _check_device, _current, _device, _like, _rows, _stream, _workspace)
+from .training import _16BIT, _check_device, _current, _device, _rows, _stream, _workspace
 
 
 class Attention(NamedTuple):

@@ -7,7 +7,9 @@
  *   fadam_attention_*   attention over packed documents, forward and backward
  *
  * Conventions, workspaces, statuses and messages are those of fadam_ops.h
- * (fadam_ops_last_error, fadam_ops_status).
+ * (fadam_ops_last_error, fadam_ops_status).  No output overlaps an input, another
+ * output or the workspace: a launch may still read one where another part of it
+ * has written the other.
  */
 #ifndef FADAM_SEQ_H_
 #define FADAM_SEQ_H_
@@ -110,8 +112,12 @@ fadam_status fadam_embed_grad_run(const fadam_embed_grad* desc, void* workspace,
  * Scores and sums are fp32; exp(s - m), for a running m, is rounded to dtype
  * for the product with v.  Documents that share 128 consecutive tokens (from a
  * multiple of 128) share tensor-core operands: an infinity or a NaN in a k or
- * v row can reach other rows of those, and rows before it of its own document.
- * Rows outside all documents reach nothing, whatever they hold.  Documents that
+ * v row can reach other rows of those, and rows before it of its own document
+ * (backward one in a q or grad_out row their grad_k and grad_v, too).  What is
+ * finite changes no bit of a row that does not see it (fp16's gradients: of one of
+ * another document).  Rows outside all documents reach nothing, whatever they hold.
+ * A row that sees keys, all of whose scores are -infinity, gets NaN and lse
+ * -infinity.  Documents that
  * decrease or lie outside give undefined results, within the outputs. */
 typedef struct {
   const void* q;
