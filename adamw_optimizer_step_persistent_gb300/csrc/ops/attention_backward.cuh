@@ -24,11 +24,11 @@
 // (A warp may be a turn ahead of another one when it has written ds, which is
 // why that has a barrier for even and one for odd turns.)
 //
-// Bound by the tensor cores: a turn of the keys' kernel takes 2600 cycles, its
-// products alone 2236; one of the queries' 2000, alone 1700 to 1940.  8192 causal
-// tokens, 32 heads of 128, bf16: 1240 us in a burst (670 and 520, stats 26), 1.1
-// PFLOP/s of the five products that a pass cannot do without, 1.55 of the seven;
-// 1320 to 1350 in a row, at the card's power limit.
+// Bound by the tensor cores: a turn of keys takes 2600 cycles, its products alone
+// 2236; one of queries 2000, alone 1700 to 1940.  8192 causal tokens, 32 heads of
+// 128, bf16: 1210 to 1240 us in a graph (26 of them the statistics), 1.1 PFLOP/s of
+// the five products that a pass cannot do without, 1.6 of the seven; 1344 to 1385
+// back to back, at the card's power limit.
 #pragma once
 
 #include "attention.cuh"

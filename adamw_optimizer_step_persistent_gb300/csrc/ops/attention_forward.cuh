@@ -17,13 +17,13 @@
 // work for the other, each fed by a warp of its own.  (One warp for both left
 // them idle during its waits: 4000 cycles a turn of both tiles.)  The two pass a
 // token: left alone, both tiles' products ran at the same time, and then both
-// tiles' scores were worked on at the same time (4040; 3030 with the token).
+// tiles' scores were worked on at the same time (4040; 3230 with the token).
 //
 // Bound by the chain of a tile's turn, some 1300 cycles for the scores and 1500
 // for its two products: from shared memory both operands of Q K^T come at 687
 // cycles for 128 x 128 x 128 where P V's one takes 569 and the tensor cores
-// alone would take 512.  8192 causal tokens, 32 heads of 128, bf16: 395 us, 1.39
-// PFLOP/s of what is not masked, tensor cores 65% active.
+// alone would take 512.  8192 causal tokens, 32 heads of 128, bf16: 392 us in a
+// graph, 1.40 PFLOP/s of what is not masked, 423 back to back; tensor cores 58% active.
 //
 // The running maximum of a row need not be its true maximum: any reference
 // gives the same quotient.  So O (in tensor memory) and the sum are only

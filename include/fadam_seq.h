@@ -28,7 +28,7 @@ extern "C" {
 #define FADAM_EMBED_PADDING 1u    /* padding_index counts */
 #define FADAM_EMBED_ACCUMULATE 2u /* the gradient is added to out, else written */
 
-/* out_t = scale * weight_tokens[t], rounded once; zero where tokens[t] ==
+/* out_t = scale * weight_tokens[t] in fp32, rounded to out_dtype; zero where tokens[t] ==
  * padding_index, NaN where a token lies outside [0, vocab) (the loss turns into
  * NaN, and the shard's screen or norm into a skipped step).
  *   tokens [rows]           int64
