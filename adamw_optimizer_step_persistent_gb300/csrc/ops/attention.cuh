@@ -2,6 +2,8 @@
 // single CTA, boxes of a head's rows, scores and masks.
 #pragma once
 
+#include <atomic>
+
 #include "attention_internal.h"
 #include "ops_device.cuh"
 #include "rows.cuh"
@@ -16,15 +18,19 @@ constexpr int kMultiply = kScoreWarps, kLoad = kMultiply + 1, kMultiply2 = kMult
 constexpr int kLaunchRegisters = 96, kScoreRegisters = 104, kOtherRegisters = 64;
 static_assert(4 * kScoreRegisters + kOtherRegisters == 5 * kLaunchRegisters, "no more than launched with");
 static_assert(kLaunchRegisters * kAttentionThreads <= 65536, "an SM's registers");
-// A kernel built with fewer would wait for its share of registers for ever.
+// A kernel built with fewer would wait for its share of registers for ever.  (Asked
+// once a process; a question that failed, for lack of memory, say, is asked again.)
 template <auto kKernel>
 fadam_status launched_with(const char* what) {
-  static const int registers = [] {
-    cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, kKernel) == cudaSuccess ? f.numRegs : -1;
-  }();
-  if (registers == kLaunchRegisters) return FADAM_OK;
-  return fail(FADAM_ECUDA, "%s was built with %d registers a thread, not %d", what, registers, kLaunchRegisters);
+  static std::atomic<bool> right{false};
+  if (right.load(std::memory_order_relaxed)) return FADAM_OK;
+  cudaFuncAttributes f{};
+  const cudaError_t e = cudaFuncGetAttributes(&f, kKernel);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+  if (f.numRegs != kLaunchRegisters)
+    return fail(FADAM_ECUDA, "%s was built with %d registers a thread, not %d", what, f.numRegs, kLaunchRegisters);
+  right.store(true, std::memory_order_relaxed);
+  return FADAM_OK;
 }
 
 constexpr int kBoxBytes = kRows * kChunk * 2;  // 128 rows of 128 bytes, 128-byte swizzle

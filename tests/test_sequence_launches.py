@@ -3,6 +3,8 @@ operators' sources have to keep to, by reading them (no GPU)."""
 import glob
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 
@@ -63,3 +65,51 @@ def test_every_thread_waits_for_the_launch_before(at):
     it stands in the kernel's (or its CTAs') outermost block, behind no condition."""
     assert _waits(at)
     assert not re.search(r"if \([^\n]*\)\s*chain_wait\(\)", FUNCTIONS[at][1])
+
+
+NVCC = "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else shutil.which("nvcc")
+
+
+@pytest.mark.skipif(NVCC is None, reason="no nvcc")
+def test_a_failed_question_for_a_kernels_registers_is_asked_again(tmp_path):
+    """With a runtime call of the test's own that fails once: the second call of
+    the operator is not refused for the first one's failure."""
+    src = tmp_path / "ask.cu"
+    src.write_text("""
+#include <stdarg.h>
+#include <stdio.h>
+#include "ops/attention.cuh"
+static int asked = 0, registers = 96;
+extern "C" int answer(cudaFuncAttributes* f) {
+  if (++asked == 1) return cudaErrorMemoryAllocation;
+  f->numRegs = registers;
+  return cudaSuccess;
+}
+namespace fadam_ops {
+fadam_status fail(fadam_status st, const char* fmt, ...) { return st; }
+fadam_status cuda_fail(cudaError_t, const char*) { return FADAM_ECUDA; }
+}
+template <int N> __global__ void kernel() {}
+int main() {
+  using fadam_ops::launched_with;
+  const int first = launched_with<kernel<0>>("it"), second = launched_with<kernel<0>>("it");
+  const int third = launched_with<kernel<0>>("it"), known = asked;
+  registers = 95;
+  const int other = launched_with<kernel<1>>("it"), again = launched_with<kernel<1>>("it");
+  printf("%d %d %d %d %d %d", first, second, third, known, other, again);
+}
+""")
+    own = tmp_path / "own.cpp"
+    own.write_text("""
+extern "C" int answer(void*);
+extern "C" int cudaFuncGetAttributes(void* f, const void*) { return answer(f); }
+""")
+    root = os.path.dirname(os.path.dirname(os.path.dirname(OPS)))
+    exe = str(tmp_path / "ask")
+    subprocess.run([NVCC, "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-cudart", "shared",
+                    "-I", os.path.dirname(OPS), "-I", os.path.join(root, "include"), str(src), str(own), "-o", exe],
+                   check=True, capture_output=True)
+    env = dict(os.environ, LD_LIBRARY_PATH=os.path.join(os.path.dirname(os.path.dirname(NVCC)), "lib64"))
+    out = subprocess.run([exe], check=True, capture_output=True, text=True, env=env).stdout
+    failed = 4      # FADAM_ECUDA
+    assert out == f"{failed} 0 0 2 {failed} {failed}"
