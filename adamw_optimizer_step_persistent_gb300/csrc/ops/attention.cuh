@@ -50,6 +50,19 @@ struct Place {
   }
 };
 
+// A wait of a whole warp: all lanes have one answer, also when it gives up, so that
+// they meet at the next instruction that takes all of them.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, unsigned parity, int* status) {
+  if (__all_sync(~0u, bar_try(bar, parity))) return true;
+  const unsigned long long t0 = now_ns();
+  while (!__all_sync(~0u, bar_try(bar, parity)))
+    if (__any_sync(~0u, now_ns() - t0 > kWaitNs)) {
+      atomicExch(status, FADAM_ETIMEOUT);
+      return false;
+    }
+  return true;
+}
+
 // ---- copies -----------------------------------------------------------------------------
 
 __device__ __forceinline__ void load_head_box(uint32_t dst, const CUtensorMap* map, int x, int head,

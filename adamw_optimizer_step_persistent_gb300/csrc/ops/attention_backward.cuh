@@ -166,10 +166,10 @@ struct Backward {
   __device__ __forceinline__ uint32_t x_at(int at) const { return x + at * kTile; }
   __device__ __forceinline__ uint32_t y_at(int at) const { return y + at * kTile; }
   __device__ __forceinline__ bool wait_x(const Place<kRingX>& p, int* status) const {
-    return bar_wait(shared_addr(&bars->x_full[p.at]), p.parity, status);
+    return warp_wait(shared_addr(&bars->x_full[p.at]), p.parity, status);
   }
   __device__ __forceinline__ bool wait_y(const Place<kRingY>& p, int* status) const {
-    return bar_wait(shared_addr(&bars->y_full[p.at]), p.parity, status);
+    return warp_wait(shared_addr(&bars->y_full[p.at]), p.parity, status);
   }
 
   // The loading thread: the CTA's own two tiles, while the others find out what
@@ -359,7 +359,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
       const auto clean = [&](uint32_t at) {
         if (g.documents) clean_rows<C>(at, query * kRows, g);
       };
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && b.wait_x(x, status) && b.wait_y(y, status);
+      bool ok = warp_wait(shared_addr(&bars->own_full), 0, status) && b.wait_x(x, status) && b.wait_y(y, status);
       if (ok) {
         clean(b.x_at(0));
         clean(b.y_at(0));
@@ -378,7 +378,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
           ok = b.wait_x(next_x, status);
           if (ok) clean(b.x_at(next_x.at));
         }
-        ok = ok && bar_wait(bar_weights, unsigned(i) & 1, status);
+        ok = ok && warp_wait(bar_weights, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
@@ -386,7 +386,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
           commit(shared_addr(&bars->y_empty[y.at]));
           if (more) scores(next_x.at);
         }
-        ok = bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
+        ok = warp_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
@@ -428,7 +428,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
         ok = b.wait_y(y, status);
         if (!ok) break;
         load_pairs(shared_addr(b.extra->lse[y.at] + part * 32), of);
-        ok = bar_wait(bar_scores, unsigned(i) & 1, status);
+        ok = warp_wait(bar_scores, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
         tmem_load32(at_s, s);
@@ -443,7 +443,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
         ok = b.wait_x(x, status);
         if (!ok) break;
         load_pairs(shared_addr(b.extra->delta[x.at] + part * 32), of);
-        ok = bar_wait(bar_dots, unsigned(i) & 1, status);
+        ok = warp_wait(bar_dots, unsigned(i) & 1, status);
         if (!ok) break;
         fence_after_sync();
         float d[32];
@@ -460,7 +460,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
     }
     // eight warps write grad_v (through v's place in shared memory), eight
     // grad_k, half of the elements to four warps
-    if (ok) ok = bar_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
+    if (ok) ok = warp_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
     fence_after_sync();
     const bool keys = part >= 2;
     const float scale = keys ? g.scale * b.inverse_factor(row) : power_of_two(-kLiftBits<T>);
@@ -559,9 +559,9 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
       const int steps = (g.width + 15) / 16;
       const uint32_t bar_read = shared_addr(&bars->scores_read);
       Place<kRingX> x;
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status);
+      bool ok = warp_wait(shared_addr(&bars->own_full), 0, status);
       for (int i = 0; ok && i < n; ++i, x.next()) {
-        ok = b.wait_x(x, status) && (i == 0 || bar_wait(bar_read, unsigned(i - 1) & 1, status));
+        ok = b.wait_x(x, status) && (i == 0 || warp_wait(bar_read, unsigned(i - 1) & 1, status));
         if (!ok) break;
         fence_after_sync();
         if (elect_one()) {
@@ -584,18 +584,18 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
         commit(shared_addr(&bars->dots));
         commit(shared_addr(&bars->y_empty[y.at]));
       };
-      bool ok = bar_wait(shared_addr(&bars->own_full), 0, status) && b.wait_y(y, status);
+      bool ok = warp_wait(shared_addr(&bars->own_full), 0, status) && b.wait_y(y, status);
       fence_after_sync();
       if (ok && elect_one()) dots();
       for (int i = 0; ok && i < n; ++i, x.next()) {
         if (i + 1 < n) {
           y.next();
-          ok = b.wait_y(y, status) && bar_wait(bar_read, unsigned(i) & 1, status);
+          ok = b.wait_y(y, status) && warp_wait(bar_read, unsigned(i) & 1, status);
           if (!ok) break;
           fence_after_sync();
           if (elect_one()) dots();
         }
-        ok = b.wait_x(x, status) && bar_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
+        ok = b.wait_x(x, status) && warp_wait(shared_addr(&bars->slopes[i & 1]), unsigned(i / 2) & 1, status);
         if (!ok) break;
         if (g.documents) clean_rows<C>(b.x_at(x.at), (first + i) * kRows, g);
         fence_after_sync();
@@ -625,7 +625,7 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
       const Cut cut(reach, tile_at, at, span.key_lo, span.key_hi);
       float s[32];
       uint32_t p[16];
-      ok = bar_wait(bar_scores, unsigned(i) & 1, status);
+      ok = warp_wait(bar_scores, unsigned(i) & 1, status);
       if (!ok) break;
       fence_after_sync();
       tmem_load32(at_s, s);
@@ -635,7 +635,7 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
       if (lane == 0) bar_arrive(bar_scores_read);
       weights<E>(s, p, f, float(at - (query0 + row)), cut, [&](int) { return lse; });
 
-      ok = bar_wait(bar_dots, unsigned(i) & 1, status);
+      ok = warp_wait(bar_dots, unsigned(i) & 1, status);
       if (!ok) break;
       fence_after_sync();
       float d[32];
@@ -653,7 +653,7 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
       __syncwarp();
       if (lane == 0) bar_arrive(shared_addr(&bars->slopes[i & 1]));
     }
-    if (ok) ok = bar_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
+    if (ok) ok = warp_wait(shared_addr(n > 0 ? &bars->done : &bars->own_full), 0, status);
     fence_after_sync();
     const float scale = g.scale * b.inverse_factor(row);
     const uint32_t place = b.own0 + (quarter * 32 + lane) * 128;

@@ -22,8 +22,8 @@
 // Bound by the chain of a tile's turn, some 1300 cycles for the scores and 1500
 // for its two products: from shared memory both operands of Q K^T come at 687
 // cycles for 128 x 128 x 128 where P V's one takes 569 and the tensor cores
-// alone would take 512.  8192 causal tokens, 32 heads of 128, bf16: 392 us in a
-// graph, 1.40 PFLOP/s of what is not masked, 423 back to back; tensor cores 58% active.
+// alone would take 512.  8192 causal tokens, 32 heads of 128, bf16: 382 us in a
+// graph, 1.44 PFLOP/s of what is not masked, 423 back to back; tensor cores 58% active.
 //
 // The running maximum of a row need not be its true maximum: any reference
 // gives the same quotient.  So O (in tensor memory) and the sum are only
@@ -166,9 +166,9 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         commit(shared_addr(&bars->k_empty[at]));
       };
       Place<kRing> keys, values;
-      bool ok = bar_wait(shared_addr(&bars->k_full[0]), 0, g.status);
-      if (ok && begin < end) ok = bar_wait(shared_addr(&bars->q_full[t]), 0, g.status);
-      if (ok && t == 1) ok = bar_wait(my_go, 0, g.status);
+      bool ok = warp_wait(shared_addr(&bars->k_full[0]), 0, g.status);
+      if (ok && begin < end) ok = warp_wait(shared_addr(&bars->q_full[t]), 0, g.status);
+      if (ok && t == 1) ok = warp_wait(my_go, 0, g.status);
       fence_after_sync();
       if (ok && elect_one()) scores(first, 0);
       keys.next();
@@ -176,14 +176,14 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       for (int j = first; ok && j < last; ++j) {
         const bool here = j >= begin && j < end, more = j + 1 < last;
         const uint32_t v_at = ring + (2 * values.at + 1) * kTile;
-        ok = bar_wait(shared_addr(&bars->v_full[values.at]), values.parity, g.status);
-        if (ok && more) ok = bar_wait(shared_addr(&bars->k_full[keys.at]), keys.parity, g.status);
+        ok = warp_wait(shared_addr(&bars->v_full[values.at]), values.parity, g.status);
+        if (ok && more) ok = warp_wait(shared_addr(&bars->k_full[keys.at]), keys.parity, g.status);
         if (ok && here) {
           if (g.documents) clean_rows<C>(v_at, j * kRows, g);
-          ok = bar_wait(bar_weights, turn, g.status);
+          ok = warp_wait(bar_weights, turn, g.status);
           turn ^= 1;
         }
-        ok = ok && bar_wait(my_go, go, g.status);
+        ok = ok && warp_wait(my_go, go, g.status);
         go ^= 1;
         if (!ok) break;
         fence_after_sync();
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     for (int j = begin; j < end; ++j) {
       // (after a wait that gave up the turns go on without waiting: the two warps
       // of a pair must meet as often)
-      ok = ok && bar_wait(bar_scores, unsigned(j - begin) & 1, g.status);
+      ok = ok && warp_wait(bar_scores, unsigned(j - begin) & 1, g.status);
       fence_after_sync();
       float s[64];
       tmem_load32(at_s, s);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
       // as an infinity elsewhere makes it)
       const bool none = span.key_lo >= span.key_hi;
       const float inverse = 1.0f / sum;
-      if (ok) ok = bar_wait(shared_addr(begin < end ? &bars->done[t] : &bars->q_full[t]), 0, g.status);
+      if (ok) ok = warp_wait(shared_addr(begin < end ? &bars->done[t] : &bars->q_full[t]), 0, g.status);
       fence_after_sync();
       const uint32_t place = q_tiles + t * kTile + (quarter * 32 + lane) * 128;
 #pragma unroll

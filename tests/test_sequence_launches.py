@@ -113,3 +113,14 @@ extern "C" int cudaFuncGetAttributes(void* f, const void*) { return answer(f); }
     out = subprocess.run([exe], check=True, capture_output=True, text=True, env=env).stdout
     failed = 4      # FADAM_ECUDA
     assert out == f"{failed} 0 0 2 {failed} {failed}"
+
+
+def test_waits_of_whole_warps_have_one_answer():
+    """Elected lanes, loads of tensor memory and group barriers take all lanes of a
+    warp: a wait that gives up does so for all of them.  (One thread alone waits in
+    the warp that loads.)"""
+    for kind in ("keys_cta", "queries_cta"):
+        assert not re.search(r"\bbar_wait\(", FUNCTIONS["attention_backward.cuh", kind][1])
+    body = FUNCTIONS["attention_forward.cuh", "attention_forward_kernel"][1]
+    _, others = body.split("} else if (warp == kMultiply || warp == kMultiply2) {")
+    assert not re.search(r"\bbar_wait\(", others) and "warp_wait(" in others
