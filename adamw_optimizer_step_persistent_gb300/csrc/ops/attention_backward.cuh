@@ -56,7 +56,7 @@ struct BackwardBarriers {
 struct BackwardExtra {
   float lse[kRingY][kRows];     // with Y: read for p, before Y is done with
   float delta[kRingX][kRows];   // with X
-  int8_t exponent[kRows];       // fp16: of the rows' ds, for the end
+  int8_t exponent[kRows];       // of the rows' ds, for the end
   BackwardBarriers bars;
 };
 template <int C>
@@ -139,15 +139,17 @@ struct Backward {
 
   // What a row's ds (2^10 of it, fp16) is multiplied by, and its sums at the end.
   // (The four lanes of a row write the same: each reads what it wrote itself.)
-  __device__ __forceinline__ float keep_factor(int row, float bound) const {
-    if constexpr (T::code != FADAM_DT_F16) return 1.0f;
-    const int exponent = ds_exponent(bound);
-    extra->exponent[row] = int8_t(exponent);
-    return power_of_two(exponent - kLiftBits<T>);
+  // Of a row that is `alone`, whose weights are 1 whatever its scores, the sums are 0
+  // but for what grad_out . v and delta differ by in their roundings.
+  static constexpr int kAlone = -128;
+  __device__ __forceinline__ float keep_factor(int row, float bound, bool alone) const {
+    const int exponent = T::code == FADAM_DT_F16 ? ds_exponent(bound) : 0;
+    extra->exponent[row] = int8_t(alone ? kAlone : exponent);
+    return T::code == FADAM_DT_F16 ? power_of_two(exponent - kLiftBits<T>) : 1.0f;
   }
   __device__ __forceinline__ float inverse_factor(int row) const {
-    if constexpr (T::code != FADAM_DT_F16) return 1.0f;
-    return power_of_two(-int(extra->exponent[row]));
+    const int exponent = extra->exponent[row];
+    return exponent == kAlone ? 0.0f : power_of_two(-exponent);
   }
 
   // What the 128 rows of the CTA need: rows are dealt to the first four warps.
@@ -309,6 +311,8 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
   if (warp < kScoreWarps && key0 + row < g.tokens) span = spans_of(g, key0 + row);
   float bound = 0.0f;
   if (warp < kScoreWarps) bound = key_bound<T>(g, kv, key0 + row);  // (on its way while the CTA meets)
+  // a document of one token
+  const bool alone = span.query_hi - span.query_lo == 1 && span.key_hi - span.key_lo == 1;
   b.load_own(&maps.k, &maps.v, kv, key0);
   const Reach reach = b.meet(span.query_lo, span.query_hi, key0 + row < g.tokens);
   const uint32_t tmem = uniform(bars->tmem);
@@ -413,7 +417,7 @@ __device__ __forceinline__ void keys_cta(unsigned char* smem, const BackwardMaps
     const uint32_t at_s = lanes + kColumnsS + part * 32, at_dots = lanes + kColumnsDots + part * 32;
     const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
     const uint32_t bar_weights = shared_addr(&bars->weights);
-    const float factor = b.keep_factor(row, bound);
+    const float factor = b.keep_factor(row, bound, alone);
     bool ok = true;
     Place<kRingX> x;
     Place<kRingY> y;
@@ -532,6 +536,7 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
   if (warp < kScoreWarps && query0 + row < g.tokens) span = spans_of(g, query0 + row);
   float bound = 0.0f;
   if (warp < kScoreWarps) bound = query_bound<T>(g, head, query0 + row);
+  const bool alone = span.key_hi - span.key_lo == 1;
   b.load_own(&maps.q, &maps.grad_out, head, query0);
   const Reach reach = b.meet(span.key_lo, span.key_hi, query0 + row < g.tokens);
   const uint32_t tmem = uniform(bars->tmem);
@@ -614,7 +619,7 @@ __device__ __forceinline__ void queries_cta(unsigned char* smem, const BackwardM
     const uint32_t bar_scores = shared_addr(&bars->scores), bar_dots = shared_addr(&bars->dots);
     const uint32_t bar_scores_read = shared_addr(&bars->scores_read);
     const uint32_t bar_dots_read = shared_addr(&bars->dots_read);
-    const float factor = b.keep_factor(row, bound);
+    const float factor = b.keep_factor(row, bound, alone);
     const int64_t pitch = int64_t(g.tiles) * kRows;
     const Pair lse = both(g.stats[head * pitch + query0 + row]);
     const Pair delta = both(g.stats[(g.heads + head) * pitch + query0 + row]);

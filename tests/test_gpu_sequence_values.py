@@ -78,3 +78,21 @@ def test_attention_walks_over_many_tiles(T, H, Hk, D, dtype, kw):
     """Up to 64 tiles of keys or queries, and twice as many where heads share
     their keys: rings and barriers go round many times."""
     _check(_case(T, H, Hk, D, dtype, seed=T, **kw))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_a_query_of_one_key_has_no_gradient_by_its_score(dtype):
+    """Its weight is 1 whatever its score: grad_q is 0, not what grad_out . v and
+    grad_out . out differ by in their roundings, and so is grad_k in a document of
+    one token."""
+    cases = [(_case(T, H, Hk, D, dtype, seed=T, sequence=1, **kw), slice(0, T), slice(0, T))
+             for T, H, Hk, D, kw in ((1, 1, 1, 128, {}), (2, 3, 3, 128, dict(causal=False)), (7, 32, 8, 64, dict(softcap=50.0)),
+                                     (300, 6, 2, 72, dict(bias=True)))]
+    some = list(range(0, 140)) + [200, 400]
+    cases.append((_case(400, 4, 2, 64, dtype, seed=3, offsets=some), [*range(0, 139), 139, 200], slice(0, 139)))
+    cases.append((_case(300, 4, 2, 64, dtype, seed=3, sequence=150), [0, 150], slice(0, 0)))
+    for c, queries, keys in cases:
+        r, d = _check(c)
+        assert (d.q.reshape(c.q.shape)[queries] == 0).all()
+        assert (d.k.reshape(c.k.shape)[keys] == 0).all()
+        assert (d.v != 0).any()
