@@ -116,9 +116,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 // exponent, and to its grad_out . v: -delta = -grad_out . out, 16 lanes to a
 // row.  Rows that see nothing, and those up to a whole tile, get -infinity: p
 // is 0.  (Their lse is -infinity, but so is that of a row that sees keys whose
-// scores all are: its gradients are NaN.)  For fp16 (kPeak) also the row's largest |grad_out|, and the documents'
-// peaks (their largest finite ones: atomics of a maximum, whose order changes
-// nothing); blocks behind those of the rows take the sums of v's magnitudes.
+// scores all are: its gradients are NaN.)  For fp16 (kPeak) also the row's largest
+// |grad_out|, and the documents' peaks (their largest finite ones: atomics of a
+// maximum, whose order changes nothing); blocks behind those of the rows take the
+// sums of v's magnitudes.
 constexpr int kStatRows = 64;  // tokens of a CTA, of one head: 16 at a time
 template <class E>
 struct StatRows {

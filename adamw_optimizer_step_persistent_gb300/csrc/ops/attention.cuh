@@ -367,8 +367,8 @@ struct Scores {
   // whose exponential and reciprocal take three times the time of the softmax's own
   // exponential, and which a warp without any leaves out.  Each score's form is its
   // own: what lies beside it, seen or not, changes no bit of it.  (4096 packed
-  // tokens, 32 heads of 128, in a graph: with a cap of 50, which no score comes near, forward 60 us
-  // and backward 158; with one of 2, where every warp has scores beyond, 93 and 201,
+  // tokens, 32 heads of 128, in a graph: with a cap of 50, which no score comes near, forward 61 us
+  // and backward 158; with one of 2, where every warp has scores beyond, 95 and 202,
   // and 68 and 171 as long as these warps took the second form for all of theirs.)
   template <int N>
   __device__ __forceinline__ void capped(float (&s)[N]) const {

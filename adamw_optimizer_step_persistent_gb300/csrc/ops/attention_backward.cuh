@@ -26,8 +26,8 @@
 //
 // Bound by the tensor cores: a turn of keys takes 2600 cycles, its products alone
 // 2236; one of queries 2000, alone 1700 to 1940.  8192 causal tokens, 32 heads of
-// 128, bf16: 1210 to 1240 us in a graph (26 of them the statistics), 1.1 PFLOP/s of
-// the five products that a pass cannot do without, 1.6 of the seven; 1344 to 1385
+// 128, bf16: 1210 to 1250 us in a graph (26 of them the statistics), 1.1 PFLOP/s of
+// the five products that a pass cannot do without, 1.6 of the seven; 1333 to 1360
 // back to back, at the card's power limit.
 #pragma once
 

@@ -23,7 +23,7 @@
 // for its two products: from shared memory both operands of Q K^T come at 687
 // cycles for 128 x 128 x 128 where P V's one takes 569 and the tensor cores
 // alone would take 512.  8192 causal tokens, 32 heads of 128, bf16: 382 us in a
-// graph, 1.44 PFLOP/s of what is not masked, 423 back to back; tensor cores 58% active.
+// graph, 1.44 PFLOP/s of what is not masked, 410 back to back; tensor cores 59% active.
 //
 // The running maximum of a row need not be its true maximum: any reference
 // gives the same quotient.  So O (in tensor memory) and the sum are only
